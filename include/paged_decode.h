@@ -78,6 +78,8 @@ typedef enum {
 #define PKD_DEVERR_LAYOUT 4u    /* a CTA's dynamic shared memory did not start 1024-byte aligned
                                    (the tcgen05 kernel relies on it for its swizzled operands and
                                    then computes nothing for that CTA; not seen on sm_103a) */
+#define PKD_DEVERR_BAD_POSITION 8u /* a rotation position was outside the table (paged_kv_append_rope
+                                      then writes nothing for that token) */
 
 /* How K/V tiles reach the arithmetic.  All variants give the same result. */
 typedef enum {
@@ -559,6 +561,212 @@ pkd_status paged_kv_append(const void* k_new, const void* v_new, const int32_t* 
                            const int32_t* context_lens, void* k_cache, void* v_cache, int num_seqs,
                            int num_kv_heads, int head_dim, int block_size, int num_blocks,
                            int max_blocks_per_seq, int* error_word, cudaStream_t stream);
+
+/*
+ * paged_kv_append_rope -- the step between a layer's projections and its
+ * attention: rotates the new queries and keys by their positions and stores
+ * the keys and values into the paged cache, for any number of new tokens per
+ * sequence (a prompt, draft tokens, or one token each).  Token j of sequence b
+ * is row t = token_starts[b] + j of q, k_new and v_new; with L =
+ * context_lens[b] (the length BEFORE the append) its logical position is
+ * L + j, and for p = positions ? positions[t] : L + j, c_i = rope_table[p][i]
+ * and s_i = rope_table[p][rotary_dim / 2 + i], pair i of a q or k head turns as
+ *   y_a = x_a c_i - x_b s_i,   y_b = x_b c_i + x_a s_i
+ * with (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved; dims
+ * from rotary_dim on, and v, are stored as they are.  Then, for every kv head
+ * g, with B = block_tables[b][(L + j) / block_size]:
+ *   q_out[t][h][:] = y of q,  K[B][g][(L + j) % block_size][:] = y of k,  V[..] = v
+ * computed in fp32 and rounded once.
+ *
+ *   q, k_new, v_new  device fp16; token t starts q_stride, k_stride, v_stride
+ *                  elements after token t - 1 (multiples of 8, at least a
+ *                  token's heads), its heads head_dim apart: the rows of one
+ *                  fused projection can be passed in place.  16-byte aligned
+ *   rope_table     device fp32 [max_positions][rotary_dim], 16-byte aligned:
+ *                  a position's cosines, then its sines (may be NULL when
+ *                  rotary_dim is 0)
+ *   token_starts   device int32 [num_seqs + 1], ascending, or NULL:
+ *                  num_tokens / num_seqs tokens each (a whole number).  Rows
+ *                  at or past token_starts[num_seqs] are left as they are
+ *   positions      device int32 [num_tokens] or NULL: rotation positions that
+ *                  differ from the logical ones (a shared prefix in front)
+ *   q_out          device fp16, tokens q_out_stride elements apart, 16-byte
+ *                  aligned; may be q itself.  With num_q_heads 0, q and q_out
+ *                  may be NULL
+ *   head_dim       a multiple of 16, at most 512; rotary_dim a multiple of 16
+ *                  in [0, head_dim]
+ *   other arguments as for paged_kv_append
+ * A token whose logical position has no room or no valid block
+ * (PKD_DEVERR_BAD_BLOCK), or whose rotation position is outside the table
+ * (PKD_DEVERR_BAD_POSITION), is skipped: nothing is written for it.
+ */
+pkd_status paged_kv_append_rope(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                long long k_stride, long long v_stride, const float* rope_table,
+                                const int32_t* token_starts, const int32_t* positions, const int32_t* block_tables,
+                                const int32_t* context_lens, void* q_out, long long q_out_stride, void* k_cache,
+                                void* v_cache, int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                int head_dim, int rotary_dim, int interleaved, int max_positions, int block_size,
+                                int num_blocks, int max_blocks_per_seq, int* error_word, cudaStream_t stream);
+
+/*
+ * paged_kv_append_rope_fp8 -- the same into E4M3 caches: the rotated fp32 key
+ * and the value, divided by k_scale / v_scale (finite, > 0; IEEE fp32
+ * division), are rounded once to E4M3, to nearest even, saturating at +-448.
+ */
+pkd_status paged_kv_append_rope_fp8(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                    long long k_stride, long long v_stride, const float* rope_table,
+                                    const int32_t* token_starts, const int32_t* positions,
+                                    const int32_t* block_tables, const int32_t* context_lens, void* q_out,
+                                    long long q_out_stride, void* k_cache, void* v_cache, int num_tokens, int num_seqs,
+                                    int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim, int interleaved,
+                                    int max_positions, int block_size, int num_blocks, int max_blocks_per_seq,
+                                    float k_scale, float v_scale, int* error_word, cudaStream_t stream);
+
+/*
+ * paged_decode_attention_prefix -- decode of a batch whose sequences share
+ * long prefixes in the cache (a system prompt, a document): the batch is cut
+ * into groups of neighbouring sequences, and every query of group y attends to
+ * the prefix_lens[y] tokens of table row prefix_tables[y], then to its own
+ * sequence's context.  The prefix is read once for all the query rows of a
+ * group.  For sequence b of group y and query token jq:
+ *   out[b][jq][h][:] = sum over prefix tokens t < prefix_lens[y] and own
+ *     tokens t <= context_lens[b] - q_len + jq of softmax(s)_t V_t
+ * (one softmax over both).  A row that sees no token gets out = 0.
+ *
+ *   q, out         device fp16 [num_seqs][q_len][num_q_heads][head_dim]
+ *   prefix_tables  device int32 [num_groups][max_prefix_blocks], prefix_lens
+ *                  device int32 [num_groups], each in [0, max_prefix_len]; a
+ *                  prefix may end inside a block
+ *   group_starts   device int32 [num_groups + 1], ascending: group y holds
+ *                  sequences group_starts[y] .. group_starts[y + 1] - 1;
+ *                  sequences in no group have no prefix.  With num_groups 0
+ *                  the three may be NULL
+ *   block_tables, context_lens, max_blocks_per_seq, max_context_len
+ *                  the sequences' own contexts, without the prefix, counting
+ *                  the q_len new tokens
+ *   workspace      paged_decode_prefix_workspace_size(...) bytes, 256-byte
+ *                  aligned (fp32 partials of both parts)
+ *   other arguments as for paged_decode_attention_multi
+ */
+pkd_status paged_decode_attention_prefix(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                         const int32_t* group_starts, const int32_t* block_tables,
+                                         const int32_t* context_lens, void* out, int num_seqs, int q_len,
+                                         int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                         int block_size, int num_blocks, int max_prefix_blocks, int max_blocks_per_seq,
+                                         int max_prefix_len, int max_context_len, float scale, void* workspace,
+                                         size_t workspace_bytes, int* error_word, cudaStream_t stream);
+
+/* paged_decode_attention_prefix_fp8 -- the same over E4M3 caches (scales as
+   for paged_decode_attention_fp8). */
+pkd_status paged_decode_attention_prefix_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                             const int32_t* group_starts, const int32_t* block_tables,
+                                             const int32_t* context_lens, void* out, int num_seqs, int q_len,
+                                             int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                             int block_size, int num_blocks, int max_prefix_blocks,
+                                             int max_blocks_per_seq, int max_prefix_len, int max_context_len,
+                                             float scale, float k_scale, float v_scale, void* workspace,
+                                             size_t workspace_bytes, int* error_word, cudaStream_t stream);
+
+/* Workspace bytes of paged_decode_attention_prefix and _fp8 (0 = none, or an
+   invalid shape). */
+size_t paged_decode_prefix_workspace_size(int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, int num_groups, int max_prefix_len, int max_context_len);
+
+/*
+ * paged_kv_block_bounds -- the key bounds that paged_kv_block_select scores
+ * blocks by: for every kv head g and every block i of sequence b with physical
+ * block p = block_tables[b][i],
+ *   bounds[p][g][0][d] = min over the block's tokens t < context_lens[b] of K[p][g][t % block_size][d]
+ *   bounds[p][g][1][d] = max over the same
+ * in the cache's type (E4M3: codes; exact either way).
+ *
+ *   bounds         device [num_blocks][num_kv_heads][2][head_dim], fp16 or
+ *                  (kv_fp8) E4M3 bytes, 16-byte aligned, written in place;
+ *                  the entries of other blocks are left as they are
+ *   start_lens     device int32 [num_seqs] or NULL: blocks before block
+ *                  start_lens[b] / block_size are left as they are, so that
+ *                  after an append only the blocks it touched are read (pass
+ *                  the lengths before it).  NULL: all blocks
+ *   max_new_tokens host upper bound of context_lens[b] - start_lens[b] (of
+ *                  context_lens[b] when start_lens is NULL)
+ *   head_dim 64 or 128, block_size 16 or 32
+ * Blocks that several sequences share must hold the same tokens for each.
+ */
+pkd_status paged_kv_block_bounds(const void* k_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                 const int32_t* start_lens, void* bounds, int num_seqs, int num_kv_heads, int head_dim,
+                                 int block_size, int num_blocks, int max_blocks_per_seq, int max_new_tokens,
+                                 int kv_fp8, int* error_word, cudaStream_t stream);
+
+/*
+ * paged_kv_block_select -- the blocks worth attending to: block i of sequence
+ * b scores, for kv head g, the largest dot product that a key inside the
+ * block's bounds could have with any query of the group,
+ *   S_i = max_{h in g} sum_d max(q[b][h][d] bounds[p][g][0][d], q[b][h][d] bounds[p][g][1][d])
+ * (an upper bound of q.k over the block; the softmax scale, taken as
+ * positive, does not change the order).  Chosen are the first sink_blocks and
+ * the last recent_blocks, and of the others those with the largest S_i, ties
+ * to the lowest i, max_selected blocks in all; every block when the sequence
+ * has no more than that.  The choice is that of the exact scores: what
+ * fp32 leaves open at the border is decided in fp64.
+ *
+ *   q              device fp16 [num_seqs][num_q_heads][head_dim]
+ *   bounds         as written by paged_kv_block_bounds, finite, for every used block
+ *   block_lists    device int32 [num_seqs][num_kv_heads][max_selected]: the
+ *                  chosen logical blocks in ascending order, then -1
+ *   list_lens      device int32 [num_seqs][num_kv_heads]: how many
+ *   sink_blocks + recent_blocks <= max_selected
+ *   max_context_len  host upper bound of context_lens; at most
+ *                  PKD_MAX_SELECT_BLOCKS blocks (PKD_ERR_UNSUPPORTED above)
+ * A block outside the pool is reported (PKD_DEVERR_BAD_BLOCK) and comes last.
+ */
+#define PKD_MAX_SELECT_BLOCKS 49152
+pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_t* block_tables,
+                                 const int32_t* context_lens, int32_t* block_lists, int32_t* list_lens, int num_seqs,
+                                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                 int max_blocks_per_seq, int max_context_len, int max_selected, int sink_blocks,
+                                 int recent_blocks, int kv_fp8, int* error_word, cudaStream_t stream);
+
+/*
+ * paged_decode_attention_blocks -- single-query decode over listed blocks:
+ * query head h of sequence b attends to the tokens of the logical blocks
+ * block_lists[b][g][0 .. list_lens[b][g] - 1] of its context and to no others
+ * (the tokens before context_lens[b] of each).  An empty list gives out = 0.
+ *
+ *   block_lists    device int32 [num_seqs][num_kv_heads][max_listed], each
+ *                  entry once, in any order but that a partly filled last
+ *                  block of the sequence, where listed, is the list's last
+ *                  entry (paged_kv_block_select's lists are).  An entry that
+ *                  breaks this, lies outside the sequence or names a block
+ *                  outside the pool is skipped (PKD_DEVERR_BAD_BLOCK)
+ *   list_lens      device int32 [num_seqs][num_kv_heads], each at most max_listed
+ *   workspace      paged_decode_blocks_workspace_size(...) bytes, 256-byte
+ *                  aligned (NULL where that is 0)
+ *   other arguments as for paged_decode_attention_ex
+ */
+pkd_status paged_decode_attention_blocks(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* context_lens,
+                                         const int32_t* block_lists, const int32_t* list_lens, void* out,
+                                         int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                         int block_size, int num_blocks, int max_blocks_per_seq, int max_listed,
+                                         float scale, void* workspace, size_t workspace_bytes, int* error_word,
+                                         cudaStream_t stream);
+
+/* paged_decode_attention_blocks_fp8 -- the same over E4M3 caches (scales as
+   for paged_decode_attention_fp8). */
+pkd_status paged_decode_attention_blocks_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens,
+                                             const int32_t* block_lists, const int32_t* list_lens, void* out,
+                                             int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                             int block_size, int num_blocks, int max_blocks_per_seq, int max_listed,
+                                             float scale, float k_scale, float v_scale, void* workspace,
+                                             size_t workspace_bytes, int* error_word, cudaStream_t stream);
+
+/* Workspace bytes of paged_decode_attention_blocks and _fp8 (0 = none, or an
+   invalid shape). */
+size_t paged_decode_blocks_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, int max_listed);
 
 /*
  * pkd_selftest_bounded_wait -- exercises the failure path of the library's

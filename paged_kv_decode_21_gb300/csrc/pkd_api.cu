@@ -12,6 +12,7 @@
 #include "pkd_aux.cuh"
 #include "pkd_decode_mma.cuh"
 #include "pkd_launch.cuh"
+#include "pkd_src_launch.h"
 #include "pkd_tc_launch.h"
 
 namespace {
@@ -1179,6 +1180,346 @@ pkd_status pkd_read_device_error(int* error_word, unsigned* host_bits, int clear
     if (cudaStreamSynchronize(stream) != cudaSuccess) return PKD_ERR_CUDA;
   }
   return v == 0 ? PKD_OK : PKD_ERR_DEVICE;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ shared prefixes, block lists
+namespace {
+
+// Tokens per partial and partials per row of one part of a call (np = 0: the
+// part has nothing to read and is not launched).
+struct PartPlan {
+  int variant = PKD_VARIANT_TMA_MMA;
+  int chunks = 1;
+  int P = 32;
+  int np = 0;
+  long long grid = 0;
+};
+
+// A shared prefix of up to max_prefix_len tokens: the chunks of all groups
+// (at most `tokens / per` full ones and a rest for each group) times the kv
+// heads are the units; each reads the prefix in as many partitions as fill the
+// GPU's resident CTAs once.  Where a group has 16 query rows or fewer per kv
+// head on average, the 16-row mma.sync tile serves it; else the 64-row tcgen05
+// one does.
+PartPlan plan_shared(const Shape& s, int q_len, int num_groups, int max_prefix_len, int kv_fp8) {
+  PartPlan p;
+  if (max_prefix_len <= 0 || num_groups <= 0 || s.num_seqs <= 0) return p;
+  const int G = s.num_q_heads / s.num_kv_heads;
+  const long long tokens = (long long)s.num_seqs * q_len;
+  const bool tc = tc_supports(s, kv_fp8) && tokens * G > 16LL * num_groups;
+  p.variant = tc ? PKD_VARIANT_TCGEN05 : PKD_VARIANT_TMA_MMA;
+  const int per = (tc ? pkd::kTcRowsPerCta : 16) / G;
+  p.chunks = (int)(tokens / per + num_groups);
+  const long long units = std::max(1LL, tokens / per + (num_groups == 1 ? 1 : num_groups)) * s.num_kv_heads;
+  int sms = sm_count();
+  if (sms <= 0) sms = 148;
+  const long long slots = (long long)sms * path_stream(p.variant, s.head_dim, G, kv_fp8 ? 1 : 2, false).ctas_per_sm;
+  const int least = tc ? kMinSmallGridPartitionTc : kMinSmallGridPartition;
+  long long np = std::max(1LL, slots / units);
+  np = std::min<long long>(np, (max_prefix_len + least - 1) / least);
+  p.P = (int)round_up((size_t)((max_prefix_len + np - 1) / np), 64);
+  p.np = (max_prefix_len + p.P - 1) / p.P;
+  p.grid = (long long)p.chunks * s.num_kv_heads * p.np;
+  return p;
+}
+
+// The own contexts behind a prefix: the automatic path and split of
+// paged_decode_attention_multi, in plain order.
+PartPlan plan_own(const Shape& s, int q_len, int kv_fp8) {
+  PartPlan p;
+  if (s.max_context_len <= 0 || s.num_seqs <= 0) return p;
+  p.variant = q_len > 1 ? auto_multi_path(s, q_len, kv_fp8) : PKD_VARIANT_TMA_MMA;
+  p.chunks = query_chunks(q_len, s.num_q_heads / s.num_kv_heads, p.variant);
+  const int P = auto_partition(s, p.variant, p.chunks);
+  const bool split = P > 0 && s.max_context_len > P;
+  p.P = split ? P : (int)round_up((size_t)s.max_context_len, 32);
+  p.np = split ? (s.max_context_len + P - 1) / P : 1;
+  p.grid = (long long)s.num_seqs * s.num_kv_heads * p.chunks * p.np;
+  return p;
+}
+
+// Fields every decode launch sets.
+pkd::DecodeParams base_params(const Shape& s, const void* q, const void* k_cache, const void* v_cache, int q_len,
+                              float scale, int kv_fp8, float k_scale, float v_scale, int* error_word) {
+  pkd::DecodeParams p{};
+  p.q = static_cast<const __half*>(q);
+  p.k_cache = static_cast<const __half*>(k_cache);
+  p.v_cache = static_cast<const __half*>(v_cache);
+  p.error_word = error_word;
+  p.num_seqs = s.num_seqs;
+  p.num_q_heads = s.num_q_heads;
+  p.num_kv_heads = s.num_kv_heads;
+  p.num_blocks = s.num_blocks;
+  p.q_len = q_len;
+  p.parts_per_cta = 1;
+  p.scale_log2 = scale * (kv_fp8 ? k_scale : 1.f) * 1.4426950408889634f;
+  p.v_scale = kv_fp8 ? v_scale : 1.f;
+  p.timeout_ns = kWaitBudgetNs;
+  return p;
+}
+
+pkd_status launch_part(const Shape& s, const PartPlan& plan, const pkd::DecodeParams& p, int kv_fp8,
+                       cudaStream_t stream) {
+  if (plan.grid <= 0) return PKD_OK;
+  if (plan.grid > 0x7fffffffLL) return PKD_ERR_SHAPE;
+  const int G = s.num_q_heads / s.num_kv_heads;
+  const int D = s.head_dim, BS = s.block_size;
+  cudaError_t e;
+  if (plan.variant == PKD_VARIANT_TCGEN05)
+    e = pkd::launch_decode_tcgen05(D, BS, p, plan.grid, stream, kv_fp8 ? 1 : 2);
+  else if (p.group_starts)
+    e = kv_fp8 ? pkd::launch_decode_shared_fp8(D, BS, G, p, plan.grid, stream)
+               : pkd::launch_decode_shared(D, BS, G, p, plan.grid, stream);
+  else if (p.block_lists)
+    e = kv_fp8 ? pkd::launch_decode_listed_fp8(D, BS, G, p, plan.grid, stream)
+               : pkd::launch_decode_listed(D, BS, G, p, plan.grid, stream);
+  else if (kv_fp8)
+    e = pkd::launch_decode_tma_mma_fp8(D, BS, G, p, plan.grid, stream);
+  else
+    e = pkd::launch_decode_tma_mma(D, BS, G, p, plan.grid, stream);
+  return e == cudaSuccess ? PKD_OK : PKD_ERR_LAUNCH;
+}
+
+pkd_status launch_merge(int head_dim, const pkd::MergeParams& m, cudaStream_t stream) {
+  if (m.rows <= 0) return PKD_OK;
+  // a programmatic dependent of the launch before it, as in launch_reduce
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)m.rows + pkd::kReduceRowsPerCta - 1) / pkd::kReduceRowsPerCta));
+  cfg.blockDim = dim3(32 * pkd::kReduceRowsPerCta);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = head_dim == 128 ? cudaLaunchKernelEx(&cfg, pkd::paged_merge_kernel<128>, m)
+                                        : cudaLaunchKernelEx(&cfg, pkd::paged_merge_kernel<64>, m);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKD_OK : PKD_ERR_LAUNCH;
+}
+
+pkd::MergeSource merge_source(const Workspace& w, const PartPlan& plan) {
+  return pkd::MergeSource{w.tmp_out, w.max_logits, w.exp_sums, plan.np, plan.P};
+}
+
+pkd_status prefix_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_tables,
+                       const int32_t* prefix_lens, const int32_t* group_starts, const int32_t* block_tables,
+                       const int32_t* context_lens, void* out, int num_seqs, int q_len, int num_groups,
+                       int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       int max_prefix_blocks, int max_blocks_per_seq, int max_prefix_len, int max_context_len,
+                       float scale, int kv_fp8, float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                       int* error_word, cudaStream_t stream) {
+  const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
+                max_context_len};
+  pkd_status st = check_shape(s);
+  if (st != PKD_OK) return st;
+  if (q_len < 1 || num_groups < 0 || max_prefix_len < 0) return PKD_ERR_SHAPE;
+  if (num_groups > 0 && (max_prefix_blocks <= 0 || (long long)max_prefix_len > (long long)max_prefix_blocks * block_size))
+    return PKD_ERR_SHAPE;
+  if (!std::isfinite(scale)) return PKD_ERR_SHAPE;
+  if (kv_fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f))
+    return PKD_ERR_SHAPE;
+  if (num_seqs == 0) return PKD_OK;
+  const long long rows = (long long)num_seqs * q_len * num_q_heads;
+  if (rows > 0x7fffffffLL) return PKD_ERR_SHAPE;
+  st = check_inputs(q, k_cache, v_cache, block_tables, context_lens);
+  if (st != PKD_OK) return st;
+  if (!out || (num_groups > 0 && (!prefix_tables || !prefix_lens || !group_starts))) return PKD_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(error_word, 4) || !aligned(prefix_tables, 4) || !aligned(prefix_lens, 4) ||
+      !aligned(group_starts, 4))
+    return PKD_ERR_ALIGN;
+  const PartPlan own = plan_own(s, q_len, kv_fp8);
+  const PartPlan pre = plan_shared(s, q_len, num_groups, max_prefix_len, kv_fp8);
+  const size_t own_bytes = own.np > 0 ? layout(nullptr, num_seqs * q_len, num_q_heads, head_dim, own.np).bytes : 0;
+  const size_t pre_bytes = pre.np > 0 ? layout(nullptr, num_seqs * q_len, num_q_heads, head_dim, pre.np).bytes : 0;
+  if (own_bytes + pre_bytes > 0) {
+    if (!workspace) return PKD_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PKD_ERR_ALIGN;
+    if (workspace_bytes < own_bytes + pre_bytes) return PKD_ERR_WORKSPACE;
+  }
+  pkd::MergeParams m{};
+  m.context_lens = context_lens;
+  m.group_starts = group_starts;
+  m.shared_lens = prefix_lens;
+  m.out = static_cast<__half*>(out);
+  m.rows = (int)rows;
+  m.q_len = q_len;
+  m.num_q_heads = num_q_heads;
+  m.num_kv_heads = num_kv_heads;
+  m.block_size = block_size;
+  m.num_groups = num_groups;
+  auto run = [&](const PartPlan& plan, void* at, bool shared) -> pkd_status {
+    const Workspace w = layout(at, num_seqs * q_len, num_q_heads, head_dim, plan.np);
+    pkd::DecodeParams p =
+        base_params(s, q, k_cache, v_cache, q_len, scale, kv_fp8, k_scale, v_scale, error_word);
+    p.block_tables = shared ? prefix_tables : block_tables;
+    p.context_lens = shared ? prefix_lens : context_lens;
+    p.max_blocks_per_seq = shared ? max_prefix_blocks : max_blocks_per_seq;
+    p.partition_size = plan.P;
+    p.max_partitions = plan.np;
+    p.q_chunks = plan.chunks;
+    p.mode = 1;
+    p.tmp_out = w.tmp_out;
+    p.max_logits = w.max_logits;
+    p.exp_sums = w.exp_sums;
+    if (shared) {
+      p.group_starts = group_starts;
+      p.num_groups = num_groups;
+    }
+    (shared ? m.shared : m.own) = merge_source(w, plan);
+    return launch_part(s, plan, p, kv_fp8, stream);
+  };
+  if (pre.np > 0 && (st = run(pre, static_cast<unsigned char*>(workspace) + own_bytes, true)) != PKD_OK) return st;
+  if (own.np > 0 && (st = run(own, workspace, false)) != PKD_OK) return st;
+  return launch_merge(head_dim, m, stream);
+}
+
+pkd_status blocks_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                       const int32_t* context_lens, const int32_t* block_lists, const int32_t* list_lens, void* out,
+                       int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       int max_blocks_per_seq, int max_listed, float scale, int kv_fp8, float k_scale, float v_scale,
+                       void* workspace, size_t workspace_bytes, int* error_word, cudaStream_t stream) {
+  if (max_listed <= 0 || block_size <= 0 || (long long)max_listed * block_size > 0x7fffffffLL) return PKD_ERR_SHAPE;
+  // the list is a context of its own, as long as max_listed blocks
+  const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, std::max(1, max_listed),
+                max_listed * block_size};
+  pkd_status st = check_shape(s);
+  if (st != PKD_OK) return st;
+  if (max_blocks_per_seq <= 0 || !std::isfinite(scale)) return PKD_ERR_SHAPE;
+  if (kv_fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f))
+    return PKD_ERR_SHAPE;
+  if (num_seqs == 0) return PKD_OK;
+  const long long rows = (long long)num_seqs * num_q_heads;
+  if (rows > 0x7fffffffLL) return PKD_ERR_SHAPE;
+  st = check_inputs(q, k_cache, v_cache, block_tables, context_lens);
+  if (st != PKD_OK) return st;
+  if (!block_lists || !list_lens || !out) return PKD_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(error_word, 4) || !aligned(block_lists, 4) || !aligned(list_lens, 4))
+    return PKD_ERR_ALIGN;
+  const PartPlan plan = plan_own(s, 1, kv_fp8);
+  const bool split = plan.np > 1;
+  pkd::DecodeParams p = base_params(s, q, k_cache, v_cache, 1, scale, kv_fp8, k_scale, v_scale, error_word);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.partition_size = plan.P;
+  p.max_partitions = plan.np;
+  p.q_chunks = 1;
+  p.mode = 0;
+  p.out = static_cast<__half*>(out);
+  p.block_lists = block_lists;
+  p.list_lens = list_lens;
+  p.max_listed = max_listed;
+  Workspace w{};
+  if (split) {
+    if (!workspace) return PKD_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PKD_ERR_ALIGN;
+    w = layout(workspace, num_seqs, num_q_heads, head_dim, plan.np);
+    if (workspace_bytes < w.bytes) return PKD_ERR_WORKSPACE;
+    p.tmp_out = w.tmp_out;
+    p.max_logits = w.max_logits;
+    p.exp_sums = w.exp_sums;
+  }
+  st = launch_part(s, plan, p, kv_fp8, stream);
+  if (st != PKD_OK || !split) return st;
+  pkd::MergeParams m{};
+  m.own = merge_source(w, plan);
+  m.context_lens = context_lens;
+  m.list_lens = list_lens;
+  m.out = static_cast<__half*>(out);
+  m.rows = (int)rows;
+  m.q_len = 1;
+  m.num_q_heads = num_q_heads;
+  m.num_kv_heads = num_kv_heads;
+  m.block_size = block_size;
+  m.skip_single = 1;
+  return launch_merge(head_dim, m, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t paged_decode_prefix_workspace_size(int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, int num_groups, int max_prefix_len, int max_context_len) {
+  const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, 1, 1 << 30, max_context_len};
+  if (check_shape(s) != PKD_OK || q_len < 1 || num_groups < 0 || max_prefix_len < 0) return 0;
+  size_t most = 0;
+  for (const int fp8 : {0, 1}) {  // the plan may differ by cache type
+    const PartPlan own = plan_own(s, q_len, fp8), pre = plan_shared(s, q_len, num_groups, max_prefix_len, fp8);
+    size_t bytes = 0;
+    if (own.np > 0) bytes += layout(nullptr, num_seqs * q_len, num_q_heads, head_dim, own.np).bytes;
+    if (pre.np > 0) bytes += layout(nullptr, num_seqs * q_len, num_q_heads, head_dim, pre.np).bytes;
+    most = std::max(most, bytes);
+  }
+  return most;
+}
+
+size_t paged_decode_blocks_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, int max_listed) {
+  if (max_listed <= 0 || block_size <= 0 || (long long)max_listed * block_size > 0x7fffffffLL) return 0;
+  const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, 1, max_listed, max_listed * block_size};
+  if (check_shape(s) != PKD_OK) return 0;
+  size_t most = 0;
+  for (const int fp8 : {0, 1}) {
+    const PartPlan p = plan_own(s, 1, fp8);
+    if (p.np > 1) most = std::max(most, layout(nullptr, num_seqs, num_q_heads, head_dim, p.np).bytes);
+  }
+  return most;
+}
+
+pkd_status paged_decode_attention_prefix(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                         const int32_t* group_starts, const int32_t* block_tables,
+                                         const int32_t* context_lens, void* out, int num_seqs, int q_len,
+                                         int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                         int block_size, int num_blocks, int max_prefix_blocks, int max_blocks_per_seq,
+                                         int max_prefix_len, int max_context_len, float scale, void* workspace,
+                                         size_t workspace_bytes, int* error_word, cudaStream_t stream) {
+  return prefix_impl(q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables, context_lens, out,
+                     num_seqs, q_len, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     max_prefix_blocks, max_blocks_per_seq, max_prefix_len, max_context_len, scale, 0, 1.f, 1.f,
+                     workspace, workspace_bytes, error_word, stream);
+}
+
+pkd_status paged_decode_attention_prefix_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                             const int32_t* group_starts, const int32_t* block_tables,
+                                             const int32_t* context_lens, void* out, int num_seqs, int q_len,
+                                             int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                             int block_size, int num_blocks, int max_prefix_blocks,
+                                             int max_blocks_per_seq, int max_prefix_len, int max_context_len,
+                                             float scale, float k_scale, float v_scale, void* workspace,
+                                             size_t workspace_bytes, int* error_word, cudaStream_t stream) {
+  return prefix_impl(q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables, context_lens, out,
+                     num_seqs, q_len, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     max_prefix_blocks, max_blocks_per_seq, max_prefix_len, max_context_len, scale, 1, k_scale,
+                     v_scale, workspace, workspace_bytes, error_word, stream);
+}
+
+pkd_status paged_decode_attention_blocks(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* context_lens,
+                                         const int32_t* block_lists, const int32_t* list_lens, void* out,
+                                         int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                         int block_size, int num_blocks, int max_blocks_per_seq, int max_listed,
+                                         float scale, void* workspace, size_t workspace_bytes, int* error_word,
+                                         cudaStream_t stream) {
+  return blocks_impl(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, out, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq, max_listed,
+                     scale, 0, 1.f, 1.f, workspace, workspace_bytes, error_word, stream);
+}
+
+pkd_status paged_decode_attention_blocks_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens,
+                                             const int32_t* block_lists, const int32_t* list_lens, void* out,
+                                             int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                             int block_size, int num_blocks, int max_blocks_per_seq, int max_listed,
+                                             float scale, float k_scale, float v_scale, void* workspace,
+                                             size_t workspace_bytes, int* error_word, cudaStream_t stream) {
+  return blocks_impl(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, out, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq, max_listed,
+                     scale, 1, k_scale, v_scale, workspace, workspace_bytes, error_word, stream);
 }
 
 }  // extern "C"

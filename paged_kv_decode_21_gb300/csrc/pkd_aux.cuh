@@ -105,6 +105,112 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_decode_reduce_ke
 }
 
 // ---------------------------------------------------------------------------
+// Merge of partials over up to two sources of keys, by the same identity as
+// paged_decode_reduce_kernel: a row's own context (or its block list) and the
+// context its group shares.  One warp per (query token, head) row; lane l owns
+// dims [V l, V l + V).  A source's partial j is (o, m, l)[row][j]; partials of
+// a row past its own length were not written and are not read.
+struct MergeSource {
+  const float* o;  // [rows][np][D] unnormalised, or null: no such source
+  const float* m;  // [rows][np] maximum (natural log units)
+  const float* l;  // [rows][np] sum of exp(s - m)
+  int np;          // partials per row
+  int part;        // tokens per partial
+};
+struct MergeParams {
+  MergeSource own, shared;
+  const int32_t* context_lens;  // [num_seqs]: own tokens
+  const int32_t* list_lens;     // [num_seqs][num_kv_heads] or null: own = that many blocks of block_size
+  const int32_t* group_starts;  // [num_groups + 1]
+  const int32_t* shared_lens;   // [num_groups]
+  __half* out;
+  int rows, q_len, num_q_heads, num_kv_heads, block_size, num_groups;
+  int skip_single;  // rows of at most one own partial were already written
+};
+template <int D>
+__global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(const MergeParams P) {
+  constexpr int V = D / 32;
+  constexpr int U = 8;  // partials in flight per lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kReduceRowsPerCta + (threadIdx.x >> 5);  // query token * Hq + head
+  if (row >= P.rows) return;
+  const int tok = row / P.num_q_heads, h = row % P.num_q_heads;
+  const int b = tok / P.q_len;
+  long long own_tokens;
+  if (P.list_lens) {
+    const int g = h / (P.num_q_heads / P.num_kv_heads);
+    own_tokens = (long long)P.list_lens[(size_t)b * P.num_kv_heads + g] * P.block_size;
+  } else {
+    own_tokens = P.context_lens[b];
+  }
+  int n[2] = {0, 0};
+  if (P.own.o && own_tokens > 0) n[0] = (int)min((own_tokens + P.own.part - 1) / P.own.part, (long long)P.own.np);
+  if (P.skip_single && n[0] <= 1) return;
+  if (P.shared.o) {
+    const int y = find_segment(P.group_starts, P.num_groups, b);
+    if (y < P.num_groups && P.group_starts[y] <= b) {
+      const int len = max(P.shared_lens[y], 0);
+      n[1] = min((len + P.shared.part - 1) / P.shared.part, P.shared.np);
+    }
+  }
+  const MergeSource src[2] = {P.own, P.shared};
+  float M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    for (int j = lane; j < n[k]; j += 32) M = fmaxf(M, src[k].m[(size_t)row * src[k].np + j]);
+#pragma unroll
+  for (int msk = 16; msk > 0; msk >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, msk));
+  float acc[V], Z = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float* o = src[k].o + (size_t)row * src[k].np * D + V * lane;
+    for (int j0 = 0; j0 < n[k]; j0 += 32) {
+      float w = 0.f;  // the weight of partial j0 + lane
+      if (j0 + lane < n[k]) {
+        const size_t at = (size_t)row * src[k].np + j0 + lane;
+        const float m = src[k].m[at];
+        w = m == -INFINITY ? 0.f : __expf(m - M);
+        Z = fmaf(w, src[k].l[at], Z);
+      }
+      const int nj = min(32, n[k] - j0);
+      for (int c = 0; c < nj; c += U) {
+        float x[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c + u < nj) {
+            const float* p = o + (size_t)(j0 + c + u) * D;
+            if constexpr (V == 4) {
+              const float4 t = *reinterpret_cast<const float4*>(p);
+              x[u][0] = t.x; x[u][1] = t.y; x[u][2] = t.z; x[u][3] = t.w;
+            } else {
+              const float2 t = *reinterpret_cast<const float2*>(p);
+              x[u][0] = t.x; x[u][1] = t.y;
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, w, (c + u) & 31);
+          if (c + u < nj) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(wu, x[u][v], acc[v]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int msk = 16; msk > 0; msk >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, msk);
+  const float invz = Z > 0.f ? 1.f / Z : 0.f;  // Z = 0: the row saw no token
+#pragma unroll
+  for (int v = 0; v < V; v += 2)
+    *reinterpret_cast<__half2*>(P.out + (size_t)row * D + V * lane + v) =
+        __floats2half2_rn(acc[v] * invz, acc[v + 1] * invz);
+}
+
+// ---------------------------------------------------------------------------
 // Paged KV append: the new token of sequence b sits at logical position
 // L = context_lens[b], i.e. in physical block block_tables[b][L / BS], slot
 // L % BS, for every kv head.  One thread moves one 16-byte chunk of the K

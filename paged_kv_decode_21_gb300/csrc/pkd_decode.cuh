@@ -73,7 +73,62 @@ struct DecodeParams {
   const int32_t* piece_order;  // nullable: grid piece p -> b * NP + j (longest first); tensor-core path only
   int parts_per_cta;           // tcgen05 path: consecutive partitions per CTA (0 or 1: one; needs no piece order)
   int tail_split;              // tcgen05 path with piece_order: pieces are b * 4 + a kPiece* code (a split tail)
+  // kListed kernels: each (sequence, kv head) reads the logical blocks block_lists[b][g][0 .. list_lens[b][g])
+  const int32_t* block_lists;  // [B][Hkv][max_listed]
+  const int32_t* list_lens;    // [B][Hkv]
+  int max_listed;
+  // kShared kernels: group y's sequences group_starts[y] .. group_starts[y + 1] - 1 all read the blocks of
+  // table row y, context_lens[y] tokens; q_chunks is the grid's chunk count over all groups
+  const int32_t* group_starts;  // [num_groups + 1]
+  int num_groups;
 };
+
+// Which keys the query rows of a tensor-core decode CTA read.
+enum KeySource : int {
+  kOwn = 0,     // each sequence its own context, through its table row
+  kListed = 1,  // each (sequence, kv head) the listed blocks of its own context (single query)
+  kShared = 2   // every query row of a group of sequences the group's shared context
+};
+
+// Chunk x of a grid over groups of sequences: the chunks of `per` query
+// tokens of group 0, then those of group 1, and so on.  Sets the group, the
+// chunk's first query token inside it, the group's query tokens and its
+// first one over the whole batch; false when x is past the last chunk.  Every
+// lane of the calling warp gets the same answer.
+struct GroupChunk {
+  int group, first, tokens, base;
+};
+__device__ __forceinline__ bool find_group_chunk(const int32_t* group_starts, int num_groups, int num_seqs,
+                                                 int q_len, int per, int x, GroupChunk* out) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;  // chunks of the groups before this round's 32
+  for (int y0 = 0; y0 < num_groups; y0 += 32) {
+    const int y = y0 + lane;
+    int s = 0, n = 0;
+    if (y < num_groups) {
+      s = min(max(group_starts[y], 0), num_seqs);
+      n = max(min(group_starts[y + 1], num_seqs) - s, 0) * q_len;
+    }
+    const int c = (n + per - 1) / per;
+    int upto = c;  // inclusive scan
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > x);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      out->group = y0 + l;
+      out->first = (x - before - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, c, l))) * per;
+      out->tokens = __shfl_sync(0xffffffffu, n, l);
+      out->base = __shfl_sync(0xffffffffu, s, l) * q_len;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
 
 // A grid walked longest first whose last round would be short splits its
 // shortest sequences in two (the tcgen05 path; piece_order_kernel chooses
@@ -144,6 +199,25 @@ __device__ __forceinline__ int row_clamped_len(const DecodeParams& P, int b) {
     return row;
   }
   return L;
+}
+
+// How many of starts[1 .. n] are <= x, for ascending starts: the segment of
+// x among n segments that begin at starts[0 .. n - 1] (n when x is past the
+// last; the caller checks starts[0] <= x).  The whole warp asks together, 32
+// places at a time, so a thousand segments take two rounds of one load each.
+// Any content of starts ends the search inside [0, n].
+__device__ __forceinline__ int find_segment(const int32_t* starts, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const long long i = lo + (long long)(lane + 1) * step;
+    const bool le = i <= hi && starts[i] <= x;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    lo += c * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {

@@ -45,6 +45,13 @@
 // tokens at or past min(partition end, L - q_len + jq + 1).  Rows 8..15 then
 // hold real queries: every lane keeps softmax state for rows r and r + 8,
 // and P.V runs one n-tile per 8 rows.
+//
+// Key sources (SRC).  kListed: the CTA's blocks are the entries of the
+// (sequence, kv head)'s block list instead of consecutive ones; the list is
+// read as a context of its own whose blocks are all full but, where the list
+// ends on the sequence's last block, the last.  kShared: the rows are query
+// tokens of a group of sequences and the context is the group's, seen whole
+// by every row (no causal limit); always partials.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -192,7 +199,7 @@ struct MmaTraits {
 };
 
 // ---------------------------------------------------------------- kernel
-template <int D, int BS, int G, int QC, int KVB = 2, int CPS = 0>
+template <int D, int BS, int G, int QC, int KVB = 2, int CPS = 0, int SRC = kOwn>
 __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
                                   MmaTraits<D, BS, G, QC, KVB, CPS>::MIN_BLOCKS)
     paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -212,6 +219,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
   const int np_grid = P.max_partitions;
   const int qc = blockIdx.x % P.q_chunks;
   const int rest = blockIdx.x / P.q_chunks;
+  static_assert(SRC != kListed || QC == 1, "block lists serve single queries");
   // a dependent grid (the split-K merge) may launch once every CTA of this
   // grid has started; it waits for this grid's completion itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -231,17 +239,40 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
     g = bg % P.num_kv_heads;
     b = bg / P.num_kv_heads;
   }
-  const int L = row_clamped_len<BS>(P, b);
-  const int QL = P.q_len;
-  const int jq0 = qc * QC;               // first query token of this CTA
-  const int nq = min(QC, QL - jq0);      // its query tokens (>= 1)
+  int jq0 = qc * QC;      // first query token of this CTA
+  int QL = P.q_len;       // query tokens of the sequence (kShared: of the group)
+  int tok0 = b * P.q_len;  // the first of them over the batch
+  if constexpr (SRC == kShared) {
+    // (b, above, is 0: the grid's rows are chunks of all groups)
+    GroupChunk ch;
+    if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len, QC, qc, &ch)) return;
+    b = ch.group;
+    jq0 = ch.first;
+    QL = ch.tokens;
+    tok0 = ch.base;
+  }
+  int L = row_clamped_len<BS>(P, b);
+  const int32_t* list = nullptr;
+  int list_nblk = 0;       // kListed: blocks of the sequence, and whether its last one is partly filled
+  bool list_ragged = false;
+  int list_n = 0;
+  if constexpr (SRC == kListed) {
+    const size_t bg = (size_t)b * P.num_kv_heads + g;
+    list = P.block_lists + bg * P.max_listed;
+    list_n = min(P.list_lens[bg], P.max_listed);
+    list_nblk = L > 0 ? (L + BS - 1) / BS : 0;
+    list_ragged = L % BS != 0;
+    const int fill = (list_n > 0 && list_ragged && list[list_n - 1] == list_nblk - 1) ? L % BS : BS;
+    L = list_n > 0 ? (list_n - 1) * BS + fill : 0;  // the list's own length in tokens
+  }
+  const int nq = min(QC, QL - jq0);      // the CTA's query tokens (>= 1)
   const int PS = P.partition_size;
   const int np_b = min((L + PS - 1) / PS, np_grid);  // partitions inside the grid
   const bool final_out = (P.mode == 0) && np_b <= 1;
   const int h0 = g * G;
   const int Hq = P.num_q_heads;
   // output / partial row of tile row rr (< G * nq)
-  auto out_row = [&](int rr) { return ((size_t)b * QL + jq0 + rr / G) * Hq + h0 + rr % G; };
+  auto out_row = [&](int rr) { return ((size_t)tok0 + jq0 + rr / G) * Hq + h0 + rr % G; };
 
   if (L <= 0) {
     if (final_out && j == 0) {
@@ -254,9 +285,9 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
 
   const int t0 = j * PS;
   // the chunk's last query sees tokens < L - QL + jq0 + nq; nothing past that is read
-  const int t1 = min(min(t0 + PS, L), L - QL + jq0 + nq);
+  const int t1 = SRC == kShared ? min(t0 + PS, L) : min(min(t0 + PS, L), L - QL + jq0 + nq);
   const int nblk = t1 > t0 ? (t1 - t0 + BS - 1) / BS : 0;
-  const int32_t* bt = P.block_tables + (size_t)b * P.max_blocks_per_seq + t0 / BS;
+  const int32_t* bt = P.block_tables + (size_t)b * P.max_blocks_per_seq + (SRC == kListed ? 0 : t0 / BS);
   const size_t head_stride = (size_t)T::TILE_BYTES;  // bytes per (block, head) tile
   const size_t block_stride = (size_t)P.num_kv_heads * head_stride;
   const char* kbase = reinterpret_cast<const char*>(P.k_cache) + (size_t)g * head_stride;
@@ -274,7 +305,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
 #pragma unroll
   for (int hf = 0; hf < NT; ++hf) {
     const int rr = r + 8 * hf;
-    lim[hf] = rr < G * nq ? min(t1, L - QL + jq0 + rr / G + 1) : t1;
+    lim[hf] = (SRC != kShared && rr < G * nq) ? min(t1, L - QL + jq0 + rr / G + 1) : t1;
   }
   const int lim_min = NT == 2 ? min(lim[0], lim[NT - 1]) : lim[0];
 
@@ -343,7 +374,19 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
   SubCursor<BS, NW> ic, cc;
   ic.start(warp);
   cc.start(warp);
-  auto block_id = [&](int k) { return k < nblk ? bt[k] : -1; };
+  auto block_id = [&](int k) -> int {
+    if (k >= nblk) return -1;
+    if constexpr (SRC == kListed) {
+      // an entry past the sequence, or its partly filled last block anywhere
+      // but at the list's end, counts as a bad block
+      const int i = t0 / BS + k;
+      const int sel = list[i];
+      const bool ok = sel >= 0 && sel < list_nblk && !(list_ragged && sel == list_nblk - 1 && i != list_n - 1);
+      return ok ? bt[sel] : -1;
+    } else {
+      return bt[k];
+    }
+  };
   int ic_pb = block_id(ic.k);
   int pf_k = warp + NW * pd;
   int pf_pb = pd > 0 ? block_id(pf_k) : -1;

@@ -1,0 +1,715 @@
+// pkd_serving.cuh -- kernels of the steps around a decode call: the rotated
+// append of new tokens, the key bounds of cache blocks, and the choice of
+// blocks by those bounds.
+#pragma once
+#include <cstdint>
+#include <cuda_fp16.h>
+#include "pkd_decode_mma.cuh"
+
+namespace pkd {
+
+constexpr uint32_t kErrBadPosition = 8u;  // a rotation position outside the table
+
+// ---------------------------------------------------------------------------
+// Rotated append.  With c_i = cos(p theta_i), s_i = sin(p theta_i) from row p
+// of the table, pair i of a head turns as
+//   y_a = x_a c_i - x_b s_i,   y_b = x_b c_i + x_a s_i
+// (a, b) = (i, i + R/2), or (2i, 2i + 1) when the pairs are interleaved; dims
+// from R on pass through.  Products and sums in fp32, rounded once to fp16 (or
+// divided by the cache's scale and rounded once to E4M3).
+//
+// One CTA per token: thread (head slot, c) owns the 16 dims of two 16-byte
+// chunks that rotate together, loads its 8 cosines and sines once, and walks
+// the token's q, k and v heads with them.  The first head's data is requested
+// before the token's sequence, position and block are looked up, so that chain
+// of dependent loads hides behind it.
+struct RopeAppendParams {
+  const __half *q, *k, *v;         // token t's heads at q + t * q_stride (elements), head_dim apart
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  const float* table;              // [max_positions][R]: R/2 cosines, then R/2 sines
+  const int32_t* token_starts;     // [num_seqs + 1], or null: num_tokens / num_seqs tokens each
+  const int32_t* positions;        // [num_tokens], or null: the logical position
+  const int32_t *block_tables, *context_lens;
+  __half* q_out;
+  void *k_cache, *v_cache;
+  int num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, rotary_dim, max_positions, block_size, num_blocks,
+      max_blocks_per_seq;
+  float k_scale, v_scale;
+  int* error_word;
+};
+
+__device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d, float scale) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fdiv_rn(b, scale)), "f"(__fdiv_rn(a, scale)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fdiv_rn(d, scale)), "f"(__fdiv_rn(c, scale)));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+}
+
+constexpr int kRopeThreads = 256;
+template <bool F8, bool PAIRS>
+__global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(const RopeAppendParams P) {
+  const int D = P.head_dim, R = P.rotary_dim, units = D / 16;
+  const int slots = kRopeThreads / units;  // heads in flight
+  const int c = threadIdx.x % units, slot = threadIdx.x / units;
+  const int heads = P.num_q_heads + 2 * P.num_kv_heads;
+  const int t = blockIdx.x;
+  const bool rot = c < R / 16;
+  const int e0 = rot && !PAIRS ? 8 * c : 16 * c;
+  const int e1 = rot && !PAIRS ? R / 2 + 8 * c : 16 * c + 8;
+  auto source = [&](int h) -> const __half* {
+    if (h < P.num_q_heads) return P.q + t * P.q_stride + (long long)h * D;
+    h -= P.num_q_heads;
+    if (h < P.num_kv_heads) return P.k + t * P.k_stride + (long long)h * D;
+    return P.v + t * P.v_stride + (long long)(h - P.num_kv_heads) * D;
+  };
+  int h = slot;
+  const bool mine = slot < slots;
+  uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
+  if (mine && h < heads) {
+    const __half* s = source(h);
+    u0 = *reinterpret_cast<const uint4*>(s + e0);
+    u1 = *reinterpret_cast<const uint4*>(s + e1);
+  }
+  // the token's sequence b and its place j in it
+  int b, j;
+  if (P.token_starts) {
+    b = find_segment(P.token_starts, P.num_seqs, t);
+    if (b >= P.num_seqs) return;  // past the last sequence: left as it is
+    j = t - P.token_starts[b];
+    if (j < 0) return;
+  } else {
+    const int per = P.num_tokens / P.num_seqs;
+    b = t / per;
+    j = t - b * per;
+  }
+  const int L = P.context_lens[b];
+  const long long at = (long long)L + j;  // logical position
+  const long long lb = at / P.block_size;
+  const long long pos = P.positions ? P.positions[t] : at;
+  int block = -1;
+  if (L >= 0 && lb < P.max_blocks_per_seq) block = P.block_tables[(size_t)b * P.max_blocks_per_seq + lb];
+  uint32_t err = 0;
+  if (block < 0 || block >= P.num_blocks) err |= kErrBadBlock;
+  if (R > 0 && (pos < 0 || pos >= P.max_positions)) err |= kErrBadPosition;
+  if (err) {
+    if (threadIdx.x == 0) record_error(P.error_word, err);
+    return;
+  }
+  float cs[8], sn[8];
+  if (rot) {
+    const float4* row = reinterpret_cast<const float4*>(P.table + pos * R + 8 * c);
+    const float4* row2 = reinterpret_cast<const float4*>(P.table + pos * R + R / 2 + 8 * c);
+    const float4 a = row[0], a2 = row[1], s = row2[0], s2 = row2[1];
+    cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w; cs[4] = a2.x; cs[5] = a2.y; cs[6] = a2.z; cs[7] = a2.w;
+    sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w; sn[4] = s2.x; sn[5] = s2.y; sn[6] = s2.z; sn[7] = s2.w;
+  }
+  const size_t row0 = ((size_t)block * P.num_kv_heads) * P.block_size + (size_t)(at - lb * P.block_size);
+  if (!mine) return;
+  for (; h < heads;) {
+    const int hn = h + slots;
+    uint4 n0 = u0, n1 = u1;
+    if (hn < heads) {
+      const __half* s = source(hn);
+      n0 = *reinterpret_cast<const uint4*>(s + e0);
+      n1 = *reinterpret_cast<const uint4*>(s + e1);
+    }
+    const bool is_q = h < P.num_q_heads, is_v = h >= P.num_q_heads + P.num_kv_heads;
+    const bool turn = rot && !is_v;
+    float x[8], y[8];
+    if (turn || (F8 && !is_q)) {
+      unpack8(u0, x);
+      unpack8(u1, y);
+    }
+    if (turn) {
+      if constexpr (PAIRS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[2 * i], d = x[2 * i + 1], a2 = y[2 * i], d2 = y[2 * i + 1];
+          x[2 * i] = fmaf(a, cs[i], -d * sn[i]);
+          x[2 * i + 1] = fmaf(d, cs[i], a * sn[i]);
+          y[2 * i] = fmaf(a2, cs[4 + i], -d2 * sn[4 + i]);
+          y[2 * i + 1] = fmaf(d2, cs[4 + i], a2 * sn[4 + i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = x[i], d = y[i];
+          x[i] = fmaf(a, cs[i], -d * sn[i]);
+          y[i] = fmaf(d, cs[i], a * sn[i]);
+        }
+      }
+    }
+    if (is_q) {
+      __half* o = P.q_out + t * P.q_out_stride + (long long)h * D;
+      *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
+      *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+    } else {
+      const int g = h - P.num_q_heads - (is_v ? P.num_kv_heads : 0);
+      const size_t row = (row0 + (size_t)g * P.block_size) * D;
+      if constexpr (F8) {
+        const float sc = is_v ? P.v_scale : P.k_scale;
+        uint8_t* o = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + row;
+        *reinterpret_cast<uint2*>(o + e0) =
+            make_uint2(pack4_e4m3(x[0], x[1], x[2], x[3], sc), pack4_e4m3(x[4], x[5], x[6], x[7], sc));
+        *reinterpret_cast<uint2*>(o + e1) =
+            make_uint2(pack4_e4m3(y[0], y[1], y[2], y[3], sc), pack4_e4m3(y[4], y[5], y[6], y[7], sc));
+      } else {
+        __half* o = static_cast<__half*>(is_v ? P.v_cache : P.k_cache) + row;
+        *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
+        *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+      }
+    }
+    h = hn;
+    u0 = n0;
+    u1 = n1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Key bounds: for a cache block's tokens t (those before the sequence's
+// length) and every dim d, lo_d = min_t k[t][d] and hi_d = max_t k[t][d], in
+// the cache's own type: both are cache values, so nothing is rounded.
+//
+// One warp per (sequence, block, kv head): the tile's rows are contiguous, so
+// a warp-wide load of 16 bytes a lane covers several whole rows, all of a
+// lane's loads are independent, and the row groups meet in a butterfly.
+struct BlockBoundsParams {
+  const void* k_cache;
+  const int32_t *block_tables, *context_lens;
+  const int32_t* start_lens;  // nullable: blocks before start_lens[b] / block_size are left as they are
+  void* bounds;               // [num_blocks][num_kv_heads][2][D]: lo, then hi
+  int num_seqs, num_kv_heads, block_size, num_blocks, max_blocks_per_seq, grid_blocks;
+  int* error_word;
+};
+
+__device__ __forceinline__ uint32_t hmin2_u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmax2_u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Two fp16 pairs that hold E4M3 values -> the four codes (exact).
+__device__ __forceinline__ uint32_t f16x2x2_to_e4m3x4(uint32_t lo, uint32_t hi) {
+  uint16_t a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(hi));
+  return (uint32_t)a | ((uint32_t)b << 16);
+}
+
+// The 16 bytes of a cache row as fp16 pairs: WORDS = 4 (fp16) or 8 (E4M3).
+template <int KVB>
+__device__ __forceinline__ void cache_words(const uint4 u, uint32_t (&w)[KVB == 2 ? 4 : 8]) {
+  if constexpr (KVB == 2) {
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else {
+    e4m3x4_to_f16x2x2(u.x, w[0], w[1]);
+    e4m3x4_to_f16x2x2(u.y, w[2], w[3]);
+    e4m3x4_to_f16x2x2(u.z, w[4], w[5]);
+    e4m3x4_to_f16x2x2(u.w, w[6], w[7]);
+  }
+}
+template <int KVB>
+__device__ __forceinline__ uint4 words_to_cache(const uint32_t (&w)[KVB == 2 ? 4 : 8]) {
+  if constexpr (KVB == 2) {
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    return make_uint4(f16x2x2_to_e4m3x4(w[0], w[1]), f16x2x2_to_e4m3x4(w[2], w[3]), f16x2x2_to_e4m3x4(w[4], w[5]),
+                      f16x2x2_to_e4m3x4(w[6], w[7]));
+  }
+}
+
+constexpr int kBoundsWarps = 8;
+template <int D, int KVB>
+__global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kernel(const BlockBoundsParams P) {
+  constexpr int CPR = D * KVB / 16;  // 16-byte chunks per row
+  constexpr int RP = 32 / CPR;       // rows per warp-wide load
+  constexpr int W = KVB == 2 ? 4 : 8;
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
+  const int g = (int)(unit % P.num_kv_heads);
+  const long long bi = unit / P.num_kv_heads;
+  const int b = (int)(bi / P.grid_blocks);
+  if (b >= P.num_seqs) return;
+  const int L = P.context_lens[b];
+  const int start = P.start_lens ? max(P.start_lens[b], 0) : 0;
+  const long long i = start / P.block_size + bi % P.grid_blocks;
+  if (i * P.block_size >= L) return;
+  int p = -1;
+  if (i < P.max_blocks_per_seq) p = P.block_tables[(size_t)b * P.max_blocks_per_seq + i];
+  if (p < 0 || p >= P.num_blocks) {
+    if (lane == 0) record_error(P.error_word, kErrBadBlock);
+    return;
+  }
+  const int valid = min(P.block_size, (int)(L - i * P.block_size));
+  const int c = lane % CPR, r0 = lane / CPR;
+  const size_t tile = (size_t)p * P.num_kv_heads + g;
+  const uint4* src = static_cast<const uint4*>(P.k_cache) + tile * P.block_size * CPR + c;
+  uint32_t lo[W], hi[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    lo[w] = 0x7C007C00u;  // +inf
+    hi[w] = 0xFC00FC00u;  // -inf
+  }
+  for (int q0 = 0; q0 < P.block_size; q0 += 8 * RP) {  // 8 loads in flight a lane
+    uint4 u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = q0 + k * RP + r0;
+      if (r < valid) u[k] = src[(size_t)r * CPR];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = q0 + k * RP + r0;
+      if (r < valid) {
+        uint32_t x[W];
+        cache_words<KVB>(u[k], x);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          lo[w] = hmin2_u(lo[w], x[w]);
+          hi[w] = hmax2_u(hi[w], x[w]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = CPR; m < 32; m <<= 1)
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      lo[w] = hmin2_u(lo[w], __shfl_xor_sync(0xffffffffu, lo[w], m));
+      hi[w] = hmax2_u(hi[w], __shfl_xor_sync(0xffffffffu, hi[w], m));
+    }
+  uint4* dst = static_cast<uint4*>(P.bounds) + tile * 2 * CPR;
+  if (r0 == 0) dst[c] = words_to_cache<KVB>(lo);
+  if (r0 == 1) dst[CPR + c] = words_to_cache<KVB>(hi);
+}
+
+// ---------------------------------------------------------------------------
+// Choice of blocks.  The score of block i for kv head g is the largest score
+// that any key inside the block's bounds could have with any of the group's
+// queries,
+//   S_i = max_h sum_d max(q_hd lo_id, q_hd hi_id)
+//       = max_h (sum_d min(q_hd, 0) lo_id + sum_d max(q_hd, 0) hi_id),
+// a product of [blocks x 2D] bounds with [2D x heads] queries: mma.m16n8k16
+// with 16 blocks as rows and the group's heads as columns, bounds going from
+// global memory straight into A fragments (a lane's 16 bytes of a row are its
+// k slots of two steps; the query fragments follow the same order of dims).
+// The first `sink` and the last `recent` blocks are always taken, and of the
+// others the best, ties to the lowest index, as if scores were exact.
+//
+// The scores are sums of 2D exact products in fp32, off by at most E; the k-th
+// largest of them, tau, is found by radix selection, and blocks above
+// tau + 2E are chosen, those below tau - 2E are not, whatever the rounding
+// did.  Those between (most often tau's own block alone, and then nothing is
+// left to decide) are scored again in fp64, and the same step runs once more
+// on their distances from tau, kept as fp32 in the places of their scores;
+// after a second such step the distances are exact in fp64's last bit.
+//
+// One cluster per (sequence, kv head): its CTAs share the pass over the
+// bounds, which is bandwidth, and write scores into the shared memory of CTA
+// 0, which selects.  The others leave, so one row's selection runs beside
+// other rows' passes.
+struct BlockSelectParams {
+  const __half* q;      // [B][Hq][D]
+  const void* bounds;   // [num_blocks][Hkv][2][D]
+  const int32_t *block_tables, *context_lens;
+  int32_t* lists;       // [B][Hkv][max_selected]
+  int32_t* list_lens;   // [B][Hkv]
+  int num_seqs, num_q_heads, num_kv_heads, block_size, num_blocks, max_blocks_per_seq, max_blocks, max_selected, sink,
+      recent, cluster;
+  int* error_word;
+};
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBinBits = 11, kSelBins = 1 << kSelBinBits;
+constexpr int kSelMaxCluster = 8;
+// Relative to sum_d |q_d| max |bound|: 2D/16 accumulating steps, each off by
+// at most 2^-20 of the terms' sum however the tensor core aligns its 16
+// products and the accumulator, with a factor of two to spare.
+constexpr float kSelErr = 1.f / 32768.f;
+
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// Exclusive sums over the CTA of two counts per thread; *tot are the totals.
+__device__ __forceinline__ int2 block_scan2(int2 v, int2* warp_sums, int2* tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 s = v;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, s.x, k), y = __shfl_up_sync(0xffffffffu, s.y, k);
+    if (lane >= k) {
+      s.x += x;
+      s.y += y;
+    }
+  }
+  __syncthreads();  // the previous use of warp_sums is over
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  int2 base = make_int2(0, 0), all = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    const int2 x = warp_sums[w];
+    if (w < warp) {
+      base.x += x.x;
+      base.y += x.y;
+    }
+    all.x += x.x;
+    all.y += x.y;
+  }
+  *tot = all;
+  return make_int2(base.x + s.x - v.x, base.y + s.y - v.y);
+}
+
+template <int D, int KVB>
+__global__ void __launch_bounds__(kSelThreads, 2) paged_kv_block_select_kernel(const BlockSelectParams P) {
+  constexpr int DPC = 16 / KVB;      // dims per 16-byte chunk
+  constexpr int JJ = D / (4 * DPC);  // chunks per lane and row
+  constexpr int W = DPC / 2;         // fp16 pairs per chunk
+  constexpr int ROWB = D * KVB;      // bytes of lo (and of hi)
+  extern __shared__ __align__(16) float s_score[];  // CTA 0: [max_blocks]
+  __shared__ int s_hist[kSelBins];
+  __shared__ __half s_q[8 * D];
+  __shared__ float s_kmax[kSelMaxCluster * kSelWarps];
+  __shared__ int2 s_sums[kSelWarps];
+  __shared__ uint32_t s_red[2 * kSelWarps];
+  __shared__ float s_qsum[8];
+  __shared__ int s_found[2];
+
+  const int row = blockIdx.x / P.cluster, rank = blockIdx.x % P.cluster;
+  const int b = row / P.num_kv_heads, g = row % P.num_kv_heads;
+  const int G = P.num_q_heads / P.num_kv_heads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = lane / 4, c = lane % 4;
+  const int K = P.max_selected;
+  const int32_t* bt = P.block_tables + (size_t)b * P.max_blocks_per_seq;
+  int32_t* list = P.lists + (size_t)row * K;
+
+  const int L = P.context_lens[b];
+  int nblk = L > 0 ? (int)(((long long)L + P.block_size - 1) / P.block_size) : 0;
+  if (nblk > P.max_blocks) {  // past the host's bound or the table row
+    if (threadIdx.x == 0 && rank == 0) record_error(P.error_word, kErrBadBlock);
+    nblk = P.max_blocks;
+  }
+  if (nblk <= K) {  // every block is taken
+    if (rank == 0) {
+      for (int i = threadIdx.x; i < K; i += kSelThreads) list[i] = i < nblk ? i : -1;
+      if (threadIdx.x == 0) P.list_lens[row] = nblk;
+    }
+    return;
+  }
+  if (P.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+
+  // ---- scores
+  uint32_t qlo[JJ * W], qhi[JJ * W];  // min(q, 0), max(q, 0) of head r (zero past the group)
+  const __half* qrow = P.q + ((size_t)b * P.num_q_heads + g * G) * D;
+#pragma unroll
+  for (int jj = 0; jj < JJ; ++jj)
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const uint32_t x =
+          r < G ? *reinterpret_cast<const uint32_t*>(qrow + (size_t)r * D + DPC * (4 * jj + c) + 2 * w) : 0u;
+      qlo[jj * W + w] = hmin2_u(x, 0u);
+      qhi[jj * W + w] = hmax2_u(x, 0u);
+    }
+  const char* base = static_cast<const char*>(P.bounds) + (size_t)g * 2 * ROWB + 16 * c;
+  const size_t block_stride = (size_t)P.num_kv_heads * 2 * ROWB;
+  const int tiles = (nblk + 15) / 16;
+  const int step = P.cluster * kSelWarps;
+  uint32_t kabs = 0;  // running maximum of |bound|, fp16 pair
+  uint32_t score0;    // CTA 0's score array in the cluster's shared window
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(score0) : "r"(smem_u32(s_score)));
+  uint32_t kmax0;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(kmax0) : "r"(smem_u32(s_kmax)));
+  bool joined = P.cluster == 1;
+  auto ids = [&](int tile, int half) -> int {
+    const int i = tile * 16 + 8 * half + r;
+    return i < nblk ? bt[i] : -1;
+  };
+  int id[2] = {-1, -1};
+  int tile = rank * kSelWarps + warp;
+  if (tile < tiles) {
+    id[0] = ids(tile, 0);
+    id[1] = ids(tile, 1);
+  }
+  for (; tile < tiles; tile += step) {
+    uint4 a[2][2][JJ];  // [row half][lo, hi][chunk]
+    bool ok[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      ok[f] = id[f] >= 0 && id[f] < P.num_blocks;
+      const char* src = base + (size_t)(ok[f] ? id[f] : 0) * block_stride;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int jj = 0; jj < JJ; ++jj)
+          a[f][e][jj] = ok[f] ? *reinterpret_cast<const uint4*>(src + e * ROWB + 64 * jj) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (tile + step < tiles) {
+      id[0] = ids(tile + step, 0);
+      id[1] = ids(tile + step, 1);
+    }
+    float acc[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int jj = 0; jj < JJ; ++jj) {
+        uint32_t w0[W], w1[W];
+        cache_words<KVB>(a[0][e][jj], w0);
+        cache_words<KVB>(a[1][e][jj], w1);
+#pragma unroll
+        for (int w = 0; w < W; ++w) kabs = hmax2_u(kabs, hmax2_u(w0[w] & 0x7fff7fffu, w1[w] & 0x7fff7fffu));
+#pragma unroll
+        for (int s = 0; s < W / 2; ++s) {
+          const uint32_t av[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
+          const uint32_t* qv = (e == 0 ? qlo : qhi) + jj * W + 2 * s;
+          mma_16816(acc[e], av, qv[0], qv[1]);
+        }
+      }
+    if (!joined) {  // CTA 0 has started: its shared memory may be written
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      joined = true;
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      // heads 2c and 2c + 1 of block row r + 8f; heads past the group do not count
+      const float s0 = 2 * c < G ? acc[0][2 * f] + acc[1][2 * f] : -INFINITY;
+      const float s1 = 2 * c + 1 < G ? acc[0][2 * f + 1] + acc[1][2 * f + 1] : -INFINITY;
+      float s = fmaxf(s0, s1);
+      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
+      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+      const int i = tile * 16 + 8 * f + r;
+      if (c == 0 && i < nblk) {
+        if (!ok[f]) {
+          record_error(P.error_word, kErrBadBlock);
+          s = -3.0e38f;  // a block outside the pool comes last
+        }
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(score0 + 4 * i), "f"(s) : "memory");
+      }
+    }
+  }
+  if (!joined) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) kabs = hmax2_u(kabs, __shfl_xor_sync(0xffffffffu, kabs, k));
+  if (lane == 0) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&kabs));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(kmax0 + 4 * (rank * kSelWarps + warp)), "f"(fmaxf(f.x, f.y))
+                 : "memory");
+  }
+  if (P.cluster > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+
+  // ---- selection, CTA 0
+  for (int i = threadIdx.x; i < G * D; i += kSelThreads) s_q[i] = qrow[i];
+  __syncthreads();
+  if (warp < G) {
+    float s = 0.f;
+    for (int d = lane; d < D; d += 32) s += fabsf(__half2float(s_q[warp * D + d]));
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (lane == 0) s_qsum[warp] = s;
+  }
+  __syncthreads();
+  float kmax = 0.f, qsum = 0.f;
+  for (int i = 0; i < P.cluster * kSelWarps; ++i) kmax = fmaxf(kmax, s_kmax[i]);
+  for (int h = 0; h < G; ++h) qsum = fmaxf(qsum, s_qsum[h]);
+  float E = kmax * qsum * kSelErr;
+  const int i0 = P.sink, i1 = nblk - P.recent;  // the blocks to choose from
+  int need = K - P.sink - P.recent;             // of which so many are taken: < i1 - i0
+  float thr = INFINITY;                         // chosen: score >= thr, and the first `ties` of score == tie
+  if (threadIdx.x == 0) s_found[0] = s_found[1] = 0;
+  float tie = INFINITY;
+  int ties = 0;
+  double center = 0.0;
+  for (int round = 0; need > 0; ++round) {
+    // tau: the need-th largest of the finite scores
+    uint32_t kmin = 0xffffffffu, kmx = 0u;
+    for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads) {
+      const float s = s_score[i];
+      if (fabsf(s) < INFINITY) {
+        kmin = min(kmin, order_key(s));
+        kmx = max(kmx, order_key(s));
+      }
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+      kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, k));
+      kmx = max(kmx, __shfl_xor_sync(0xffffffffu, kmx, k));
+    }
+    __syncthreads();
+    if (lane == 0) {
+      s_red[warp] = kmin;
+      s_red[kSelWarps + warp] = kmx;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      kmin = min(kmin, s_red[w]);
+      kmx = max(kmx, s_red[kSelWarps + w]);
+    }
+    uint32_t lo = kmin, span = kmx - kmin;  // tau's key lies in [lo, lo + span]
+    int left = need;
+    while (span > 0) {
+      const int bits = 32 - __clz(span);
+      const int shift = bits > kSelBinBits ? bits - kSelBinBits : 0;
+      for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) s_hist[i] = 0;
+      __syncthreads();
+      for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads) {
+        const float s = s_score[i];
+        const uint32_t k = order_key(s) - lo;
+        if (fabsf(s) < INFINITY && k <= span) atomicAdd(&s_hist[k >> shift], 1);
+      }
+      __syncthreads();
+      constexpr int PER = kSelBins / kSelThreads;
+      int mine = 0;  // this thread's bins, from the highest down
+#pragma unroll
+      for (int k = 0; k < PER; ++k) mine += s_hist[kSelBins - 1 - (threadIdx.x * PER + k)];
+      int2 tot;
+      int above = block_scan2(make_int2(mine, 0), s_sums, &tot).x;
+      if (above < left && left <= above + mine) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int bin = kSelBins - 1 - (threadIdx.x * PER + k);
+          const int n = s_hist[bin];
+          if (above < left && left <= above + n) {
+            s_found[0] = bin;
+            s_found[1] = above;
+          }
+          above += n;
+        }
+      }
+      __syncthreads();
+      lo += (uint32_t)s_found[0] << shift;
+      left -= s_found[1];
+      span = (1u << shift) - 1u;
+    }
+    const float tau = key_value(lo);
+    const float wlo = __fsub_rd(tau, 2.f * E), whi = __fadd_ru(tau, 2.f * E);
+    int2 n = make_int2(0, 0);  // above the window, inside it
+    for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads) {
+      const float s = s_score[i];
+      if (fabsf(s) < INFINITY) {
+        n.x += s > whi;
+        n.y += s >= wlo && s <= whi;
+      }
+    }
+    int2 tot;
+    block_scan2(n, s_sums, &tot);
+    if (tot.x + tot.y == need) {  // the whole window is in
+      thr = wlo;
+      break;
+    }
+    if (E == 0.f) {  // equal scores: the lowest indices
+      tie = tau;
+      ties = need - tot.x;
+      // those above are chosen: mark them
+      for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads)
+        if (s_score[i] > tau) s_score[i] = INFINITY;
+      break;
+    }
+    // score the window again, exactly, as distances from tau
+    const double next = center + (double)tau;
+    for (int ib = i0 + 32 * warp; ib < i1; ib += kSelThreads) {
+      const int i = ib + lane;
+      const float s = i < i1 ? s_score[i] : -INFINITY;
+      const bool in = s >= wlo && s <= whi;
+      if (i < i1 && !in) s_score[i] = s > whi ? INFINITY : -INFINITY;
+      for (unsigned todo = __ballot_sync(0xffffffffu, in); todo; todo &= todo - 1) {
+        const int k = ib + __ffs(todo) - 1;
+        const int pb = bt[k];
+        double best = -3.0e38;
+        if (pb >= 0 && pb < P.num_blocks) {
+          constexpr int V = D / 32;
+          const char* src = static_cast<const char*>(P.bounds) + (size_t)pb * block_stride + (size_t)g * 2 * ROWB;
+          double kl[V], kh[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            if constexpr (KVB == 2) {
+              kl[v] = (double)__half2float(reinterpret_cast<const __half*>(src)[lane * V + v]);
+              kh[v] = (double)__half2float(reinterpret_cast<const __half*>(src + ROWB)[lane * V + v]);
+            } else {
+              uint32_t x, y;
+              e4m3x4_to_f16x2x2((uint32_t) reinterpret_cast<const uint8_t*>(src)[lane * V + v], x, y);
+              kl[v] = (double)__half2float(__ushort_as_half((unsigned short)(x & 0xffffu)));
+              e4m3x4_to_f16x2x2((uint32_t) reinterpret_cast<const uint8_t*>(src + ROWB)[lane * V + v], x, y);
+              kh[v] = (double)__half2float(__ushort_as_half((unsigned short)(x & 0xffffu)));
+            }
+          }
+          for (int h = 0; h < G; ++h) {
+            double s2 = 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              const double x = (double)__half2float(s_q[h * D + lane * V + v]);
+              s2 += fmax(x * kl[v], x * kh[v]);
+            }
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, m);
+            best = fmax(best, s2);
+          }
+        }
+        if (lane == 0) s_score[k] = (float)(best - next);
+      }
+    }
+    __syncthreads();
+    center = next;
+    need -= tot.x;
+    // a distance is at most a few E; its rounding to fp32 is off by 2^-24 of it.  The
+    // next round's distances from a point this near are exact.
+    E = round == 0 ? E * (1.f / (1 << 21)) : 0.f;
+  }
+  __syncthreads();
+
+  // ---- the chosen blocks in ascending order
+  const int per = (nblk + kSelThreads - 1) / kSelThreads;
+  const int from = min(nblk, (int)threadIdx.x * per), to = min(nblk, from + per);
+  auto chosen = [&](int i) { return i < i0 || i >= i1 || s_score[i] >= thr || s_score[i] == INFINITY; };
+  int2 n = make_int2(0, 0);
+  for (int i = from; i < to; ++i) {
+    const bool in = chosen(i);
+    n.x += in;
+    n.y += !in && ties > 0 && s_score[i] == tie;
+  }
+  int2 tot;
+  int2 at = block_scan2(n, s_sums, &tot);
+  for (int i = from; i < to; ++i) {
+    const bool in = chosen(i);
+    const bool eq = !in && ties > 0 && s_score[i] == tie;
+    if (in || (eq && at.y < ties)) {
+      const int place = at.x + min(at.y, ties);
+      if (place < K) list[place] = i;
+    }
+    at.x += in;
+    at.y += eq;
+  }
+  // (fewer than K only where a bound was not a number: such a block is never chosen)
+  const int count = min(K, tot.x + min(tot.y, ties));
+  for (int i = count + threadIdx.x; i < K; i += kSelThreads) list[i] = -1;
+  if (threadIdx.x == 0) P.list_lens[row] = count;
+}
+
+}  // namespace pkd

@@ -25,6 +25,8 @@ VARIANTS = {"auto": 0, "no_prefetch": 1, "l2_prefetch": 2, "tma_staged": 3, "tma
 DEVERR_BAD_BLOCK = 1
 DEVERR_TIMEOUT = 2
 DEVERR_LAYOUT = 4
+DEVERR_BAD_POSITION = 8
+MAX_SELECT_BLOCKS = 49152
 
 _lock = threading.Lock()
 _lib = None
@@ -105,6 +107,30 @@ def lib():
         L.pkd_read_device_error.restype = I
         L.paged_decode_attention_static_scratch.argtypes = attn + [I, I, I, P, P]
         L.paged_decode_attention_static_scratch.restype = I
+        LL = ctypes.c_longlong
+        rope = [P, P, P, LL, LL, LL, P, P, P, P, P, P, LL, P, P] + [I] * 11
+        L.paged_kv_append_rope.argtypes = rope + [P, P]
+        L.paged_kv_append_rope.restype = I
+        L.paged_kv_append_rope_fp8.argtypes = rope + [F, F, P, P]
+        L.paged_kv_append_rope_fp8.restype = I
+        prefix = [P] * 9 + [I] * 12 + [F]
+        L.paged_decode_attention_prefix.argtypes = prefix + [P, S, P, P]
+        L.paged_decode_attention_prefix.restype = I
+        L.paged_decode_attention_prefix_fp8.argtypes = prefix + [F, F, P, S, P, P]
+        L.paged_decode_attention_prefix_fp8.restype = I
+        L.paged_decode_prefix_workspace_size.argtypes = [I] * 9
+        L.paged_decode_prefix_workspace_size.restype = S
+        L.paged_kv_block_bounds.argtypes = [P] * 5 + [I] * 8 + [P, P]
+        L.paged_kv_block_bounds.restype = I
+        L.paged_kv_block_select.argtypes = [P] * 6 + [I] * 12 + [P, P]
+        L.paged_kv_block_select.restype = I
+        blocks = [P] * 8 + [I] * 8 + [F]
+        L.paged_decode_attention_blocks.argtypes = blocks + [P, S, P, P]
+        L.paged_decode_attention_blocks.restype = I
+        L.paged_decode_attention_blocks_fp8.argtypes = blocks + [F, F, P, S, P, P]
+        L.paged_decode_attention_blocks_fp8.restype = I
+        L.paged_decode_blocks_workspace_size.argtypes = [I] * 6
+        L.paged_decode_blocks_workspace_size.restype = S
         L.pkd_status_string.argtypes = [I]
         L.pkd_status_string.restype = ctypes.c_char_p
         L.pkd_version.argtypes = []
@@ -501,6 +527,281 @@ def paged_kv_append(k_new, v_new, block_tables, context_lens, k_cache, v_cache, 
                                _ptr(k_cache), _ptr(v_cache), B, Hkv, D, BS, NB,
                                block_tables.shape[1], _ptr(error_word), _stream(stream))
     _check(st, "paged_kv_append")
+
+
+# ------------------------------------------------------------ rotated append, shared prefixes, block lists
+# These entries launch on the current device; their tensors must be on it.
+def _here(t: torch.Tensor, *others):
+    d = t.device
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+    for o in others:
+        if o is not None and o.device != d:
+            raise ValueError("all tensors must be on the same device")
+
+
+def _want_heads(t: torch.Tensor, name: str) -> int:
+    """A [tokens][heads][head_dim] fp16 tensor whose heads are contiguous: its token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype != torch.float16:
+        raise ValueError(f"{name} must be a 3-D float16 CUDA tensor")
+    st, sh = t.stride(), t.shape
+    if sh[0] == 0 or sh[1] == 0:
+        return sh[1] * sh[2]
+    if (st[2] != 1 and sh[2] > 1) or (st[1] != sh[2] and sh[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st[0] if sh[0] > 1 else max(sh[1] * sh[2], (st[0] // 8) * 8)
+
+
+def _want_i32(t: torch.Tensor, name: str, shape):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _want_caches(k_cache, v_cache, fp8: bool):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if fp8:
+            _want_fp8_cache(t, name)
+        else:
+            _want(t, name, torch.float16, 4)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache / v_cache shape mismatch")
+
+
+def _append_rope(name, fp8, q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache, scales,
+                 token_starts, positions, interleaved, q_out, error_word, stream):
+    ks, vs = _want_heads(k_new, "k_new"), _want_heads(v_new, "v_new")
+    _want_caches(k_cache, v_cache, fp8)
+    _want(rope_table, "rope_table", torch.float32, 2)
+    NB, Hkv, BS, D = k_cache.shape
+    T = k_new.shape[0]
+    if k_new.shape[1:] != (Hkv, D) or v_new.shape != k_new.shape:
+        raise ValueError("k_new / v_new must be [num_tokens][num_kv_heads][head_dim]")
+    Hq = qs = os_ = 0
+    if q is not None:
+        qs, Hq = _want_heads(q, "q"), q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.float16, device=q.device)
+        os_ = _want_heads(q_out, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    B, R = context_lens.shape[0], rope_table.shape[1]
+    _want_i32(context_lens, "context_lens", (B,))
+    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
+    if token_starts is not None:
+        _want_i32(token_starts, "token_starts", (B + 1,))
+    if positions is not None:
+        _want_i32(positions, "positions", (T,))
+    _here(k_new, q, v_new, rope_table, token_starts, positions, block_tables, context_lens, q_out, k_cache, v_cache,
+          error_word)
+    fn = lib().paged_kv_append_rope_fp8 if fp8 else lib().paged_kv_append_rope
+    _check(fn(_ptr(q), _ptr(k_new), _ptr(v_new), qs, ks, vs, _ptr(rope_table), _ptr(token_starts), _ptr(positions),
+              _ptr(block_tables), _ptr(context_lens), _ptr(q_out), os_, _ptr(k_cache), _ptr(v_cache), T, B, Hq, Hkv,
+              D, R, int(bool(interleaved)), rope_table.shape[0], BS, NB, block_tables.shape[1], *scales,
+              _ptr(error_word), _stream(stream)), name)
+    return q_out
+
+
+def paged_kv_append_rope(q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache,
+                         token_starts=None, positions=None, interleaved=False, q_out=None, error_word=None,
+                         stream=None):
+    """Rotate the new tokens' q and k ([T][heads][D], any token stride) by their positions and write
+    k and v into the paged caches; token j of sequence b is row token_starts[b] + j and goes to
+    logical position context_lens[b] + j.  rope_table is fp32 [max_positions][rotary_dim], cosines
+    then sines.  Returns the rotated queries (``q_out``; may be ``q``; None when ``q`` is None)."""
+    return _append_rope("paged_kv_append_rope", False, q, k_new, v_new, rope_table, block_tables, context_lens,
+                        k_cache, v_cache, (), token_starts, positions, interleaved, q_out, error_word, stream)
+
+
+def paged_kv_append_rope_fp8(q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache, k_scale,
+                             v_scale, token_starts=None, positions=None, interleaved=False, q_out=None,
+                             error_word=None, stream=None):
+    """paged_kv_append_rope into E4M3 caches (value = code * k_scale / v_scale)."""
+    return _append_rope("paged_kv_append_rope_fp8", True, q, k_new, v_new, rope_table, block_tables, context_lens,
+                        k_cache, v_cache, (float(k_scale), float(v_scale)), token_starts, positions, interleaved,
+                        q_out, error_word, stream)
+
+
+def paged_decode_prefix_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_groups,
+                                       max_prefix_len, max_context_len) -> int:
+    return int(lib().paged_decode_prefix_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, head_dim,
+                                                        block_size, num_groups, max_prefix_len, max_context_len))
+
+
+def _attention_prefix(name, fp8, q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables,
+                      context_lens, scale, scales, out, max_prefix_len, max_context_len, workspace, error_word,
+                      stream):
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be [num_seqs][num_q_heads][head_dim] or [num_seqs][q_len][num_q_heads][head_dim]")
+    _want(q, "q", torch.float16)
+    _want_caches(k_cache, v_cache, fp8)
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    QL = q.shape[1] if q.dim() == 4 else 1
+    NB, Hkv, BS, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("q / k_cache head_dim mismatch")
+    Y = prefix_tables.shape[0]
+    _want_i32(prefix_tables, "prefix_tables", (Y, prefix_tables.shape[1]))
+    _want_i32(prefix_lens, "prefix_lens", (Y,))
+    _want_i32(group_starts, "group_starts", (Y + 1,))
+    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
+    _want_i32(context_lens, "context_lens", (B,))
+    if out is None:
+        out = torch.empty_like(q)
+    _want(out, "out", torch.float16)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _here(q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables, context_lens, out, workspace,
+          error_word)
+    mp, mc = _max_len(prefix_lens, max_prefix_len), _max_len(context_lens, max_context_len)
+    if workspace is None:
+        workspace = alloc_workspace(paged_decode_prefix_workspace_size(B, QL, Hq, Hkv, D, BS, Y, mp, mc), q.device)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    fn = lib().paged_decode_attention_prefix_fp8 if fp8 else lib().paged_decode_attention_prefix
+    _check(fn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_tables), _ptr(prefix_lens), _ptr(group_starts),
+              _ptr(block_tables), _ptr(context_lens), _ptr(out), B, QL, Y, Hq, Hkv, D, BS, NB,
+              prefix_tables.shape[1], block_tables.shape[1], mp, mc, float(scale), *scales, _ptr(workspace), wsb,
+              _ptr(error_word), _stream(stream)), name)
+    return out
+
+
+def paged_decode_attention_prefix(q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables,
+                                  context_lens, scale, out=None, max_prefix_len=None, max_context_len=None,
+                                  workspace=None, error_word=None, stream=None) -> torch.Tensor:
+    """Decode of groups of sequences that share a prefix: every query of group y (sequences
+    group_starts[y] .. group_starts[y + 1] - 1) attends to the prefix_lens[y] tokens of table row
+    prefix_tables[y], read once for the group, and to its own context.  q is [B][Hq][D] or
+    [B][q_len][Hq][D] (causal among the new tokens)."""
+    return _attention_prefix("paged_decode_attention_prefix", False, q, k_cache, v_cache, prefix_tables, prefix_lens,
+                             group_starts, block_tables, context_lens, scale, (), out, max_prefix_len,
+                             max_context_len, workspace, error_word, stream)
+
+
+def paged_decode_attention_prefix_fp8(q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables,
+                                      context_lens, scale, k_scale, v_scale, out=None, max_prefix_len=None,
+                                      max_context_len=None, workspace=None, error_word=None,
+                                      stream=None) -> torch.Tensor:
+    """paged_decode_attention_prefix over E4M3 caches."""
+    return _attention_prefix("paged_decode_attention_prefix_fp8", True, q, k_cache, v_cache, prefix_tables,
+                             prefix_lens, group_starts, block_tables, context_lens, scale,
+                             (float(k_scale), float(v_scale)), out, max_prefix_len, max_context_len, workspace,
+                             error_word, stream)
+
+
+def paged_kv_block_bounds(k_cache, block_tables, context_lens, bounds, start_lens=None, max_new_tokens=None,
+                          error_word=None, stream=None) -> torch.Tensor:
+    """Elementwise minimum and maximum of the keys of every block (from block start_lens[b] /
+    block_size on) into ``bounds`` [num_blocks][num_kv_heads][2][head_dim] of the cache's type.
+    ``max_new_tokens`` bounds context_lens - start_lens from above (default: the table's row)."""
+    fp8 = isinstance(k_cache, torch.Tensor) and k_cache.element_size() == 1
+    if fp8:
+        _want_fp8_cache(k_cache, "k_cache")
+        _want_fp8_cache(bounds, "bounds")
+    else:
+        _want(k_cache, "k_cache", torch.float16, 4)
+        _want(bounds, "bounds", torch.float16, 4)
+    NB, Hkv, BS, D = k_cache.shape
+    if tuple(bounds.shape) != (NB, Hkv, 2, D):
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
+    B = context_lens.shape[0]
+    _want_i32(context_lens, "context_lens", (B,))
+    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
+    if start_lens is not None:
+        _want_i32(start_lens, "start_lens", (B,))
+    _here(k_cache, block_tables, context_lens, start_lens, bounds, error_word)
+    most = block_tables.shape[1] * BS if max_new_tokens is None else int(max_new_tokens)
+    _check(lib().paged_kv_block_bounds(_ptr(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(start_lens),
+                                       _ptr(bounds), B, Hkv, D, BS, NB, block_tables.shape[1], most, int(fp8),
+                                       _ptr(error_word), _stream(stream)), "paged_kv_block_bounds")
+    return bounds
+
+
+def paged_kv_block_select(q, bounds, block_tables, context_lens, max_selected, block_size, sink_blocks=1,
+                          recent_blocks=1, max_context_len=None, block_lists=None, list_lens=None, error_word=None,
+                          stream=None):
+    """The ``max_selected`` blocks of each (sequence, kv head) worth attending to: the first
+    ``sink_blocks``, the last ``recent_blocks`` and those whose bounds allow the largest scores.
+    Returns (block_lists int32 [B][Hkv][max_selected], ascending then -1; list_lens [B][Hkv])."""
+    _want(q, "q", torch.float16, 3)
+    fp8 = isinstance(bounds, torch.Tensor) and bounds.element_size() == 1
+    if fp8:
+        _want_fp8_cache(bounds, "bounds")
+    else:
+        _want(bounds, "bounds", torch.float16, 4)
+    B, Hq, D = q.shape
+    NB, Hkv, two, D2 = bounds.shape
+    if D2 != D or two != 2:
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
+    K = int(max_selected)
+    _want_i32(context_lens, "context_lens", (B,))
+    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
+    if block_lists is None:
+        block_lists = torch.empty((B, Hkv, max(K, 0)), dtype=torch.int32, device=q.device)
+    if list_lens is None:
+        list_lens = torch.empty((B, Hkv), dtype=torch.int32, device=q.device)
+    _want_i32(block_lists, "block_lists", (B, Hkv, K))
+    _want_i32(list_lens, "list_lens", (B, Hkv))
+    _here(q, bounds, block_tables, context_lens, block_lists, list_lens, error_word)
+    _check(lib().paged_kv_block_select(_ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens),
+                                       _ptr(block_lists), _ptr(list_lens), B, Hq, Hkv, D, int(block_size), NB,
+                                       block_tables.shape[1], _max_len(context_lens, max_context_len), K,
+                                       int(sink_blocks), int(recent_blocks), int(fp8), _ptr(error_word),
+                                       _stream(stream)), "paged_kv_block_select")
+    return block_lists, list_lens
+
+
+def paged_decode_blocks_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_listed) -> int:
+    return int(lib().paged_decode_blocks_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                        max_listed))
+
+
+def _attention_blocks(name, fp8, q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, scale,
+                      scales, out, workspace, error_word, stream):
+    _want(q, "q", torch.float16, 3)
+    _want_caches(k_cache, v_cache, fp8)
+    B, Hq, D = q.shape
+    NB, Hkv, BS, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("q / k_cache head_dim mismatch")
+    _want_i32(context_lens, "context_lens", (B,))
+    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
+    K = block_lists.shape[-1]
+    _want_i32(block_lists, "block_lists", (B, Hkv, K))
+    _want_i32(list_lens, "list_lens", (B, Hkv))
+    if out is None:
+        out = torch.empty_like(q)
+    _want(out, "out", torch.float16)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _here(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, out, workspace, error_word)
+    if workspace is None:
+        workspace = alloc_workspace(paged_decode_blocks_workspace_size(B, Hq, Hkv, D, BS, K), q.device)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    fn = lib().paged_decode_attention_blocks_fp8 if fp8 else lib().paged_decode_attention_blocks
+    _check(fn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(block_lists),
+              _ptr(list_lens), _ptr(out), B, Hq, Hkv, D, BS, NB, block_tables.shape[1], K, float(scale), *scales,
+              _ptr(workspace), wsb, _ptr(error_word), _stream(stream)), name)
+    return out
+
+
+def paged_decode_attention_blocks(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, scale,
+                                  out=None, workspace=None, error_word=None, stream=None) -> torch.Tensor:
+    """Single-query decode over the listed logical blocks of each (sequence, kv head) alone
+    (lists as paged_kv_block_select writes them); returns ``out``."""
+    return _attention_blocks("paged_decode_attention_blocks", False, q, k_cache, v_cache, block_tables, context_lens,
+                             block_lists, list_lens, scale, (), out, workspace, error_word, stream)
+
+
+def paged_decode_attention_blocks_fp8(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, scale,
+                                      k_scale, v_scale, out=None, workspace=None, error_word=None,
+                                      stream=None) -> torch.Tensor:
+    """paged_decode_attention_blocks over E4M3 caches."""
+    return _attention_blocks("paged_decode_attention_blocks_fp8", True, q, k_cache, v_cache, block_tables,
+                             context_lens, block_lists, list_lens, scale, (float(k_scale), float(v_scale)), out,
+                             workspace, error_word, stream)
 
 
 def pkd_read_device_error(error_word, clear=True, stream=None) -> int:
