@@ -1194,34 +1194,61 @@ struct PartPlan {
   int chunks = 1;
   int P = 32;
   int np = 0;
+  int rows = 0;  // kSharedTc: query rows per chunk
   long long grid = 0;
 };
 
-// A shared prefix of up to max_prefix_len tokens: the chunks of all groups
-// (at most `tokens / per` full ones and a rest for each group) times the kv
-// heads are the units; each reads the prefix in as many partitions as fill the
-// GPU's resident CTAs once.  Where a group has 16 query rows or fewer per kv
-// head on average, the 16-row mma.sync tile serves it; else the 64-row tcgen05
-// one does.
+// The data path of paged_shared_tc_kernel, beside the pkd_variant values.
+constexpr int kSharedTc = 100;
+constexpr int kSharedSplit = 9;       // partitions per unit from which it takes chunks of 128 rows
+constexpr int kFewSharedRows = 64;    // rows per group and kv head up to which,
+constexpr int kShortPrefix = 1024;    // with prefixes up to this long, the mma.sync kernel serves them
+
+// A shared prefix of up to max_prefix_len tokens: chunks of a group's query
+// rows times the kv heads are the units; each reads the prefix in as many
+// partitions as fill the GPU's resident CTAs once, of kMinSmallGridPartition
+// tokens at least.  Two kernels:
+//  * the shared-context tcgen05 kernel, chunks of 256 rows (two tiles that
+//    share each K and V tile), or of 128 where 256 would leave every unit nine
+//    partitions or more: with so few units the longer chain of a CTA with two
+//    row tiles costs more than the second read (256 rows x 8 kv heads, 2500
+//    tokens: 24 against 32 us for the whole call; 512 rows, 8192 tokens: 47
+//    against 49; but 672 rows x 2 groups x 4, 8192 tokens: 80 against 70);
+//  * the mma.sync kernel's 16-row tiles, three CTAs per SM, for groups of up
+//    to 64 rows on average and prefixes of up to 1024 tokens, where a CTA's
+//    start is what counts (16 rows x 8, 1000 tokens: 15.7 against 17.2 us; 2500
+//    tokens: 17.9 against 16.6), and for E4M3 caches at head_dim 64.
 PartPlan plan_shared(const Shape& s, int q_len, int num_groups, int max_prefix_len, int kv_fp8) {
   PartPlan p;
   if (max_prefix_len <= 0 || num_groups <= 0 || s.num_seqs <= 0) return p;
   const int G = s.num_q_heads / s.num_kv_heads;
-  const long long tokens = (long long)s.num_seqs * q_len;
-  const bool tc = tc_supports(s, kv_fp8) && tokens * G > 16LL * num_groups;
-  p.variant = tc ? PKD_VARIANT_TCGEN05 : PKD_VARIANT_TMA_MMA;
-  const int per = (tc ? pkd::kTcRowsPerCta : 16) / G;
-  p.chunks = (int)(tokens / per + num_groups);
-  const long long units = std::max(1LL, tokens / per + (num_groups == 1 ? 1 : num_groups)) * s.num_kv_heads;
+  const long long tokens = (long long)s.num_seqs * q_len, rows = tokens * G;
   int sms = sm_count();
   if (sms <= 0) sms = 148;
-  const long long slots = (long long)sms * path_stream(p.variant, s.head_dim, G, kv_fp8 ? 1 : 2, false).ctas_per_sm;
-  const int least = tc ? kMinSmallGridPartitionTc : kMinSmallGridPartition;
+  // chunks of all groups: with one group as many as its rows need, else at
+  // most the full ones and a rest for each group
+  auto chunks_of = [&](long long n, int per) {
+    return num_groups == 1 ? (n + per - 1) / per : n / per + num_groups;
+  };
+  long long chunks, slots;
+  if (!tc_supports(s, kv_fp8) || (rows <= kFewSharedRows * num_groups && max_prefix_len <= kShortPrefix)) {
+    p.variant = PKD_VARIANT_TMA_MMA;
+    chunks = chunks_of(tokens, 16 / G);
+    slots = (long long)sms * path_stream(p.variant, s.head_dim, G, kv_fp8 ? 1 : 2, false).ctas_per_sm;
+  } else {
+    p.variant = kSharedTc;
+    slots = sms;
+    p.rows = pkd::kSharedRowsPerCta;
+    if (chunks_of(rows, p.rows) * s.num_kv_heads * kSharedSplit <= slots) p.rows /= 2;
+    chunks = chunks_of(rows, p.rows);
+  }
+  p.chunks = (int)chunks;
+  const long long units = chunks * s.num_kv_heads;
   long long np = std::max(1LL, slots / units);
-  np = std::min<long long>(np, (max_prefix_len + least - 1) / least);
+  np = std::min<long long>(np, (max_prefix_len + kMinSmallGridPartition - 1) / kMinSmallGridPartition);
   p.P = (int)round_up((size_t)((max_prefix_len + np - 1) / np), 64);
   p.np = (max_prefix_len + p.P - 1) / p.P;
-  p.grid = (long long)p.chunks * s.num_kv_heads * p.np;
+  p.grid = units * p.np;
   return p;
 }
 
@@ -1267,7 +1294,9 @@ pkd_status launch_part(const Shape& s, const PartPlan& plan, const pkd::DecodePa
   const int G = s.num_q_heads / s.num_kv_heads;
   const int D = s.head_dim, BS = s.block_size;
   cudaError_t e;
-  if (plan.variant == PKD_VARIANT_TCGEN05)
+  if (plan.variant == kSharedTc)
+    e = pkd::launch_shared_tc(D, BS, p, plan.grid, stream, kv_fp8 ? 1 : 2);
+  else if (plan.variant == PKD_VARIANT_TCGEN05)
     e = pkd::launch_decode_tcgen05(D, BS, p, plan.grid, stream, kv_fp8 ? 1 : 2);
   else if (p.group_starts)
     e = kv_fp8 ? pkd::launch_decode_shared_fp8(D, BS, G, p, plan.grid, stream)
@@ -1366,6 +1395,7 @@ pkd_status prefix_impl(const void* q, const void* k_cache, const void* v_cache, 
     if (shared) {
       p.group_starts = group_starts;
       p.num_groups = num_groups;
+      p.rows_per_chunk = plan.rows;
     }
     (shared ? m.shared : m.own) = merge_source(w, plan);
     return launch_part(s, plan, p, kv_fp8, stream);

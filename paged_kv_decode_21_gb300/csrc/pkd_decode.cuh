@@ -81,6 +81,7 @@ struct DecodeParams {
   // table row y, context_lens[y] tokens; q_chunks is the grid's chunk count over all groups
   const int32_t* group_starts;  // [num_groups + 1]
   int num_groups;
+  int rows_per_chunk;  // paged_shared_tc_kernel: query rows per chunk
 };
 
 // Which keys the query rows of a tensor-core decode CTA read.
@@ -91,10 +92,11 @@ enum KeySource : int {
 };
 
 // Chunk x of a grid over groups of sequences: the chunks of `per` query
-// tokens of group 0, then those of group 1, and so on.  Sets the group, the
-// chunk's first query token inside it, the group's query tokens and its
-// first one over the whole batch; false when x is past the last chunk.  Every
-// lane of the calling warp gets the same answer.
+// tokens of group 0, then those of group 1, and so on (q_len query tokens, or
+// whatever else is counted, per sequence).  Sets the group, the chunk's first
+// query token inside it, the group's query tokens and its first one over the
+// whole batch; false when x is past the last chunk.  Every lane of the calling
+// warp gets the same answer.
 struct GroupChunk {
   int group, first, tokens, base;
 };

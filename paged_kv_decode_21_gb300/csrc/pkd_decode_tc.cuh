@@ -145,8 +145,7 @@ struct TcTraits {
 
 // RUNS: the build for runs of consecutive partitions per CTA (P.parts_per_cta
 // > 1); the other build has one partition per CTA fixed at compile time.
-// SRC: kOwn, or kShared (see pkd_decode_mma.cuh).
-template <int BS, int KVB, int HD, bool RUNS = false, int SRC = kOwn>
+template <int BS, int KVB, int HD, bool RUNS = false>
 __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, KVB, HD>::MIN_BLOCKS)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                            const DecodeParams P) {
@@ -205,25 +204,16 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
     g = bg % P.num_kv_heads;
     b = bg / P.num_kv_heads;
   }
-  int jq0 = qc * (T::ROWS / G);  // first query token of this CTA
-  int QL = P.q_len;              // query tokens of the sequence (kShared: of the group)
-  int tok0 = b * P.q_len;        // the first of them over the batch
-  if constexpr (SRC == kShared) {
-    GroupChunk ch;
-    if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len, T::ROWS / G, qc, &ch)) return;
-    b = ch.group;
-    jq0 = ch.first;
-    QL = ch.tokens;
-    tok0 = ch.base;
-  }
   const int L = row_clamped_len<BS>(P, b);
+  const int QL = P.q_len;
+  const int jq0 = qc * (T::ROWS / G);         // first query token of this CTA
   const int nq = min(T::ROWS / G, QL - jq0);  // its query tokens (>= 1)
   const int rows = G * nq;                    // tile rows in use
   const int PS = half ? tail_half_partition(L) : P.partition_size;
   const int np_b = min((L + PS - 1) / PS, np_grid);
   const bool final_out = (P.mode == 0) && np_b <= 1;
   const int Hq = P.num_q_heads;
-  auto out_row = [&](int rr) { return ((size_t)tok0 + jq0 + rr / G) * Hq + g * G + rr % G; };
+  auto out_row = [&](int rr) { return ((size_t)b * QL + jq0 + rr / G) * Hq + g * G + rr % G; };
 
   if (L <= 0) {
     if (final_out && j == 0) {
@@ -241,7 +231,7 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
 
   const int t0 = j * PS;
   // the chunk's last query sees tokens < L - QL + jq0 + nq; nothing past that is read
-  const int t1 = SRC == kShared ? min(j_end * PS, L) : min(min(j_end * PS, L), L - QL + jq0 + nq);
+  const int t1 = min(min(j_end * PS, L), L - QL + jq0 + nq);
   const int ntiles = t1 > t0 ? (t1 - t0 + TN - 1) / TN : 0;
   const int nblk = t1 > t0 ? (t1 - t0 + BS - 1) / BS : 0;
   const int32_t* bt = P.block_tables + (size_t)b * P.max_blocks_per_seq + t0 / BS;
@@ -621,7 +611,7 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
     const bool live = rr < rows;
     // tokens at or past lim are masked for this row; an unused row takes the
     // last used row's limit, so that the warp takes one path through the mask
-    const int lim = SRC == kShared ? t1 : min(t1, L - QL + jq0 + (live ? rr : rows - 1) / G + 1);
+    const int lim = min(t1, L - QL + jq0 + (live ? rr : rows - 1) / G + 1);
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
     float m = -INFINITY, mt = -INFINITY, l = 0.f;  // running shift, exact maximum, sum of p
     // The result of partition pj: O / l to the output (a sequence of one

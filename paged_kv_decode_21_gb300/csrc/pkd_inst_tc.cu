@@ -15,8 +15,7 @@ cudaError_t launch_tc_bs(const CUtensorMap& mk, const CUtensorMap& mv, const Dec
                          cudaStream_t stream) {
   using T = TcTraits<BS, KVB, HD>;
   // runs of partitions per CTA: head_dim 128 only (the plan asks for them there)
-  auto* fn = p.group_starts ? paged_decode_tc_kernel<BS, KVB, HD, false, kShared>
-             : (HD == 128 && p.parts_per_cta > 1) ? paged_decode_tc_kernel<BS, KVB, HD, HD == 128>
+  auto* fn = (HD == 128 && p.parts_per_cta > 1) ? paged_decode_tc_kernel<BS, KVB, HD, HD == 128>
                                                  : paged_decode_tc_kernel<BS, KVB, HD, false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
   if (e != cudaSuccess) return e;

@@ -85,6 +85,20 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same, giving up early when another role of the CTA raised *abort_flag
+// (read only once the barrier was found incomplete: under a stream of MMAs
+// that read their operands from shared memory, every access costs a hundred
+// cycles and more).
+__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                                   const volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 63u && (*abort_flag || globaltimer_ns() - t0 > budget_ns)) return false;
+  }
+}
+
 // ---------------------------------------------------------------- TMA
 // 4-D tiled load of the box at coordinates (c0..c3) of `tmap` into shared
 // memory at `dst`, completing `bytes` on `bar`.  c0 (innermost) must be a

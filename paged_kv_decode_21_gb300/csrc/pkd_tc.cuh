@@ -58,6 +58,19 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// One lane of a converged warp (always the same one).  Code under it may issue
+// single-thread tcgen05 operations while the warp's control flow around it
+// stays uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // ---------------------------------------------------------------- MMA
 // D (tensor memory) = A * B (+ D when `accumulate`), fp16 inputs from shared
 // memory through descriptors, fp32 accumulation.  One thread issues it.

@@ -16,4 +16,13 @@ constexpr int kTcRowsPerCta = 64;
 cudaError_t launch_decode_tcgen05(int D, int BS, const DecodeParams& p, long long grid, cudaStream_t stream,
                                   int kvb = 2);
 
+// Query rows one CTA of the shared-context kernel (pkd_shared_tc.cuh) serves.
+constexpr int kSharedRowsPerCta = 256;
+
+// Launch `grid` CTAs of the shared-context kernel: p.q_chunks chunks of
+// p.rows_per_chunk (at most kSharedRowsPerCta) query rows of all groups, times
+// p.max_partitions, times the kv heads; partials.  kvb, head_dim and block
+// size as for launch_decode_tcgen05.
+cudaError_t launch_shared_tc(int D, int BS, const DecodeParams& p, long long grid, cudaStream_t stream, int kvb);
+
 }  // namespace pkd

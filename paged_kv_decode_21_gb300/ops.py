@@ -530,78 +530,125 @@ def paged_kv_append(k_new, v_new, block_tables, context_lens, k_cache, v_cache, 
 
 
 # ------------------------------------------------------------ rotated append, shared prefixes, block lists
-# These entries launch on the current device; their tensors must be on it.
-def _here(t: torch.Tensor, *others):
-    d = t.device
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
-    for o in others:
-        if o is not None and o.device != d:
-            raise ValueError("all tensors must be on the same device")
+# These entries run once a decode step and layer, so their checks are kept to a
+# few attribute reads a tensor; their tensors must be on the current device.
+_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
 
 
-def _want_heads(t: torch.Tensor, name: str) -> int:
-    """A [tokens][heads][head_dim] fp16 tensor whose heads are contiguous: its token stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype != torch.float16:
-        raise ValueError(f"{name} must be a 3-D float16 CUDA tensor")
-    st, sh = t.stride(), t.shape
-    if sh[0] == 0 or sh[1] == 0:
-        return sh[1] * sh[2]
-    if (st[2] != 1 and sh[2] > 1) or (st[1] != sh[2] and sh[1] > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st[0] if sh[0] > 1 else max(sh[1] * sh[2], (st[0] // 8) * 8)
+def _on(t, name: str, dtype, shape, dev: int):
+    """A contiguous tensor of this type and shape on device ``dev``: its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _want_i32(t: torch.Tensor, name: str, shape):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
-    if tuple(t.shape) != shape:
+def _opt(t, name: str, dtype, shape, dev: int):
+    return None if t is None else _on(t, name, dtype, shape, dev)
+
+
+def _device(t, name: str) -> int:
+    """The current device, which ``t`` has to be on (and the library loaded)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if _lib is None:
+        lib()
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _word(error_word, dev: int):
+    """The error word's address: the first element of an int32 tensor."""
+    if error_word is None:
+        return None
+    if error_word.dtype is not _I32 or error_word.get_device() != dev or error_word.numel() < 1:
+        raise ValueError(f"error_word must be an int32 tensor on cuda:{dev}")
+    return error_word.data_ptr()
+
+
+def _space(workspace, dev: int):
+    """(address, bytes) of a workspace."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _heads(t, name: str, dev: int, shape=None):
+    """(address, token stride) of a [tokens][heads][head_dim] fp16 tensor whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F16 or t.dim() != 3 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a 3-D float16 tensor on cuda:{dev}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    T, H, D = t.shape
+    if T == 0 or H == 0:
+        return t.data_ptr(), H * D
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (st if T > 1 else H * D)
 
 
-def _want_caches(k_cache, v_cache, fp8: bool):
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if fp8:
-            _want_fp8_cache(t, name)
-        else:
-            _want(t, name, torch.float16, 4)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache / v_cache shape mismatch")
+def _cache(t, name: str, fp8: bool, dev: int, shape=None):
+    """Address of a [num_blocks][num_kv_heads][rows][head_dim] fp16 or E4M3 byte tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.get_device() != dev or not t.is_contiguous() or (
+            t.element_size() != 1 if fp8 else t.dtype is not _F16):
+        raise ValueError(f"{name} must be a contiguous 4-D {'byte (uint8 or float8_e4m3fn)' if fp8 else 'float16'} "
+                         f"tensor on cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _table(t, name: str, rows: int, dev: int):
+    """(address, row length) of an int32 block table."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    width = t.shape[1]
+    return _on(t, name, _I32, (rows, width), dev), width
 
 
 def _append_rope(name, fp8, q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache, scales,
                  token_starts, positions, interleaved, q_out, error_word, stream):
-    ks, vs = _want_heads(k_new, "k_new"), _want_heads(v_new, "v_new")
-    _want_caches(k_cache, v_cache, fp8)
-    _want(rope_table, "rope_table", torch.float32, 2)
+    dev = _device(k_new, "k_new")
+    kc = _cache(k_cache, "k_cache", fp8, dev)
+    vc = _cache(v_cache, "v_cache", fp8, dev, k_cache.shape)
     NB, Hkv, BS, D = k_cache.shape
     T = k_new.shape[0]
-    if k_new.shape[1:] != (Hkv, D) or v_new.shape != k_new.shape:
-        raise ValueError("k_new / v_new must be [num_tokens][num_kv_heads][head_dim]")
+    kp, ks = _heads(k_new, "k_new", dev, (T, Hkv, D))
+    vp, vs = _heads(v_new, "v_new", dev, (T, Hkv, D))
+    qp = op = None
     Hq = qs = os_ = 0
     if q is not None:
-        qs, Hq = _want_heads(q, "q"), q.shape[1]
+        qp, qs = _heads(q, "q", dev)
+        Hq = q.shape[1]
         if q.shape[0] != T or q.shape[2] != D:
             raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.float16, device=q.device)
-        os_ = _want_heads(q_out, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    B, R = context_lens.shape[0], rope_table.shape[1]
-    _want_i32(context_lens, "context_lens", (B,))
-    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
-    if token_starts is not None:
-        _want_i32(token_starts, "token_starts", (B + 1,))
-    if positions is not None:
-        _want_i32(positions, "positions", (T,))
-    _here(k_new, q, v_new, rope_table, token_starts, positions, block_tables, context_lens, q_out, k_cache, v_cache,
-          error_word)
-    fn = lib().paged_kv_append_rope_fp8 if fp8 else lib().paged_kv_append_rope
-    _check(fn(_ptr(q), _ptr(k_new), _ptr(v_new), qs, ks, vs, _ptr(rope_table), _ptr(token_starts), _ptr(positions),
-              _ptr(block_tables), _ptr(context_lens), _ptr(q_out), os_, _ptr(k_cache), _ptr(v_cache), T, B, Hq, Hkv,
-              D, R, int(bool(interleaved)), rope_table.shape[0], BS, NB, block_tables.shape[1], *scales,
-              _ptr(error_word), _stream(stream)), name)
+            q_out = torch.empty((T, Hq, D), dtype=_F16, device=q.device)
+        op, os_ = _heads(q_out, "q_out", dev, q.shape)
+    if not isinstance(rope_table, torch.Tensor) or rope_table.dim() != 2:
+        raise ValueError("rope_table must be [max_positions][rotary_dim]")
+    MP, R = rope_table.shape
+    rp = _on(rope_table, "rope_table", _F32, rope_table.shape, dev)
+    B = context_lens.shape[0]
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    fn = _lib.paged_kv_append_rope_fp8 if fp8 else _lib.paged_kv_append_rope
+    st = fn(qp, kp, vp, qs, ks, vs, rp if R else None, _opt(token_starts, "token_starts", _I32, (B + 1,), dev),
+            _opt(positions, "positions", _I32, (T,), dev), bt, cl, op, os_, kc, vc, T, B, Hq, Hkv, D, R,
+            1 if interleaved else 0, MP, BS, NB, MB, *scales, _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, name)
     return q_out
 
 
@@ -634,37 +681,34 @@ def paged_decode_prefix_workspace_size(num_seqs, q_len, num_q_heads, num_kv_head
 def _attention_prefix(name, fp8, q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables,
                       context_lens, scale, scales, out, max_prefix_len, max_context_len, workspace, error_word,
                       stream):
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+    dev = _device(q, "q")
+    if q.dim() not in (3, 4):
         raise ValueError("q must be [num_seqs][num_q_heads][head_dim] or [num_seqs][q_len][num_q_heads][head_dim]")
-    _want(q, "q", torch.float16)
-    _want_caches(k_cache, v_cache, fp8)
-    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
-    QL = q.shape[1] if q.dim() == 4 else 1
+    B, QL, Hq, D = q.shape if q.dim() == 4 else (q.shape[0], 1, q.shape[1], q.shape[2])
+    qp = _on(q, "q", _F16, q.shape, dev)
+    kc = _cache(k_cache, "k_cache", fp8, dev)
+    vc = _cache(v_cache, "v_cache", fp8, dev, k_cache.shape)
     NB, Hkv, BS, D2 = k_cache.shape
     if D2 != D:
         raise ValueError("q / k_cache head_dim mismatch")
-    Y = prefix_tables.shape[0]
-    _want_i32(prefix_tables, "prefix_tables", (Y, prefix_tables.shape[1]))
-    _want_i32(prefix_lens, "prefix_lens", (Y,))
-    _want_i32(group_starts, "group_starts", (Y + 1,))
-    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
-    _want_i32(context_lens, "context_lens", (B,))
+    Y = prefix_lens.shape[0]
+    pt, MP = _table(prefix_tables, "prefix_tables", Y, dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    pl = _on(prefix_lens, "prefix_lens", _I32, (Y,), dev)
+    gs = _on(group_starts, "group_starts", _I32, (Y + 1,), dev)
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     if out is None:
         out = torch.empty_like(q)
-    _want(out, "out", torch.float16)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    _here(q, k_cache, v_cache, prefix_tables, prefix_lens, group_starts, block_tables, context_lens, out, workspace,
-          error_word)
+    op = _on(out, "out", _F16, q.shape, dev)
     mp, mc = _max_len(prefix_lens, max_prefix_len), _max_len(context_lens, max_context_len)
     if workspace is None:
         workspace = alloc_workspace(paged_decode_prefix_workspace_size(B, QL, Hq, Hkv, D, BS, Y, mp, mc), q.device)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    fn = lib().paged_decode_attention_prefix_fp8 if fp8 else lib().paged_decode_attention_prefix
-    _check(fn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_tables), _ptr(prefix_lens), _ptr(group_starts),
-              _ptr(block_tables), _ptr(context_lens), _ptr(out), B, QL, Y, Hq, Hkv, D, BS, NB,
-              prefix_tables.shape[1], block_tables.shape[1], mp, mc, float(scale), *scales, _ptr(workspace), wsb,
-              _ptr(error_word), _stream(stream)), name)
+    ws, wsb = _space(workspace, dev)
+    fn = _lib.paged_decode_attention_prefix_fp8 if fp8 else _lib.paged_decode_attention_prefix
+    st = fn(qp, kc, vc, pt, pl, gs, bt, cl, op, B, QL, Y, Hq, Hkv, D, BS, NB, MP, MB, mp, mc, scale, *scales, ws, wsb,
+            _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, name)
     return out
 
 
@@ -696,26 +740,19 @@ def paged_kv_block_bounds(k_cache, block_tables, context_lens, bounds, start_len
     """Elementwise minimum and maximum of the keys of every block (from block start_lens[b] /
     block_size on) into ``bounds`` [num_blocks][num_kv_heads][2][head_dim] of the cache's type.
     ``max_new_tokens`` bounds context_lens - start_lens from above (default: the table's row)."""
-    fp8 = isinstance(k_cache, torch.Tensor) and k_cache.element_size() == 1
-    if fp8:
-        _want_fp8_cache(k_cache, "k_cache")
-        _want_fp8_cache(bounds, "bounds")
-    else:
-        _want(k_cache, "k_cache", torch.float16, 4)
-        _want(bounds, "bounds", torch.float16, 4)
+    dev = _device(k_cache, "k_cache")
+    fp8 = k_cache.element_size() == 1
+    kc = _cache(k_cache, "k_cache", fp8, dev)
     NB, Hkv, BS, D = k_cache.shape
-    if tuple(bounds.shape) != (NB, Hkv, 2, D):
-        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
+    bo = _cache(bounds, "bounds", fp8, dev, (NB, Hkv, 2, D))
     B = context_lens.shape[0]
-    _want_i32(context_lens, "context_lens", (B,))
-    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
-    if start_lens is not None:
-        _want_i32(start_lens, "start_lens", (B,))
-    _here(k_cache, block_tables, context_lens, start_lens, bounds, error_word)
-    most = block_tables.shape[1] * BS if max_new_tokens is None else int(max_new_tokens)
-    _check(lib().paged_kv_block_bounds(_ptr(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(start_lens),
-                                       _ptr(bounds), B, Hkv, D, BS, NB, block_tables.shape[1], most, int(fp8),
-                                       _ptr(error_word), _stream(stream)), "paged_kv_block_bounds")
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    most = MB * BS if max_new_tokens is None else int(max_new_tokens)
+    st = _lib.paged_kv_block_bounds(kc, bt, cl, _opt(start_lens, "start_lens", _I32, (B,), dev), bo, B, Hkv, D, BS, NB,
+                                    MB, most, 1 if fp8 else 0, _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_kv_block_bounds")
     return bounds
 
 
@@ -725,31 +762,30 @@ def paged_kv_block_select(q, bounds, block_tables, context_lens, max_selected, b
     """The ``max_selected`` blocks of each (sequence, kv head) worth attending to: the first
     ``sink_blocks``, the last ``recent_blocks`` and those whose bounds allow the largest scores.
     Returns (block_lists int32 [B][Hkv][max_selected], ascending then -1; list_lens [B][Hkv])."""
-    _want(q, "q", torch.float16, 3)
-    fp8 = isinstance(bounds, torch.Tensor) and bounds.element_size() == 1
-    if fp8:
-        _want_fp8_cache(bounds, "bounds")
-    else:
-        _want(bounds, "bounds", torch.float16, 4)
+    dev = _device(q, "q")
+    if q.dim() != 3 or not isinstance(bounds, torch.Tensor):
+        raise ValueError("q must have 3 dimensions and bounds be a tensor")
+    qp = _on(q, "q", _F16, q.shape, dev)
+    fp8 = bounds.element_size() == 1
+    bo = _cache(bounds, "bounds", fp8, dev)
     B, Hq, D = q.shape
     NB, Hkv, two, D2 = bounds.shape
     if D2 != D or two != 2:
         raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
     K = int(max_selected)
-    _want_i32(context_lens, "context_lens", (B,))
-    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
     if block_lists is None:
-        block_lists = torch.empty((B, Hkv, max(K, 0)), dtype=torch.int32, device=q.device)
+        block_lists = torch.empty((B, Hkv, max(K, 0)), dtype=_I32, device=q.device)
     if list_lens is None:
-        list_lens = torch.empty((B, Hkv), dtype=torch.int32, device=q.device)
-    _want_i32(block_lists, "block_lists", (B, Hkv, K))
-    _want_i32(list_lens, "list_lens", (B, Hkv))
-    _here(q, bounds, block_tables, context_lens, block_lists, list_lens, error_word)
-    _check(lib().paged_kv_block_select(_ptr(q), _ptr(bounds), _ptr(block_tables), _ptr(context_lens),
-                                       _ptr(block_lists), _ptr(list_lens), B, Hq, Hkv, D, int(block_size), NB,
-                                       block_tables.shape[1], _max_len(context_lens, max_context_len), K,
-                                       int(sink_blocks), int(recent_blocks), int(fp8), _ptr(error_word),
-                                       _stream(stream)), "paged_kv_block_select")
+        list_lens = torch.empty((B, Hkv), dtype=_I32, device=q.device)
+    st = _lib.paged_kv_block_select(qp, bo, bt, cl, _on(block_lists, "block_lists", _I32, (B, Hkv, K), dev),
+                                    _on(list_lens, "list_lens", _I32, (B, Hkv), dev), B, Hq, Hkv, D, int(block_size),
+                                    NB, MB, _max_len(context_lens, max_context_len), K, int(sink_blocks),
+                                    int(recent_blocks), 1 if fp8 else 0, _word(error_word, dev),
+                                    _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_kv_block_select")
     return block_lists, list_lens
 
 
@@ -760,30 +796,32 @@ def paged_decode_blocks_workspace_size(num_seqs, num_q_heads, num_kv_heads, head
 
 def _attention_blocks(name, fp8, q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, scale,
                       scales, out, workspace, error_word, stream):
-    _want(q, "q", torch.float16, 3)
-    _want_caches(k_cache, v_cache, fp8)
+    dev = _device(q, "q")
+    if q.dim() != 3 or not isinstance(block_lists, torch.Tensor):
+        raise ValueError("q must have 3 dimensions and block_lists be a tensor")
+    qp = _on(q, "q", _F16, q.shape, dev)
+    kc = _cache(k_cache, "k_cache", fp8, dev)
+    vc = _cache(v_cache, "v_cache", fp8, dev, k_cache.shape)
     B, Hq, D = q.shape
     NB, Hkv, BS, D2 = k_cache.shape
     if D2 != D:
         raise ValueError("q / k_cache head_dim mismatch")
-    _want_i32(context_lens, "context_lens", (B,))
-    _want_i32(block_tables, "block_tables", (B, block_tables.shape[1]))
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
     K = block_lists.shape[-1]
-    _want_i32(block_lists, "block_lists", (B, Hkv, K))
-    _want_i32(list_lens, "list_lens", (B, Hkv))
+    bl = _on(block_lists, "block_lists", _I32, (B, Hkv, K), dev)
+    ll = _on(list_lens, "list_lens", _I32, (B, Hkv), dev)
     if out is None:
         out = torch.empty_like(q)
-    _want(out, "out", torch.float16)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    _here(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, out, workspace, error_word)
+    op = _on(out, "out", _F16, q.shape, dev)
     if workspace is None:
         workspace = alloc_workspace(paged_decode_blocks_workspace_size(B, Hq, Hkv, D, BS, K), q.device)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    fn = lib().paged_decode_attention_blocks_fp8 if fp8 else lib().paged_decode_attention_blocks
-    _check(fn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(block_lists),
-              _ptr(list_lens), _ptr(out), B, Hq, Hkv, D, BS, NB, block_tables.shape[1], K, float(scale), *scales,
-              _ptr(workspace), wsb, _ptr(error_word), _stream(stream)), name)
+    ws, wsb = _space(workspace, dev)
+    fn = _lib.paged_decode_attention_blocks_fp8 if fp8 else _lib.paged_decode_attention_blocks
+    st = fn(qp, kc, vc, bt, cl, bl, ll, op, B, Hq, Hkv, D, BS, NB, MB, K, scale, *scales, ws, wsb,
+            _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, name)
     return out
 
 
