@@ -1194,7 +1194,8 @@ struct PartPlan {
   int chunks = 1;
   int P = 32;
   int np = 0;
-  int rows = 0;  // kSharedTc: query rows per chunk
+  int rows = 0;       // kSharedTc: query rows per chunk
+  bool wide = false;  // E4M3 block lists: the four-per-SM build
   long long grid = 0;
 };
 
@@ -1203,6 +1204,7 @@ constexpr int kSharedTc = 100;
 constexpr int kSharedSplit = 9;       // partitions per unit from which it takes chunks of 128 rows
 constexpr int kFewSharedRows = 64;    // rows per group and kv head up to which,
 constexpr int kShortPrefix = 1024;    // with prefixes up to this long, the mma.sync kernel serves them
+constexpr int kMinListedPartition = 64;  // the shortest partition of a block list
 
 // A shared prefix of up to max_prefix_len tokens: chunks of a group's query
 // rows times the kv heads are the units; each reads the prefix in as many
@@ -1267,6 +1269,34 @@ PartPlan plan_own(const Shape& s, int q_len, int kv_fp8) {
   return p;
 }
 
+// Block lists (as contexts of max_listed blocks): the shortest power-of-two
+// partition whose grid still fits one resident wave, else none; a list is read
+// once and is short, so a second, partly filled wave costs more than it levels
+// (fp16, 256 units of 2048 tokens: unsplit 46 us, 512-token partitions 55).
+// E4M3 grids past three CTAs per SM run the four-per-SM build (256 units of
+// 4096 tokens: 2 x 256 CTAs on it 59 us, 256 CTAs of the other 66; 192 units,
+// 2 x 192 CTAs: 49 against 45).
+PartPlan plan_listed(const Shape& s, int kv_fp8) {
+  PartPlan p;
+  if (s.num_seqs <= 0) return p;
+  int sms = sm_count();
+  if (sms <= 0) sms = 148;
+  const long long units = (long long)s.num_seqs * s.num_kv_heads;
+  const int resident = path_stream(PKD_VARIANT_TMA_MMA, s.head_dim, s.num_q_heads / s.num_kv_heads, 2, false).ctas_per_sm;
+  const long long slots = (long long)sms * (kv_fp8 ? resident + 1 : resident);
+  p.P = (int)round_up((size_t)s.max_context_len, 32);
+  p.np = 1;
+  for (long long q = kMinListedPartition; q < s.max_context_len; q *= 2)
+    if (units * ((s.max_context_len + q - 1) / q) <= slots) {
+      p.P = (int)q;
+      p.np = (int)((s.max_context_len + q - 1) / q);
+      break;
+    }
+  p.grid = units * p.np;
+  p.wide = kv_fp8 && p.grid > (long long)sms * resident;
+  return p;
+}
+
 // Fields every decode launch sets.
 pkd::DecodeParams base_params(const Shape& s, const void* q, const void* k_cache, const void* v_cache, int q_len,
                               float scale, int kv_fp8, float k_scale, float v_scale, int* error_word) {
@@ -1302,8 +1332,9 @@ pkd_status launch_part(const Shape& s, const PartPlan& plan, const pkd::DecodePa
     e = kv_fp8 ? pkd::launch_decode_shared_fp8(D, BS, G, p, plan.grid, stream)
                : pkd::launch_decode_shared(D, BS, G, p, plan.grid, stream);
   else if (p.block_lists)
-    e = kv_fp8 ? pkd::launch_decode_listed_fp8(D, BS, G, p, plan.grid, stream)
-               : pkd::launch_decode_listed(D, BS, G, p, plan.grid, stream);
+    e = !kv_fp8     ? pkd::launch_decode_listed(D, BS, G, p, plan.grid, stream)
+        : plan.wide ? pkd::launch_decode_listed_fp8_w4(D, BS, G, p, plan.grid, stream)
+                    : pkd::launch_decode_listed_fp8(D, BS, G, p, plan.grid, stream);
   else if (kv_fp8)
     e = pkd::launch_decode_tma_mma_fp8(D, BS, G, p, plan.grid, stream);
   else
@@ -1427,7 +1458,7 @@ pkd_status blocks_impl(const void* q, const void* k_cache, const void* v_cache, 
   if (!block_lists || !list_lens || !out) return PKD_ERR_NULL;
   if (!aligned(out, 16) || !aligned(error_word, 4) || !aligned(block_lists, 4) || !aligned(list_lens, 4))
     return PKD_ERR_ALIGN;
-  const PartPlan plan = plan_own(s, 1, kv_fp8);
+  const PartPlan plan = plan_listed(s, kv_fp8);
   const bool split = plan.np > 1;
   pkd::DecodeParams p = base_params(s, q, k_cache, v_cache, 1, scale, kv_fp8, k_scale, v_scale, error_word);
   p.block_tables = block_tables;
@@ -1493,7 +1524,7 @@ size_t paged_decode_blocks_workspace_size(int num_seqs, int num_q_heads, int num
   if (check_shape(s) != PKD_OK) return 0;
   size_t most = 0;
   for (const int fp8 : {0, 1}) {
-    const PartPlan p = plan_own(s, 1, fp8);
+    const PartPlan p = plan_listed(s, fp8);
     if (p.np > 1) most = std::max(most, layout(nullptr, num_seqs, num_q_heads, head_dim, p.np).bytes);
   }
   return most;

@@ -201,18 +201,33 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   p.sink = sink_blocks;
   p.recent = recent_blocks;
   p.error_word = error_word;
-  // CTAs of a cluster: enough that a warp has about two tiles of 16 blocks
+  // Rows (sequence, kv head) are what runs side by side.  Many rows: one CTA
+  // each, of 128 threads, so that four rows share an SM and one's selection
+  // runs beside another's pass.  Few: clusters, until they would fill the GPU
+  // twice over or a warp would be without a tile of 16 blocks.
+  int sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 148;
+  const long long rows = (long long)num_seqs * num_kv_heads;
   const int tiles = (max_blocks + 15) / 16;
+  const bool narrow = rows > 2LL * sms;
   p.cluster = 1;
-  while (p.cluster < pkd::kSelMaxCluster && 2 * p.cluster * pkd::kSelWarps * 2 <= tiles) p.cluster *= 2;
-  const long long grid = (long long)num_seqs * num_kv_heads * p.cluster;
+  while (!narrow && p.cluster < pkd::kSelMaxCluster && rows * 2 * p.cluster <= 2LL * sms &&
+         2 * p.cluster * pkd::kSelMaxWarps <= tiles)
+    p.cluster *= 2;
+  const long long grid = rows * p.cluster;
   if (grid > 0x7fffffffLL) return PKD_ERR_SHAPE;
-  auto* fn = kv_fp8 ? (head_dim == 128 ? pkd::paged_kv_block_select_kernel<128, 1>
-                                       : pkd::paged_kv_block_select_kernel<64, 1>)
-                    : (head_dim == 128 ? pkd::paged_kv_block_select_kernel<128, 2>
-                                       : pkd::paged_kv_block_select_kernel<64, 2>);
-  const int smem = std::max(16, max_blocks * 4);
+  const int nt = narrow ? 128 : 256;
+#define PKD_SELECT(D_, KVB_) \
+  (narrow ? pkd::paged_kv_block_select_kernel<D_, KVB_, 128> : pkd::paged_kv_block_select_kernel<D_, KVB_, 256>)
+  auto* fn = kv_fp8 ? (head_dim == 128 ? PKD_SELECT(128, 1) : PKD_SELECT(64, 1))
+                    : (head_dim == 128 ? PKD_SELECT(128, 2) : PKD_SELECT(64, 2));
+#undef PKD_SELECT
+  const int smem = 4 * (max_blocks + (max_blocks + 31) / 32) + 16;  // scores, a bit per block
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return PKD_ERR_LAUNCH;
+  if (p.cluster > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return PKD_ERR_LAUNCH;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -221,7 +236,7 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(pkd::kSelThreads);
+  cfg.blockDim = dim3((unsigned)nt);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;

@@ -311,13 +311,16 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kerne
 // The first `sink` and the last `recent` blocks are always taken, and of the
 // others the best, ties to the lowest index, as if scores were exact.
 //
-// The scores are sums of 2D exact products in fp32, off by at most E; the k-th
-// largest of them, tau, is found by radix selection, and blocks above
-// tau + 2E are chosen, those below tau - 2E are not, whatever the rounding
-// did.  Those between (most often tau's own block alone, and then nothing is
-// left to decide) are scored again in fp64, and the same step runs once more
-// on their distances from tau, kept as fp32 in the places of their scores;
-// after a second such step the distances are exact in fp64's last bit.
+// The scores are sums of 2D exact products in fp32, off by at most E.  If tau
+// is the k-th largest of them, blocks above tau + 2E are chosen and those below
+// tau - 2E are not, whatever the rounding did; those between are scored again
+// in fp64.  One pass of 2048 bins over the scores' range finds the bin of tau;
+// the blocks of that bin and of those within 2E of it, a handful, are ranked
+// directly.  Where they are many (equal blocks, a wide E) the general way
+// takes over: radix selection finds tau, the blocks between are scored in
+// fp64, and the same step runs again on their distances from tau, kept as fp32
+// in the places of their scores, until the distances are exact in fp64's last
+// bit.
 //
 // One cluster per (sequence, kv head): its CTAs share the pass over the
 // bounds, which is bandwidth, and write scores into the shared memory of CTA
@@ -334,14 +337,14 @@ struct BlockSelectParams {
   int* error_word;
 };
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBinBits = 11, kSelBins = 1 << kSelBinBits;
-constexpr int kSelMaxCluster = 8;
-// Relative to sum_d |q_d| max |bound|: 2D/16 accumulating steps, each off by
-// at most 2^-20 of the terms' sum however the tensor core aligns its 16
-// products and the accumulator, with a factor of two to spare.
-constexpr float kSelErr = 1.f / 32768.f;
+constexpr int kSelMaxCluster = 16;
+constexpr int kSelMaxWarps = 8;  // CTAs of 128 or 256 threads
+// The bound of a score's error, relative to sum_d |q_d| max |bound|: one step
+// adds 16 exact products, each cut at worst at 2^-23 of the largest, so 2^-19
+// of its terms' magnitudes; every step starts from zero, and the up to 16
+// results are summed in fp32 (2^-20 of all): 1.5 x 2^-19.
+constexpr float kSelErr = 1.5f / 524288.f;
 
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t u = __float_as_uint(f);
@@ -351,50 +354,89 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// Exclusive sums over the CTA of two counts per thread; *tot are the totals.
-__device__ __forceinline__ int2 block_scan2(int2 v, int2* warp_sums, int2* tot) {
+// The block's score in fp64, from its bounds at `lo` (then hi) and the group's
+// queries; whole warp, the same value in every lane.
+template <int D, int KVB>
+__device__ __forceinline__ double exact_score(const char* lo, const __half* q, int G) {
+  constexpr int DPC = 16 / KVB;
+  const int lane = threadIdx.x & 31, h = lane / 4, c = lane % 4;  // four lanes a head, D / 4 dims each
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  if (h < G) {
+#pragma unroll
+    for (int jj = 0; jj < D / (4 * DPC); ++jj) {
+      const int d0 = DPC * (4 * jj + c);
+      uint32_t wl[DPC / 2], wh[DPC / 2];
+      cache_words<KVB>(*reinterpret_cast<const uint4*>(lo + d0 * KVB), wl);
+      cache_words<KVB>(*reinterpret_cast<const uint4*>(lo + (size_t)(D + d0) * KVB), wh);
+#pragma unroll
+      for (int w = 0; w < DPC / 2; ++w) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + (size_t)h * D + d0 + 2 * w));
+        const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&wl[w]));
+        const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&wh[w]));
+        // the larger of the two products of each dim, exact in fp32
+        s[(2 * w) % 4] += (double)(x.x * (x.x < 0.f ? l.x : u.x));
+        s[(2 * w + 1) % 4] += (double)(x.y * (x.y < 0.f ? l.y : u.y));
+      }
+    }
+  }
+  double t = (s[0] + s[1]) + (s[2] + s[3]);
+  t += __shfl_xor_sync(0xffffffffu, t, 1);
+  t += __shfl_xor_sync(0xffffffffu, t, 2);
+  if (h >= G) t = -3.0e38;
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1) t = fmax(t, __shfl_xor_sync(0xffffffffu, t, m));
+  return t;
+}
+
+// Exclusive sum over the CTA's WARPS warps of one count per thread; *tot is the total.
+template <int WARPS>
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* tot) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int2 s = v;
+  int s = v;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, s.x, k), y = __shfl_up_sync(0xffffffffu, s.y, k);
-    if (lane >= k) {
-      s.x += x;
-      s.y += y;
-    }
+    const int x = __shfl_up_sync(0xffffffffu, s, k);
+    if (lane >= k) s += x;
   }
   __syncthreads();  // the previous use of warp_sums is over
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  int2 base = make_int2(0, 0), all = make_int2(0, 0);
+  int base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const int2 x = warp_sums[w];
-    if (w < warp) {
-      base.x += x.x;
-      base.y += x.y;
-    }
-    all.x += x.x;
-    all.y += x.y;
+  for (int w = 0; w < WARPS; ++w) {
+    const int x = warp_sums[w];
+    base += w < warp ? x : 0;
+    all += x;
   }
   *tot = all;
-  return make_int2(base.x + s.x - v.x, base.y + s.y - v.y);
+  return base + s - v;
 }
 
-template <int D, int KVB>
-__global__ void __launch_bounds__(kSelThreads, 2) paged_kv_block_select_kernel(const BlockSelectParams P) {
+// What a warp of the cluster hands to CTA 0 with its scores.
+struct SelWarpStats {
+  float kmax;        // largest |bound| it read
+  float smin, smax;  // range of its scores that are to choose from
+};
+
+template <int D, int KVB, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(const BlockSelectParams P) {
+  constexpr int NW = NT / 32;
   constexpr int DPC = 16 / KVB;      // dims per 16-byte chunk
   constexpr int JJ = D / (4 * DPC);  // chunks per lane and row
   constexpr int W = DPC / 2;         // fp16 pairs per chunk
   constexpr int ROWB = D * KVB;      // bytes of lo (and of hi)
-  extern __shared__ __align__(16) float s_score[];  // CTA 0: [max_blocks]
-  __shared__ int s_hist[kSelBins];
-  __shared__ __half s_q[8 * D];
-  __shared__ float s_kmax[kSelMaxCluster * kSelWarps];
-  __shared__ int2 s_sums[kSelWarps];
-  __shared__ uint32_t s_red[2 * kSelWarps];
-  __shared__ float s_qsum[8];
-  __shared__ int s_found[2];
+  constexpr int PER = kSelBins / NT;
+  // blocks around the border are ranked directly where they are NT or fewer, one a thread
+  extern __shared__ __align__(16) float s_score[];  // CTA 0: [max_blocks], then a bit per block
+  __shared__ __align__(16) int s_hist[kSelBins];
+  __shared__ SelWarpStats s_stats[kSelMaxCluster * NW];
+  __shared__ int s_sums[NW];
+  __shared__ uint32_t s_red[2 * NW];
+  __shared__ int s_found[2], s_n;
+  __shared__ float s_tau;
+  __shared__ float s_ws[NT];   // blocks around the border: score,
+  __shared__ int s_wi[NT];     // index,
+  __shared__ double s_wd[NT];  // exact score where it counts
 
   const int row = blockIdx.x / P.cluster, rank = blockIdx.x % P.cluster;
   const int b = row / P.num_kv_heads, g = row % P.num_kv_heads;
@@ -413,16 +455,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_kv_block_select_kernel(c
   }
   if (nblk <= K) {  // every block is taken
     if (rank == 0) {
-      for (int i = threadIdx.x; i < K; i += kSelThreads) list[i] = i < nblk ? i : -1;
+      for (int i = threadIdx.x; i < K; i += NT) list[i] = i < nblk ? i : -1;
       if (threadIdx.x == 0) P.list_lens[row] = nblk;
     }
     return;
   }
   if (P.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int i0 = P.sink, i1 = nblk - P.recent;  // the blocks to choose from
+  int need = K - P.sink - P.recent;             // of which so many are taken: < i1 - i0
 
   // ---- scores
   uint32_t qlo[JJ * W], qhi[JJ * W];  // min(q, 0), max(q, 0) of head r (zero past the group)
   const __half* qrow = P.q + ((size_t)b * P.num_q_heads + g * G) * D;
+  float qsum = 0.f;
 #pragma unroll
   for (int jj = 0; jj < JJ; ++jj)
 #pragma unroll
@@ -431,80 +476,101 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_kv_block_select_kernel(c
           r < G ? *reinterpret_cast<const uint32_t*>(qrow + (size_t)r * D + DPC * (4 * jj + c) + 2 * w) : 0u;
       qlo[jj * W + w] = hmin2_u(x, 0u);
       qhi[jj * W + w] = hmax2_u(x, 0u);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+      qsum += fabsf(f.x) + fabsf(f.y);
     }
   const char* base = static_cast<const char*>(P.bounds) + (size_t)g * 2 * ROWB + 16 * c;
   const size_t block_stride = (size_t)P.num_kv_heads * 2 * ROWB;
+  // a warp takes TT tiles of 16 blocks at a time: 8 KiB of bounds in flight (D = 128)
+  constexpr int TT = KVB == 2 ? 1 : 2;
   const int tiles = (nblk + 15) / 16;
-  const int step = P.cluster * kSelWarps;
+  const int step = P.cluster * NW;
   uint32_t kabs = 0;  // running maximum of |bound|, fp16 pair
-  uint32_t score0;    // CTA 0's score array in the cluster's shared window
+  float smin = INFINITY, smax = -INFINITY;
+  uint32_t score0, stats0;  // CTA 0's arrays in the cluster's shared window
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(score0) : "r"(smem_u32(s_score)));
-  uint32_t kmax0;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(kmax0) : "r"(smem_u32(s_kmax)));
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(stats0) : "r"(smem_u32(s_stats)));
   bool joined = P.cluster == 1;
-  auto ids = [&](int tile, int half) -> int {
-    const int i = tile * 16 + 8 * half + r;
-    return i < nblk ? bt[i] : -1;
-  };
-  int id[2] = {-1, -1};
-  int tile = rank * kSelWarps + warp;
-  if (tile < tiles) {
-    id[0] = ids(tile, 0);
-    id[1] = ids(tile, 1);
-  }
-  for (; tile < tiles; tile += step) {
-    uint4 a[2][2][JJ];  // [row half][lo, hi][chunk]
-    bool ok[2];
+  int id[TT][2];
+  auto load_ids = [&](int tile) {
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      ok[f] = id[f] >= 0 && id[f] < P.num_blocks;
-      const char* src = base + (size_t)(ok[f] ? id[f] : 0) * block_stride;
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int i = (tile + t * step) * 16 + 8 * f + r;
+        id[t][f] = i < nblk ? bt[i] : -1;
+      }
+  };
+  int tile = rank * NW + warp;
+  load_ids(tile);
+  if (rank == 0) {  // the bins start empty
+#pragma unroll
+    for (int k = 0; k < PER / 4; ++k) reinterpret_cast<int4*>(s_hist)[threadIdx.x + NT * k] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) s_found[0] = s_found[1] = s_n = 0;
+  }
+  for (; tile < tiles; tile += TT * step) {
+    uint4 a[TT][2][2][JJ];  // [tile][row half][lo, hi][chunk]
+    bool ok[TT][2];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        ok[t][f] = id[t][f] >= 0 && id[t][f] < P.num_blocks;
+        const char* src = base + (size_t)(ok[t][f] ? id[t][f] : 0) * block_stride;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int jj = 0; jj < JJ; ++jj)
+            a[t][f][e][jj] =
+                ok[t][f] ? *reinterpret_cast<const uint4*>(src + e * ROWB + 64 * jj) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    load_ids(tile + TT * step);
+    float sum[TT][4];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      sum[t][0] = sum[t][1] = sum[t][2] = sum[t][3] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int jj = 0; jj < JJ; ++jj)
-          a[f][e][jj] = ok[f] ? *reinterpret_cast<const uint4*>(src + e * ROWB + 64 * jj) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (tile + step < tiles) {
-      id[0] = ids(tile + step, 0);
-      id[1] = ids(tile + step, 1);
-    }
-    float acc[2][4];
+        for (int jj = 0; jj < JJ; ++jj) {
+          uint32_t w0[W], w1[W];
+          cache_words<KVB>(a[t][0][e][jj], w0);
+          cache_words<KVB>(a[t][1][e][jj], w1);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+          for (int w = 0; w < W; ++w) kabs = hmax2_u(kabs, hmax2_u(w0[w] & 0x7fff7fffu, w1[w] & 0x7fff7fffu));
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+          for (int s = 0; s < W / 2; ++s) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t av[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
+            const uint32_t* qv = (e == 0 ? qlo : qhi) + jj * W + 2 * s;
+            mma_16816(acc, av, qv[0], qv[1]);
 #pragma unroll
-      for (int jj = 0; jj < JJ; ++jj) {
-        uint32_t w0[W], w1[W];
-        cache_words<KVB>(a[0][e][jj], w0);
-        cache_words<KVB>(a[1][e][jj], w1);
-#pragma unroll
-        for (int w = 0; w < W; ++w) kabs = hmax2_u(kabs, hmax2_u(w0[w] & 0x7fff7fffu, w1[w] & 0x7fff7fffu));
-#pragma unroll
-        for (int s = 0; s < W / 2; ++s) {
-          const uint32_t av[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
-          const uint32_t* qv = (e == 0 ? qlo : qhi) + jj * W + 2 * s;
-          mma_16816(acc[e], av, qv[0], qv[1]);
+            for (int k = 0; k < 4; ++k) sum[t][k] += acc[k];
+          }
         }
-      }
+    }
     if (!joined) {  // CTA 0 has started: its shared memory may be written
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       joined = true;
     }
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int u = 0; u < 2 * TT; ++u) {
+      const int t = u / 2, f = u % 2;
       // heads 2c and 2c + 1 of block row r + 8f; heads past the group do not count
-      const float s0 = 2 * c < G ? acc[0][2 * f] + acc[1][2 * f] : -INFINITY;
-      const float s1 = 2 * c + 1 < G ? acc[0][2 * f + 1] + acc[1][2 * f + 1] : -INFINITY;
+      const float s0 = 2 * c < G ? sum[t][2 * f] : -INFINITY;
+      const float s1 = 2 * c + 1 < G ? sum[t][2 * f + 1] : -INFINITY;
       float s = fmaxf(s0, s1);
       s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
       s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
-      const int i = tile * 16 + 8 * f + r;
+      const int i = (tile + t * step) * 16 + 8 * f + r;
       if (c == 0 && i < nblk) {
-        if (!ok[f]) {
+        if (!ok[t][f]) {
           record_error(P.error_word, kErrBadBlock);
           s = -3.0e38f;  // a block outside the pool comes last
+        }
+        if (i >= i0 && i < i1) {
+          smin = fminf(smin, s);
+          smax = fmaxf(smax, s);
         }
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(score0 + 4 * i), "f"(s) : "memory");
       }
@@ -512,204 +578,303 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_kv_block_select_kernel(c
   }
   if (!joined) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) kabs = hmax2_u(kabs, __shfl_xor_sync(0xffffffffu, kabs, k));
+  for (int k = 16; k > 0; k >>= 1) {
+    kabs = hmax2_u(kabs, __shfl_xor_sync(0xffffffffu, kabs, k));
+    smin = fminf(smin, __shfl_xor_sync(0xffffffffu, smin, k));
+    smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, k));
+  }
   if (lane == 0) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&kabs));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(kmax0 + 4 * (rank * kSelWarps + warp)), "f"(fmaxf(f.x, f.y))
-                 : "memory");
+    const uint32_t at = stats0 + (uint32_t)(rank * NW + warp) * (uint32_t)sizeof(SelWarpStats);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(fmaxf(f.x, f.y)) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(smin) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(smax) : "memory");
   }
   if (P.cluster > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (rank != 0) return;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
   }
 
   // ---- selection, CTA 0
-  for (int i = threadIdx.x; i < G * D; i += kSelThreads) s_q[i] = qrow[i];
-  __syncthreads();
-  if (warp < G) {
-    float s = 0.f;
-    for (int d = lane; d < D; d += 32) s += fabsf(__half2float(s_q[warp * D + d]));
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if (lane == 0) s_qsum[warp] = s;
+  // every warp has sum_d |q_hd| of head r in its lanes of that row
+  qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
+  qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
+  SelWarpStats st = {0.f, INFINITY, -INFINITY};
+  for (int i = lane; i < step; i += 32) {
+    st.kmax = fmaxf(st.kmax, s_stats[i].kmax);
+    st.smin = fminf(st.smin, s_stats[i].smin);
+    st.smax = fmaxf(st.smax, s_stats[i].smax);
   }
-  __syncthreads();
-  float kmax = 0.f, qsum = 0.f;
-  for (int i = 0; i < P.cluster * kSelWarps; ++i) kmax = fmaxf(kmax, s_kmax[i]);
-  for (int h = 0; h < G; ++h) qsum = fmaxf(qsum, s_qsum[h]);
-  float E = kmax * qsum * kSelErr;
-  const int i0 = P.sink, i1 = nblk - P.recent;  // the blocks to choose from
-  int need = K - P.sink - P.recent;             // of which so many are taken: < i1 - i0
-  float thr = INFINITY;                         // chosen: score >= thr, and the first `ties` of score == tie
-  if (threadIdx.x == 0) s_found[0] = s_found[1] = 0;
-  float tie = INFINITY;
-  int ties = 0;
-  double center = 0.0;
-  for (int round = 0; need > 0; ++round) {
-    // tau: the need-th largest of the finite scores
-    uint32_t kmin = 0xffffffffu, kmx = 0u;
-    for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads) {
-      const float s = s_score[i];
-      if (fabsf(s) < INFINITY) {
-        kmin = min(kmin, order_key(s));
-        kmx = max(kmx, order_key(s));
-      }
-    }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) {
-      kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, k));
-      kmx = max(kmx, __shfl_xor_sync(0xffffffffu, kmx, k));
-    }
+  for (int k = 16; k > 0; k >>= 1) {
+    qsum = fmaxf(qsum, __shfl_xor_sync(0xffffffffu, qsum, k));
+    st.kmax = fmaxf(st.kmax, __shfl_xor_sync(0xffffffffu, st.kmax, k));
+    st.smin = fminf(st.smin, __shfl_xor_sync(0xffffffffu, st.smin, k));
+    st.smax = fmaxf(st.smax, __shfl_xor_sync(0xffffffffu, st.smax, k));
+  }
+  float E = st.kmax * qsum * kSelErr;
+  uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_score + P.max_blocks);  // a bit per chosen block
+  const int words = (nblk + 31) / 32;
+  auto bounds_of = [&](int pb) { return static_cast<const char*>(P.bounds) + (size_t)pb * block_stride + (size_t)g * 2 * ROWB; };
+  auto exact = [&](int i) {
+    const int pb = bt[i];
+    return pb >= 0 && pb < P.num_blocks ? exact_score<D, KVB>(bounds_of(pb), qrow, G) : -3.0e38;
+  };
+  bool settled = false;
+  int ties = 0;  // of the blocks in the second mask (s_hist), the first `ties` are chosen too
+
+  // bin of a score: non-decreasing in it, 0 .. kSelBins - 1
+  const float bin_scale = (float)kSelBins / (st.smax - st.smin);
+  auto bin_of = [&](float s) { return min(kSelBins - 1, (int)((s - st.smin) * bin_scale)); };
+  const float reach = 2.f * E * bin_scale + 2.f;  // bins that 2E reaches, one more for the rounding of a place
+  if (need > 0 && st.smax > st.smin && bin_scale < INFINITY && reach < 64.f) {
+    const int delta = (int)reach;
+    for (int i = i0 + threadIdx.x; i < i1; i += NT) atomicAdd(&s_hist[bin_of(s_score[i])], 1);
     __syncthreads();
-    if (lane == 0) {
-      s_red[warp] = kmin;
-      s_red[kSelWarps + warp] = kmx;
+    // this thread's bins, from the highest down
+    int bins[PER];
+#pragma unroll
+    for (int k = 0; k < PER / 4; ++k) {
+      const int4 x = reinterpret_cast<const int4*>(s_hist)[kSelBins / 4 - 1 - (int)threadIdx.x * (PER / 4) - k];
+      bins[4 * k] = x.w;
+      bins[4 * k + 1] = x.z;
+      bins[4 * k + 2] = x.y;
+      bins[4 * k + 3] = x.x;
     }
-    __syncthreads();
+    int mine = 0;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-      kmin = min(kmin, s_red[w]);
-      kmx = max(kmx, s_red[kSelWarps + w]);
-    }
-    uint32_t lo = kmin, span = kmx - kmin;  // tau's key lies in [lo, lo + span]
-    int left = need;
-    while (span > 0) {
-      const int bits = 32 - __clz(span);
-      const int shift = bits > kSelBinBits ? bits - kSelBinBits : 0;
-      for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) s_hist[i] = 0;
-      __syncthreads();
-      for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads) {
-        const float s = s_score[i];
-        const uint32_t k = order_key(s) - lo;
-        if (fabsf(s) < INFINITY && k <= span) atomicAdd(&s_hist[k >> shift], 1);
-      }
-      __syncthreads();
-      constexpr int PER = kSelBins / kSelThreads;
-      int mine = 0;  // this thread's bins, from the highest down
+    for (int k = 0; k < PER; ++k) mine += bins[k];
+    int tot;
+    int above = block_scan<NW>(mine, s_sums, &tot);
+    if (above < need && need <= above + mine) {  // the need-th largest is in one of this thread's bins
 #pragma unroll
-      for (int k = 0; k < PER; ++k) mine += s_hist[kSelBins - 1 - (threadIdx.x * PER + k)];
-      int2 tot;
-      int above = block_scan2(make_int2(mine, 0), s_sums, &tot).x;
-      if (above < left && left <= above + mine) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
+      for (int k = 0; k < PER; ++k) {
+        if (above < need && need <= above + bins[k]) {
           const int bin = kSelBins - 1 - (threadIdx.x * PER + k);
-          const int n = s_hist[bin];
-          if (above < left && left <= above + n) {
-            s_found[0] = bin;
-            s_found[1] = above;
-          }
-          above += n;
+          const int top = min(kSelBins - 1, bin + delta);
+          int higher = above;  // blocks in bins past top
+          for (int t = bin + 1; t <= top; ++t) higher -= s_hist[t];
+          s_found[0] = bin;
+          s_found[1] = higher;
         }
-      }
-      __syncthreads();
-      lo += (uint32_t)s_found[0] << shift;
-      left -= s_found[1];
-      span = (1u << shift) - 1u;
-    }
-    const float tau = key_value(lo);
-    const float wlo = __fsub_rd(tau, 2.f * E), whi = __fadd_ru(tau, 2.f * E);
-    int2 n = make_int2(0, 0);  // above the window, inside it
-    for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads) {
-      const float s = s_score[i];
-      if (fabsf(s) < INFINITY) {
-        n.x += s > whi;
-        n.y += s >= wlo && s <= whi;
-      }
-    }
-    int2 tot;
-    block_scan2(n, s_sums, &tot);
-    if (tot.x + tot.y == need) {  // the whole window is in
-      thr = wlo;
-      break;
-    }
-    if (E == 0.f) {  // equal scores: the lowest indices
-      tie = tau;
-      ties = need - tot.x;
-      // those above are chosen: mark them
-      for (int i = i0 + threadIdx.x; i < i1; i += kSelThreads)
-        if (s_score[i] > tau) s_score[i] = INFINITY;
-      break;
-    }
-    // score the window again, exactly, as distances from tau
-    const double next = center + (double)tau;
-    for (int ib = i0 + 32 * warp; ib < i1; ib += kSelThreads) {
-      const int i = ib + lane;
-      const float s = i < i1 ? s_score[i] : -INFINITY;
-      const bool in = s >= wlo && s <= whi;
-      if (i < i1 && !in) s_score[i] = s > whi ? INFINITY : -INFINITY;
-      for (unsigned todo = __ballot_sync(0xffffffffu, in); todo; todo &= todo - 1) {
-        const int k = ib + __ffs(todo) - 1;
-        const int pb = bt[k];
-        double best = -3.0e38;
-        if (pb >= 0 && pb < P.num_blocks) {
-          constexpr int V = D / 32;
-          const char* src = static_cast<const char*>(P.bounds) + (size_t)pb * block_stride + (size_t)g * 2 * ROWB;
-          double kl[V], kh[V];
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            if constexpr (KVB == 2) {
-              kl[v] = (double)__half2float(reinterpret_cast<const __half*>(src)[lane * V + v]);
-              kh[v] = (double)__half2float(reinterpret_cast<const __half*>(src + ROWB)[lane * V + v]);
-            } else {
-              uint32_t x, y;
-              e4m3x4_to_f16x2x2((uint32_t) reinterpret_cast<const uint8_t*>(src)[lane * V + v], x, y);
-              kl[v] = (double)__half2float(__ushort_as_half((unsigned short)(x & 0xffffu)));
-              e4m3x4_to_f16x2x2((uint32_t) reinterpret_cast<const uint8_t*>(src + ROWB)[lane * V + v], x, y);
-              kh[v] = (double)__half2float(__ushort_as_half((unsigned short)(x & 0xffffu)));
-            }
-          }
-          for (int h = 0; h < G; ++h) {
-            double s2 = 0.0;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-              const double x = (double)__half2float(s_q[h * D + lane * V + v]);
-              s2 += fmax(x * kl[v], x * kh[v]);
-            }
-#pragma unroll
-            for (int m = 16; m > 0; m >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, m);
-            best = fmax(best, s2);
-          }
-        }
-        if (lane == 0) s_score[k] = (float)(best - next);
+        above += bins[k];
       }
     }
     __syncthreads();
-    center = next;
-    need -= tot.x;
-    // a distance is at most a few E; its rounding to fp32 is off by 2^-24 of it.  The
-    // next round's distances from a point this near are exact.
-    E = round == 0 ? E * (1.f / (1 << 21)) : 0.f;
+    const int top = s_found[0] + delta, bottom = s_found[0] - delta;
+    // mark the blocks that are in whatever the border's order; gather those around it
+    for (int w = warp; w < words; w += NW) {
+      const int i = 32 * w + lane;
+      bool in = i < nblk && (i < i0 || i >= i1);
+      if (i >= i0 && i < i1) {
+        const float s = s_score[i];
+        const int bin = bin_of(s);
+        in = bin > top;
+        if (!in && bin >= bottom) {
+          const int at = atomicAdd(&s_n, 1);
+          if (at < NT) {
+            s_ws[at] = s;
+            s_wi[at] = i;
+          }
+        }
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) s_mask[w] = m;
+    }
+    __syncthreads();
+    const int n = s_n, left = need - s_found[1];  // 0 < left <= n
+    if (n <= NT) {
+      settled = true;
+      // one block a thread: its rank by (score, then index), which fixes tau
+      const bool in = (int)threadIdx.x < n;
+      const float s = in ? s_ws[threadIdx.x] : 0.f;
+      const int idx = in ? s_wi[threadIdx.x] : 0;
+      int rank_s = 0;
+      if (32 * warp < n)
+        for (int k = 0; k < n; ++k) rank_s += s_ws[k] > s || (s_ws[k] == s && s_wi[k] < idx);
+      if (in && rank_s == left - 1) s_tau = s;
+      __syncthreads();
+      const float wlo = __fsub_rd(s_tau, 2.f * E), whi = __fadd_ru(s_tau, 2.f * E);
+      const bool sure = in && s > whi;
+      const bool open = in && s <= whi && s >= wlo;
+      const int n_sure = __syncthreads_count(sure), n_open = __syncthreads_count(open);
+      bool take = sure;
+      if (n_sure + n_open == left) {
+        take = sure || open;
+      } else if (E == 0.f) {
+        take = in && rank_s < left;
+      } else {
+        // the open ones, a warp each in turn
+        int at = 0;
+        for (int k0 = 0; k0 < n; k0 += 32) {
+          const float sk = k0 + lane < n ? s_ws[k0 + lane] : -INFINITY;
+          for (unsigned todo = __ballot_sync(0xffffffffu, sk <= whi && sk >= wlo); todo; todo &= todo - 1, ++at) {
+            if (at % NW != warp) continue;
+            const int k = k0 + __ffs(todo) - 1;
+            const double x = exact(s_wi[k]);
+            if (lane == 0) s_wd[k] = x;
+          }
+        }
+        __syncthreads();
+        if (open) {
+          const double x = s_wd[threadIdx.x];
+          int ahead = 0;
+          for (int k = 0; k < n; ++k)
+            if (s_ws[k] <= whi && s_ws[k] >= wlo) ahead += s_wd[k] > x || (s_wd[k] == x && s_wi[k] < idx);
+          take = ahead < left - n_sure;
+        }
+      }
+      if (take) atomicOr(&s_mask[idx >> 5], 1u << (idx & 31));
+    }
+  }
+
+  if (!settled) {
+    // the general way: chosen are scores >= thr and the first `ties` of those equal to tie
+    float thr = INFINITY, tie = INFINITY;
+    double center = 0.0;
+    for (int round = 0; need > 0; ++round) {
+      // tau: the need-th largest of the finite scores, by radix selection on their order
+      uint32_t kmin = 0xffffffffu, kmx = 0u;
+      for (int i = i0 + threadIdx.x; i < i1; i += NT) {
+        const float s = s_score[i];
+        if (fabsf(s) < INFINITY) {
+          kmin = min(kmin, order_key(s));
+          kmx = max(kmx, order_key(s));
+        }
+      }
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) {
+        kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, k));
+        kmx = max(kmx, __shfl_xor_sync(0xffffffffu, kmx, k));
+      }
+      __syncthreads();
+      if (lane == 0) {
+        s_red[warp] = kmin;
+        s_red[NW + warp] = kmx;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        kmin = min(kmin, s_red[w]);
+        kmx = max(kmx, s_red[NW + w]);
+      }
+      uint32_t lo = kmin, span = kmx >= kmin ? kmx - kmin : 0u;  // tau's key lies in [lo, lo + span]
+      int left = need;
+      while (span > 0) {
+        const int bits = 32 - __clz(span);
+        const int shift = bits > kSelBinBits ? bits - kSelBinBits : 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < kSelBins; i += NT) s_hist[i] = 0;
+        __syncthreads();
+        for (int i = i0 + threadIdx.x; i < i1; i += NT) {
+          const float s = s_score[i];
+          const uint32_t k = order_key(s) - lo;
+          if (fabsf(s) < INFINITY && k <= span) atomicAdd(&s_hist[k >> shift], 1);
+        }
+        __syncthreads();
+        int mine = 0, tot;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) mine += s_hist[kSelBins - 1 - (threadIdx.x * PER + k)];
+        int above = block_scan<NW>(mine, s_sums, &tot);
+        if (above < left && left <= above + mine) {
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int bin = kSelBins - 1 - (threadIdx.x * PER + k);
+            const int x = s_hist[bin];
+            if (above < left && left <= above + x) {
+              s_found[0] = bin;
+              s_found[1] = above;
+            }
+            above += x;
+          }
+        }
+        __syncthreads();
+        lo += (uint32_t)s_found[0] << shift;
+        left -= s_found[1];
+        span = (1u << shift) - 1u;
+      }
+      const float tau = key_value(lo);
+      const float wlo = __fsub_rd(tau, 2.f * E), whi = __fadd_ru(tau, 2.f * E);
+      int n_above = 0, n_in = 0, above, inside;  // the window's, of this thread and of all
+      for (int i = i0 + threadIdx.x; i < i1; i += NT) {
+        const float s = s_score[i];
+        if (fabsf(s) < INFINITY) {
+          n_above += s > whi;
+          n_in += s >= wlo && s <= whi;
+        }
+      }
+      block_scan<NW>(n_above, s_sums, &above);
+      block_scan<NW>(n_in, s_sums, &inside);
+      if (above + inside == need) {  // the whole window is in
+        thr = wlo;
+        break;
+      }
+      if (E == 0.f) {  // equal scores: the lowest indices
+        tie = tau;
+        ties = need - above;
+        // those above are chosen: mark them
+        for (int i = i0 + threadIdx.x; i < i1; i += NT)
+          if (s_score[i] > tau) s_score[i] = INFINITY;
+        break;
+      }
+      // score the window again, exactly, as distances from tau
+      const double next = center + (double)tau;
+      for (int ib = i0 + 32 * warp; ib < i1; ib += NT) {
+        const int i = ib + lane;
+        const float s = i < i1 ? s_score[i] : -INFINITY;
+        const bool in = s >= wlo && s <= whi;
+        if (i < i1 && !in) s_score[i] = s > whi ? INFINITY : -INFINITY;
+        for (unsigned todo = __ballot_sync(0xffffffffu, in); todo; todo &= todo - 1) {
+          const int k = ib + __ffs(todo) - 1;
+          const double x = exact(k);
+          if (lane == 0) s_score[k] = (float)(x - next);
+        }
+      }
+      __syncthreads();
+      center = next;
+      need -= above;
+      // a distance is at most a few E; its rounding to fp32 is off by 2^-24 of it.  The
+      // next round's distances from a point this near are exact.
+      E = round == 0 ? E * (1.f / (1 << 21)) : 0.f;
+    }
+    __syncthreads();
+    for (int w = warp; w < words; w += NW) {
+      const int i = 32 * w + lane;
+      const float s = i < nblk ? s_score[i] : -INFINITY;
+      const bool in = i < nblk && (i < i0 || i >= i1 || s >= thr || s == INFINITY);
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      const unsigned e = __ballot_sync(0xffffffffu, i < nblk && !in && ties > 0 && s == tie);
+      if (lane == 0) {
+        s_mask[w] = m;
+        s_hist[w] = (int)e;
+      }
+    }
   }
   __syncthreads();
 
-  // ---- the chosen blocks in ascending order
-  const int per = (nblk + kSelThreads - 1) / kSelThreads;
-  const int from = min(nblk, (int)threadIdx.x * per), to = min(nblk, from + per);
-  auto chosen = [&](int i) { return i < i0 || i >= i1 || s_score[i] >= thr || s_score[i] == INFINITY; };
-  int2 n = make_int2(0, 0);
-  for (int i = from; i < to; ++i) {
-    const bool in = chosen(i);
-    n.x += in;
-    n.y += !in && ties > 0 && s_score[i] == tie;
+  // ---- the chosen blocks in ascending order: a run of mask words a thread
+  const int per = (words + NT - 1) / NT;
+  const int from = min(words, (int)threadIdx.x * per), to = min(words, from + per);
+  int all_eq;
+  if (ties > 0) {  // the first `ties` of the equal ones join
+    int n_eq = 0;
+    for (int w = from; w < to; ++w) n_eq += __popc((uint32_t)s_hist[w]);
+    int before = block_scan<NW>(n_eq, s_sums, &all_eq);
+    for (int w = from; w < to; ++w)
+      for (uint32_t e = (uint32_t)s_hist[w]; e && before < ties; e &= e - 1, ++before) s_mask[w] |= e & (0u - e);
   }
-  int2 tot;
-  int2 at = block_scan2(n, s_sums, &tot);
-  for (int i = from; i < to; ++i) {
-    const bool in = chosen(i);
-    const bool eq = !in && ties > 0 && s_score[i] == tie;
-    if (in || (eq && at.y < ties)) {
-      const int place = at.x + min(at.y, ties);
-      if (place < K) list[place] = i;
-    }
-    at.x += in;
-    at.y += eq;
-  }
+  int n_in = 0, count;
+  for (int w = from; w < to; ++w) n_in += __popc(s_mask[w]);
+  int place = block_scan<NW>(n_in, s_sums, &count);
+  for (int w = from; w < to; ++w)
+    for (uint32_t m = s_mask[w]; m; m &= m - 1, ++place)
+      if (place < K) list[place] = 32 * w + __ffs(m) - 1;
   // (fewer than K only where a bound was not a number: such a block is never chosen)
-  const int count = min(K, tot.x + min(tot.y, ties));
-  for (int i = count + threadIdx.x; i < K; i += kSelThreads) list[i] = -1;
-  if (threadIdx.x == 0) P.list_lens[row] = count;
+  for (int i = count + threadIdx.x; i < K; i += NT) list[i] = -1;
+  if (threadIdx.x == 0) P.list_lens[row] = min(count, K);
 }
 
 }  // namespace pkd
