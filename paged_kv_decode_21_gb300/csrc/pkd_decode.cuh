@@ -82,6 +82,8 @@ struct DecodeParams {
   const int32_t* group_starts;  // [num_groups + 1]
   int num_groups;
   int rows_per_chunk;  // paged_shared_tc_kernel: query rows per chunk
+  int after_grid;      // kShared kernels: launched as a programmatic dependent of the grid before, whose
+                       // completion each CTA awaits at its end
 };
 
 // Which keys the query rows of a tensor-core decode CTA read.

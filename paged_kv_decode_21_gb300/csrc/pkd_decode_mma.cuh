@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
   // a dependent grid (the split-K merge) may launch once every CTA of this
   // grid has started; it waits for this grid's completion itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  auto leave = [&]() {  // kShared: see after_grid
+    if (SRC == kShared && P.after_grid) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   int j, b, g;
   if (P.piece_order) {
     // longest first: the grid walks pieces p (all kv heads of a piece side by
@@ -245,7 +248,10 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
   if constexpr (SRC == kShared) {
     // (b, above, is 0: the grid's rows are chunks of all groups)
     GroupChunk ch;
-    if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len, QC, qc, &ch)) return;
+    if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len, QC, qc, &ch)) {
+      leave();
+      return;
+    }
     b = ch.group;
     jq0 = ch.first;
     QL = ch.tokens;
@@ -279,9 +285,13 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
       for (int i = threadIdx.x; i < G * nq * D; i += blockDim.x)
         P.out[out_row(i / D) * D + i % D] = __float2half_rn(0.f);
     }
+    leave();
     return;
   }
-  if (j >= np_b) return;
+  if (j >= np_b) {
+    leave();
+    return;
+  }
 
   const int t0 = j * PS;
   // the chunk's last query sees tokens < L - QL + jq0 + nq; nothing past that is read
@@ -661,6 +671,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
       }
     }
   }
+  leave();
 }
 
 }  // namespace pkd

@@ -63,12 +63,13 @@ cudaError_t launch_qc(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
   auto* fn = paged_decode_mma_kernel<D, BS, G, QC, KVB, CPS, SRC>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  if (!p.piece_order) {
+  if (!p.piece_order && !p.after_grid) {
     fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(mk, mv, p);
     return cudaGetLastError();
   }
   // a programmatic dependent of the order kernel: the CTAs become resident
-  // while it runs and wait for its order with griddepcontrol.wait
+  // while it runs and wait for its order with griddepcontrol.wait (or of the
+  // grid before a shared context's, awaited at the CTAs' end)
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -152,7 +152,19 @@ pkd_status paged_kv_block_bounds(const void* k_cache, const int32_t* block_table
   // on; from token 0 when no starts are given
   p.grid_blocks = start_lens ? (int)(((long long)max_new_tokens + block_size - 2) / block_size + 1)
                              : (int)(((long long)max_new_tokens + block_size - 1) / block_size);
-  const long long units = (long long)num_seqs * p.grid_blocks * num_kv_heads;
+  // A warp's kv heads: up to eight, whose tiles stream one behind the other,
+  // while 32 warps an SM remain (32 prompts of up to 8192 tokens, 8 heads: 78
+  // us, against 128 with one head a warp); one where the call is small.
+  int sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 148;
+  const long long blocks = (long long)num_seqs * p.grid_blocks;
+  p.heads_per_warp = 1;
+  while (p.heads_per_warp < 8 && p.heads_per_warp < num_kv_heads &&
+         blocks * num_kv_heads >= 2LL * p.heads_per_warp * 32 * sms)
+    p.heads_per_warp *= 2;
+  const long long units = blocks * ((num_kv_heads + p.heads_per_warp - 1) / p.heads_per_warp);
   const long long grid = (units + pkd::kBoundsWarps - 1) / pkd::kBoundsWarps;
   if (grid > 0x7fffffffLL) return PKD_ERR_SHAPE;
   auto* fn = kv_fp8 ? (head_dim == 128 ? pkd::paged_kv_block_bounds_kernel<128, 1>

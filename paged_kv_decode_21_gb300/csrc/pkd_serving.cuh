@@ -58,7 +58,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
 }
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 template <bool F8, bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(const RopeAppendParams P) {
   const int D = P.head_dim, R = P.rotary_dim, units = D / 16;
@@ -192,6 +192,7 @@ struct BlockBoundsParams {
   const int32_t* start_lens;  // nullable: blocks before start_lens[b] / block_size are left as they are
   void* bounds;               // [num_blocks][num_kv_heads][2][D]: lo, then hi
   int num_seqs, num_kv_heads, block_size, num_blocks, max_blocks_per_seq, grid_blocks;
+  int heads_per_warp;
   int* error_word;
 };
 
@@ -234,15 +235,18 @@ __device__ __forceinline__ uint4 words_to_cache(const uint32_t (&w)[KVB == 2 ? 4
 }
 
 constexpr int kBoundsWarps = 8;
+constexpr int kBoundsLoads = 8;  // loads in flight a lane
 template <int D, int KVB>
 __global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kernel(const BlockBoundsParams P) {
   constexpr int CPR = D * KVB / 16;  // 16-byte chunks per row
   constexpr int RP = 32 / CPR;       // rows per warp-wide load
   constexpr int W = KVB == 2 ? 4 : 8;
+  constexpr int U = kBoundsLoads;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
-  const int g = (int)(unit % P.num_kv_heads);
-  const long long bi = unit / P.num_kv_heads;
+  const int runs = (P.num_kv_heads + P.heads_per_warp - 1) / P.heads_per_warp;
+  const int g0 = (int)(unit % runs) * P.heads_per_warp;
+  const long long bi = unit / runs;
   const int b = (int)(bi / P.grid_blocks);
   if (b >= P.num_seqs) return;
   const int L = P.context_lens[b];
@@ -257,24 +261,40 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kerne
   }
   const int valid = min(P.block_size, (int)(L - i * P.block_size));
   const int c = lane % CPR, r0 = lane / CPR;
-  const size_t tile = (size_t)p * P.num_kv_heads + g;
-  const uint4* src = static_cast<const uint4*>(P.k_cache) + tile * P.block_size * CPR + c;
+  const size_t tile0 = (size_t)p * P.num_kv_heads + g0;
+  const uint4* src = static_cast<const uint4*>(P.k_cache) + tile0 * P.block_size * CPR + c;
+  uint4* dst = static_cast<uint4*>(P.bounds) + tile0 * 2 * CPR;
+  // The warp's tiles (kv heads of one block) lie behind one another; steps of
+  // U loads a lane run over them, the next step's loads requested before this
+  // step's values are used.
+  const int steps = (P.block_size + U * RP - 1) / (U * RP);  // per tile
+  const int heads = min(P.heads_per_warp, P.num_kv_heads - g0);
+  uint4 next[U];
+  auto request = [&](int s) {  // step s: rows (s % steps) * U * RP + k * RP + r0 of tile s / steps
+    const uint4* t = src + (size_t)(s / steps) * P.block_size * CPR;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int r = (s % steps) * U * RP + k * RP + r0;
+      if (r < valid) next[k] = t[(size_t)r * CPR];
+    }
+  };
+  request(0);
   uint32_t lo[W], hi[W];
+  for (int s = 0; s < heads * steps; ++s) {
+    uint4 u[U];
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    lo[w] = 0x7C007C00u;  // +inf
-    hi[w] = 0xFC00FC00u;  // -inf
-  }
-  for (int q0 = 0; q0 < P.block_size; q0 += 8 * RP) {  // 8 loads in flight a lane
-    uint4 u[8];
+    for (int k = 0; k < U; ++k) u[k] = next[k];
+    if (s + 1 < heads * steps) request(s + 1);
+    if (s % steps == 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = q0 + k * RP + r0;
-      if (r < valid) u[k] = src[(size_t)r * CPR];
+      for (int w = 0; w < W; ++w) {
+        lo[w] = 0x7C007C00u;  // +inf
+        hi[w] = 0xFC00FC00u;  // -inf
+      }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = q0 + k * RP + r0;
+    for (int k = 0; k < U; ++k) {
+      const int r = (s % steps) * U * RP + k * RP + r0;
       if (r < valid) {
         uint32_t x[W];
         cache_words<KVB>(u[k], x);
@@ -285,17 +305,18 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kerne
         }
       }
     }
-  }
+    if (s % steps == steps - 1) {
 #pragma unroll
-  for (int m = CPR; m < 32; m <<= 1)
+      for (int m = CPR; m < 32; m <<= 1)
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      lo[w] = hmin2_u(lo[w], __shfl_xor_sync(0xffffffffu, lo[w], m));
-      hi[w] = hmax2_u(hi[w], __shfl_xor_sync(0xffffffffu, hi[w], m));
+        for (int w = 0; w < W; ++w) {
+          lo[w] = hmin2_u(lo[w], __shfl_xor_sync(0xffffffffu, lo[w], m));
+          hi[w] = hmax2_u(hi[w], __shfl_xor_sync(0xffffffffu, hi[w], m));
+        }
+      if (r0 == 0) dst[(size_t)(s / steps) * 2 * CPR + c] = words_to_cache<KVB>(lo);
+      if (r0 == 1) dst[(size_t)(s / steps) * 2 * CPR + CPR + c] = words_to_cache<KVB>(hi);
     }
-  uint4* dst = static_cast<uint4*>(P.bounds) + tile * 2 * CPR;
-  if (r0 == 0) dst[c] = words_to_cache<KVB>(lo);
-  if (r0 == 1) dst[CPR + c] = words_to_cache<KVB>(hi);
+  }
 }
 
 // ---------------------------------------------------------------------------
