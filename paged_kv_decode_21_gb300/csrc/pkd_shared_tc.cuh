@@ -64,8 +64,8 @@ struct SharedTcTraits {
   static constexpr int K_OFF = Q_OFF + 2 * NH * QH;
   static constexpr int V_OFF = K_OFF + NS * TILE;
   static constexpr int MAIN = V_OFF + NS * TILE;
-  // kfull, kempty, vfull, vempty [NS]; sfull, pfull, pfree [2][2]; drain [2]; E4M3: kland, vland [NS]
-  static constexpr int NBAR = 4 * NS + 12 + 2 + (F8 ? 2 * NS : 0);
+  // full, kempty, vempty [NS]; sfull, pfull, pfree [2][2]; drain [2]; E4M3: kland, vland [NS]
+  static constexpr int NBAR = 3 * NS + 12 + 2 + (F8 ? 2 * NS : 0);
   static constexpr int W_MMA = 8, W_K = 10, W_V = 11;
   static constexpr int THREADS = 384;  // three warps per scheduler: 168 registers a thread
   static constexpr int TAIL = NBAR * 8 + 8 + NS * 4;
@@ -99,10 +99,9 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     leave();
     return;
   }
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + T::MAIN);  // [NS] a K tile is in shared memory
-  uint64_t* kempty = kfull + NS;   // [NS] S of the tile computed, for every row tile
-  uint64_t* vfull = kempty + NS;   // [NS] a V tile is in shared memory (with its bad-block mask)
-  uint64_t* vempty = vfull + NS;   // [NS] P V of the tile completed, for every row tile
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::MAIN);  // [NS] a tile's K and V are in shared memory
+  uint64_t* kempty = full + NS;    // [NS] S of the tile computed, for every row tile
+  uint64_t* vempty = kempty + NS;  // [NS] P V of the tile completed, for every row tile
   uint64_t* sfull = vempty + NS;   // [2][2] S of a tile is in buffer h of row tile x
   uint64_t* pfull = sfull + 4;     // [2][2] P of a tile is over its S columns
   uint64_t* pfree = pfull + 4;     // [2][2] P V of a tile completed (the buffer free, O stable)
@@ -153,8 +152,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&kfull[s], F8 ? 32 : 1);
-      mbar_init(&vfull[s], F8 ? 32 : 1);
+      mbar_init(&full[s], F8 ? 64 : 2);  // the K warp and the V warp
       mbar_init(&kempty[s], nx);
       mbar_init(&vempty[s], nx);
       if (F8) {
@@ -190,8 +188,13 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     }
     fence_proxy_async_smem();
   }
+  // Whether any block id of the partition is bad: where none is, as always but
+  // for a caller's mistake, the softmax need not read the tiles' masks (a
+  // shared-memory read costs it over a hundred cycles a tile).
+  int wrong_id = 0;
+  for (int k = threadIdx.x; k < nblk; k += T::THREADS) wrong_id |= bt[k] < 0 || bt[k] >= P.num_blocks;
   tc_fence_before();
-  __syncthreads();
+  const bool any_bad = __syncthreads_or(wrong_id);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -202,7 +205,6 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     const bool is_k = warp == T::W_K;
     const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
     uint64_t* empty = is_k ? kempty : vempty;
-    uint64_t* full = is_k ? kfull : vfull;
     uint64_t* land = F8 ? (is_k ? kland : vland) : full;
     const uint32_t ring = is_k ? T::K_OFF : T::V_OFF;
     const L2Hints l2h = make_l2_hints(false);
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
         uint32_t bad = 0;
 #pragma unroll
         for (int kk = 0; kk < T::NBT; ++kk) bad |= ((wrong >> (kk * BS / 16)) & 1u) << kk;
-        // the mask is read by threads that waited for the V stage's full barrier
+        // the mask is read by threads that waited for the stage's full barrier
         if (!is_k) vbad[st] = bad;
         if (is_k && bad) record_error(P.error_word, kErrBadBlock);
         mbar_arrive_expect_tx(&land[st], (uint32_t)boxes * 16 * 128);
@@ -294,14 +296,15 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     const uint32_t qs = sbase + T::Q_OFF + x * T::NH * T::QH;
     const uint32_t scol = tmem + T::S_COL + 128 * x, ocol = tmem + T::O_COL + 128 * x;
     bool ok = true;
-    auto await = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(bar, parity, P.timeout_ns, abort_flag));
+    // Two barriers are waited for at once, each by half of the lanes: a test
+    // costs its two hundred cycles either way.
+    auto await = [&](uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2) {
+      const bool second = lane & 1;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(second ? bar2 : bar, second ? parity2 : parity,
+                                                            P.timeout_ns, abort_flag));
+      tc_fence_after();
     };
     auto issue_qk = [&](int s) {
-      await(&kfull[s % NS], (s / NS) & 1);
-      // the S buffer is free once P V of the tile two before, which read P from it, completed
-      if (s >= 2) await(&pfree[2 * x + (s & 1)], ((s >> 1) - 1) & 1);
-      tc_fence_after();
       if (ok && elect_one()) {
         const uint32_t ks = sbase + T::K_OFF + (s % NS) * T::TILE;
 #pragma unroll
@@ -313,11 +316,16 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       }
       __syncwarp();
     };
+    await(&full[0], 0, &full[0], 0);
     issue_qk(0);
-    if (ntiles > 1 && ok) issue_qk(1);
+    if (ntiles > 1) {
+      await(&full[1], 0, &full[1], 0);
+      issue_qk(1);
+    }
     for (int s = 0; s < ntiles && ok; ++s) {
-      await(&pfull[2 * x + (s & 1)], (s >> 1) & 1);
-      tc_fence_after();
+      // P of this tile, and K of the tile after next
+      const int n = min(s + 2, ntiles - 1);
+      await(&pfull[2 * x + (s & 1)], (s >> 1) & 1, &full[n % NS], (n / NS) & 1);
       if (ok && elect_one()) {
         const uint32_t vs = sbase + T::V_OFF + (s % NS) * T::TILE;
         const uint32_t pa = scol + 64 * (s & 1);  // P: 8 columns per 16 tokens
@@ -329,7 +337,11 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
         tc_commit(&vempty[s % NS]);
       }
       __syncwarp();
-      if (ok && s + 2 < ntiles) issue_qk(s + 2);
+      if (s + 2 < ntiles && ok) {
+        // the S buffer is free once P V, which reads P from it, completed
+        await(&pfree[2 * x + (s & 1)], (s >> 1) & 1, &pfree[2 * x + (s & 1)], (s >> 1) & 1);
+        issue_qk(s + 2);
+      }
     }
     if (!ok) {
       if (lane == 0 && !*abort_flag) record_error(P.error_word, kErrTimeout);
@@ -359,12 +371,14 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       float sc[2][32];
       tmem_ld32(tsx + 64 * h, sc[0]);
       tmem_ld32(tsx + 64 * h + 32, sc[1]);
-      // the tile's V and its bad-block mask
-      ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&vfull[sv], (s / NS) & 1, P.timeout_ns, abort_flag));
-      const uint32_t bad = vbad[sv];
+      const int nv = t1 - (t0 + s * TN);  // tokens of the tile inside the partition
+      uint32_t bad = 0;
+      if (any_bad || nv < TN) {  // the tile's V and its bad-block mask are needed below
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&full[sv], (s / NS) & 1, P.timeout_ns, abort_flag));
+        bad = vbad[sv];
+      }
       tmem_ld_wait();
       if (!ok) break;
-      const int nv = t1 - (t0 + s * TN);  // tokens of the tile inside the partition
       const bool raw = nv >= TN && bad == 0 && P.scale_log2 >= 0.f;
       if (!raw) {
 #pragma unroll

@@ -535,27 +535,21 @@ def paged_kv_append(k_new, v_new, block_tables, context_lens, k_cache, v_cache, 
 _F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
 
 
-def _on(t, name: str, dtype, shape, dev: int):
-    """A contiguous tensor of this type and shape on device ``dev``: its address."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (
-            not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _opt(t, name: str, dtype, shape, dev: int):
-    return None if t is None else _on(t, name, dtype, shape, dev)
+def _on(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device ``dev``."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{dev}, not "
+                     f"{t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _device(t, name: str) -> int:
     """The current device, which ``t`` has to be on (and the library loaded)."""
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if _lib is None:
         lib()
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
     return dev
 
 
@@ -569,9 +563,9 @@ def _word(error_word, dev: int):
     """The error word's address: the first element of an int32 tensor."""
     if error_word is None:
         return None
-    if error_word.dtype is not _I32 or error_word.get_device() != dev or error_word.numel() < 1:
-        raise ValueError(f"error_word must be an int32 tensor on cuda:{dev}")
-    return error_word.data_ptr()
+    if error_word.dtype is _I32 and error_word.get_device() == dev and error_word.numel() > 0:
+        return error_word.data_ptr()
+    raise ValueError(f"error_word must be an int32 tensor on cuda:{dev}")
 
 
 def _space(workspace, dev: int):
@@ -583,69 +577,69 @@ def _space(workspace, dev: int):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _heads(t, name: str, dev: int, shape=None):
+def _heads(t, name: str, dev: int, shape):
     """(address, token stride) of a [tokens][heads][head_dim] fp16 tensor whose heads are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _F16 or t.dim() != 3 or t.get_device() != dev:
-        raise ValueError(f"{name} must be a 3-D float16 tensor on cuda:{dev}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    T, H, D = t.shape
-    if T == 0 or H == 0:
-        return t.data_ptr(), H * D
+    if t.dtype is not _F16 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {_F16} tensor of shape {list(shape)} on cuda:{dev}, not {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    T, H, D = shape
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (st if T > 1 else H * D)
+        if T and H:
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (st if T > 1 and H else H * D)
 
 
-def _cache(t, name: str, fp8: bool, dev: int, shape=None):
+def _cache(t, name: str, fp8: bool, dev: int, shape) -> int:
     """Address of a [num_blocks][num_kv_heads][rows][head_dim] fp16 or E4M3 byte tensor."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.get_device() != dev or not t.is_contiguous() or (
-            t.element_size() != 1 if fp8 else t.dtype is not _F16):
-        raise ValueError(f"{name} must be a contiguous 4-D {'byte (uint8 or float8_e4m3fn)' if fp8 else 'float16'} "
-                         f"tensor on cuda:{dev}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    if (t.element_size() == 1 if fp8 else t.dtype is _F16) and t.shape == shape and len(shape) == 4 and (
+            t.is_contiguous()) and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {'byte (uint8 or float8_e4m3fn)' if fp8 else 'float16'} tensor of "
+                     f"shape {list(shape)} (4 dimensions) on cuda:{dev}, not {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _table(t, name: str, rows: int, dev: int):
     """(address, row length) of an int32 block table."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions")
-    width = t.shape[1]
-    return _on(t, name, _I32, (rows, width), dev), width
+    shape = t.shape
+    if len(shape) == 2 and shape[0] == rows and t.dtype is _I32 and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr(), shape[1]
+    raise ValueError(f"{name} must be a contiguous {_I32} tensor of {rows} rows on cuda:{dev}, not {t.dtype} "
+                     f"{list(t.shape)} on {t.device}")
 
 
 def _append_rope(name, fp8, q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache, scales,
                  token_starts, positions, interleaved, q_out, error_word, stream):
     dev = _device(k_new, "k_new")
-    kc = _cache(k_cache, "k_cache", fp8, dev)
-    vc = _cache(v_cache, "v_cache", fp8, dev, k_cache.shape)
-    NB, Hkv, BS, D = k_cache.shape
+    shape = k_cache.shape
+    kc = _cache(k_cache, "k_cache", fp8, dev, shape)
+    vc = _cache(v_cache, "v_cache", fp8, dev, shape)
+    NB, Hkv, BS, D = shape
     T = k_new.shape[0]
-    kp, ks = _heads(k_new, "k_new", dev, (T, Hkv, D))
-    vp, vs = _heads(v_new, "v_new", dev, (T, Hkv, D))
+    kv = (T, Hkv, D)
+    kp, ks = _heads(k_new, "k_new", dev, kv)
+    vp, vs = _heads(v_new, "v_new", dev, kv)
     qp = op = None
     Hq = qs = os_ = 0
     if q is not None:
-        qp, qs = _heads(q, "q", dev)
         Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D:
-            raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
+        shape = (T, Hq, D)
+        qp, qs = _heads(q, "q", dev, shape)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=_F16, device=q.device)
-        op, os_ = _heads(q_out, "q_out", dev, q.shape)
-    if not isinstance(rope_table, torch.Tensor) or rope_table.dim() != 2:
+            q_out = torch.empty(shape, dtype=_F16, device=q.device)
+        op, os_ = _heads(q_out, "q_out", dev, shape)
+    shape = rope_table.shape
+    rp = _on(rope_table, "rope_table", _F32, shape, dev)
+    if len(shape) != 2:
         raise ValueError("rope_table must be [max_positions][rotary_dim]")
-    MP, R = rope_table.shape
-    rp = _on(rope_table, "rope_table", _F32, rope_table.shape, dev)
+    MP, R = shape
     B = context_lens.shape[0]
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     bt, MB = _table(block_tables, "block_tables", B, dev)
     fn = _lib.paged_kv_append_rope_fp8 if fp8 else _lib.paged_kv_append_rope
-    st = fn(qp, kp, vp, qs, ks, vs, rp if R else None, _opt(token_starts, "token_starts", _I32, (B + 1,), dev),
-            _opt(positions, "positions", _I32, (T,), dev), bt, cl, op, os_, kc, vc, T, B, Hq, Hkv, D, R,
+    ts = None if token_starts is None else _on(token_starts, "token_starts", _I32, (B + 1,), dev)
+    pos = None if positions is None else _on(positions, "positions", _I32, (T,), dev)
+    st = fn(qp, kp, vp, qs, ks, vs, rp if R else None, ts, pos, bt, cl, op, os_, kc, vc, T, B, Hq, Hkv, D, R,
             1 if interleaved else 0, MP, BS, NB, MB, *scales, _word(error_word, dev), _raw_stream(stream, dev))
     if st:
         _check(st, name)
@@ -682,13 +676,19 @@ def _attention_prefix(name, fp8, q, k_cache, v_cache, prefix_tables, prefix_lens
                       context_lens, scale, scales, out, max_prefix_len, max_context_len, workspace, error_word,
                       stream):
     dev = _device(q, "q")
-    if q.dim() not in (3, 4):
+    qshape = q.shape
+    if len(qshape) == 3:
+        B, Hq, D = qshape
+        QL = 1
+    elif len(qshape) == 4:
+        B, QL, Hq, D = qshape
+    else:
         raise ValueError("q must be [num_seqs][num_q_heads][head_dim] or [num_seqs][q_len][num_q_heads][head_dim]")
-    B, QL, Hq, D = q.shape if q.dim() == 4 else (q.shape[0], 1, q.shape[1], q.shape[2])
-    qp = _on(q, "q", _F16, q.shape, dev)
-    kc = _cache(k_cache, "k_cache", fp8, dev)
-    vc = _cache(v_cache, "v_cache", fp8, dev, k_cache.shape)
-    NB, Hkv, BS, D2 = k_cache.shape
+    qp = _on(q, "q", _F16, qshape, dev)
+    shape = k_cache.shape
+    kc = _cache(k_cache, "k_cache", fp8, dev, shape)
+    vc = _cache(v_cache, "v_cache", fp8, dev, shape)
+    NB, Hkv, BS, D2 = shape
     if D2 != D:
         raise ValueError("q / k_cache head_dim mismatch")
     Y = prefix_lens.shape[0]
@@ -699,7 +699,7 @@ def _attention_prefix(name, fp8, q, k_cache, v_cache, prefix_tables, prefix_lens
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     if out is None:
         out = torch.empty_like(q)
-    op = _on(out, "out", _F16, q.shape, dev)
+    op = _on(out, "out", _F16, qshape, dev)
     mp, mc = _max_len(prefix_lens, max_prefix_len), _max_len(context_lens, max_context_len)
     if workspace is None:
         workspace = alloc_workspace(paged_decode_prefix_workspace_size(B, QL, Hq, Hkv, D, BS, Y, mp, mc), q.device)
@@ -742,14 +742,16 @@ def paged_kv_block_bounds(k_cache, block_tables, context_lens, bounds, start_len
     ``max_new_tokens`` bounds context_lens - start_lens from above (default: the table's row)."""
     dev = _device(k_cache, "k_cache")
     fp8 = k_cache.element_size() == 1
-    kc = _cache(k_cache, "k_cache", fp8, dev)
-    NB, Hkv, BS, D = k_cache.shape
+    shape = k_cache.shape
+    kc = _cache(k_cache, "k_cache", fp8, dev, shape)
+    NB, Hkv, BS, D = shape
     bo = _cache(bounds, "bounds", fp8, dev, (NB, Hkv, 2, D))
     B = context_lens.shape[0]
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     bt, MB = _table(block_tables, "block_tables", B, dev)
     most = MB * BS if max_new_tokens is None else int(max_new_tokens)
-    st = _lib.paged_kv_block_bounds(kc, bt, cl, _opt(start_lens, "start_lens", _I32, (B,), dev), bo, B, Hkv, D, BS, NB,
+    sl = None if start_lens is None else _on(start_lens, "start_lens", _I32, (B,), dev)
+    st = _lib.paged_kv_block_bounds(kc, bt, cl, sl, bo, B, Hkv, D, BS, NB,
                                     MB, most, 1 if fp8 else 0, _word(error_word, dev), _raw_stream(stream, dev))
     if st:
         _check(st, "paged_kv_block_bounds")
@@ -763,13 +765,14 @@ def paged_kv_block_select(q, bounds, block_tables, context_lens, max_selected, b
     ``sink_blocks``, the last ``recent_blocks`` and those whose bounds allow the largest scores.
     Returns (block_lists int32 [B][Hkv][max_selected], ascending then -1; list_lens [B][Hkv])."""
     dev = _device(q, "q")
-    if q.dim() != 3 or not isinstance(bounds, torch.Tensor):
-        raise ValueError("q must have 3 dimensions and bounds be a tensor")
-    qp = _on(q, "q", _F16, q.shape, dev)
+    qshape, shape = q.shape, bounds.shape
+    qp = _on(q, "q", _F16, qshape, dev)
+    if len(qshape) != 3:
+        raise ValueError("q must have 3 dimensions")
     fp8 = bounds.element_size() == 1
-    bo = _cache(bounds, "bounds", fp8, dev)
-    B, Hq, D = q.shape
-    NB, Hkv, two, D2 = bounds.shape
+    bo = _cache(bounds, "bounds", fp8, dev, shape)
+    B, Hq, D = qshape
+    NB, Hkv, two, D2 = shape
     if D2 != D or two != 2:
         raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
     K = int(max_selected)
@@ -797,13 +800,14 @@ def paged_decode_blocks_workspace_size(num_seqs, num_q_heads, num_kv_heads, head
 def _attention_blocks(name, fp8, q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, scale,
                       scales, out, workspace, error_word, stream):
     dev = _device(q, "q")
-    if q.dim() != 3 or not isinstance(block_lists, torch.Tensor):
-        raise ValueError("q must have 3 dimensions and block_lists be a tensor")
-    qp = _on(q, "q", _F16, q.shape, dev)
-    kc = _cache(k_cache, "k_cache", fp8, dev)
-    vc = _cache(v_cache, "v_cache", fp8, dev, k_cache.shape)
-    B, Hq, D = q.shape
-    NB, Hkv, BS, D2 = k_cache.shape
+    qshape, shape = q.shape, k_cache.shape
+    qp = _on(q, "q", _F16, qshape, dev)
+    if len(qshape) != 3:
+        raise ValueError("q must have 3 dimensions")
+    kc = _cache(k_cache, "k_cache", fp8, dev, shape)
+    vc = _cache(v_cache, "v_cache", fp8, dev, shape)
+    B, Hq, D = qshape
+    NB, Hkv, BS, D2 = shape
     if D2 != D:
         raise ValueError("q / k_cache head_dim mismatch")
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
@@ -813,7 +817,7 @@ def _attention_blocks(name, fp8, q, k_cache, v_cache, block_tables, context_lens
     ll = _on(list_lens, "list_lens", _I32, (B, Hkv), dev)
     if out is None:
         out = torch.empty_like(q)
-    op = _on(out, "out", _F16, q.shape, dev)
+    op = _on(out, "out", _F16, qshape, dev)
     if workspace is None:
         workspace = alloc_workspace(paged_decode_blocks_workspace_size(B, Hq, Hkv, D, BS, K), q.device)
     ws, wsb = _space(workspace, dev)
