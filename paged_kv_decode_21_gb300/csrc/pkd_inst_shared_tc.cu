@@ -10,6 +10,15 @@ static_assert(kSharedRows == kSharedRowsPerCta, "rows per CTA of the kernel and 
 
 namespace {
 
+// A CTA holds all 512 columns of its SM's tensor memory, so it and a CTA of the
+// tcgen05 decode kernel, which may run beside it, must not share an SM: one
+// would wait for the other's columns.  Their shared memory rules it out.
+template <int KVB, int HD>
+constexpr bool apart() {
+  return SharedTcTraits<16, KVB, HD>::SMEM_BYTES + TcTraits<16, KVB, HD>::SMEM_BYTES > 226 * 1024;
+}
+static_assert(apart<2, 128>() && apart<2, 64>() && apart<1, 128>(), "never on one SM");
+
 template <int BS, int KVB, int HD>
 cudaError_t launch_bs(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, long long grid,
                       cudaStream_t stream) {

@@ -215,17 +215,23 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   p.error_word = error_word;
   // Rows (sequence, kv head) are what runs side by side.  Many rows: one CTA
   // each, of 128 threads, so that four rows share an SM and one's selection
-  // runs beside another's pass.  Few: clusters, until they would fill the GPU
-  // twice over or a warp would be without a tile of 16 blocks.
+  // runs beside another's pass (1024 rows of 256 blocks: 33 us, against 43 with
+  // 256 threads).  Few: clusters, until they would fill the GPU twice over or a
+  // warp would be without a tile of 16 blocks (8 rows of 2048 blocks: 11 us
+  // with 16 CTAs a row, 23 with one; 256 rows: 46 with one, 50 with two, 68
+  // with eight).  Sixteen need a GPC that holds them all at once, so they are
+  // left to score arrays of which an SM holds two.
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
     sms = 148;
   const long long rows = (long long)num_seqs * num_kv_heads;
   const int tiles = (max_blocks + 15) / 16;
+  const int smem = 4 * (max_blocks + (max_blocks + 31) / 32) + 16;  // scores, a bit per block
   const bool narrow = rows > 2LL * sms;
+  const int most = smem <= 64 * 1024 ? pkd::kSelMaxCluster : 8;
   p.cluster = 1;
-  while (!narrow && p.cluster < pkd::kSelMaxCluster && rows * 2 * p.cluster <= 2LL * sms &&
+  while (!narrow && p.cluster < most && rows * 2 * p.cluster <= 2LL * sms &&
          2 * p.cluster * pkd::kSelMaxWarps <= tiles)
     p.cluster *= 2;
   const long long grid = rows * p.cluster;
@@ -236,7 +242,6 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   auto* fn = kv_fp8 ? (head_dim == 128 ? PKD_SELECT(128, 1) : PKD_SELECT(64, 1))
                     : (head_dim == 128 ? PKD_SELECT(128, 2) : PKD_SELECT(64, 2));
 #undef PKD_SELECT
-  const int smem = 4 * (max_blocks + (max_blocks + 31) / 32) + 16;  // scores, a bit per block
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return PKD_ERR_LAUNCH;
   if (p.cluster > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)

@@ -18,22 +18,29 @@
 //                   columns each for A and for B, P as fp16 pairs over S
 //   shared memory   Q of both tiles; rings of K and V tiles
 // Two S buffers per row tile let Q K^T of the tile after next run behind the
-// softmax of the next.  (One buffer of 128 tokens needs a third less shared-
-// memory bandwidth, 64 cycles per 128 tokens and k step against 2 x 48, but
-// leaves S, softmax, P V in one chain: 4900 cycles per 128 tokens.)
+// softmax of the next.
+//
+// What bounds it.  Per 64 tokens both row tiles together need 512 cycles of
+// tensor math for Q K^T and 512 for P V.  Q K^T with both operands in shared
+// memory reads 6 KiB per 32-cycle step at N = 64, so it takes 48; with that,
+// 1280 cycles; measured 1700-1750 (256 x 7 rows over 32768 tokens, 4 kv heads:
+// 97 us, 1.25 PFLOP/s, 58% of the tensor cycles).  The rest is the chain
+// P -> P V -> free S buffer -> Q K^T of one issuing warp, in which every test
+// of a barrier takes over a hundred cycles while the MMAs stream operands from
+// shared memory.  (One 128-token S buffer per row tile, a third less shared-
+// memory traffic but S, softmax and P V in one chain: 2450 per 64 tokens.)
 //
 // Roles:
 //   warps 0-3, 4-7  softmax of tile A, B: one thread per row, as in
 //                   pkd_decode_tc.cuh
 //   warps 8, 9      MMA issuers of A and B: the whole warp waits on the next
-//                   barrier of its chain, one elected lane issues.  (One warp
-//                   polling the conditions of both chains took 2450 cycles per
-//                   64 tokens: while the MMAs stream their operands from
-//                   shared memory a barrier test takes over a hundred.  One
-//                   warp for S and one for P V keep A and B in step, so that
-//                   both softmaxes run at once: 2150 against 1950.)
-//   warps 10, 11    K and V tiles: copies, one lane per box; E4M3: they also
-//                   widen the landed bytes to fp16 in place
+//                   barriers of its chain, one elected lane issues.  (One warp
+//                   polling the conditions of both chains: 2450 cycles; one for
+//                   S and one for P V of both, which keeps both softmaxes in
+//                   step: 2150; four warps, at 128 registers a thread: as two.)
+//   warps 10, 11    K and V tiles: copies, one lane per box; E4M3: they and
+//   (12, 13)        warps 12 and 13 widen the landed bytes to fp16 in place,
+//                   half of a tile's rows each
 // Every wait is bounded; a role that gives up raises the abort flag.
 #pragma once
 #include <cstdint>
@@ -67,7 +74,10 @@ struct SharedTcTraits {
   // full, kempty, vempty [NS]; sfull, pfull, pfree [2][2]; drain [2]; E4M3: kland, vland [NS]
   static constexpr int NBAR = 3 * NS + 12 + 2 + (F8 ? 2 * NS : 0);
   static constexpr int W_MMA = 8, W_K = 10, W_V = 11;
-  static constexpr int THREADS = 384;  // three warps per scheduler: 168 registers a thread
+  // fp16: three warps per scheduler, 168 registers a thread.  E4M3: two more
+  // that widen, at 128 registers and a few spilled bytes
+  static constexpr int WIDENERS = F8 ? 2 : 0;  // per ring: its copy warp and one more
+  static constexpr int THREADS = F8 ? 448 : 384;
   static constexpr int TAIL = NBAR * 8 + 8 + NS * 4;
   static constexpr int SMEM_BYTES = MAIN + ((TAIL + 15) / 16) * 16;
   static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
@@ -99,7 +109,11 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     leave();
     return;
   }
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::MAIN);  // [NS] a tile's K and V are in shared memory
+  // full: K tile n and V tile n - 2 (with its bad-block mask) are in shared
+  // memory: what an issuer needs next, when it has P of tile n - 2.  One test a
+  // tile instead of two; n runs to ntiles + 1, with no V for n < 2 and no K for
+  // the last two.
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::MAIN);  // [NS]
   uint64_t* kempty = full + NS;    // [NS] S of the tile computed, for every row tile
   uint64_t* vempty = kempty + NS;  // [NS] P V of the tile completed, for every row tile
   uint64_t* sfull = vempty + NS;   // [2][2] S of a tile is in buffer h of row tile x
@@ -152,7 +166,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], F8 ? 64 : 2);  // the K warp and the V warp
+      mbar_init(&full[s], F8 ? 2 * 32 * T::WIDENERS : 2);  // the K warps and the V warps
       mbar_init(&kempty[s], nx);
       mbar_init(&vempty[s], nx);
       if (F8) {
@@ -198,14 +212,21 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == T::W_K || warp == T::W_V) {
+  if (warp >= T::W_K) {
     // ------------------------------------------------------------ K, V tiles
     // Lane l copies box l % NBOX of 64-dim half l / NBOX (E4M3: one box holds
     // whole rows); its block id is read one tile ahead.
-    const bool is_k = warp == T::W_K;
+    const bool is_k = warp % 2 == T::W_K % 2;
+    const int part = (warp - T::W_K) / 2;  // E4M3: the rows it widens; part 0 copies
     const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
     uint64_t* empty = is_k ? kempty : vempty;
-    uint64_t* land = F8 ? (is_k ? kland : vland) : full;
+    const int lead = is_k ? 0 : 2;  // tile t's full barrier is number t + lead
+    // fp16: the copies complete on the full barrier; E4M3: on a landing barrier
+    auto land_bar = [&](int t) -> uint64_t* {
+      if constexpr (F8) return is_k ? &kland[t % NS] : &vland[t % NS];
+      return &full[(t + lead) % NS];
+    };
+    auto land_parity = [&](int t) -> uint32_t { return F8 ? (t / NS) & 1 : ((t + lead) / NS) & 1; };
     const uint32_t ring = is_k ? T::K_OFF : T::V_OFF;
     const L2Hints l2h = make_l2_hints(false);
     const int box = lane % T::NBOX, h = lane / T::NBOX;
@@ -214,7 +235,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       const int k = i * T::NBT + box * 16 / BS;
       return mine && i < ntiles && k < nblk ? bt[k] : -1;
     };
-    int issued = 0, id = block_of(0);
+    int issued = 0, issued_idle = 0, id = block_of(0);
     auto issue = [&]() {
       const int st = issued % NS;
       const bool in = mine && issued * T::NBT + box * 16 / BS < nblk;
@@ -228,41 +249,63 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
         // the mask is read by threads that waited for the stage's full barrier
         if (!is_k) vbad[st] = bad;
         if (is_k && bad) record_error(P.error_word, kErrBadBlock);
-        mbar_arrive_expect_tx(&land[st], (uint32_t)boxes * 16 * 128);
+        mbar_arrive_expect_tx(land_bar(issued), (uint32_t)boxes * 16 * 128);
       }
       __syncwarp();
       if (ok)
-        tma_load_3d(sbase + ring + st * T::TILE + (F8 ? 0 : h * T::KVH) + box * 16 * T::ROWB, map, &land[st],
-                    F8 ? 0 : 64 * h, g * BS + (box * 16) % BS, id, l2h);
+        tma_load_3d(sbase + ring + st * T::TILE + (F8 ? 0 : h * T::KVH) + box * 16 * T::ROWB, map,
+                    land_bar(issued), F8 ? 0 : 64 * h, g * BS + (box * 16) % BS, id, l2h);
       ++issued;
       id = block_of(issued);
     };
     bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, P.timeout_ns, abort_flag));
+    };
+    // A stage is free for tile t once the tile NS before it was used; and an
+    // arrival for full barrier n may only follow the completion of its number
+    // n - NS, which that implies but for the first V tiles.
+    auto wait_free = [&](int t) {
+      if (t >= NS)
+        wait(&empty[t % NS], ((t / NS) - 1) & 1);
+      else if (t + lead >= NS)
+        wait(&full[(t + lead) % NS], 0);
+    };
+    auto arrive_idle = [&]() {  // for a full barrier without a tile of this ring
+      if (F8 || lane == 0) mbar_arrive(&full[(issued_idle) % NS]);
+    };
+    if (!is_k)
+      for (issued_idle = 0; issued_idle < 2; ++issued_idle) arrive_idle();
     for (int t = 0; t < ntiles && ok; ++t) {
       if constexpr (F8) {
         // keep copies going as far as stages are free; at least tile t's
-        while (issued < ntiles && issued < t + NS) {
-          const int st = issued % NS;
-          const uint32_t ph = ((issued / NS) - 1) & 1;
-          if (issued >= NS && issued > t && !__all_sync(0xffffffffu, mbar_test(&empty[st], ph))) break;
-          if (issued >= NS && issued == t)
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&empty[st], ph, P.timeout_ns, abort_flag));
+        while (part == 0 && issued < ntiles && issued < t + NS) {
+          if (issued > t && issued >= NS &&
+              !__all_sync(0xffffffffu, mbar_test(&empty[issued % NS], ((issued / NS) - 1) & 1)))
+            break;
+          if (issued > t && issued < NS && issued + lead >= NS &&
+              !__all_sync(0xffffffffu, mbar_test(&full[(issued + lead) % NS], 0)))
+            break;
+          wait_free(issued);
           if (!ok) break;
           issue();
         }
-        // widen tile t: row r's 128 bytes landed at its place in the first
-        // 64-dim half; every lane reads its 16 chunks before any writes
+        // widen this warp's rows of tile t: row r's 128 bytes landed at its
+        // place in the first 64-dim half; every lane reads its chunks before
+        // any writes
         const int st = t % NS;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&land[st], (t / NS) & 1, P.timeout_ns, abort_flag));
+        if (ok) wait(land_bar(t), land_parity(t));
         if (!ok) break;
         unsigned char* stg = smem + ring + st * T::TILE;
-        uint4 in[16];
+        constexpr int CH = TN * 8 / 32 / (F8 ? T::WIDENERS : 1);  // 16-byte chunks a lane
+        uint4 in[CH];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) in[k] = *reinterpret_cast<const uint4*>(stg + 16 * (lane + 32 * k));
+        for (int k = 0; k < CH; ++k)
+          in[k] = *reinterpret_cast<const uint4*>(stg + 16 * (32 * CH * part + lane + 32 * k));
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int q = lane + 32 * k, r = q >> 3;
+        for (int k = 0; k < CH; ++k) {
+          const int q = 32 * CH * part + lane + 32 * k, r = q >> 3;
           const int c = (q & 7) ^ (r & 7);  // dims 16 c .. 16 c + 15 of row r
           uint4 lo, hi;
           e4m3x4_to_f16x2x2(in[k].x, lo.x, lo.y);
@@ -274,30 +317,33 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
           *reinterpret_cast<uint4*>(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4)) = hi;
         }
         fence_proxy_async_smem();  // visible to the tensor cores
-        mbar_arrive(&full[st]);
+        mbar_arrive(&full[(t + lead) % NS]);
       } else {
-        if (t >= NS)
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_or_abort(&empty[t % NS], ((t / NS) - 1) & 1, P.timeout_ns, abort_flag));
+        wait_free(t);
         if (ok) issue();
       }
     }
+    if (is_k)
+      for (issued_idle = ntiles; issued_idle < ntiles + 2 && ok; ++issued_idle) {
+        wait_free(issued_idle);
+        if (ok) arrive_idle();
+      }
     if (!ok) {
       if (lane == 0 && !*abort_flag) record_error(P.error_word, kErrTimeout);
       *abort_flag = 1;
     }
     __syncwarp();
-    if (*abort_flag && lane == 0)  // let the copies in flight land before the CTA exits
+    if (*abort_flag && lane == 0 && part == 0)  // let the copies in flight land before the CTA exits
       for (int t = max(0, issued - NS); t < issued; ++t)
-        mbar_wait_bounded(&land[t % NS], (t / NS) & 1, P.timeout_ns);
+        mbar_wait_bounded(land_bar(t), land_parity(t), P.timeout_ns);
   } else if (warp >= T::W_MMA && warp - T::W_MMA < nx) {
     // ------------------------------------------------------------ MMA issuer of row tile x
     const int x = warp - T::W_MMA;
     const uint32_t qs = sbase + T::Q_OFF + x * T::NH * T::QH;
     const uint32_t scol = tmem + T::S_COL + 128 * x, ocol = tmem + T::O_COL + 128 * x;
     bool ok = true;
-    // Two barriers are waited for at once, each by half of the lanes: a test
-    // costs its two hundred cycles either way.
+    // (A test of a barrier costs over a hundred cycles while the MMAs stream
+    // their operands from shared memory: three a tile is what is needed.)
     auto await = [&](uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2) {
       const bool second = lane & 1;
       ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(second ? bar2 : bar, second ? parity2 : parity,
@@ -323,9 +369,8 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       issue_qk(1);
     }
     for (int s = 0; s < ntiles && ok; ++s) {
-      // P of this tile, and K of the tile after next
-      const int n = min(s + 2, ntiles - 1);
-      await(&pfull[2 * x + (s & 1)], (s >> 1) & 1, &full[n % NS], (n / NS) & 1);
+      // P and V of this tile, and K of the tile after next
+      await(&pfull[2 * x + (s & 1)], (s >> 1) & 1, &full[(s + 2) % NS], ((s + 2) / NS) & 1);
       if (ok && elect_one()) {
         const uint32_t vs = sbase + T::V_OFF + (s % NS) * T::TILE;
         const uint32_t pa = scol + 64 * (s & 1);  // P: 8 columns per 16 tokens
@@ -374,7 +419,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       const int nv = t1 - (t0 + s * TN);  // tokens of the tile inside the partition
       uint32_t bad = 0;
       if (any_bad || nv < TN) {  // the tile's V and its bad-block mask are needed below
-        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&full[sv], (s / NS) & 1, P.timeout_ns, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&full[(s + 2) % NS], ((s + 2) / NS) & 1, P.timeout_ns, abort_flag));
         bad = vbad[sv];
       }
       tmem_ld_wait();
