@@ -137,6 +137,20 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(con
   if (row >= P.rows) return;
   const int tok = row / P.num_q_heads, h = row % P.num_q_heads;
   const int b = tok / P.q_len;
+  const MergeSource src[2] = {P.own, P.shared};
+  // The first 32 partials' statistics are requested along with the lengths
+  // that tell how many of them there are (places past that hold anything and
+  // are dropped), so that two rounds of memory latency remain, not five.
+  float m0[2], l0[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    m0[k] = -INFINITY;
+    l0[k] = 0.f;
+    if (src[k].o && lane < src[k].np) {
+      m0[k] = src[k].m[(size_t)row * src[k].np + lane];
+      l0[k] = src[k].l[(size_t)row * src[k].np + lane];
+    }
+  }
   long long own_tokens;
   if (P.list_lens) {
     const int g = h / (P.num_q_heads / P.num_kv_heads);
@@ -145,30 +159,74 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(con
     own_tokens = P.context_lens[b];
   }
   int n[2] = {0, 0};
+  if (P.shared.o) {
+    int len = 0;
+    if (P.num_groups <= 32) {  // every group a lane: its start, its end's successor and its length at once
+      const int start = lane < P.num_groups ? P.group_starts[lane] : 0;
+      const int end = lane < P.num_groups ? P.group_starts[lane + 1] : 0;
+      const int sl = lane < P.num_groups ? P.shared_lens[lane] : 0;
+      const unsigned mine = __ballot_sync(0xffffffffu, lane < P.num_groups && start <= b && b < end);
+      if (mine) len = __shfl_sync(0xffffffffu, sl, __ffs(mine) - 1);
+    } else {
+      const int y = find_segment(P.group_starts, P.num_groups, b);
+      if (y < P.num_groups && P.group_starts[y] <= b) len = P.shared_lens[y];
+    }
+    len = max(len, 0);
+    n[1] = min((len + P.shared.part - 1) / P.shared.part, P.shared.np);
+  }
   if (P.own.o && own_tokens > 0) n[0] = (int)min((own_tokens + P.own.part - 1) / P.own.part, (long long)P.own.np);
   if (P.skip_single && n[0] <= 1) return;
-  if (P.shared.o) {
-    const int y = find_segment(P.group_starts, P.num_groups, b);
-    if (y < P.num_groups && P.group_starts[y] <= b) {
-      const int len = max(P.shared_lens[y], 0);
-      n[1] = min((len + P.shared.part - 1) / P.shared.part, P.shared.np);
-    }
-  }
-  const MergeSource src[2] = {P.own, P.shared};
   float M = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int j = lane; j < n[k]; j += 32) M = fmaxf(M, src[k].m[(size_t)row * src[k].np + j]);
+  for (int k = 0; k < 2; ++k) {
+    if (lane < n[k]) M = fmaxf(M, m0[k]);
+    for (int j = lane + 32; j < n[k]; j += 32) M = fmaxf(M, src[k].m[(size_t)row * src[k].np + j]);
+  }
 #pragma unroll
   for (int msk = 16; msk > 0; msk >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, msk));
   float acc[V], Z = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  float w0[2];  // weights of the first 32
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const float* o = src[k].o + (size_t)row * src[k].np * D + V * lane;
-    for (int j0 = 0; j0 < n[k]; j0 += 32) {
-      float w = 0.f;  // the weight of partial j0 + lane
+    w0[k] = lane < n[k] && m0[k] != -INFINITY ? __expf(m0[k] - M) : 0.f;
+    if (lane < n[k]) Z = fmaf(w0[k], l0[k], Z);
+  }
+  auto load = [&](const float* p, float (&x)[V]) {
+    if constexpr (V == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(p);
+      x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(p);
+      x[0] = t.x; x[1] = t.y;
+    }
+  };
+  const float* o[2] = {src[0].o + (size_t)row * src[0].np * D + V * lane,
+                       src[1].o + (size_t)row * src[1].np * D + V * lane};
+  // both sources' first 32 as one run, U vectors in flight
+  const int c0 = min(n[0], 32), all = c0 + min(n[1], 32);
+  for (int e0 = 0; e0 < all; e0 += U) {
+    float x[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (e0 + u < all) load(e0 + u < c0 ? o[0] + (size_t)(e0 + u) * D : o[1] + (size_t)(e0 + u - c0) * D, x[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = e0 + u;
+      const float wa = __shfl_sync(0xffffffffu, w0[0], e & 31), wb = __shfl_sync(0xffffffffu, w0[1], (e - c0) & 31);
+      if (e < all) {
+        const float wu = e < c0 ? wa : wb;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(wu, x[u][v], acc[v]);
+      }
+    }
+  }
+  // any further ones
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    for (int j0 = 32; j0 < n[k]; j0 += 32) {
+      float w = 0.f;
       if (j0 + lane < n[k]) {
         const size_t at = (size_t)row * src[k].np + j0 + lane;
         const float m = src[k].m[at];
@@ -180,16 +238,7 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(con
         float x[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (c + u < nj) {
-            const float* p = o + (size_t)(j0 + c + u) * D;
-            if constexpr (V == 4) {
-              const float4 t = *reinterpret_cast<const float4*>(p);
-              x[u][0] = t.x; x[u][1] = t.y; x[u][2] = t.z; x[u][3] = t.w;
-            } else {
-              const float2 t = *reinterpret_cast<const float2*>(p);
-              x[u][0] = t.x; x[u][1] = t.y;
-            }
-          }
+          if (c + u < nj) load(o[k] + (size_t)(j0 + c + u) * D, x[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float wu = __shfl_sync(0xffffffffu, w, (c + u) & 31);
@@ -200,14 +249,16 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(con
         }
       }
     }
-  }
 #pragma unroll
   for (int msk = 16; msk > 0; msk >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, msk);
   const float invz = Z > 0.f ? 1.f / Z : 0.f;  // Z = 0: the row saw no token
-#pragma unroll
-  for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<__half2*>(P.out + (size_t)row * D + V * lane + v) =
-        __floats2half2_rn(acc[v] * invz, acc[v + 1] * invz);
+  if constexpr (V == 4) {
+    const __half2 a = __floats2half2_rn(acc[0] * invz, acc[1] * invz), c = __floats2half2_rn(acc[2] * invz, acc[3] * invz);
+    *reinterpret_cast<uint2*>(P.out + (size_t)row * D + V * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+  } else {
+    *reinterpret_cast<__half2*>(P.out + (size_t)row * D + V * lane) = __floats2half2_rn(acc[0] * invz, acc[1] * invz);
+  }
 }
 
 // ---------------------------------------------------------------------------
