@@ -15,7 +15,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 pkd_status launched() { return cudaGetLastError() == cudaSuccess ? PKD_OK : PKD_ERR_LAUNCH; }
 
-constexpr int kMaxRopeHeadDim = 512;  // 16 dims a thread, 8 heads in flight at least
+constexpr int kMaxRopeHeadDim = 512;  // 16 dims a thread, at least four heads in flight
 
 pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long long q_stride, long long k_stride,
                        long long v_stride, const float* rope_table, const int32_t* token_starts,

@@ -23,6 +23,10 @@ constexpr uint32_t kErrBadPosition = 8u;  // a rotation position outside the tab
 // the token's q, k and v heads with them.  The first head's data is requested
 // before the token's sequence, position and block are looked up, so that chain
 // of dependent loads hides behind it.
+//
+// Bound by HBM: every byte is moved once.  CTAs of 128 threads, sixteen heads
+// at D = 128, keep more tokens in different phases on an SM than 256: prompts
+// of 26k tokens, 40 q and 8 kv heads, 133 against 155 us, 6.2 TB/s.
 struct RopeAppendParams {
   const __half *q, *k, *v;         // token t's heads at q + t * q_stride (elements), head_dim apart
   long long q_stride, k_stride, v_stride, q_out_stride;
@@ -183,9 +187,12 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
 // length) and every dim d, lo_d = min_t k[t][d] and hi_d = max_t k[t][d], in
 // the cache's own type: both are cache values, so nothing is rounded.
 //
-// One warp per (sequence, block, kv head): the tile's rows are contiguous, so
-// a warp-wide load of 16 bytes a lane covers several whole rows, all of a
-// lane's loads are independent, and the row groups meet in a butterfly.
+// A warp takes up to eight kv heads of one (sequence, block): their tiles lie
+// behind one another, a warp-wide load of 16 bytes a lane covers several whole
+// rows, all of a step's loads are independent and the next step's are
+// requested first, and the row groups meet in a butterfly.  Bound by HBM: 32
+// prompts of 4000-8192 tokens, 8 heads, 78 us, 5.8 TB/s (one head a warp: 128,
+// and 90 without the next step's loads).
 struct BlockBoundsParams {
   const void* k_cache;
   const int32_t *block_tables, *context_lens;

@@ -173,6 +173,38 @@ def test_repeats_bit_for_bit_on_a_stream_and_in_a_graph():
         check(out, ref, mag, 1030, values(vc).abs().max().item())
 
 
+@pytest.mark.parametrize("seed", range(30))
+def test_random_shapes(seed):
+    import random
+    r = random.Random(1000 + seed)
+    Hkv = r.choice((1, 2, 4, 8))
+    Hq, D, BS, fp8, q_len = Hkv * r.randint(1, 8), r.choice((64, 128, 128)), r.choice((16, 32)), r.random() < 0.5, r.choice((1, 1, 2, 7))
+    sizes = [r.randint(0, 40) for _ in range(r.randint(1, 4))]
+    outside = r.randint(0 if sum(sizes) else 1, 3)
+    plens = [r.choice((r.randint(0, 70), r.randint(0, 3000))) for _ in sizes]
+    lens = [r.choice((0, r.randint(0, 20), r.randint(0, 700))) for _ in range(sum(sizes) + outside)]
+    run_and_check(problem(sizes, plens, lens, q_len, Hq, Hkv, D, BS, seed, fp8, outside), BS, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_negative_and_zero_scales(fp8):
+    p = problem([40], [300], [20] * 40, 1, 8, 2, 128, 16, seed=15, fp8=fp8)
+    ks, vs = workloads.E4M3_SCALES["full"] if fp8 else (1.0, 1.0)
+    for scale in (-0.05, 0.0):
+        out = (ops.paged_decode_attention_prefix_fp8(*p, scale, ks, vs) if fp8
+               else ops.paged_decode_attention_prefix(*p, scale))
+        ref, mag = prefix_attention(*p, scale, ks, vs, 16)
+        check(out, ref, mag, 320, values(p[2]).abs().max().item() * vs)
+
+
+def test_groups_that_reach_past_the_batch_stay_inside_it():
+    # group starts past the batch (or below zero) are cut to it
+    p = list(problem([5, 3], [200, 100], [30] * 8, 1, 8, 2, 128, 16, seed=16))
+    want = ops.paged_decode_attention_prefix(*p, 0.1)
+    p[5] = torch.tensor([-4, 5, 1000], dtype=torch.int32, device="cuda")
+    assert torch.equal(ops.paged_decode_attention_prefix(*p, 0.1), want)
+
+
 def test_bad_blocks_are_reported_and_nothing_else_is_read():
     p = problem([3], [100], [40, 40, 40], 1, 8, 2, 128, 16, seed=12)
     q, kc, vc, ptab, plens, starts, bt, lens = p

@@ -162,6 +162,107 @@ def test_choice_at_the_largest_number_of_blocks():
                                   i32([5]), 100, 16, max_context_len=16 * blocks + 1)
 
 
+def test_choice_avoids_and_reports_blocks_outside_the_pool():
+    q, kc, vc, bt, cl = problem([900, 700], 8, 2, 128, 16, 31)
+    bounds = full_bounds(kc, bt, cl, False)
+    bad = bt.clone()
+    bad[0, 7], bad[0, 30], bad[1, 11] = kc.shape[0], -1, 1 << 30
+    ew = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lists, counts = ops.paged_kv_block_select(q, bounds, bad, cl, 20, 16, 1, 1, error_word=ew)
+    assert ops.pkd_read_device_error(ew) == ops.DEVERR_BAD_BLOCK
+    # as if those blocks scored below all others (whose bounds have zero inside)
+    low = torch.cat((bounds, torch.zeros_like(bounds[:1])))
+    good = torch.where((bad < 0) | (bad >= kc.shape[0]), kc.shape[0], bad)
+    want, _ = block_select(q, low, good, cl.tolist(), 20, 1, 1, 16)
+    assert torch.equal(lists.cpu(), want) and (counts == 20).all()
+    # chosen all the same where there is nothing else
+    lists, counts = ops.paged_kv_block_select(q, bounds, bad, cl, 55, 16, 1, 1, error_word=ew)
+    assert ops.pkd_read_device_error(ew) == ops.DEVERR_BAD_BLOCK
+    assert counts.tolist() == [[55, 55], [44, 44]]
+    assert not {7, 30} & set(lists[0].flatten().tolist())
+
+
+def test_lengths_past_the_callers_bound_are_reported():
+    q, kc, vc, bt, cl = problem([900, 700], 8, 2, 128, 16, 32)
+    bounds = full_bounds(kc, bt, cl, False)
+    ew = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lists, counts = ops.paged_kv_block_select(q, bounds, bt, cl, 10, 16, 1, 1, max_context_len=800, error_word=ew)
+    assert ops.pkd_read_device_error(ew) == ops.DEVERR_BAD_BLOCK
+    want, _ = block_select(q, bounds, bt, [800, 700], 10, 1, 1, 16)
+    assert torch.equal(lists.cpu(), want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_blocks_past_32_bits_of_a_large_pool(fp8):
+    """A pool of more than 2^31 elements: the sequences' blocks lie at both ends of it."""
+    Hq, Hkv, D, BS, lens = 32, 8, 128, 16, [600, 333]
+    pool = (1 << 31) // (Hkv * BS * D) + 5000
+    per = [-(-n // BS) for n in lens]
+    ids = torch.cat((torch.arange(40), torch.arange(pool - sum(per) + 40, pool)))
+    bt = torch.full((2, max(per)), -1, dtype=torch.int32)
+    bt[0, :per[0]], bt[1, :per[1]] = ids[:per[0]].int(), ids[per[0]:].flip(0).int()
+    kind = torch.uint8 if fp8 else torch.float16
+    kc, vc = (torch.empty((pool, Hkv, BS, D), dtype=kind, device="cuda") for _ in range(2))
+    kc[ids.cuda()], vc[ids.cuda()] = (make_cache((len(ids), Hkv, BS, D), k, fp8) for k in (1, 2))
+    bt, cl = bt.cuda(), i32(lens)
+    bounds = torch.empty((pool, Hkv, 2, D), dtype=kind, device="cuda")
+    ops.paged_kv_block_bounds(kc, bt, cl, bounds)
+    small = torch.zeros((pool,), dtype=torch.bool, device="cuda")
+    small[ids.cuda()] = True
+    for b, n in enumerate(lens):
+        for i in (0, per[b] - 1):
+            x = values(kc[int(bt[b, i]), :, :min(BS, n - i * BS)])
+            got = values(bounds[int(bt[b, i])])
+            assert torch.equal(got[:, 0], x.amin(1)) and torch.equal(got[:, 1], x.amax(1))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = workloads.randn_f16((2, Hq, D), g, "cuda")
+    lists, counts = select_and_check(q, bounds, bt, lens, 12, 1, 1, BS)
+    attend_and_check(q, kc, vc, bt, lens, lists, counts, BS, fp8)
+    # and a prefix at the far end
+    from serving_ref import prefix_attention
+    ptab = bt[1:, :per[1]].contiguous()
+    ks, vs = workloads.E4M3_SCALES["full"] if fp8 else (1.0, 1.0)
+    q4 = workloads.randn_f16((3, 1, Hq, D), g, "cuda")
+    args = (q4, kc, vc, ptab, i32([lens[1]]), i32([0, 3]), bt[[0, 0, 0]].contiguous(), i32([600, 1, 17]))
+    out = (ops.paged_decode_attention_prefix_fp8(*args, D ** -0.5, ks, vs) if fp8
+           else ops.paged_decode_attention_prefix(*args, D ** -0.5))
+    ref, mag = prefix_attention(*args, D ** -0.5, ks, vs, BS)
+    check(out, ref, mag, 1000, 448 * vs if fp8 else 6.0)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(seed):
+    import random
+    r = random.Random(seed)
+    Hkv = r.choice((1, 2, 3, 8))
+    Hq, D, BS, fp8 = Hkv * r.randint(1, 8), r.choice((64, 128)), r.choice((16, 32)), r.random() < 0.5
+    lens = [r.choice((1, r.randint(1, 60), r.randint(1, 6000))) for _ in range(r.randint(1, 40))]
+    K = r.choice((1, 2, 7, 31, 64, 130))
+    sink = r.randint(0, min(2, K))
+    recent = r.randint(0, K - sink)
+    q, kc, vc, bt, cl = problem(lens, Hq, Hkv, D, BS, seed, fp8)
+    lists, counts = select_and_check(q, full_bounds(kc, bt, cl, fp8), bt, lens, K, sink, recent, BS)
+    attend_and_check(q, kc, vc, bt, lens, lists, counts, BS, fp8)
+
+
+def test_calls_on_another_stream_repeat_bit_for_bit():
+    q, kc, vc, bt, cl = problem([3000, 1501, 40], 28, 4, 128, 16, 33)
+    bounds = full_bounds(kc, bt, cl, False)
+    lists, counts = ops.paged_kv_block_select(q, bounds, bt, cl, 50, 16)
+    out = ops.paged_decode_attention_blocks(q, kc, vc, bt, cl, lists, counts, 0.1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # the current stream
+        b2 = new_bounds(kc.shape[0], 4, 128, False)
+        ops.paged_kv_block_bounds(kc, bt, cl, b2)
+    l2, c2 = ops.paged_kv_block_select(q, b2, bt, cl, 50, 16, stream=side)  # a given one
+    o2 = ops.paged_decode_attention_blocks(q, kc, vc, bt, cl, l2, c2, 0.1, stream=side)
+    side.synchronize()
+    used = torch.unique(bt[bt >= 0]).long()
+    assert torch.equal(bounds[used], b2[used]) and torch.equal(lists, l2) and torch.equal(counts, c2)
+    assert torch.equal(out, o2)
+
+
 def attend_and_check(q, kc, vc, bt, lens, lists, counts, BS, fp8, **kw):
     ks, vs = workloads.E4M3_SCALES["full"] if fp8 else (1.0, 1.0)
     scale = q.shape[-1] ** -0.5
@@ -173,7 +274,7 @@ def attend_and_check(q, kc, vc, bt, lens, lists, counts, BS, fp8, **kw):
         out = ops.paged_decode_attention_blocks(q, kc, vc, bt, i32(lens), lists, counts, scale, error_word=ew, **kw)
     assert ops.pkd_read_device_error(ew) == 0
     ref, mag = listed_attention(q, kc, vc, bt, lens, lists, counts, scale, ks, vs, BS)
-    check(out, ref, mag, lists.shape[-1] * BS, values(vc).abs().max().item() * vs)
+    check(out, ref, mag, lists.shape[-1] * BS, values(vc[torch.unique(bt[bt >= 0]).long()]).abs().max().item() * vs)
     return out
 
 
