@@ -38,9 +38,9 @@
 //                   polling the conditions of both chains: 2450 cycles; one for
 //                   S and one for P V of both, which keeps both softmaxes in
 //                   step: 2150; four warps, at 128 registers a thread: as two.)
-//   warps 10, 11    K and V tiles: copies, one lane per box; E4M3: they and
-//   (12, 13)        warps 12 and 13 widen the landed bytes to fp16 in place,
-//                   half of a tile's rows each
+//   warps 10, 11    K and V tiles: copies, one lane per box
+//   warps 12-15     E4M3: widen the landed bytes to fp16 in place, two warps per
+//                   ring (a warp that also copied took 2560 cycles a tile)
 // Every wait is bounded; a role that gives up raises the abort flag.
 #pragma once
 #include <cstdint>
@@ -73,11 +73,11 @@ struct SharedTcTraits {
   static constexpr int MAIN = V_OFF + NS * TILE;
   // full, kempty, vempty [NS]; sfull, pfull, pfree [2][2]; drain [2]; E4M3: kland, vland [NS]
   static constexpr int NBAR = 3 * NS + 12 + 2 + (F8 ? 2 * NS : 0);
-  static constexpr int W_MMA = 8, W_K = 10, W_V = 11;
-  // fp16: three warps per scheduler, 168 registers a thread.  E4M3: two more
+  static constexpr int W_MMA = 8, W_K = 10, W_V = 11, W_WIDE = 12;
+  // fp16: three warps per scheduler, 168 registers a thread.  E4M3: four more
   // that widen, at 128 registers and a few spilled bytes
-  static constexpr int WIDENERS = F8 ? 2 : 0;  // per ring: its copy warp and one more
-  static constexpr int THREADS = F8 ? 448 : 384;
+  static constexpr int WIDENERS = F8 ? 2 : 0;  // per ring
+  static constexpr int THREADS = F8 ? 512 : 384;
   static constexpr int TAIL = NBAR * 8 + 8 + NS * 4;
   static constexpr int SMEM_BYTES = MAIN + ((TAIL + 15) / 16) * 16;
   static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
@@ -214,50 +214,16 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
 
   if (warp >= T::W_K) {
     // ------------------------------------------------------------ K, V tiles
-    // Lane l copies box l % NBOX of 64-dim half l / NBOX (E4M3: one box holds
-    // whole rows); its block id is read one tile ahead.
     const bool is_k = warp % 2 == T::W_K % 2;
-    const int part = (warp - T::W_K) / 2;  // E4M3: the rows it widens; part 0 copies
-    const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
     uint64_t* empty = is_k ? kempty : vempty;
     const int lead = is_k ? 0 : 2;  // tile t's full barrier is number t + lead
+    const uint32_t ring = is_k ? T::K_OFF : T::V_OFF;
     // fp16: the copies complete on the full barrier; E4M3: on a landing barrier
     auto land_bar = [&](int t) -> uint64_t* {
       if constexpr (F8) return is_k ? &kland[t % NS] : &vland[t % NS];
       return &full[(t + lead) % NS];
     };
     auto land_parity = [&](int t) -> uint32_t { return F8 ? (t / NS) & 1 : ((t + lead) / NS) & 1; };
-    const uint32_t ring = is_k ? T::K_OFF : T::V_OFF;
-    const L2Hints l2h = make_l2_hints(false);
-    const int box = lane % T::NBOX, h = lane / T::NBOX;
-    const bool mine = lane < (F8 ? 1 : T::NH) * T::NBOX;
-    auto block_of = [&](int i) {
-      const int k = i * T::NBT + box * 16 / BS;
-      return mine && i < ntiles && k < nblk ? bt[k] : -1;
-    };
-    int issued = 0, issued_idle = 0, id = block_of(0);
-    auto issue = [&]() {
-      const int st = issued % NS;
-      const bool in = mine && issued * T::NBT + box * 16 / BS < nblk;
-      const bool ok = in && id >= 0 && id < P.num_blocks;
-      const unsigned wrong = __ballot_sync(0xffffffffu, in && !ok && h == 0);
-      const int boxes = __popc(__ballot_sync(0xffffffffu, ok));
-      if (lane == 0) {
-        uint32_t bad = 0;
-#pragma unroll
-        for (int kk = 0; kk < T::NBT; ++kk) bad |= ((wrong >> (kk * BS / 16)) & 1u) << kk;
-        // the mask is read by threads that waited for the stage's full barrier
-        if (!is_k) vbad[st] = bad;
-        if (is_k && bad) record_error(P.error_word, kErrBadBlock);
-        mbar_arrive_expect_tx(land_bar(issued), (uint32_t)boxes * 16 * 128);
-      }
-      __syncwarp();
-      if (ok)
-        tma_load_3d(sbase + ring + st * T::TILE + (F8 ? 0 : h * T::KVH) + box * 16 * T::ROWB, map,
-                    land_bar(issued), F8 ? 0 : 64 * h, g * BS + (box * 16) % BS, id, l2h);
-      ++issued;
-      id = block_of(issued);
-    };
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, P.timeout_ns, abort_flag));
@@ -271,32 +237,62 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       else if (t + lead >= NS)
         wait(&full[(t + lead) % NS], 0);
     };
-    auto arrive_idle = [&]() {  // for a full barrier without a tile of this ring
-      if (F8 || lane == 0) mbar_arrive(&full[(issued_idle) % NS]);
+    // The arrivals for full barriers without a tile of this ring: the first
+    // two (V), the last two (K).
+    auto idle_arrivals = [&](int from) {
+      for (int n = from; n < from + 2 && ok; ++n) {
+        wait_free(n - lead);
+        if (ok && (F8 || lane == 0)) mbar_arrive(&full[n % NS]);
+      }
     };
-    if (!is_k)
-      for (issued_idle = 0; issued_idle < 2; ++issued_idle) arrive_idle();
-    for (int t = 0; t < ntiles && ok; ++t) {
-      if constexpr (F8) {
-        // keep copies going as far as stages are free; at least tile t's
-        while (part == 0 && issued < ntiles && issued < t + NS) {
-          if (issued > t && issued >= NS &&
-              !__all_sync(0xffffffffu, mbar_test(&empty[issued % NS], ((issued / NS) - 1) & 1)))
-            break;
-          if (issued > t && issued < NS && issued + lead >= NS &&
-              !__all_sync(0xffffffffu, mbar_test(&full[(issued + lead) % NS], 0)))
-            break;
-          wait_free(issued);
-          if (!ok) break;
-          issue();
-        }
-        // widen this warp's rows of tile t: row r's 128 bytes landed at its
-        // place in the first 64-dim half; every lane reads its chunks before
-        // any writes
-        const int st = t % NS;
-        if (ok) wait(land_bar(t), land_parity(t));
+    int issued = 0;
+    if (!F8 || warp < T::W_WIDE) {
+      // Copies: lane l copies box l % NBOX of 64-dim half l / NBOX (E4M3: one
+      // box holds whole rows); its block id is read one tile ahead.
+      const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+      const L2Hints l2h = make_l2_hints(false);
+      const int box = lane % T::NBOX, h = lane / T::NBOX;
+      const bool mine = lane < (F8 ? 1 : T::NH) * T::NBOX;
+      auto block_of = [&](int i) {
+        const int k = i * T::NBT + box * 16 / BS;
+        return mine && i < ntiles && k < nblk ? bt[k] : -1;
+      };
+      int id = block_of(0);
+      if (!F8 && !is_k) idle_arrivals(0);
+      for (; issued < ntiles; ++issued) {
+        wait_free(issued);
         if (!ok) break;
-        unsigned char* stg = smem + ring + st * T::TILE;
+        const int st = issued % NS;
+        const bool in = mine && issued * T::NBT + box * 16 / BS < nblk;
+        const bool good = in && id >= 0 && id < P.num_blocks;
+        const unsigned wrong = __ballot_sync(0xffffffffu, in && !good && h == 0);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, good));
+        if (lane == 0) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int kk = 0; kk < T::NBT; ++kk) bad |= ((wrong >> (kk * BS / 16)) & 1u) << kk;
+          // the mask is read by threads that waited for the tile's full barrier
+          if (!is_k) vbad[st] = bad;
+          if (is_k && bad) record_error(P.error_word, kErrBadBlock);
+          mbar_arrive_expect_tx(land_bar(issued), (uint32_t)boxes * 16 * 128);
+        }
+        __syncwarp();
+        if (good)
+          tma_load_3d(sbase + ring + st * T::TILE + (F8 ? 0 : h * T::KVH) + box * 16 * T::ROWB, map,
+                      land_bar(issued), F8 ? 0 : 64 * h, g * BS + (box * 16) % BS, id, l2h);
+        id = block_of(issued + 1);
+      }
+      if (!F8 && is_k) idle_arrivals(ntiles);
+    } else {
+      // E4M3: widen this warp's rows of every tile.  Row r's 128 bytes landed
+      // at its place in the first 64-dim half; every lane reads its chunks
+      // before any writes both halves.
+      const int part = (warp - T::W_WIDE) / 2;
+      if (!is_k) idle_arrivals(0);
+      for (int t = 0; t < ntiles; ++t) {
+        wait(land_bar(t), land_parity(t));
+        if (!ok) break;
+        unsigned char* stg = smem + ring + (t % NS) * T::TILE;
         constexpr int CH = TN * 8 / 32 / (F8 ? T::WIDENERS : 1);  // 16-byte chunks a lane
         uint4 in[CH];
 #pragma unroll
@@ -318,22 +314,15 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
         }
         fence_proxy_async_smem();  // visible to the tensor cores
         mbar_arrive(&full[(t + lead) % NS]);
-      } else {
-        wait_free(t);
-        if (ok) issue();
       }
+      if (is_k && ok) idle_arrivals(ntiles);
     }
-    if (is_k)
-      for (issued_idle = ntiles; issued_idle < ntiles + 2 && ok; ++issued_idle) {
-        wait_free(issued_idle);
-        if (ok) arrive_idle();
-      }
     if (!ok) {
       if (lane == 0 && !*abort_flag) record_error(P.error_word, kErrTimeout);
       *abort_flag = 1;
     }
     __syncwarp();
-    if (*abort_flag && lane == 0 && part == 0)  // let the copies in flight land before the CTA exits
+    if (*abort_flag && lane == 0)  // let the copies in flight land before the CTA exits
       for (int t = max(0, issued - NS); t < issued; ++t)
         mbar_wait_bounded(land_bar(t), land_parity(t), P.timeout_ns);
   } else if (warp >= T::W_MMA && warp - T::W_MMA < nx) {
