@@ -82,8 +82,8 @@ struct DecodeParams {
   const int32_t* group_starts;  // [num_groups + 1]
   int num_groups;
   int rows_per_chunk;  // paged_shared_tc_kernel: query rows per chunk
-  int after_grid;      // kShared kernels: launched as a programmatic dependent of the grid before, whose
-                       // completion each CTA awaits at its end
+  int after_grid;  // launched as a programmatic dependent of a grid whose results it does not read: its last
+                   // CTA awaits that grid, so that this one completes after it (await_grid_before)
 };
 
 // Which keys the query rows of a tensor-core decode CTA read.
@@ -222,6 +222,14 @@ __device__ __forceinline__ int find_segment(const int32_t* starts, int n, int x)
     hi = min(hi, lo + step - 1);
   }
   return lo;
+}
+
+// At the end of every CTA of a grid that runs beside the one before it in its
+// stream (after_grid): a dependent of this grid then sees both complete.  One
+// waiting CTA is enough, and the last one, which starts last, holds its place
+// the shortest.
+__device__ __forceinline__ void await_grid_before(const DecodeParams& P) {
+  if (P.after_grid && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {

@@ -223,9 +223,6 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
   // a dependent grid (the split-K merge) may launch once every CTA of this
   // grid has started; it waits for this grid's completion itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto leave = [&]() {  // kShared: see after_grid
-    if (SRC == kShared && P.after_grid) asm volatile("griddepcontrol.wait;" ::: "memory");
-  };
   int j, b, g;
   if (P.piece_order) {
     // longest first: the grid walks pieces p (all kv heads of a piece side by
@@ -249,7 +246,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
     // (b, above, is 0: the grid's rows are chunks of all groups)
     GroupChunk ch;
     if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len, QC, qc, &ch)) {
-      leave();
+      await_grid_before(P);
       return;
     }
     b = ch.group;
@@ -285,11 +282,11 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
       for (int i = threadIdx.x; i < G * nq * D; i += blockDim.x)
         P.out[out_row(i / D) * D + i % D] = __float2half_rn(0.f);
     }
-    leave();
+    await_grid_before(P);
     return;
   }
   if (j >= np_b) {
-    leave();
+    await_grid_before(P);
     return;
   }
 
@@ -671,7 +668,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
       }
     }
   }
-  leave();
+  await_grid_before(P);
 }
 
 }  // namespace pkd

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the swizzled operands need 1024-byte aligned groups
     if (threadIdx.x == 0) record_error(P.error_word, kErrLayout);
+    await_grid_before(P);
     return;
   }
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + T::MAIN);  // [NSK] a K tile landed
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int piece = P.piece_order[rest / P.num_kv_heads];
     if (P.tail_split) {
-      if (piece < 0) return;  // a slot past the batch's pieces
+      if (piece < 0) return;  // a slot past the batch's pieces (an ordered grid is never after_grid)
       b = piece >> 2;
       j = (piece & 3) == kPieceSecondHalf ? 1 : 0;
       half = (piece & 3) != kPieceWhole;
@@ -220,9 +221,13 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
       for (int i = threadIdx.x; i < rows * D; i += blockDim.x)
         P.out[out_row(i / D) * D + i % D] = __float2half_rn(0.f);
     }
+    await_grid_before(P);
     return;
   }
-  if (j >= np_b) return;
+  if (j >= np_b) {
+    await_grid_before(P);
+    return;
+  }
   // the CTA's partitions [j, j_end); with R > 1 the partition size is a
   // multiple of TN, so every tile lies in one partition, tpp tiles each
   const int j_end = min(j + R, np_b);
@@ -832,6 +837,7 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
     tc_fence_after();
     tmem_dealloc(tmem, T::TMEM_COLS);
   }
+  await_grid_before(P);
 }
 
 }  // namespace pkd

@@ -26,18 +26,8 @@ cudaError_t launch_bs(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
   auto* fn = paged_shared_tc_kernel<BS, KVB, HD>;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(T::THREADS);
-  cfg.dynamicSmemBytes = T::SMEM_BYTES;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.after_grid ? 1 : 0;
-  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, fn, mk, mv, p);
-  return e2 == cudaSuccess ? cudaGetLastError() : e2;
+  fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(mk, mv, p);
+  return cudaGetLastError();
 }
 
 }  // namespace

@@ -25,8 +25,9 @@ cudaError_t launch_tc_bs(const CUtensorMap& mk, const CUtensorMap& mv, const Dec
   cfg.blockDim = dim3(T::THREADS);
   cfg.dynamicSmemBytes = T::SMEM_BYTES;
   cfg.stream = stream;
-  if (p.piece_order) {
-    // a programmatic dependent of the order kernel (griddepcontrol.wait in the kernel)
+  if (p.piece_order || p.after_grid) {
+    // a programmatic dependent of the order kernel (griddepcontrol.wait in the
+    // kernel), or of a grid it runs beside (awaited by its last CTA)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;

@@ -68,8 +68,8 @@ cudaError_t launch_qc(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
     return cudaGetLastError();
   }
   // a programmatic dependent of the order kernel: the CTAs become resident
-  // while it runs and wait for its order with griddepcontrol.wait (or of the
-  // grid before a shared context's, awaited at the CTAs' end)
+  // while it runs and wait for its order with griddepcontrol.wait (or of a
+  // grid it runs beside, awaited by its last CTA)
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

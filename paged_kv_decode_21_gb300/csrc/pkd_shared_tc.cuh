@@ -99,14 +99,8 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
   unsigned char* smem = smem_sh;
   const uint32_t sbase = smem_u32(smem);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // this grid completes only after the one it may have started beside, so that
-  // a dependent of it (the merge) sees both
-  auto leave = [&]() {
-    if (P.after_grid) asm volatile("griddepcontrol.wait;" ::: "memory");
-  };
   if (sbase & 1023u) {  // the swizzled operands need 1024-byte aligned groups
     if (threadIdx.x == 0) record_error(P.error_word, kErrLayout);
-    leave();
     return;
   }
   // full: K tile n and V tile n - 2 (with its bad-block mask) are in shared
@@ -132,10 +126,8 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
   const int j = rest % P.max_partitions, g = rest / P.max_partitions;
   GroupChunk ch;
   if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len * G, P.rows_per_chunk,
-                        blockIdx.x % P.q_chunks, &ch)) {
-    leave();
+                        blockIdx.x % P.q_chunks, &ch))
     return;
-  }
   const int rows = min(P.rows_per_chunk, ch.tokens - ch.first);
   const size_t tok0 = (size_t)(ch.base / G);  // the group's first query token over the batch
   const int Hq = P.num_q_heads;
@@ -150,10 +142,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
   }
   const int PS = P.partition_size;
   const int t0 = j * PS;
-  if (t0 >= L) {  // the merge reads no partial past the context
-    leave();
-    return;
-  }
+  if (t0 >= L) return;  // the merge reads no partial past the context
   const int t1 = min(t0 + PS, L);
   const int ntiles = (t1 - t0 + TN - 1) / TN;
   const int nblk = (t1 - t0 + BS - 1) / BS;
@@ -523,7 +512,6 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, T::TMEM_COLS);
   }
-  leave();
 }
 
 }  // namespace pkd

@@ -205,6 +205,35 @@ def test_groups_that_reach_past_the_batch_stay_inside_it():
     assert torch.equal(ops.paged_decode_attention_prefix(*p, 0.1), want)
 
 
+@pytest.mark.parametrize("fp8,q_len", [(False, 1), (True, 1), (False, 5), (True, 5)])
+def test_calls_back_to_back_on_one_workspace(fp8, q_len):
+    """The two grids of a call overlap, and the merge starts early: calls in a row on one stream and one
+    workspace, each on other queries, give what each gives alone."""
+    p = problem([60], [3000], [q_len + (i * 37) % 300 for i in range(60)], q_len, 28, 4, 128, 16, seed=17, fp8=fp8)
+    ks, vs = workloads.E4M3_SCALES["full"] if fp8 else (1.0, 1.0)
+    g = torch.Generator(device="cuda").manual_seed(18)
+    qs = [workloads.randn_f16(p[0].shape, g, "cuda") for _ in range(4)]
+    kw = dict(max_prefix_len=3000, max_context_len=p[6].shape[1] * 16)
+
+    def call(q, **more):
+        if fp8:
+            return ops.paged_decode_attention_prefix_fp8(q, *p[1:], 0.09, ks, vs, **kw, **more)
+        return ops.paged_decode_attention_prefix(q, *p[1:], 0.09, **kw, **more)
+
+    alone = []
+    for q in qs:
+        alone.append(call(q))
+        torch.cuda.synchronize()
+    ws = ops.alloc_workspace(
+        ops.paged_decode_prefix_workspace_size(60, q_len, 28, 4, 128, 16, 1, 3000, kw["max_context_len"]), "cuda")
+    outs = [torch.empty_like(qs[0]) for _ in range(40)]
+    for i, out in enumerate(outs):
+        call(qs[i % 4], out=out, workspace=ws)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, alone[i % 4]), i
+
+
 def test_bad_blocks_are_reported_and_nothing_else_is_read():
     p = problem([3], [100], [40, 40, 40], 1, 8, 2, 128, 16, seed=12)
     q, kc, vc, ptab, plens, starts, bt, lens = p
