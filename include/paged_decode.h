@@ -591,7 +591,7 @@ pkd_status paged_kv_append(const void* k_new, const void* v_new, const int32_t* 
  *   positions      device int32 [num_tokens] or NULL: rotation positions that
  *                  differ from the logical ones (a shared prefix in front)
  *   q_out          device fp16, tokens q_out_stride elements apart, 16-byte
- *                  aligned; may be q itself.  With num_q_heads 0, q and q_out
+ *                  aligned; may be q itself (with q's stride).  With num_q_heads 0, q and q_out
  *                  may be NULL
  *   head_dim       a multiple of 16, at most 512; rotary_dim a multiple of 16
  *                  in [0, head_dim]
@@ -636,7 +636,8 @@ pkd_status paged_kv_append_rope_fp8(const void* q, const void* k_new, const void
  *   q, out         device fp16 [num_seqs][q_len][num_q_heads][head_dim]
  *   prefix_tables  device int32 [num_groups][max_prefix_blocks], prefix_lens
  *                  device int32 [num_groups], each in [0, max_prefix_len]; a
- *                  prefix may end inside a block
+ *                  prefix may end inside a block.  max_prefix_len and
+ *                  max_context_len are at most 2^30
  *   group_starts   device int32 [num_groups + 1], ascending: group y holds
  *                  sequences group_starts[y] .. group_starts[y + 1] - 1;
  *                  sequences in no group have no prefix.  With num_groups 0
@@ -740,7 +741,8 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
  *                  entry (paged_kv_block_select's lists are).  An entry that
  *                  breaks this, lies outside the sequence or names a block
  *                  outside the pool is skipped (PKD_DEVERR_BAD_BLOCK)
- *   list_lens      device int32 [num_seqs][num_kv_heads], each at most max_listed
+ *   list_lens      device int32 [num_seqs][num_kv_heads], each at most max_listed;
+ *                  max_listed * block_size is at most 2^30
  *   workspace      paged_decode_blocks_workspace_size(...) bytes, 256-byte
  *                  aligned (NULL where that is 0)
  *   other arguments as for paged_decode_attention_ex

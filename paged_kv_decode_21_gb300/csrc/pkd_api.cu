@@ -621,7 +621,7 @@ pkd_status check_inputs(const void* q, const void* k_cache, const void* v_cache,
 
 extern "C" {
 
-int pkd_version(void) { return 1 * 10000 + 1 * 100 + 0; }
+int pkd_version(void) { return 1 * 10000 + 2 * 100 + 0; }
 
 const char* pkd_status_string(int status) {
   switch (status) {
@@ -1205,6 +1205,7 @@ constexpr int kSharedSplit = 9;       // partitions per unit from which it takes
 constexpr int kFewSharedRows = 64;    // rows per group and kv head up to which,
 constexpr int kShortPrefix = 1024;    // with prefixes up to this long, the mma.sync kernel serves them
 constexpr int kMinListedPartition = 64;  // the shortest partition of a block list
+constexpr int kMaxPartTokens = 1 << 30;  // the longest prefix, list or context: partition ends stay in 32 bits
 
 // A shared prefix of up to max_prefix_len tokens: chunks of a group's query
 // rows times the kv heads are the units; each reads the prefix in as many
@@ -1228,12 +1229,13 @@ PartPlan plan_shared(const Shape& s, int q_len, int num_groups, int max_prefix_l
   int sms = sm_count();
   if (sms <= 0) sms = 148;
   // chunks of all groups: with one group as many as its rows need, else at
-  // most the full ones and a rest for each group
+  // most the full ones and a rest for each group that is not empty
+  const int groups = std::min(num_groups, s.num_seqs);
   auto chunks_of = [&](long long n, int per) {
-    return num_groups == 1 ? (n + per - 1) / per : n / per + num_groups;
+    return groups == 1 ? (n + per - 1) / per : n / per + groups;
   };
   long long chunks, slots;
-  if (!tc_supports(s, kv_fp8) || (rows <= kFewSharedRows * num_groups && max_prefix_len <= kShortPrefix)) {
+  if (!tc_supports(s, kv_fp8) || (rows <= (long long)kFewSharedRows * groups && max_prefix_len <= kShortPrefix)) {
     p.variant = PKD_VARIANT_TMA_MMA;
     chunks = chunks_of(tokens, 16 / G);
     slots = (long long)sms * path_stream(p.variant, s.head_dim, G, kv_fp8 ? 1 : 2, false).ctas_per_sm;
@@ -1375,6 +1377,7 @@ pkd_status prefix_impl(const void* q, const void* k_cache, const void* v_cache, 
   pkd_status st = check_shape(s);
   if (st != PKD_OK) return st;
   if (q_len < 1 || num_groups < 0 || max_prefix_len < 0) return PKD_ERR_SHAPE;
+  if (max_prefix_len > kMaxPartTokens || max_context_len > kMaxPartTokens) return PKD_ERR_SHAPE;
   if (num_groups > 0 && (max_prefix_blocks <= 0 || (long long)max_prefix_len > (long long)max_prefix_blocks * block_size))
     return PKD_ERR_SHAPE;
   if (!std::isfinite(scale)) return PKD_ERR_SHAPE;
@@ -1437,8 +1440,8 @@ pkd_status prefix_impl(const void* q, const void* k_cache, const void* v_cache, 
   // or latency, starts first; the own contexts', bound by HBM, starts as soon as
   // that one's CTAs have started, and takes the SMs it leaves and then the ones
   // it frees.  (It reads nothing that grid writes, and that grid starts after
-  // all work before the call.)  The other order: 128 -> 118 us for 256 x 28
-  // query heads over 32768 shared tokens.
+  // all work before the call.)  256 x 28 query heads over 32768 shared tokens:
+  // 121 us; with the own contexts first, 129; one after the other, 139.
   if (pre.np > 0 && (st = run(pre, static_cast<unsigned char*>(workspace) + own_bytes, true)) != PKD_OK) return st;
   if (own.np > 0 && (st = run(own, workspace, false)) != PKD_OK) return st;
   return launch_merge(head_dim, m, stream);
@@ -1449,7 +1452,8 @@ pkd_status blocks_impl(const void* q, const void* k_cache, const void* v_cache, 
                        int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
                        int max_blocks_per_seq, int max_listed, float scale, int kv_fp8, float k_scale, float v_scale,
                        void* workspace, size_t workspace_bytes, int* error_word, cudaStream_t stream) {
-  if (max_listed <= 0 || block_size <= 0 || (long long)max_listed * block_size > 0x7fffffffLL) return PKD_ERR_SHAPE;
+  if (max_listed <= 0 || block_size <= 0 || (long long)max_listed * block_size > kMaxPartTokens)
+    return PKD_ERR_SHAPE;
   // the list is a context of its own, as long as max_listed blocks
   const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, std::max(1, max_listed),
                 max_listed * block_size};
@@ -1514,6 +1518,8 @@ size_t paged_decode_prefix_workspace_size(int num_seqs, int q_len, int num_q_hea
                                           int block_size, int num_groups, int max_prefix_len, int max_context_len) {
   const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, 1, 1 << 30, max_context_len};
   if (check_shape(s) != PKD_OK || q_len < 1 || num_groups < 0 || max_prefix_len < 0) return 0;
+  if (max_prefix_len > kMaxPartTokens || max_context_len > kMaxPartTokens) return 0;
+  if ((long long)num_seqs * q_len * num_q_heads > 0x7fffffffLL) return 0;
   size_t most = 0;
   for (const int fp8 : {0, 1}) {  // the plan may differ by cache type
     const PartPlan own = plan_own(s, q_len, fp8), pre = plan_shared(s, q_len, num_groups, max_prefix_len, fp8);
@@ -1527,7 +1533,8 @@ size_t paged_decode_prefix_workspace_size(int num_seqs, int q_len, int num_q_hea
 
 size_t paged_decode_blocks_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                           int block_size, int max_listed) {
-  if (max_listed <= 0 || block_size <= 0 || (long long)max_listed * block_size > 0x7fffffffLL) return 0;
+  if (max_listed <= 0 || block_size <= 0 || (long long)max_listed * block_size > kMaxPartTokens) return 0;
+  if ((long long)num_seqs * num_q_heads > 0x7fffffffLL) return 0;
   const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, 1, max_listed, max_listed * block_size};
   if (check_shape(s) != PKD_OK) return 0;
   size_t most = 0;

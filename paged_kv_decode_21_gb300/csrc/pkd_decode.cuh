@@ -127,7 +127,7 @@ __device__ __forceinline__ bool find_group_chunk(const int32_t* group_starts, in
       out->first = (x - before - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, c, l))) * per;
       out->tokens = __shfl_sync(0xffffffffu, n, l);
       out->base = __shfl_sync(0xffffffffu, s, l) * q_len;
-      return true;
+      return out->first >= 0 && out->first < out->tokens;  // (fails only where starts that are no groups overflow)
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }

@@ -47,6 +47,8 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
     return PKD_ERR_ALIGN;
   if (num_q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8 != 0 || q_out_stride % 8 != 0))
     return PKD_ERR_ALIGN;
+  // rotated in place, every token's row is its own
+  if (num_q_heads > 0 && num_tokens > 1 && q == q_out && q_stride != q_out_stride) return PKD_ERR_SHAPE;
   pkd::RopeAppendParams p{};
   p.q = static_cast<const __half*>(q);
   p.k = static_cast<const __half*>(k_new);
@@ -152,6 +154,7 @@ pkd_status paged_kv_block_bounds(const void* k_cache, const int32_t* block_table
   // on; from token 0 when no starts are given
   p.grid_blocks = start_lens ? (int)(((long long)max_new_tokens + block_size - 2) / block_size + 1)
                              : (int)(((long long)max_new_tokens + block_size - 1) / block_size);
+  p.grid_blocks = std::min(p.grid_blocks, max_blocks_per_seq);
   // A warp's kv heads: up to eight, whose tiles stream one behind the other,
   // while 32 warps an SM remain (32 prompts of up to 8192 tokens, 8 heads: 78
   // us, against 128 with one head a warp); one where the call is small.

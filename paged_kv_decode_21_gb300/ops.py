@@ -559,6 +559,18 @@ def _raw_stream(stream, dev: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _used_on(stream, *tensors) -> None:
+    """Tensors allocated here for a call on a given stream: their memory is not handed out again
+    before that stream has passed the call."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _word(error_word, dev: int):
     """The error word's address: the first element of an int32 tensor."""
     if error_word is None:
@@ -627,6 +639,7 @@ def _append_rope(name, fp8, q, k_new, v_new, rope_table, block_tables, context_l
         qp, qs = _heads(q, "q", dev, shape)
         if q_out is None:
             q_out = torch.empty(shape, dtype=_F16, device=q.device)
+            _used_on(stream, q_out)
         op, os_ = _heads(q_out, "q_out", dev, shape)
     shape = rope_table.shape
     rp = _on(rope_table, "rope_table", _F32, shape, dev)
@@ -699,10 +712,12 @@ def _attention_prefix(name, fp8, q, k_cache, v_cache, prefix_tables, prefix_lens
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     if out is None:
         out = torch.empty_like(q)
+        _used_on(stream, out)
     op = _on(out, "out", _F16, qshape, dev)
     mp, mc = _max_len(prefix_lens, max_prefix_len), _max_len(context_lens, max_context_len)
     if workspace is None:
         workspace = alloc_workspace(paged_decode_prefix_workspace_size(B, QL, Hq, Hkv, D, BS, Y, mp, mc), q.device)
+        _used_on(stream, workspace)
     ws, wsb = _space(workspace, dev)
     fn = _lib.paged_decode_attention_prefix_fp8 if fp8 else _lib.paged_decode_attention_prefix
     st = fn(qp, kc, vc, pt, pl, gs, bt, cl, op, B, QL, Y, Hq, Hkv, D, BS, NB, MP, MB, mp, mc, scale, *scales, ws, wsb,
@@ -780,8 +795,10 @@ def paged_kv_block_select(q, bounds, block_tables, context_lens, max_selected, b
     bt, MB = _table(block_tables, "block_tables", B, dev)
     if block_lists is None:
         block_lists = torch.empty((B, Hkv, max(K, 0)), dtype=_I32, device=q.device)
+        _used_on(stream, block_lists)
     if list_lens is None:
         list_lens = torch.empty((B, Hkv), dtype=_I32, device=q.device)
+        _used_on(stream, list_lens)
     st = _lib.paged_kv_block_select(qp, bo, bt, cl, _on(block_lists, "block_lists", _I32, (B, Hkv, K), dev),
                                     _on(list_lens, "list_lens", _I32, (B, Hkv), dev), B, Hq, Hkv, D, int(block_size),
                                     NB, MB, _max_len(context_lens, max_context_len), K, int(sink_blocks),
@@ -817,9 +834,11 @@ def _attention_blocks(name, fp8, q, k_cache, v_cache, block_tables, context_lens
     ll = _on(list_lens, "list_lens", _I32, (B, Hkv), dev)
     if out is None:
         out = torch.empty_like(q)
+        _used_on(stream, out)
     op = _on(out, "out", _F16, qshape, dev)
     if workspace is None:
         workspace = alloc_workspace(paged_decode_blocks_workspace_size(B, Hq, Hkv, D, BS, K), q.device)
+        _used_on(stream, workspace)
     ws, wsb = _space(workspace, dev)
     fn = _lib.paged_decode_attention_blocks_fp8 if fp8 else _lib.paged_decode_attention_blocks
     st = fn(qp, kc, vc, bt, cl, bl, ll, op, B, Hq, Hkv, D, BS, NB, MB, K, scale, *scales, ws, wsb,

@@ -32,6 +32,7 @@ def test_append_rope(L, fp8):
     assert call(st=None, T=5) == 2                                    # runs of one length need a whole number
     assert call(qs=1016) == 2 and call(ks=248) == 2 and call(os_=0) == 2   # a token's heads do not fit
     assert call(qs=1028) == 4 and call(ks=260) == 4                   # 16-byte steps
+    assert call(qs=2048) == 2                                         # in place, rows would meet other tokens'
     for name in ("k", "v", "bt", "cl", "kc", "vc", "q", "qo", "tab"):
         assert call(**{name: None}) == 1, name
         assert call(**{name: ODD}) == 4, name
@@ -54,6 +55,8 @@ def test_prefix(L, fp8):
     assert call(B=0) == 0
     assert call(B=-1) == 2 and call(QL=0) == 2 and call(Y=-1) == 2 and call(mp=-1) == 2
     assert call(mp=129) == 2 and call(mc=129) == 2 and call(MP=0) == 2
+    assert call(mp=(1 << 30) + 1, MP=1 << 27) == 2 and call(mc=(1 << 30) + 1, MB=1 << 27) == 2
+    assert call(QL=1 << 29) == 2                                      # rows past 32 bits
     assert call(Hq=7) == 2 and call(Hq=18) == 3 and call(D=96) == 3 and call(BS=8) == 3
     assert call(scale=float("nan")) == 2
     for i in range(9):
@@ -67,6 +70,11 @@ def test_prefix(L, fp8):
     assert size > 0 and call(wsb=size // 4) == 5
     assert L.paged_decode_prefix_workspace_size(4, 1, 8, 2, 128, 16, 0, 0, 0) == 0
     assert L.paged_decode_prefix_workspace_size(4, 0, 8, 2, 128, 16, 2, 100, 100) == 0
+    assert L.paged_decode_prefix_workspace_size(4, 1, 8, 2, 128, 16, 2, (1 << 30) + 1, 100) == 0
+    assert L.paged_decode_prefix_workspace_size(4, 1 << 29, 8, 2, 128, 16, 2, 100, 100) == 0
+    # groups past the batch's sequences are empty: they cost no workspace, and their number no overflow
+    assert (L.paged_decode_prefix_workspace_size(4, 1, 8, 2, 128, 16, 0x7fffffff, 100, 100)
+            == L.paged_decode_prefix_workspace_size(4, 1, 8, 2, 128, 16, 4, 100, 100))
 
 
 def test_bounds(L):
@@ -106,7 +114,7 @@ def test_blocks(L, fp8):
         return L.paged_decode_attention_blocks(*a, ws, wsb, err, None)
     assert call(B=0) == 0
     assert call(K=0) == 2 and call(MB=0) == 2 and call(Hq=7) == 2 and call(scale=float("inf")) == 2
-    assert call(K=1 << 28) == 2
+    assert call(K=1 << 28) == 2 and call(K=(1 << 26) + 1) == 2
     assert call(Hq=18) == 3 and call(D=96) == 3 and call(BS=8) == 3
     for i in range(8):
         assert call(p={i: None}) == 1 and call(p={i: ODD}) == 4, i

@@ -197,6 +197,44 @@ def test_negative_and_zero_scales(fp8):
         check(out, ref, mag, 320, values(p[2]).abs().max().item() * vs)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("before,size,after", [(0, 3, 61), (70, 40, 5), (1500, 9, 600)])
+def test_more_groups_than_sequences(before, size, after, fp8):
+    # a table of fixed size whose other groups are empty
+    plens = [17] * before + [1500] + [300] * after
+    p = problem([0] * before + [size] + [0] * after, plens, [30 + i for i in range(size)], 1, 8, 2, 128, 16,
+                seed=19, fp8=fp8)
+    run_and_check(p, 16, fp8)
+
+
+@pytest.mark.parametrize("which", ["torch", "raw"])
+def test_temporaries_of_a_call_on_another_stream_stay_its_own(which, monkeypatch):
+    """The workspace allocated inside a call on a given stream is not handed out again while that
+    stream has yet to run the call."""
+    p = problem([40], [1000], [200] * 40, 1, 8, 2, 128, 16, seed=20)
+    want = ops.paged_decode_attention_prefix(*p, 0.1, max_prefix_len=1000, max_context_len=200)
+    spaces, alloc = [], ops.alloc_workspace
+
+    def noted(n, dev):
+        t = alloc(n, dev)
+        spaces.append((t.data_ptr(), n))
+        return t
+
+    monkeypatch.setattr(ops, "alloc_workspace", noted)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # 0.1 s
+    out = ops.paged_decode_attention_prefix(*p, 0.1, max_prefix_len=1000, max_context_len=200,
+                                            stream=side if which == "torch" else side.cuda_stream)
+    later = [torch.empty(spaces[0][1] + 256, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not side.query()
+    at, n = spaces[0]
+    assert all(x.data_ptr() + x.numel() <= at or at + n <= x.data_ptr() for x in later)
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_groups_that_reach_past_the_batch_stay_inside_it():
     # group starts past the batch (or below zero) are cut to it
     p = list(problem([5, 3], [200, 100], [30] * 8, 1, 8, 2, 128, 16, seed=16))
