@@ -96,20 +96,21 @@ enum KeySource : int {
 // Chunk x of a grid over groups of sequences: the chunks of `per` query
 // tokens of group 0, then those of group 1, and so on (q_len query tokens, or
 // whatever else is counted, per sequence).  Sets the group, the chunk's first
-// query token inside it, the group's query tokens and its first one over the
-// whole batch; false when x is past the last chunk.  Every lane of the calling
+// query token inside it, the group's query tokens, its first one over the
+// whole batch and its shared length (lens, read along with the starts); false when x is past the last chunk.  Every lane of the calling
 // warp gets the same answer.
 struct GroupChunk {
-  int group, first, tokens, base;
+  int group, first, tokens, base, len;
 };
-__device__ __forceinline__ bool find_group_chunk(const int32_t* group_starts, int num_groups, int num_seqs,
-                                                 int q_len, int per, int x, GroupChunk* out) {
+__device__ __forceinline__ bool find_group_chunk(const int32_t* group_starts, const int32_t* lens, int num_groups,
+                                                 int num_seqs, int q_len, int per, int x, GroupChunk* out) {
   const int lane = threadIdx.x & 31;
   int before = 0;  // chunks of the groups before this round's 32
   for (int y0 = 0; y0 < num_groups; y0 += 32) {
     const int y = y0 + lane;
-    int s = 0, n = 0;
+    int s = 0, n = 0, len = 0;
     if (y < num_groups) {
+      len = lens[y];
       s = min(max(group_starts[y], 0), num_seqs);
       n = max(min(group_starts[y + 1], num_seqs) - s, 0) * q_len;
     }
@@ -124,6 +125,7 @@ __device__ __forceinline__ bool find_group_chunk(const int32_t* group_starts, in
     if (past) {
       const int l = __ffs(past) - 1;
       out->group = y0 + l;
+      out->len = __shfl_sync(0xffffffffu, len, l);
       out->first = (x - before - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, c, l))) * per;
       out->tokens = __shfl_sync(0xffffffffu, n, l);
       out->base = __shfl_sync(0xffffffffu, s, l) * q_len;

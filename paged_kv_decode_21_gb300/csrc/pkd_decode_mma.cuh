@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
   if constexpr (SRC == kShared) {
     // (b, above, is 0: the grid's rows are chunks of all groups)
     GroupChunk ch;
-    if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len, QC, qc, &ch)) {
+    if (!find_group_chunk(P.group_starts, P.context_lens, P.num_groups, P.num_seqs, P.q_len, QC, qc, &ch)) {
       await_grid_before(P);
       return;
     }

@@ -78,7 +78,7 @@ struct SharedTcTraits {
   // that widen, at 128 registers and a few spilled bytes
   static constexpr int WIDENERS = F8 ? 2 : 0;  // per ring
   static constexpr int THREADS = F8 ? 512 : 384;
-  static constexpr int TAIL = NBAR * 8 + 8 + NS * 4;
+  static constexpr int TAIL = NBAR * 8 + 8 + NS * 4 + 4;
   static constexpr int SMEM_BYTES = MAIN + ((TAIL + 15) / 16) * 16;
   static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
   static_assert(2 * SMEM_BYTES > 227 * 1024, "never two: a second one's tensor-memory allocation would wait");
@@ -119,13 +119,14 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2 + (F8 ? 2 * NS : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* vbad = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);  // [NS]
+  volatile int* bad_flag = reinterpret_cast<volatile int*>(tmem_slot + 2 + NS);
 
   // work item: row chunk fastest (its CTAs read the same K and V), then partition, then kv head
   const int G = P.num_q_heads / P.num_kv_heads;
   const int rest = blockIdx.x / P.q_chunks;
   const int j = rest % P.max_partitions, g = rest / P.max_partitions;
   GroupChunk ch;
-  if (!find_group_chunk(P.group_starts, P.num_groups, P.num_seqs, P.q_len * G, P.rows_per_chunk,
+  if (!find_group_chunk(P.group_starts, P.context_lens, P.num_groups, P.num_seqs, P.q_len * G, P.rows_per_chunk,
                         blockIdx.x % P.q_chunks, &ch))
     return;
   const int rows = min(P.rows_per_chunk, ch.tokens - ch.first);
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     const int r = ch.first + rr;
     return (tok0 + r / G) * Hq + g * G + r % G;
   };
-  int L = P.context_lens[ch.group];
+  int L = ch.len;
   if (L > P.max_blocks_per_seq * BS) {
     if (threadIdx.x == 0) record_error(P.error_word, kErrBadBlock);
     L = P.max_blocks_per_seq * BS;
@@ -173,33 +174,49 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       mbar_init(&drain[x], 1);
     }
     *abort_flag = 0;
+    *bad_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == T::W_MMA) {
-    tmem_alloc(tmem_slot, T::TMEM_COLS);
-    tmem_relinquish();
-  }
-  if (warp < 8) {
-    // Q rows into the 64-dim halves of their tile, 128-byte swizzled; unused rows zero
-    const int rr = threadIdx.x;
-    const __half* qr = rr < rows ? P.q + out_row(rr) * D : nullptr;
-    unsigned char* dst = smem + T::Q_OFF + (rr / 128) * T::NH * T::QH + (rr % 128) * T::ROWB;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 v = qr ? *reinterpret_cast<const uint4*>(qr + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(dst + (c / 8) * T::QH + (((c % 8) ^ (rr % 8)) << 4)) = v;
+  __syncthreads();
+  // From here the copies run, beside the loading of Q by the softmax warps.
+  uint32_t tmem = 0;
+  bool any_bad = false;
+  if (warp < T::W_K) {
+    if (warp == T::W_MMA) {
+      tmem_alloc(tmem_slot, T::TMEM_COLS);
+      tmem_relinquish();
     }
-    fence_proxy_async_smem();
+    if (warp < 8) {
+      // Q rows into the 64-dim halves of their tile, 128-byte swizzled; unused rows
+      // zero.  The warp's 32 rows, one or two whole rows a load, all in flight.
+      constexpr int CPR = D / 8, RP = 32 / CPR;  // 16-byte chunks per row, rows per load
+      const int c = lane % CPR;
+      uint4 v[32 / RP];
+#pragma unroll
+      for (int i = 0; i < 32 / RP; ++i) {
+        const int rr = 32 * warp + RP * i + lane / CPR;
+        v[i] = rr < rows ? *reinterpret_cast<const uint4*>(P.q + out_row(rr) * D + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      // Whether any block id of the partition is bad: where none is, as always but
+      // for a caller's mistake, the softmax need not read the tiles' masks (a
+      // shared-memory read costs it over a hundred cycles a tile).
+      int wrong_id = 0;
+      for (int k = threadIdx.x; k < nblk; k += 256) wrong_id |= bt[k] < 0 || bt[k] >= P.num_blocks;
+      if (wrong_id) *bad_flag = 1;
+#pragma unroll
+      for (int i = 0; i < 32 / RP; ++i) {
+        const int rr = 32 * warp + RP * i + lane / CPR;
+        *reinterpret_cast<uint4*>(smem + T::Q_OFF + ((rr / 128) * T::NH + c / 8) * T::QH + (rr % 128) * T::ROWB +
+                                  (((c % 8) ^ (rr % 8)) << 4)) = v[i];
+      }
+      fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * T::W_K) : "memory");  // the softmax and issuing warps
+    tc_fence_after();
+    tmem = *tmem_slot;
+    any_bad = *bad_flag != 0;
   }
-  // Whether any block id of the partition is bad: where none is, as always but
-  // for a caller's mistake, the softmax need not read the tiles' masks (a
-  // shared-memory read costs it over a hundred cycles a tile).
-  int wrong_id = 0;
-  for (int k = threadIdx.x; k < nblk; k += T::THREADS) wrong_id |= bt[k] < 0 || bt[k] >= P.num_blocks;
-  tc_fence_before();
-  const bool any_bad = __syncthreads_or(wrong_id);
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp >= T::W_K) {
     // ------------------------------------------------------------ K, V tiles
@@ -483,20 +500,38 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     } else {
       tc_fence_after();
       // partials relative to the exact maximum mt; O and l to the shift m
-      const size_t pidx = (live ? out_row(rr) : 0) * P.max_partitions + j;
+      const uint32_t orow = live ? (uint32_t)out_row(rr) : 0u;
+      const size_t pidx = (size_t)orow * P.max_partitions + j;
       const float f = m == -INFINITY ? 0.f : ex2_approx(m - mt);
       const float fo = f * P.v_scale;
+      // O leaves through the row tile's part of Q's place (its last product is
+      // complete), 32 rows x CC columns a warp and pass, so that a store covers
+      // whole 128-byte lines of a row or two: a store of 16 bytes from each of
+      // 32 rows took 6 us for 256 rows in 140 CTAs at once.
+      constexpr int CC = 32 * T::NH, CPR = CC / 4;
+      unsigned char* stage = smem + T::Q_OFF + x * T::NH * T::QH + (warp & 3) * (T::NH * T::QH / 4);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        tmem_ld32(to + 32 * c, o);
-        tmem_ld_wait();
-        if (!live) continue;
-        float* dst = P.tmp_out + pidx * D + 32 * c;
+      for (int c0 = 0; c0 < D; c0 += CC) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<float4*>(dst + 4 * q) =
-              make_float4(o[4 * q] * fo, o[4 * q + 1] * fo, o[4 * q + 2] * fo, o[4 * q + 3] * fo);
+        for (int cc = 0; cc < CC; cc += 32) {
+          float o[32];
+          tmem_ld32(to + c0 + cc, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(stage + lane * 16 * CPR + (((cc / 4 + q) ^ (lane & 7)) << 4)) =
+                make_float4(o[4 * q] * fo, o[4 * q + 1] * fo, o[4 * q + 2] * fo, o[4 * q + 3] * fo);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < CPR; ++i) {
+          const int r = (32 * i + lane) / CPR, q = lane % CPR;
+          const uint32_t at = __shfl_sync(0xffffffffu, orow, r);
+          const float4 v = *reinterpret_cast<const float4*>(stage + r * 16 * CPR + ((q ^ (r & 7)) << 4));
+          if (32 * warp + r < rows)
+            *reinterpret_cast<float4*>(P.tmp_out + ((size_t)at * P.max_partitions + j) * D + c0 + 4 * q) = v;
+        }
+        __syncwarp();
       }
       if (live) {
         P.max_logits[pidx] = mt * 0.69314718055994530942f;
