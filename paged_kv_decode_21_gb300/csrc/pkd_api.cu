@@ -1207,6 +1207,44 @@ constexpr int kShortPrefix = 1024;    // with prefixes up to this long, the mma.
 constexpr int kMinListedPartition = 64;  // the shortest partition of a block list
 constexpr int kMaxPartTokens = 1 << 30;  // the longest prefix, list or context: partition ends stay in 32 bits
 
+// How many partitions, of at most `most`, for the shared-context kernel.  Its
+// CTAs take an SM each and hardly read; the own contexts' kernel, which is
+// bound by HBM, runs beside them on the SMs that are left, and takes all of
+// them afterwards.  So the partitions that fill the GPU are the fastest alone,
+// and fewer and longer ones, down to half, where the own contexts have much to
+// read.  Chosen is the least estimated time of the two and the merge, from what
+// was measured: a CTA takes 8 us and 0.74 a tile of 64 tokens (E4M3 0.93; 0.6
+// and 0.75 with 128 rows), the own kernel reads 42 KB/us an SM beside it and
+// 6.5 MB/us after it, up to 4 us after the SMs came free, contexts being 0.55
+// of their bound, and a partition of all rows costs its fp32 outputs twice at
+// 6 MB/us.
+//   64 x 32/8 heads, 4096 shared + up to 1024 own tokens: 37.6 us with four
+//   partitions, 44.2 with eight; 256 x 28/4, 32768 + up to 512: 113 with four,
+//   117 with five; without own contexts, five: 91.  (Below half the estimate
+//   is too rough: 128 x 28/4, 2 x 16384 + up to 4096: 126 with two of seven,
+//   117 with seven.)
+long long shared_split(const Shape& s, int q_len, int max_prefix_len, int kv_fp8, int rows, long long units, int sms,
+                       long long most) {
+  const double tile = rows > 128 ? (kv_fp8 ? 0.93 : 0.74) : (kv_fp8 ? 0.75 : 0.6);
+  const double own = 0.55 * s.num_seqs * s.max_context_len * s.num_kv_heads * s.head_dim * (kv_fp8 ? 2.0 : 4.0);
+  const double merge = (double)s.num_seqs * q_len * s.num_q_heads * s.head_dim * 8.0 / 6e6;
+  long long best = most;
+  double least = INFINITY;
+  for (long long np = (most + 1) / 2; np <= most; ++np) {
+    const long long tiles = ((max_prefix_len + np - 1) / np + 63) / 64;
+    const long long n = ((max_prefix_len + 63) / 64 + tiles - 1) / tiles;
+    const double t = 8.0 + tile * tiles;
+    const double busy = std::min<double>(sms, (double)units * n);
+    const double left = own - t * 42e3 * (sms - busy);
+    const double total = t + (left > 0.0 ? 4.0 * busy / sms + left / 6.5e6 : 0.0) + merge * n;
+    if (total < least) {
+      least = total;
+      best = np;
+    }
+  }
+  return best;
+}
+
 // A shared prefix of up to max_prefix_len tokens: chunks of a group's query
 // rows times the kv heads are the units; each reads the prefix in as many
 // partitions as fill the GPU's resident CTAs once, of kMinSmallGridPartition
@@ -1250,6 +1288,7 @@ PartPlan plan_shared(const Shape& s, int q_len, int num_groups, int max_prefix_l
   const long long units = chunks * s.num_kv_heads;
   long long np = std::max(1LL, slots / units);
   np = std::min<long long>(np, (max_prefix_len + kMinSmallGridPartition - 1) / kMinSmallGridPartition);
+  if (p.variant == kSharedTc) np = shared_split(s, q_len, max_prefix_len, kv_fp8, p.rows, units, sms, np);
   p.P = (int)round_up((size_t)((max_prefix_len + np - 1) / np), 64);
   p.np = (max_prefix_len + p.P - 1) / p.P;
   p.grid = units * p.np;

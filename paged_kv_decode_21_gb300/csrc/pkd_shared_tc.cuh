@@ -62,7 +62,9 @@ struct SharedTcTraits {
   static constexpr int TN = 64;          // tokens per tile
   static constexpr int NBT = TN / BS;    // cache blocks per tile
   static constexpr int NBOX = TN / 16;   // 16-row boxes per tile and half
-  static constexpr int NS = HD == 128 ? 4 : 8;  // stages of the K and of the V ring
+  // stages of the K and of the V ring.  (fp16 at D = 128: a fifth costs 4%, in
+  // the issuer's chain; E4M3: the widened tiles want it, 6%)
+  static constexpr int NS = HD == 64 ? 8 : KVB == 1 ? 5 : 4;
   static constexpr int ROWB = 128;       // bytes per swizzled row: 64 fp16
   static constexpr int QH = 128 * ROWB;  // one 64-dim half of a row tile's Q
   static constexpr int KVH = TN * ROWB;  // one 64-dim half of a K or V tile
@@ -191,12 +193,14 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       // zero.  The warp's 32 rows, one or two whole rows a load, all in flight.
       constexpr int CPR = D / 8, RP = 32 / CPR;  // 16-byte chunks per row, rows per load
       const int c = lane % CPR;
+      const uint32_t qrow = (uint32_t)out_row(min((int)threadIdx.x, rows - 1));
       uint4 v[32 / RP];
+      const __half* src[32 / RP];
 #pragma unroll
-      for (int i = 0; i < 32 / RP; ++i) {
-        const int rr = 32 * warp + RP * i + lane / CPR;
-        v[i] = rr < rows ? *reinterpret_cast<const uint4*>(P.q + out_row(rr) * D + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int i = 0; i < 32 / RP; ++i)
+        src[i] = P.q + (size_t)__shfl_sync(0xffffffffu, qrow, RP * i + lane / CPR) * D + 8 * c;
+#pragma unroll
+      for (int i = 0; i < 32 / RP; ++i) v[i] = *reinterpret_cast<const uint4*>(src[i]);
       // Whether any block id of the partition is bad: where none is, as always but
       // for a caller's mistake, the softmax need not read the tiles' masks (a
       // shared-memory read costs it over a hundred cycles a tile).
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
       for (int i = 0; i < 32 / RP; ++i) {
         const int rr = 32 * warp + RP * i + lane / CPR;
         *reinterpret_cast<uint4*>(smem + T::Q_OFF + ((rr / 128) * T::NH + c / 8) * T::QH + (rr % 128) * T::ROWB +
-                                  (((c % 8) ^ (rr % 8)) << 4)) = v[i];
+                                  (((c % 8) ^ (rr % 8)) << 4)) = rr < rows ? v[i] : make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
     }
