@@ -1207,26 +1207,46 @@ constexpr int kShortPrefix = 1024;    // with prefixes up to this long, the mma.
 constexpr int kMinListedPartition = 64;  // the shortest partition of a block list
 constexpr int kMaxPartTokens = 1 << 30;  // the longest prefix, list or context: partition ends stay in 32 bits
 
+// The own contexts behind a prefix: the automatic path and split of
+// paged_decode_attention_multi, in plain order.
+PartPlan plan_own(const Shape& s, int q_len, int kv_fp8) {
+  PartPlan p;
+  if (s.max_context_len <= 0 || s.num_seqs <= 0) return p;
+  p.variant = q_len > 1 ? auto_multi_path(s, q_len, kv_fp8) : PKD_VARIANT_TMA_MMA;
+  p.chunks = query_chunks(q_len, s.num_q_heads / s.num_kv_heads, p.variant);
+  const int P = auto_partition(s, p.variant, p.chunks);
+  const bool split = P > 0 && s.max_context_len > P;
+  p.P = split ? P : (int)round_up((size_t)s.max_context_len, 32);
+  p.np = split ? (s.max_context_len + P - 1) / P : 1;
+  p.grid = (long long)s.num_seqs * s.num_kv_heads * p.chunks * p.np;
+  return p;
+}
+
 // How many partitions, of at most `most`, for the shared-context kernel.  Its
 // CTAs take an SM each and hardly read; the own contexts' kernel, which is
-// bound by HBM, runs beside them on the SMs that are left, and takes all of
-// them afterwards.  So the partitions that fill the GPU are the fastest alone,
-// and fewer and longer ones, down to half, where the own contexts have much to
-// read.  Chosen is the least estimated time of the two and the merge, from what
-// was measured: a CTA takes 8 us and 0.74 a tile of 64 tokens (E4M3 0.93; 0.6
-// and 0.75 with 128 rows), the own kernel reads 42 KB/us an SM beside it and
-// 6.5 MB/us after it, up to 4 us after the SMs came free, contexts being 0.55
-// of their bound, and a partition of all rows costs its fp32 outputs twice at
-// 6 MB/us.
+// bound by HBM or by its CTAs' latency, runs beside them on the SMs that are
+// left, and takes all of them afterwards.  So the partitions that fill the GPU
+// are the fastest alone, and fewer and longer ones, down to half, where the own
+// contexts have much to do.  Chosen is the least estimated time of the two and
+// the merge, from what was measured: a CTA takes 8 us and 0.74 a tile of 64
+// tokens (E4M3 0.93; 0.6 and 0.75 with 128 rows); the own kernel reads 42 KB/us
+// an SM beside it and 6.5 MB/us after it, up to 4 us (tcgen05: 12, a CTA's time)
+// after the SMs came free, contexts being 0.55 of their bound and a CTA's start
+// and end as long as reading 28 KB (147); a partition of all rows costs its fp32
+// outputs twice at 6 MB/us.  `units` is the expected number.
 //   64 x 32/8 heads, 4096 shared + up to 1024 own tokens: 37.6 us with four
 //   partitions, 44.2 with eight; 256 x 28/4, 32768 + up to 512: 113 with four,
-//   117 with five; without own contexts, five: 91.  (Below half the estimate
-//   is too rough: 128 x 28/4, 2 x 16384 + up to 4096: 126 with two of seven,
-//   117 with seven.)
-long long shared_split(const Shape& s, int q_len, int max_prefix_len, int kv_fp8, int rows, long long units, int sms,
+//   117 with five; without own contexts, five: 91; 48 x 4 tokens x 28/4, E4M3,
+//   2 x 8192 + up to 512: 49 with four, 53.5 with five.  (Below half the
+//   estimate is too rough: 128 x 28/4, 2 x 16384 + up to 4096: 126 with two of
+//   seven, 117 with seven, 110 with four.)
+long long shared_split(const Shape& s, int q_len, int max_prefix_len, int kv_fp8, int rows, double units, int sms,
                        long long most) {
+  const PartPlan op = plan_own(s, q_len, kv_fp8);
+  const bool own_tc = op.variant == PKD_VARIANT_TCGEN05;
   const double tile = rows > 128 ? (kv_fp8 ? 0.93 : 0.74) : (kv_fp8 ? 0.75 : 0.6);
-  const double own = 0.55 * s.num_seqs * s.max_context_len * s.num_kv_heads * s.head_dim * (kv_fp8 ? 2.0 : 4.0);
+  const double own = 0.55 * s.num_seqs * s.max_context_len * s.num_kv_heads * s.head_dim * (kv_fp8 ? 2.0 : 4.0) +
+                     (op.np > 1 ? 0.75 : 1.0) * op.grid * (own_tc ? 147e3 : 28e3);
   const double merge = (double)s.num_seqs * q_len * s.num_q_heads * s.head_dim * 8.0 / 6e6;
   long long best = most;
   double least = INFINITY;
@@ -1234,9 +1254,9 @@ long long shared_split(const Shape& s, int q_len, int max_prefix_len, int kv_fp8
     const long long tiles = ((max_prefix_len + np - 1) / np + 63) / 64;
     const long long n = ((max_prefix_len + 63) / 64 + tiles - 1) / tiles;
     const double t = 8.0 + tile * tiles;
-    const double busy = std::min<double>(sms, (double)units * n);
+    const double busy = std::min<double>(sms, units * n);
     const double left = own - t * 42e3 * (sms - busy);
-    const double total = t + (left > 0.0 ? 4.0 * busy / sms + left / 6.5e6 : 0.0) + merge * n;
+    const double total = t + (left > 0.0 ? (own_tc ? 12.0 : 4.0) * busy / sms + left / 6.5e6 : 0.0) + merge * n;
     if (total < least) {
       least = total;
       best = np;
@@ -1288,25 +1308,13 @@ PartPlan plan_shared(const Shape& s, int q_len, int num_groups, int max_prefix_l
   const long long units = chunks * s.num_kv_heads;
   long long np = std::max(1LL, slots / units);
   np = std::min<long long>(np, (max_prefix_len + kMinSmallGridPartition - 1) / kMinSmallGridPartition);
-  if (p.variant == kSharedTc) np = shared_split(s, q_len, max_prefix_len, kv_fp8, p.rows, units, sms, np);
+  if (p.variant == kSharedTc) {
+    const double expected = groups == 1 ? (double)chunks : (double)rows / p.rows + 0.5 * groups;
+    np = shared_split(s, q_len, max_prefix_len, kv_fp8, p.rows, expected * s.num_kv_heads, sms, np);
+  }
   p.P = (int)round_up((size_t)((max_prefix_len + np - 1) / np), 64);
   p.np = (max_prefix_len + p.P - 1) / p.P;
   p.grid = units * p.np;
-  return p;
-}
-
-// The own contexts behind a prefix: the automatic path and split of
-// paged_decode_attention_multi, in plain order.
-PartPlan plan_own(const Shape& s, int q_len, int kv_fp8) {
-  PartPlan p;
-  if (s.max_context_len <= 0 || s.num_seqs <= 0) return p;
-  p.variant = q_len > 1 ? auto_multi_path(s, q_len, kv_fp8) : PKD_VARIANT_TMA_MMA;
-  p.chunks = query_chunks(q_len, s.num_q_heads / s.num_kv_heads, p.variant);
-  const int P = auto_partition(s, p.variant, p.chunks);
-  const bool split = P > 0 && s.max_context_len > P;
-  p.P = split ? P : (int)round_up((size_t)s.max_context_len, 32);
-  p.np = split ? (s.max_context_len + P - 1) / P : 1;
-  p.grid = (long long)s.num_seqs * s.num_kv_heads * p.chunks * p.np;
   return p;
 }
 
@@ -1469,6 +1477,7 @@ pkd_status prefix_impl(const void* q, const void* k_cache, const void* v_cache, 
       p.group_starts = group_starts;
       p.num_groups = num_groups;
       p.rows_per_chunk = plan.rows;
+      p.chunks_outer = plan.grid <= sm_count() ? 1 : 0;
     } else {
       p.after_grid = pre.np > 0 ? 1 : 0;
     }

@@ -82,6 +82,7 @@ struct DecodeParams {
   const int32_t* group_starts;  // [num_groups + 1]
   int num_groups;
   int rows_per_chunk;  // paged_shared_tc_kernel: query rows per chunk
+  int chunks_outer;    // paged_shared_tc_kernel: the grid runs over chunks slowest, not fastest
   int after_grid;  // launched as a programmatic dependent of a grid whose results it does not read: its last
                    // CTA awaits that grid, so that this one completes after it (await_grid_before)
 };

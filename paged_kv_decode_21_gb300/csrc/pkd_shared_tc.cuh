@@ -123,13 +123,19 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
   volatile uint32_t* vbad = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);  // [NS]
   volatile int* bad_flag = reinterpret_cast<volatile int*>(tmem_slot + 2 + NS);
 
-  // work item: row chunk fastest (its CTAs read the same K and V), then partition, then kv head
+  // Work item: row chunk fastest (its CTAs read the same K and V), then
+  // partition, then kv head.  Where all CTAs run at once the chunks go slowest:
+  // those past the last row, whose CTAs leave at once, are then the last CTAs
+  // and leave pairs of SMs (TPCs) free, not one SM here and there, because own
+  // contexts beside a CTA in its TPC slow it down by a third (48 x 4 x 28/4
+  // rows in two groups over 8192 E4M3 tokens: CTAs of 28 us, 37 so).
   const int G = P.num_q_heads / P.num_kv_heads;
-  const int rest = blockIdx.x / P.q_chunks;
+  const int others = P.max_partitions * P.num_kv_heads;
+  const int rest = P.chunks_outer ? blockIdx.x % others : blockIdx.x / P.q_chunks;
   const int j = rest % P.max_partitions, g = rest / P.max_partitions;
   GroupChunk ch;
   if (!find_group_chunk(P.group_starts, P.context_lens, P.num_groups, P.num_seqs, P.q_len * G, P.rows_per_chunk,
-                        blockIdx.x % P.q_chunks, &ch))
+                        P.chunks_outer ? blockIdx.x / others : blockIdx.x % P.q_chunks, &ch))
     return;
   const int rows = min(P.rows_per_chunk, ch.tokens - ch.first);
   const size_t tok0 = (size_t)(ch.base / G);  // the group's first query token over the batch
