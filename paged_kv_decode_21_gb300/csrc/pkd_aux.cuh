@@ -131,55 +131,77 @@ template <int D>
 __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(const MergeParams P) {
   constexpr int V = D / 32;
   constexpr int U = 8;  // partials in flight per lane
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kReduceRowsPerCta + (threadIdx.x >> 5);  // query token * Hq + head
-  if (row >= P.rows) return;
-  const int tok = row / P.num_q_heads, h = row % P.num_q_heads;
-  const int b = tok / P.q_len;
+  const bool live = row < P.rows;
   const MergeSource src[2] = {P.own, P.shared};
-  // The first 32 partials' statistics are requested along with the lengths
-  // that tell how many of them there are (places past that hold anything and
-  // are dropped), so that two rounds of memory latency remain, not five.
+  // How many partials of each source the row has, from the call's inputs: read
+  // while the grids before still run.
+  int n[2] = {0, 0};
+  if (live) {
+    const int tok = row / P.num_q_heads, h = row % P.num_q_heads;
+    const int b = tok / P.q_len;
+    long long own_tokens;
+    if (P.list_lens) {
+      const int g = h / (P.num_q_heads / P.num_kv_heads);
+      own_tokens = (long long)P.list_lens[(size_t)b * P.num_kv_heads + g] * P.block_size;
+    } else {
+      own_tokens = P.context_lens[b];
+    }
+    if (P.shared.o) {
+      int len = 0;
+      if (P.num_groups <= 32) {  // every group a lane: its start, its end's successor and its length at once
+        const int start = lane < P.num_groups ? P.group_starts[lane] : 0;
+        const int end = lane < P.num_groups ? P.group_starts[lane + 1] : 0;
+        const int sl = lane < P.num_groups ? P.shared_lens[lane] : 0;
+        const unsigned mine = __ballot_sync(0xffffffffu, lane < P.num_groups && start <= b && b < end);
+        if (mine) len = __shfl_sync(0xffffffffu, sl, __ffs(mine) - 1);
+      } else {
+        const int y = find_segment(P.group_starts, P.num_groups, b);
+        if (y < P.num_groups && P.group_starts[y] <= b) len = P.shared_lens[y];
+      }
+      len = max(len, 0);
+      n[1] = min((len + P.shared.part - 1) / P.shared.part, P.shared.np);
+    }
+    if (P.own.o && own_tokens > 0) n[0] = (int)min((own_tokens + P.own.part - 1) / P.own.part, (long long)P.own.np);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live || (P.skip_single && n[0] <= 1)) return;
+  auto load = [&](const float* p, float (&x)[V]) {
+    if constexpr (V == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(p);
+      x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(p);
+      x[0] = t.x; x[1] = t.y;
+    }
+  };
+  const float* o[2] = {src[0].o + (size_t)row * src[0].np * D + V * lane,
+                       src[1].o + (size_t)row * src[1].np * D + V * lane};
+  // Both sources' first 32 partials as one run, U vectors in flight; the first
+  // U are requested along with the statistics.
+  const int c0 = min(n[0], 32), all = c0 + min(n[1], 32);
+  float x[U][V];
+  auto request = [&](int e0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (e0 + u < all) load(e0 + u < c0 ? o[0] + (size_t)(e0 + u) * D : o[1] + (size_t)(e0 + u - c0) * D, x[u]);
+  };
   float m0[2], l0[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     m0[k] = -INFINITY;
     l0[k] = 0.f;
-    if (src[k].o && lane < src[k].np) {
+    if (lane < n[k]) {
       m0[k] = src[k].m[(size_t)row * src[k].np + lane];
       l0[k] = src[k].l[(size_t)row * src[k].np + lane];
     }
   }
-  long long own_tokens;
-  if (P.list_lens) {
-    const int g = h / (P.num_q_heads / P.num_kv_heads);
-    own_tokens = (long long)P.list_lens[(size_t)b * P.num_kv_heads + g] * P.block_size;
-  } else {
-    own_tokens = P.context_lens[b];
-  }
-  int n[2] = {0, 0};
-  if (P.shared.o) {
-    int len = 0;
-    if (P.num_groups <= 32) {  // every group a lane: its start, its end's successor and its length at once
-      const int start = lane < P.num_groups ? P.group_starts[lane] : 0;
-      const int end = lane < P.num_groups ? P.group_starts[lane + 1] : 0;
-      const int sl = lane < P.num_groups ? P.shared_lens[lane] : 0;
-      const unsigned mine = __ballot_sync(0xffffffffu, lane < P.num_groups && start <= b && b < end);
-      if (mine) len = __shfl_sync(0xffffffffu, sl, __ffs(mine) - 1);
-    } else {
-      const int y = find_segment(P.group_starts, P.num_groups, b);
-      if (y < P.num_groups && P.group_starts[y] <= b) len = P.shared_lens[y];
-    }
-    len = max(len, 0);
-    n[1] = min((len + P.shared.part - 1) / P.shared.part, P.shared.np);
-  }
-  if (P.own.o && own_tokens > 0) n[0] = (int)min((own_tokens + P.own.part - 1) / P.own.part, (long long)P.own.np);
-  if (P.skip_single && n[0] <= 1) return;
+  request(0);
   float M = -INFINITY;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (lane < n[k]) M = fmaxf(M, m0[k]);
+    M = fmaxf(M, m0[k]);
     for (int j = lane + 32; j < n[k]; j += 32) M = fmaxf(M, src[k].m[(size_t)row * src[k].np + j]);
   }
 #pragma unroll
@@ -193,24 +215,8 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(con
     w0[k] = lane < n[k] && m0[k] != -INFINITY ? __expf(m0[k] - M) : 0.f;
     if (lane < n[k]) Z = fmaf(w0[k], l0[k], Z);
   }
-  auto load = [&](const float* p, float (&x)[V]) {
-    if constexpr (V == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(p);
-      x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-    } else {
-      const float2 t = *reinterpret_cast<const float2*>(p);
-      x[0] = t.x; x[1] = t.y;
-    }
-  };
-  const float* o[2] = {src[0].o + (size_t)row * src[0].np * D + V * lane,
-                       src[1].o + (size_t)row * src[1].np * D + V * lane};
-  // both sources' first 32 as one run, U vectors in flight
-  const int c0 = min(n[0], 32), all = c0 + min(n[1], 32);
   for (int e0 = 0; e0 < all; e0 += U) {
-    float x[U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (e0 + u < all) load(e0 + u < c0 ? o[0] + (size_t)(e0 + u) * D : o[1] + (size_t)(e0 + u - c0) * D, x[u]);
+    if (e0 > 0) request(e0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int e = e0 + u;
@@ -235,7 +241,6 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(con
       }
       const int nj = min(32, n[k] - j0);
       for (int c = 0; c < nj; c += U) {
-        float x[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (c + u < nj) load(o[k] + (size_t)(j0 + c + u) * D, x[u]);

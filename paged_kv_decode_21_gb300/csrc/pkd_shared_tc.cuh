@@ -196,29 +196,28 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     }
     if (warp < 8) {
       // Q rows into the 64-dim halves of their tile, 128-byte swizzled; unused rows
-      // zero.  The warp's 32 rows, one or two whole rows a load, all in flight.
-      constexpr int CPR = D / 8, RP = 32 / CPR;  // 16-byte chunks per row, rows per load
+      // zero.  Asynchronous copies of the warp's 32 rows, one or two whole rows
+      // each, from a short loop: the code of a call is cold after the caches took
+      // its data, and unrolled loads took 3 us here.
+      constexpr int CPR = D / 8, RP = 32 / CPR;  // 16-byte chunks per row, rows per copy
       const int c = lane % CPR;
       const uint32_t qrow = (uint32_t)out_row(min((int)threadIdx.x, rows - 1));
-      uint4 v[32 / RP];
-      const __half* src[32 / RP];
-#pragma unroll
-      for (int i = 0; i < 32 / RP; ++i)
-        src[i] = P.q + (size_t)__shfl_sync(0xffffffffu, qrow, RP * i + lane / CPR) * D + 8 * c;
-#pragma unroll
-      for (int i = 0; i < 32 / RP; ++i) v[i] = *reinterpret_cast<const uint4*>(src[i]);
+      const __half* src = P.q + 8 * c;
+      const uint32_t dst = sbase + T::Q_OFF + ((warp / 4) * T::NH + c / 8) * T::QH + (warp % 4) * 32 * T::ROWB;
+#pragma unroll 1
+      for (int i = lane / CPR; i < 32; i += RP) {
+        const uint32_t at = __shfl_sync(0xffffffffu, qrow, i);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * T::ROWB + (((c % 8) ^ (i % 8)) << 4)),
+                     "l"(src + (size_t)at * D), "r"(32 * warp + i < rows ? 16 : 0)
+                     : "memory");
+      }
       // Whether any block id of the partition is bad: where none is, as always but
       // for a caller's mistake, the softmax need not read the tiles' masks (a
       // shared-memory read costs it over a hundred cycles a tile).
       int wrong_id = 0;
       for (int k = threadIdx.x; k < nblk; k += 256) wrong_id |= bt[k] < 0 || bt[k] >= P.num_blocks;
       if (wrong_id) *bad_flag = 1;
-#pragma unroll
-      for (int i = 0; i < 32 / RP; ++i) {
-        const int rr = 32 * warp + RP * i + lane / CPR;
-        *reinterpret_cast<uint4*>(smem + T::Q_OFF + ((rr / 128) * T::NH + c / 8) * T::QH + (rr % 128) * T::ROWB +
-                                  (((c % 8) ^ (rr % 8)) << 4)) = rr < rows ? v[i] : make_uint4(0u, 0u, 0u, 0u);
-      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
     }
     tc_fence_before();
