@@ -207,6 +207,15 @@ def test_more_groups_than_sequences(before, size, after, fp8):
     run_and_check(p, 16, fp8)
 
 
+@pytest.mark.parametrize("sizes,fp8", [([330], False), ([300], True), ([100, 0, 171, 30], False)])
+def test_more_row_chunks_than_sms(sizes, fp8):
+    # 8 kv heads x 20 and more chunks of rows: the shared part's grid takes more than one wave
+    B = sum(sizes)
+    p = problem(sizes, [1300 + 10 * y for y in range(len(sizes))], [4 + i % 30 for i in range(B)], 4, 32, 8, 128, 16,
+                seed=21, fp8=fp8)
+    run_and_check(p, 16, fp8)
+
+
 @pytest.mark.parametrize("which", ["torch", "raw"])
 def test_temporaries_of_a_call_on_another_stream_stay_its_own(which, monkeypatch):
     """The workspace allocated inside a call on a given stream is not handed out again while that
