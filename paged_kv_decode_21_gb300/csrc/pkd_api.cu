@@ -1201,9 +1201,9 @@ struct PartPlan {
 
 // The data path of paged_shared_tc_kernel, beside the pkd_variant values.
 constexpr int kSharedTc = 100;
-constexpr int kSharedSplit = 9;       // partitions per unit from which it takes chunks of 128 rows
-constexpr int kFewSharedRows = 64;    // rows per group and kv head up to which,
-constexpr int kShortPrefix = 1024;    // with prefixes up to this long, the mma.sync kernel serves them
+constexpr long long kFewSharedWork = 36 * 1024;  // 16-row tiles x tokens up to which the mma.sync kernel is the faster
+constexpr long long kHalfRowsWork = 36 * 1024;   // units x tokens up to which chunks are of 128 rows,
+constexpr int kHalfRowsUnits = 18;               // with so many partitions left for a unit of 256
 constexpr int kMinListedPartition = 64;  // the shortest partition of a block list
 constexpr int kMaxPartTokens = 1 << 30;  // the longest prefix, list or context: partition ends stay in 32 bits
 
@@ -1270,15 +1270,16 @@ long long shared_split(const Shape& s, int q_len, int max_prefix_len, int kv_fp8
 // partitions as fill the GPU's resident CTAs once, of kMinSmallGridPartition
 // tokens at least.  Two kernels:
 //  * the shared-context tcgen05 kernel, chunks of 256 rows (two tiles that
-//    share each K and V tile), or of 128 where 256 would leave every unit nine
-//    partitions or more: with so few units the longer chain of a CTA with two
-//    row tiles costs more than the second read (256 rows x 8 kv heads, 2500
-//    tokens: 24 against 32 us for the whole call; 512 rows, 8192 tokens: 47
-//    against 49; but 672 rows x 2 groups x 4, 8192 tokens: 80 against 70);
-//  * the mma.sync kernel's 16-row tiles, three CTAs per SM, for groups of up
-//    to 64 rows on average and prefixes of up to 1024 tokens, where a CTA's
-//    start is what counts (16 rows x 8, 1000 tokens: 15.7 against 17.2 us; 2500
-//    tokens: 17.9 against 16.6), and for E4M3 caches at head_dim 64.
+//    share each K and V tile), or of 128 where the units are few and the prefix
+//    too short for its partitions to fill the GPU with 256 (256 rows x 8 kv
+//    heads: 3000 tokens 23.1 us, with 128 rows 20.8; 5500: 23.7, 25.2; 8192:
+//    26.9, 30.5; 252 rows x 4: 5000 tokens 18.9, 17.4; 8192: 21.4, 19.0; but 945
+//    rows x 8, 981 tokens: 27.5, 30.3);
+//  * the mma.sync kernel's 16-row tiles, three CTAs per SM, where there is
+//    little to do, a CTA an SM, and a CTA's start is what counts (16 rows x 8: 1000 tokens
+//    10.3 against 14.7 us, 4096: 14.0, 14.5; 64 rows x 8: 1000 tokens 12.9,
+//    14.4, 1500: 15.2, 14.4; 96 rows x 8: 300 tokens 11.0, 12.1, 1000: 15.9,
+//    13.9; 225 rows x 32, 44 tokens, three CTAs an SM: 22.9, 19.3), and for E4M3 caches at head_dim 64.
 PartPlan plan_shared(const Shape& s, int q_len, int num_groups, int max_prefix_len, int kv_fp8) {
   PartPlan p;
   if (max_prefix_len <= 0 || num_groups <= 0 || s.num_seqs <= 0) return p;
@@ -1293,15 +1294,17 @@ PartPlan plan_shared(const Shape& s, int q_len, int num_groups, int max_prefix_l
     return groups == 1 ? (n + per - 1) / per : n / per + groups;
   };
   long long chunks, slots;
-  if (!tc_supports(s, kv_fp8) || (rows <= (long long)kFewSharedRows * groups && max_prefix_len <= kShortPrefix)) {
+  chunks = chunks_of(tokens, 16 / G);
+  if (!tc_supports(s, kv_fp8) ||
+      (chunks * s.num_kv_heads <= sms && chunks * s.num_kv_heads * max_prefix_len <= kFewSharedWork)) {
     p.variant = PKD_VARIANT_TMA_MMA;
-    chunks = chunks_of(tokens, 16 / G);
     slots = (long long)sms * path_stream(p.variant, s.head_dim, G, kv_fp8 ? 1 : 2, false).ctas_per_sm;
   } else {
     p.variant = kSharedTc;
     slots = sms;
     p.rows = pkd::kSharedRowsPerCta;
-    if (chunks_of(rows, p.rows) * s.num_kv_heads * kSharedSplit <= slots) p.rows /= 2;
+    const long long wide = chunks_of(rows, p.rows) * s.num_kv_heads;
+    if (wide * kHalfRowsUnits <= slots && wide * max_prefix_len <= kHalfRowsWork) p.rows /= 2;
     chunks = chunks_of(rows, p.rows);
   }
   p.chunks = (int)chunks;
