@@ -23,12 +23,15 @@
 // What bounds it.  Per 64 tokens both row tiles together need 512 cycles of
 // tensor math for Q K^T and 512 for P V.  Q K^T with both operands in shared
 // memory reads 6 KiB per 32-cycle step at N = 64, so it takes 48; with that,
-// 1280 cycles; measured 1700-1750 (256 x 7 rows over 32768 tokens, 4 kv heads:
-// 97 us, 1.25 PFLOP/s, 58% of the tensor cycles).  The rest is the chain
+// 1280 cycles; measured 0.74 us in a long prefix (E4M3 0.93), 1.45-1.5 thousand
+// cycles: 256 x 7 rows over 32768 tokens, 4 kv heads, 112 CTAs of 128 tiles: 106
+// us, the tensor pipe busy 67% of their cycles.  The rest is the chain
 // P -> P V -> free S buffer -> Q K^T of one issuing warp, in which every test
 // of a barrier takes over a hundred cycles while the MMAs stream operands from
 // shared memory.  (One 128-token S buffer per row tile, a third less shared-
-// memory traffic but S, softmax and P V in one chain: 2450 per 64 tokens.)
+// memory traffic but S, softmax and P V in one chain, took 1.4 times the time.)
+// A CTA's start and end take 8 us: the group's lengths 1.1, the first tiles and
+// Q 4, the last 64 tokens' chain and the outputs 3.
 //
 // Roles:
 //   warps 0-3, 4-7  softmax of tile A, B: one thread per row, as in
