@@ -548,7 +548,7 @@ def _device(t, name: str) -> int:
     if _lib is None:
         lib()
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
     return dev
 
