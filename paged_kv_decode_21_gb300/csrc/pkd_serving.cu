@@ -86,6 +86,9 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   return launched();
 }
 
+// Dynamic shared memory of the choice among `blocks` blocks: scores, a bit per block.
+constexpr int select_smem(int blocks) { return 4 * (blocks + (blocks + 31) / 32) + 16; }
+
 pkd_status check_blocks(int num_seqs, int num_kv_heads, int head_dim, int block_size, int num_blocks,
                         int max_blocks_per_seq) {
   if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
@@ -230,7 +233,7 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
     sms = 148;
   const long long rows = (long long)num_seqs * num_kv_heads;
   const int tiles = (max_blocks + 15) / 16;
-  const int smem = 4 * (max_blocks + (max_blocks + 31) / 32) + 16;  // scores, a bit per block
+  const int smem = select_smem(max_blocks);
   const bool narrow = rows > 2LL * sms;
   const int most = smem <= 64 * 1024 ? pkd::kSelMaxCluster : 8;
   p.cluster = 1;
@@ -245,7 +248,11 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   auto* fn = kv_fp8 ? (head_dim == 128 ? PKD_SELECT(128, 1) : PKD_SELECT(64, 1))
                     : (head_dim == 128 ? PKD_SELECT(128, 2) : PKD_SELECT(64, 2));
 #undef PKD_SELECT
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // (The attribute belongs to the kernel, not to the call: what the largest call
+  // needs, the same for all, so that a call of another host thread in between
+  // changes nothing.)
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, select_smem(PKD_MAX_SELECT_BLOCKS)) !=
+      cudaSuccess)
     return PKD_ERR_LAUNCH;
   if (p.cluster > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return PKD_ERR_LAUNCH;
