@@ -7,6 +7,7 @@ stream.  There is no fallback: if the library is missing, loading fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -559,16 +560,34 @@ def _raw_stream(stream, dev: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tensors allocated here for a call on a given stream: their memory is not handed out again
-    before that stream has passed the call."""
+@contextlib.contextmanager
+def _behind(stream, dev: int):
+    """Make ``stream`` the current one where it is given: tensors allocated inside get memory of that stream's
+    own pool (memory freed behind work that is still pending on the caller's current stream is not written by
+    the call, nor the call's written by that work), and reads of lengths wait for what the stream has to run."""
     if stream is None:
+        yield
         return
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        yield
+
+
+def _returned(stream, dev: int, *tensors) -> None:
+    """Results allocated for a given stream: their memory is not handed out again before the caller's current
+    stream, which goes on with them, has passed where they are freed."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(dev))
+
+
+def _longest(lens, most, stream, dev: int) -> int:
+    """The host's bound of ``lens``, or their maximum as the given stream leaves them."""
+    if most is not None:
+        return int(most)
+    with _behind(stream, dev):
+        return _max_len(lens, None)
 
 
 def _word(error_word, dev: int):
@@ -638,8 +657,9 @@ def _append_rope(name, fp8, q, k_new, v_new, rope_table, block_tables, context_l
         shape = (T, Hq, D)
         qp, qs = _heads(q, "q", dev, shape)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=_F16, device=q.device)
-            _used_on(stream, q_out)
+            with _behind(stream, dev):
+                q_out = torch.empty(shape, dtype=_F16, device=q.device)
+            _returned(stream, dev, q_out)
         op, os_ = _heads(q_out, "q_out", dev, shape)
     shape = rope_table.shape
     rp = _on(rope_table, "rope_table", _F32, shape, dev)
@@ -711,13 +731,14 @@ def _attention_prefix(name, fp8, q, k_cache, v_cache, prefix_tables, prefix_lens
     gs = _on(group_starts, "group_starts", _I32, (Y + 1,), dev)
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     if out is None:
-        out = torch.empty_like(q)
-        _used_on(stream, out)
+        with _behind(stream, dev):
+            out = torch.empty_like(q)
+        _returned(stream, dev, out)
     op = _on(out, "out", _F16, qshape, dev)
-    mp, mc = _max_len(prefix_lens, max_prefix_len), _max_len(context_lens, max_context_len)
+    mp, mc = _longest(prefix_lens, max_prefix_len, stream, dev), _longest(context_lens, max_context_len, stream, dev)
     if workspace is None:
-        workspace = alloc_workspace(paged_decode_prefix_workspace_size(B, QL, Hq, Hkv, D, BS, Y, mp, mc), q.device)
-        _used_on(stream, workspace)
+        with _behind(stream, dev):
+            workspace = alloc_workspace(paged_decode_prefix_workspace_size(B, QL, Hq, Hkv, D, BS, Y, mp, mc), q.device)
     ws, wsb = _space(workspace, dev)
     fn = _lib.paged_decode_attention_prefix_fp8 if fp8 else _lib.paged_decode_attention_prefix
     st = fn(qp, kc, vc, pt, pl, gs, bt, cl, op, B, QL, Y, Hq, Hkv, D, BS, NB, MP, MB, mp, mc, scale, *scales, ws, wsb,
@@ -794,14 +815,16 @@ def paged_kv_block_select(q, bounds, block_tables, context_lens, max_selected, b
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     bt, MB = _table(block_tables, "block_tables", B, dev)
     if block_lists is None:
-        block_lists = torch.empty((B, Hkv, max(K, 0)), dtype=_I32, device=q.device)
-        _used_on(stream, block_lists)
+        with _behind(stream, dev):
+            block_lists = torch.empty((B, Hkv, max(K, 0)), dtype=_I32, device=q.device)
+        _returned(stream, dev, block_lists)
     if list_lens is None:
-        list_lens = torch.empty((B, Hkv), dtype=_I32, device=q.device)
-        _used_on(stream, list_lens)
+        with _behind(stream, dev):
+            list_lens = torch.empty((B, Hkv), dtype=_I32, device=q.device)
+        _returned(stream, dev, list_lens)
     st = _lib.paged_kv_block_select(qp, bo, bt, cl, _on(block_lists, "block_lists", _I32, (B, Hkv, K), dev),
                                     _on(list_lens, "list_lens", _I32, (B, Hkv), dev), B, Hq, Hkv, D, int(block_size),
-                                    NB, MB, _max_len(context_lens, max_context_len), K, int(sink_blocks),
+                                    NB, MB, _longest(context_lens, max_context_len, stream, dev), K, int(sink_blocks),
                                     int(recent_blocks), 1 if fp8 else 0, _word(error_word, dev),
                                     _raw_stream(stream, dev))
     if st:
@@ -833,12 +856,13 @@ def _attention_blocks(name, fp8, q, k_cache, v_cache, block_tables, context_lens
     bl = _on(block_lists, "block_lists", _I32, (B, Hkv, K), dev)
     ll = _on(list_lens, "list_lens", _I32, (B, Hkv), dev)
     if out is None:
-        out = torch.empty_like(q)
-        _used_on(stream, out)
+        with _behind(stream, dev):
+            out = torch.empty_like(q)
+        _returned(stream, dev, out)
     op = _on(out, "out", _F16, qshape, dev)
     if workspace is None:
-        workspace = alloc_workspace(paged_decode_blocks_workspace_size(B, Hq, Hkv, D, BS, K), q.device)
-        _used_on(stream, workspace)
+        with _behind(stream, dev):
+            workspace = alloc_workspace(paged_decode_blocks_workspace_size(B, Hq, Hkv, D, BS, K), q.device)
     ws, wsb = _space(workspace, dev)
     fn = _lib.paged_decode_attention_blocks_fp8 if fp8 else _lib.paged_decode_attention_blocks
     st = fn(qp, kc, vc, bt, cl, bl, ll, op, B, Hq, Hkv, D, BS, NB, MB, K, scale, *scales, ws, wsb,
