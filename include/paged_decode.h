@@ -713,7 +713,9 @@ pkd_status paged_kv_block_bounds(const void* k_cache, const int32_t* block_table
  * fp32 leaves open at the border is decided in fp64.
  *
  *   q              device fp16 [num_seqs][num_q_heads][head_dim]
- *   bounds         as written by paged_kv_block_bounds, finite, for every used block
+ *   bounds         as written by paged_kv_block_bounds for every used block.  A
+ *                  block with a bound that is not finite, or whose score is
+ *                  not a number, scores +inf: it comes before the others
  *   block_lists    device int32 [num_seqs][num_kv_heads][max_selected]: the
  *                  chosen logical blocks in ascending order, then -1
  *   list_lens      device int32 [num_seqs][num_kv_heads]: how many

@@ -350,7 +350,9 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kerne
 // global memory straight into A fragments (a lane's 16 bytes of a row are its
 // k slots of two steps; the query fragments follow the same order of dims).
 // The first `sink` and the last `recent` blocks are always taken, and of the
-// others the best, ties to the lowest index, as if scores were exact.
+// others the best, ties to the lowest index, as if scores were exact.  A bound
+// that is not finite makes one of its two products +inf or not a number whatever
+// the query's sign (0 * inf is not a number): its block counts as the best.
 //
 // The scores are sums of 2D exact products in fp32, off by at most E.  If tau
 // is the k-th largest of them, blocks above tau + 2E are chosen and those below
@@ -394,6 +396,27 @@ constexpr int kSelMaxWarps = 8;  // CTAs of 128 or 256 threads
 // results are summed in fp32 (2^-20 of all): 1.5 x 2^-19.
 constexpr float kSelErr = 1.5f / 524288.f;
 
+// The largest score, which also stands for +inf and for one that is not a
+// number: finite, so that such blocks are ranked, counted and tied as any other.
+// Its negative is the lowest: a head of -inf, a block outside the pool.  Finite
+// fp16 scores end at 2^9 * 2^32.
+constexpr float kSelTop = 3.0e38f;
+constexpr uint32_t kHalfMax2 = 0x7BFF7BFFu;  // 65504, twice
+
+__device__ __forceinline__ uint32_t hmin2_nan_u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmax2_nan_u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t u = __float_as_uint(f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
@@ -421,16 +444,17 @@ __device__ __forceinline__ double exact_score(const char* lo, const __half* q, i
         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + (size_t)h * D + d0 + 2 * w));
         const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&wl[w]));
         const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&wh[w]));
-        // the larger of the two products of each dim, exact in fp32
-        s[(2 * w) % 4] += (double)(x.x * (x.x < 0.f ? l.x : u.x));
-        s[(2 * w + 1) % 4] += (double)(x.y * (x.y < 0.f ? l.y : u.y));
+        // the larger of the two products of each dim, exact in fp32: one of these is zero
+        s[(2 * w) % 4] += (double)((x.x < 0.f ? x.x : 0.f) * l.x + (x.x < 0.f ? 0.f : x.x) * u.x);
+        s[(2 * w + 1) % 4] += (double)((x.y < 0.f ? x.y : 0.f) * l.y + (x.y < 0.f ? 0.f : x.y) * u.y);
       }
     }
   }
   double t = (s[0] + s[1]) + (s[2] + s[3]);
   t += __shfl_xor_sync(0xffffffffu, t, 1);
   t += __shfl_xor_sync(0xffffffffu, t, 2);
-  if (h >= G) t = -3.0e38;
+  t = t < (double)kSelTop ? fmax(t, -(double)kSelTop) : (double)kSelTop;
+  if (h >= G) t = -(double)kSelTop;
 #pragma unroll
   for (int m = 4; m < 32; m <<= 1) t = fmax(t, __shfl_xor_sync(0xffffffffu, t, m));
   return t;
@@ -522,10 +546,11 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
     for (int w = 0; w < W; ++w) {
       const uint32_t x =
           r < G ? *reinterpret_cast<const uint32_t*>(qrow + (size_t)r * D + DPC * (4 * jj + c) + 2 * w) : 0u;
-      qlo[jj * W + w] = hmin2_u(x, 0u);
-      qhi[jj * W + w] = hmax2_u(x, 0u);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-      qsum += fabsf(f.x) + fabsf(f.y);
+      qlo[jj * W + w] = hmin2_nan_u(x, 0u);
+      qhi[jj * W + w] = hmax2_nan_u(x, 0u);
+      const uint32_t a = hmin2_u(x & 0x7FFF7FFFu, kHalfMax2);  // what is not finite does not widen the error bound
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+      qsum += f.x + f.y;
     }
   const char* base = static_cast<const char*>(P.bounds) + (size_t)g * 2 * ROWB + 16 * c;
   const size_t block_stride = (size_t)P.num_kv_heads * 2 * ROWB;
@@ -606,14 +631,15 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
       // heads 2c and 2c + 1 of block row r + 8f; heads past the group do not count
       const float s0 = 2 * c < G ? sum[t][f].x : -INFINITY;
       const float s1 = 2 * c + 1 < G ? sum[t][f].y : -INFINITY;
-      float s = fmaxf(s0, s1);
-      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
-      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+      float s = fmax_nan(s0, s1);
+      s = fmax_nan(s, __shfl_xor_sync(0xffffffffu, s, 1));
+      s = fmax_nan(s, __shfl_xor_sync(0xffffffffu, s, 2));
+      s = s < kSelTop ? fmaxf(s, -kSelTop) : kSelTop;
       const int i = (tile + t * step) * 16 + 8 * f + r;
       if (c == 0 && i < nblk) {
         if (!ok[t][f]) {
           record_error(P.error_word, kErrBadBlock);
-          s = -3.0e38f;  // a block outside the pool comes last
+          s = -kSelTop;  // a block outside the pool comes last
         }
         if (i >= i0 && i < i1) {
           smin = fminf(smin, s);
@@ -631,6 +657,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
     smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, k));
   }
   if (lane == 0) {
+    kabs = hmin2_u(kabs, kHalfMax2);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&kabs));
     const uint32_t at = stats0 + (uint32_t)(rank * NW + warp) * (uint32_t)sizeof(SelWarpStats);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(fmaxf(f.x, f.y)) : "memory");
@@ -668,7 +695,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
   auto bounds_of = [&](int pb) { return static_cast<const char*>(P.bounds) + (size_t)pb * block_stride + (size_t)g * 2 * ROWB; };
   auto exact = [&](int i) {
     const int pb = bt[i];
-    return pb >= 0 && pb < P.num_blocks ? exact_score<D, KVB>(bounds_of(pb), qrow, G) : -3.0e38;
+    return pb >= 0 && pb < P.num_blocks ? exact_score<D, KVB>(bounds_of(pb), qrow, G) : -(double)kSelTop;
   };
   bool settled = false;
   int ties = 0;  // of the blocks in the second mask (s_hist), the first `ties` are chosen too
@@ -919,9 +946,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
   for (int w = from; w < to; ++w)
     for (uint32_t m = s_mask[w]; m; m &= m - 1, ++place)
       if (place < K) list[place] = 32 * w + __ffs(m) - 1;
-  // (fewer than K only where a bound was not a number: such a block is never chosen)
-  for (int i = count + threadIdx.x; i < K; i += NT) list[i] = -1;
-  if (threadIdx.x == 0) P.list_lens[row] = min(count, K);
+  if (threadIdx.x == 0) P.list_lens[row] = K;  // count, always: more than K blocks, all scores finite
 }
 
 }  // namespace pkd
