@@ -510,11 +510,11 @@ __global__ void validate_tables_kernel(const int32_t* block_tables, const int32_
   const int b = blockIdx.x;
   if (b >= num_seqs) return;
   const int L = context_lens[b];
-  if (L < 0 || L > max_blocks_per_seq * block_size) {
+  if (L < 0 || L > (long long)max_blocks_per_seq * block_size) {
     if (threadIdx.x == 0) record_error(error_word, kErrBadBlock);
     return;
   }
-  const int nb = (L + block_size - 1) / block_size;
+  const int nb = (int)(((long long)L + block_size - 1) / block_size);
   for (int i = threadIdx.x; i < nb; i += blockDim.x) {
     const int p = block_tables[(size_t)b * max_blocks_per_seq + i];
     if (p < 0 || p >= num_blocks) record_error(error_word, kErrBadBlock);

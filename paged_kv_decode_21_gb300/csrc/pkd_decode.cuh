@@ -200,10 +200,10 @@ __device__ __forceinline__ void record_error(int* err, uint32_t bits) {
 template <int BS>
 __device__ __forceinline__ int row_clamped_len(const DecodeParams& P, int b) {
   const int L = P.context_lens[b];
-  const int row = P.max_blocks_per_seq * BS;
+  const long long row = (long long)P.max_blocks_per_seq * BS;  // (may pass 32 bits)
   if (L > row) {
     record_error(P.error_word, kErrBadBlock);
-    return row;
+    return (int)row;
   }
   return L;
 }

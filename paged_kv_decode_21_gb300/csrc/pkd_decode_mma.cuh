@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
     const size_t bg = (size_t)b * P.num_kv_heads + g;
     list = P.block_lists + bg * P.max_listed;
     list_n = min(P.list_lens[bg], P.max_listed);
-    list_nblk = L > 0 ? (L + BS - 1) / BS : 0;
+    list_nblk = L > 0 ? (L - 1) / BS + 1 : 0;
     list_ragged = L % BS != 0;
     const int fill = (list_n > 0 && list_ragged && list[list_n - 1] == list_nblk - 1) ? L % BS : BS;
     L = list_n > 0 ? (list_n - 1) * BS + fill : 0;  // the list's own length in tokens
