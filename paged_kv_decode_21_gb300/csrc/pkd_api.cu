@@ -81,8 +81,8 @@ pkd_status check_shape(const Shape& s) {
 
 int sm_count() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (pkd::failed(cudaGetDevice(&dev))) return 0;
+  if (pkd::failed(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev))) return 0;
   return n;
 }
 
@@ -190,10 +190,7 @@ DeviceNumbers g_dev_numbers[kMaxDevices];
 
 DeviceNumbers device_numbers() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();  // no device: leave no sticky error behind
-    return DeviceNumbers{148, 126LL << 20, 8.0e12};
-  }
+  if (pkd::failed(cudaGetDevice(&dev))) return DeviceNumbers{148, 126LL << 20, 8.0e12};  // no device
   if (dev < 0 || dev >= kMaxDevices) return query_device_numbers(dev);
   if (!g_dev_ready[dev].load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(g_dev_mu);
@@ -605,7 +602,7 @@ pkd_status launch_reduce(const float* tmp_out, const float* max_logits, const fl
   } else {
     return PKD_ERR_UNSUPPORTED;
   }
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKD_OK : PKD_ERR_LAUNCH;
+  return pkd::failed(e) ? PKD_ERR_LAUNCH : PKD_OK;
 }
 
 pkd_status check_inputs(const void* q, const void* k_cache, const void* v_cache,
@@ -972,9 +969,9 @@ pkd_status paged_decode_attention_host(const void* q, const void* k_cache, const
   const size_t bt_bytes = (size_t)num_seqs * max_blocks_per_seq * sizeof(int32_t);
   const size_t cl_bytes = (size_t)num_seqs * sizeof(int32_t);
   // the small inputs: one copy each
-  if (cudaMemcpyAsync(q_dev, q, q_bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-      cudaMemcpyAsync(block_tables_dev, block_tables, bt_bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-      cudaMemcpyAsync(context_lens_dev, context_lens, cl_bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess)
+  if (pkd::failed(cudaMemcpyAsync(q_dev, q, q_bytes, cudaMemcpyHostToDevice, stream)) ||
+      pkd::failed(cudaMemcpyAsync(block_tables_dev, block_tables, bt_bytes, cudaMemcpyHostToDevice, stream)) ||
+      pkd::failed(cudaMemcpyAsync(context_lens_dev, context_lens, cl_bytes, cudaMemcpyHostToDevice, stream)))
     return PKD_ERR_CUDA;
   // the pools: the used blocks read in place from mapped host memory, or
   // (not mapped, or asked for) one copy of each whole pool
@@ -984,8 +981,8 @@ pkd_status paged_decode_attention_host(const void* q, const void* k_cache, const
                       cudaHostGetDevicePointer(&v_map, const_cast<void*>(v_cache), 0) == cudaSuccess;
   if (!gather) {
     (void)cudaGetLastError();  // a failed mapping query is not an error of this call
-    if (cudaMemcpyAsync(k_cache_dev, k_cache, pool_bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaMemcpyAsync(v_cache_dev, v_cache, pool_bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess)
+    if (pkd::failed(cudaMemcpyAsync(k_cache_dev, k_cache, pool_bytes, cudaMemcpyHostToDevice, stream)) ||
+        pkd::failed(cudaMemcpyAsync(v_cache_dev, v_cache, pool_bytes, cudaMemcpyHostToDevice, stream)))
       return PKD_ERR_CUDA;
   } else {
     const int mb = std::min(max_blocks_per_seq, (max_context_len + block_size - 1) / block_size);
@@ -1002,8 +999,7 @@ pkd_status paged_decode_attention_host(const void* q, const void* k_cache, const
                    num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
                    max_context_len, scale, 0, PKD_VARIANT_AUTO, 0, workspace, workspace_bytes, error_word, stream);
   if (st != PKD_OK) return st;
-  return cudaMemcpyAsync(out, out_dev, q_bytes, cudaMemcpyDeviceToHost, stream) == cudaSuccess ? PKD_OK
-                                                                                               : PKD_ERR_CUDA;
+  return pkd::failed(cudaMemcpyAsync(out, out_dev, q_bytes, cudaMemcpyDeviceToHost, stream)) ? PKD_ERR_CUDA : PKD_OK;
 }
 
 pkd_status paged_decode_attention(const void* q, const void* k_cache, const void* v_cache,
@@ -1171,13 +1167,13 @@ pkd_status pkd_selftest_bounded_wait(int* error_word, unsigned long long budget_
 pkd_status pkd_read_device_error(int* error_word, unsigned* host_bits, int clear, cudaStream_t stream) {
   if (!error_word || !host_bits) return PKD_ERR_NULL;
   unsigned v = 0;
-  if (cudaMemcpyAsync(&v, error_word, sizeof(unsigned), cudaMemcpyDeviceToHost, stream) != cudaSuccess)
+  if (pkd::failed(cudaMemcpyAsync(&v, error_word, sizeof(unsigned), cudaMemcpyDeviceToHost, stream)))
     return PKD_ERR_CUDA;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return PKD_ERR_CUDA;
+  if (pkd::failed(cudaStreamSynchronize(stream))) return PKD_ERR_CUDA;
   *host_bits = v;
   if (clear) {
-    if (cudaMemsetAsync(error_word, 0, sizeof(int), stream) != cudaSuccess) return PKD_ERR_CUDA;
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return PKD_ERR_CUDA;
+    if (pkd::failed(cudaMemsetAsync(error_word, 0, sizeof(int), stream))) return PKD_ERR_CUDA;
+    if (pkd::failed(cudaStreamSynchronize(stream))) return PKD_ERR_CUDA;
   }
   return v == 0 ? PKD_OK : PKD_ERR_DEVICE;
 }
@@ -1408,7 +1404,7 @@ pkd_status launch_merge(int head_dim, const pkd::MergeParams& m, cudaStream_t st
   cfg.numAttrs = 1;
   const cudaError_t e = head_dim == 128 ? cudaLaunchKernelEx(&cfg, pkd::paged_merge_kernel<128>, m)
                                         : cudaLaunchKernelEx(&cfg, pkd::paged_merge_kernel<64>, m);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKD_OK : PKD_ERR_LAUNCH;
+  return pkd::failed(e) ? PKD_ERR_LAUNCH : PKD_OK;
 }
 
 pkd::MergeSource merge_source(const Workspace& w, const PartPlan& plan) {

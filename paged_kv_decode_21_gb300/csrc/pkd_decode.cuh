@@ -42,6 +42,14 @@
 
 namespace pkd {
 
+// Whether a runtime call on the host failed.  The runtime also keeps a failure
+// for the thread's next cudaGetLastError, which must not meet it after another
+// launch: it is taken here.
+inline bool failed(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e != cudaSuccess;
+}
+
 enum Variant : int { kNoPrefetch = 1, kL2Prefetch = 2, kTmaStaged = 3 };
 
 constexpr float kLazyTau = 8.0f;  // log2-domain slack of the lazy running max

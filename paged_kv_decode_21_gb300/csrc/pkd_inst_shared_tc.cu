@@ -25,7 +25,7 @@ cudaError_t launch_bs(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
   using T = SharedTcTraits<BS, KVB, HD>;
   auto* fn = paged_shared_tc_kernel<BS, KVB, HD>;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(mk, mv, p);
   return cudaGetLastError();
 }
@@ -37,7 +37,7 @@ cudaError_t launch_shared_tc(int D, int BS, const DecodeParams& p, long long gri
     return cudaErrorInvalidValue;
   CUtensorMap mk, mv;
   const cudaError_t e = mma_host::make_maps(p, D, BS, kvb, &mk, &mv);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   if (kvb == 1) return BS == 16 ? launch_bs<16, 1, 128>(mk, mv, p, grid, stream) : launch_bs<32, 1, 128>(mk, mv, p, grid, stream);
   if (D == 64) return BS == 16 ? launch_bs<16, 2, 64>(mk, mv, p, grid, stream) : launch_bs<32, 2, 64>(mk, mv, p, grid, stream);
   return BS == 16 ? launch_bs<16, 2, 128>(mk, mv, p, grid, stream) : launch_bs<32, 2, 128>(mk, mv, p, grid, stream);

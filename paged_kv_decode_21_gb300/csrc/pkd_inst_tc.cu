@@ -18,7 +18,7 @@ cudaError_t launch_tc_bs(const CUtensorMap& mk, const CUtensorMap& mv, const Dec
   auto* fn = (HD == 128 && p.parts_per_cta > 1) ? paged_decode_tc_kernel<BS, KVB, HD, HD == 128>
                                                  : paged_decode_tc_kernel<BS, KVB, HD, false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -34,7 +34,7 @@ cudaError_t launch_tc_bs(const CUtensorMap& mk, const CUtensorMap& mv, const Dec
     cfg.numAttrs = 1;
   }
   e = cudaLaunchKernelEx(&cfg, fn, mk, mv, p);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   return cudaGetLastError();
 }
 
@@ -46,7 +46,7 @@ cudaError_t launch_decode_tcgen05(int D, int BS, const DecodeParams& p, long lon
     return cudaErrorInvalidValue;
   CUtensorMap mk, mv;
   cudaError_t e = mma_host::make_maps(p, D, BS, kvb, &mk, &mv);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   if (kvb == 1)
     return BS == 16 ? launch_tc_bs<16, 1, 128>(mk, mv, p, grid, stream) : launch_tc_bs<32, 1, 128>(mk, mv, p, grid, stream);
   if (D == 64)

@@ -16,13 +16,13 @@ cudaError_t launch_decode_inst(const DecodeParams& p, long long grid, cudaStream
     using T = WsTraits<D, BS, G>;
     auto* fn = paged_decode_ws_kernel<D, BS, G>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
+    if (failed(e)) return e;
     fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(p);
   } else {
     using T = DecodeTraits<D, BS, G, VARIANT>;
     auto* fn = paged_decode_kernel<D, BS, G, VARIANT>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
+    if (failed(e)) return e;
     fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(p);
   }
   return cudaGetLastError();

@@ -52,7 +52,7 @@ inline cudaError_t make_map(CUtensorMap* m, const void* base, int D, int rows_pe
 
 inline cudaError_t make_maps(const DecodeParams& p, int D, int BS, int kvb, CUtensorMap* mk, CUtensorMap* mv) {
   cudaError_t e = make_map(mk, p.k_cache, D, p.num_kv_heads * BS, p.num_blocks, kvb);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   return make_map(mv, p.v_cache, D, p.num_kv_heads * BS, p.num_blocks, kvb);
 }
 
@@ -62,7 +62,7 @@ cudaError_t launch_qc(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
   using T = MmaTraits<D, BS, G, QC, KVB, CPS>;
   auto* fn = paged_decode_mma_kernel<D, BS, G, QC, KVB, CPS, SRC>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   if (!p.piece_order && !p.after_grid) {
     fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(mk, mv, p);
     return cudaGetLastError();
@@ -81,7 +81,7 @@ cudaError_t launch_qc(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, fn, mk, mv, p);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
   return cudaGetLastError();
 }
 
@@ -92,7 +92,7 @@ template <template <int> class QCOF, int KVB = 2, int CPS = 0, int SRC = kOwn>
 cudaError_t launch_all(int D, int BS, int G, const DecodeParams& p, long long grid, cudaStream_t stream) {
   CUtensorMap mk, mv;
   cudaError_t e = make_maps(p, D, BS, KVB, &mk, &mv);
-  if (e != cudaSuccess) return e;
+  if (failed(e)) return e;
 #define PKD_CASE_G(D_, BS_)                                                                  \
   switch (G) {                                                                               \
     case 1: return launch_qc<D_, BS_, 1, QCOF<1>::value, KVB, CPS, SRC>(mk, mv, p, grid, stream); \

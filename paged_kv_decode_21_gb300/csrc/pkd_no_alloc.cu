@@ -83,7 +83,10 @@ extern "C" pkd_status paged_decode_attention_static_scratch(
 
   cudaError_t err;
   unsigned char* base = static_cast<unsigned char*>(scratch_for_current_device(&err));
-  if (!base) return PKD_ERR_CUDA;
+  if (!base) {
+    (void)cudaGetLastError();  // reported here, not by the next launch
+    return PKD_ERR_CUDA;
+  }
   float* tmp_out = reinterpret_cast<float*>(base);
   float* max_logits = reinterpret_cast<float*>(base + o_bytes);
   float* exp_sums = reinterpret_cast<float*>(base + o_bytes + m_bytes);

@@ -162,8 +162,8 @@ pkd_status paged_kv_block_bounds(const void* k_cache, const int32_t* block_table
   // while 32 warps an SM remain (32 prompts of up to 8192 tokens, 8 heads: 78
   // us, against 128 with one head a warp); one where the call is small.
   int sms = 0, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+  if (pkd::failed(cudaGetDevice(&dev)) ||
+      pkd::failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
     sms = 148;
   const long long blocks = (long long)num_seqs * p.grid_blocks;
   p.heads_per_warp = 1;
@@ -228,8 +228,8 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   // with eight).  Sixteen need a GPC that holds them all at once, so they are
   // left to score arrays of which an SM holds two.
   int sms = 0, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+  if (pkd::failed(cudaGetDevice(&dev)) ||
+      pkd::failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
     sms = 148;
   const long long rows = (long long)num_seqs * num_kv_heads;
   const int tiles = (max_blocks + 15) / 16;
@@ -251,10 +251,10 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   // (The attribute belongs to the kernel, not to the call: what the largest call
   // needs, the same for all, so that a call of another host thread in between
   // changes nothing.)
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, select_smem(PKD_MAX_SELECT_BLOCKS)) !=
-      cudaSuccess)
+  if (pkd::failed(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       select_smem(PKD_MAX_SELECT_BLOCKS))))
     return PKD_ERR_LAUNCH;
-  if (p.cluster > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (p.cluster > 8 && pkd::failed(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)))
     return PKD_ERR_LAUNCH;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -268,7 +268,7 @@ pkd_status paged_kv_block_select(const void* q, const void* bounds, const int32_
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) return PKD_ERR_LAUNCH;
+  if (pkd::failed(cudaLaunchKernelEx(&cfg, fn, p))) return PKD_ERR_LAUNCH;
   return launched();
 }
 
