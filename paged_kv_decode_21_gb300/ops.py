@@ -189,17 +189,59 @@ def _max_len(context_lens, max_context_len):
     return int(context_lens.max().item()) if context_lens.numel() else 0
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _behind(stream, dev: int):
+    """A context in which ``stream`` is the current one where it is given: tensors allocated inside get memory of
+    that stream's own pool (memory freed behind work that is still pending on the caller's current stream is not
+    written by the call, nor the call's written by that work), and reads of lengths wait for what the stream has
+    to run."""
+    if stream is None:
+        return _AS_IT_IS
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _returned(stream, dev: int, *tensors) -> None:
+    """Results allocated for a given stream: their memory is not handed out again before the caller's current
+    stream, which goes on with them, has passed where they are freed."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(dev))
+
+
+def _new_like(q, stream) -> torch.Tensor:
+    """An uninitialised result of q's shape for a call on ``stream``."""
+    if stream is None:
+        return torch.empty_like(q)
+    dev = q.get_device()
+    with _behind(stream, dev):
+        out = torch.empty_like(q)
+    _returned(stream, dev, out)
+    return out
+
+
+def _longest(lens, most, stream, dev: int) -> int:
+    """The host's bound of ``lens``, or their maximum as the given stream leaves them."""
+    if most is not None:
+        return int(most)
+    with _behind(stream, dev):
+        return _max_len(lens, None)
+
+
 def paged_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale, out=None,
                            max_context_len=None, stream=None) -> torch.Tensor:
     """Unsplit decode attention (no workspace); returns ``out``."""
     B, Hq, Hkv, D, BS, NB, MB = _shape(q, k_cache, v_cache, block_tables, context_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     _want(out, "out", torch.float16, 3)
     st = lib().paged_decode_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                       _ptr(context_lens), _ptr(out), B, Hq, Hkv, D, BS, NB, MB,
-                                      _max_len(context_lens, max_context_len), float(scale),
-                                      _stream(stream))
+                                      _longest(context_lens, max_context_len, stream, q.get_device()),
+                                      float(scale), _stream(stream))
     _check(st, "paged_decode_attention")
     return out
 
@@ -326,13 +368,14 @@ def paged_decode_attention_ex(q, k_cache, v_cache, block_tables, context_lens, s
     None and a split is needed."""
     B, Hq, Hkv, D, BS, NB, MB = _shape(q, k_cache, v_cache, block_tables, context_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     _want(out, "out", torch.float16, 3)
-    ml = _max_len(context_lens, max_context_len)
+    ml = _longest(context_lens, max_context_len, stream, q.get_device())
     var = _variant(variant)
     if workspace is None:
         need = paged_decode_workspace_size(B, Hq, Hkv, D, BS, ml, partition_size, var)
-        workspace = alloc_workspace(need, q.device)
+        with _behind(stream, q.get_device()):
+            workspace = alloc_workspace(need, q.device)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().paged_decode_attention_ex(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                          _ptr(context_lens), _ptr(out), B, Hq, Hkv, D, BS, NB, MB,
@@ -354,9 +397,10 @@ def paged_decode_attention_host(q, k_cache, v_cache, block_tables, context_lens,
     NB, Hkv, BS, _ = k_cache.shape
     MB = block_tables.shape[1]
     ml = int(max_context_len) if max_context_len is not None else (int(context_lens.max()) if B else 0)
-    out_dev = dev.out if getattr(dev, "out", None) is not None else torch.empty_like(dev.q)
-    if workspace is None:
-        workspace = alloc_workspace(paged_decode_workspace_size(B, Hq, Hkv, D, BS, ml, 0, "auto"), dev.q.device)
+    with _behind(stream, dev.q.get_device()):
+        out_dev = dev.out if getattr(dev, "out", None) is not None else torch.empty_like(dev.q)
+        if workspace is None:
+            workspace = alloc_workspace(paged_decode_workspace_size(B, Hq, Hkv, D, BS, ml, 0, "auto"), dev.q.device)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().paged_decode_attention_host(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(out),
@@ -378,7 +422,7 @@ def paged_decode_partitions(q, k_cache, v_cache, block_tables, context_lens, sca
     var = _variant(variant)
     st = lib().paged_decode_partitions(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                        _ptr(context_lens), B, Hq, Hkv, D, BS, NB, MB,
-                                       _max_len(context_lens, max_context_len), float(scale),
+                                       _longest(context_lens, max_context_len, stream, q.get_device()), float(scale),
                                        int(partition_size), var, int(prefetch_distance),
                                        _ptr(tmp_out), _ptr(max_logits), _ptr(exp_sums), npmax,
                                        _ptr(error_word), _stream(stream))
@@ -420,12 +464,13 @@ def paged_decode_attention_multi(q, k_cache, v_cache, block_tables, context_lens
     B, QL, Hq, D = q.shape
     _, _, Hkv, _, BS, NB, MB = _shape(q.view(B, QL * Hq, D), k_cache, v_cache, block_tables, context_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     _want(out, "out", torch.float16, 4)
-    maxlen = _max_len(context_lens, max_context_len)
+    maxlen = _longest(context_lens, max_context_len, stream, q.get_device())
     need = paged_decode_multi_workspace_size(B, QL, Hq, Hkv, D, BS, maxlen, partition_size)
     if workspace is None:
-        workspace = alloc_workspace(need, q.device)
+        with _behind(stream, q.get_device()):
+            workspace = alloc_workspace(need, q.device)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().paged_decode_attention_multi_ex(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                                _ptr(context_lens), _ptr(out), B, QL, Hq, Hkv, D, BS, NB, MB,
@@ -463,12 +508,13 @@ def paged_decode_attention_fp8(q, k_cache, v_cache, block_tables, context_lens, 
     if block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("block_tables / context_lens batch mismatch")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     _want(out, "out", torch.float16, q.dim())
-    maxlen = _max_len(context_lens, max_context_len)
+    maxlen = _longest(context_lens, max_context_len, stream, q.get_device())
     need = paged_decode_multi_workspace_size(B, QL, Hq, Hkv, D, BS, maxlen, partition_size)
     if workspace is None:
-        workspace = alloc_workspace(need, q.device)
+        with _behind(stream, q.get_device()):
+            workspace = alloc_workspace(need, q.device)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if variant is None:
         st = lib().paged_decode_attention_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
@@ -558,36 +604,6 @@ def _raw_stream(stream, dev: int) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-@contextlib.contextmanager
-def _behind(stream, dev: int):
-    """Make ``stream`` the current one where it is given: tensors allocated inside get memory of that stream's
-    own pool (memory freed behind work that is still pending on the caller's current stream is not written by
-    the call, nor the call's written by that work), and reads of lengths wait for what the stream has to run."""
-    if stream is None:
-        yield
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
-        yield
-
-
-def _returned(stream, dev: int, *tensors) -> None:
-    """Results allocated for a given stream: their memory is not handed out again before the caller's current
-    stream, which goes on with them, has passed where they are freed."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(torch.cuda.current_stream(dev))
-
-
-def _longest(lens, most, stream, dev: int) -> int:
-    """The host's bound of ``lens``, or their maximum as the given stream leaves them."""
-    if most is not None:
-        return int(most)
-    with _behind(stream, dev):
-        return _max_len(lens, None)
 
 
 def _word(error_word, dev: int):
@@ -731,9 +747,7 @@ def _attention_prefix(name, fp8, q, k_cache, v_cache, prefix_tables, prefix_lens
     gs = _on(group_starts, "group_starts", _I32, (Y + 1,), dev)
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     if out is None:
-        with _behind(stream, dev):
-            out = torch.empty_like(q)
-        _returned(stream, dev, out)
+        out = _new_like(q, stream)
     op = _on(out, "out", _F16, qshape, dev)
     mp, mc = _longest(prefix_lens, max_prefix_len, stream, dev), _longest(context_lens, max_context_len, stream, dev)
     if workspace is None:
@@ -856,9 +870,7 @@ def _attention_blocks(name, fp8, q, k_cache, v_cache, block_tables, context_lens
     bl = _on(block_lists, "block_lists", _I32, (B, Hkv, K), dev)
     ll = _on(list_lens, "list_lens", _I32, (B, Hkv), dev)
     if out is None:
-        with _behind(stream, dev):
-            out = torch.empty_like(q)
-        _returned(stream, dev, out)
+        out = _new_like(q, stream)
     op = _on(out, "out", _F16, qshape, dev)
     if workspace is None:
         with _behind(stream, dev):
@@ -919,12 +931,11 @@ def paged_decode_attention_static_scratch(q, k_cache, v_cache, block_tables, con
     the GPU (they share the array)."""
     B, Hq, Hkv, D, BS, NB, MB = _shape(q, k_cache, v_cache, block_tables, context_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     _want(out, "out", torch.float16, 3)
     st = lib().paged_decode_attention_static_scratch(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(out),
-        B, Hq, Hkv, D, BS, NB, MB, _max_len(context_lens, max_context_len), float(scale),
-        int(partition_size), _variant(variant), int(prefetch_distance), _ptr(error_word),
-        _stream(stream))
+        B, Hq, Hkv, D, BS, NB, MB, _longest(context_lens, max_context_len, stream, q.get_device()), float(scale),
+        int(partition_size), _variant(variant), int(prefetch_distance), _ptr(error_word), _stream(stream))
     _check(st, "paged_decode_attention_static_scratch")
     return out
