@@ -681,7 +681,9 @@ size_t paged_decode_prefix_workspace_size(int num_seqs, int q_len, int num_q_hea
  * block p = block_tables[b][i],
  *   bounds[p][g][0][d] = min over the block's tokens t < context_lens[b] of K[p][g][t % block_size][d]
  *   bounds[p][g][1][d] = max over the same
- * in the cache's type (E4M3: codes; exact either way).
+ * in the cache's type (E4M3: codes; exact either way).  A key that is not a
+ * number makes its dim's bounds so, and paged_kv_block_select then takes its
+ * block first.
  *
  *   bounds         device [num_blocks][num_kv_heads][2][head_dim], fp16 or
  *                  (kv_fp8) E4M3 bytes, 16-byte aligned, written in place;

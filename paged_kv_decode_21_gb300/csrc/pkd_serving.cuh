@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
 // ---------------------------------------------------------------------------
 // Key bounds: for a cache block's tokens t (those before the sequence's
 // length) and every dim d, lo_d = min_t k[t][d] and hi_d = max_t k[t][d], in
-// the cache's own type: both are cache values, so nothing is rounded.
+// the cache's own type: both are cache values, so nothing is rounded.  A key that
+// is not a number makes both so.
 //
 // A warp takes up to eight kv heads of one (sequence, block): their tiles lie
 // behind one another, a warp-wide load of 16 bytes a lane covers several whole
@@ -209,6 +210,14 @@ __device__ __forceinline__ uint32_t hmin2_u(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t hmax2_u(uint32_t a, uint32_t b) {
   const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmin2_nan_u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmax2_nan_u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t hmax2_abs(uint32_t a, uint32_t b) {  // max(a, |b|)
@@ -320,8 +329,8 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kerne
         cache_words<KVB>(u[k], x);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          lo[w] = hmin2_u(lo[w], x[w]);
-          hi[w] = hmax2_u(hi[w], x[w]);
+          lo[w] = hmin2_nan_u(lo[w], x[w]);
+          hi[w] = hmax2_nan_u(hi[w], x[w]);
         }
       }
     }
@@ -330,8 +339,8 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) paged_kv_block_bounds_kerne
       for (int m = CPR; m < 32; m <<= 1)
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          lo[w] = hmin2_u(lo[w], __shfl_xor_sync(0xffffffffu, lo[w], m));
-          hi[w] = hmax2_u(hi[w], __shfl_xor_sync(0xffffffffu, hi[w], m));
+          lo[w] = hmin2_nan_u(lo[w], __shfl_xor_sync(0xffffffffu, lo[w], m));
+          hi[w] = hmax2_nan_u(hi[w], __shfl_xor_sync(0xffffffffu, hi[w], m));
         }
       if (r0 == 0) dst[(size_t)(s / steps) * 2 * CPR + c] = words_to_cache<KVB>(lo);
       if (r0 == 1) dst[(size_t)(s / steps) * 2 * CPR + CPR + c] = words_to_cache<KVB>(hi);
@@ -403,14 +412,6 @@ constexpr float kSelErr = 1.5f / 524288.f;
 constexpr float kSelTop = 3.0e38f;
 constexpr uint32_t kHalfMax2 = 0x7BFF7BFFu;  // 65504, twice
 
-__device__ __forceinline__ uint32_t hmin2_nan_u(uint32_t a, uint32_t b) {
-  const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t hmax2_nan_u(uint32_t a, uint32_t b) {
-  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ float fmax_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));

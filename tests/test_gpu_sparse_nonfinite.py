@@ -108,3 +108,31 @@ def test_the_largest_finite_bounds_and_queries():
     q = workloads.randn_f16((1, Hq, D), torch.Generator(device="cuda").manual_seed(9), "cuda")
     q[0, 0, ::2], q[0, 0, 1::2] = 65504.0, -65504.0
     run(q, bounds, bt, [blocks], 30, 1, 2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,BS", [(128, 16), (64, 16), (128, 32), (64, 32)])
+def test_bounds_of_keys_that_are_not_finite(D, BS, fp8):
+    """A NaN key makes both bounds of its dim NaN, wherever it lies among the block's tokens; infinities are
+    ordinary; what lies behind the last token does not count."""
+    Hkv, lens = 3, [5 * BS + 3, 1, 2 * BS]
+    bt = torch.tensor([[0, 1, 2, 3, 4, 5], [6] + [-1] * 5, [7, 8] + [-1] * 4], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(D + BS)
+    kc = workloads.randn_f16((9, Hkv, BS, D), g, "cuda")
+    if fp8:
+        kc = kc.to(torch.float8_e4m3fn).view(torch.uint8)
+    nan = 0x7F if fp8 else NAN
+    kc[0, 0, 0, 3], kc[1, 1, BS - 1, D - 1], kc[2, 2, 7, 40], kc[3, 0, :, 9] = nan, nan, nan, nan
+    kc[5, 1, 2, 5], kc[5, 1, 3:, 6], kc[6, 0, 0, 0], kc[6, 0, 1:, 1] = nan, nan, nan, nan
+    if not fp8:
+        kc[7, 0, 4, 2], kc[7, 0, 5, 2], kc[8, 1, :, 8] = INF, -INF, INF
+    bounds = torch.zeros((9, Hkv, 2, D), dtype=kc.dtype, device="cuda")
+    ops.paged_kv_block_bounds(kc, bt, i32(lens), bounds)
+    for b, n in enumerate(lens):
+        for i in range(-(-n // BS)):
+            p = int(bt[b, i])
+            x = values(kc[p, :, :min(BS, n - i * BS)])
+            got = values(bounds[p])
+            for e, want in enumerate((x.amin(1), x.amax(1))):  # (amin and amax keep NaN)
+                assert torch.equal(torch.isnan(got[:, e]), torch.isnan(want))
+                assert torch.equal(got[:, e].nan_to_num(0.0, 1e9, -1e9), want.nan_to_num(0.0, 1e9, -1e9))
