@@ -72,3 +72,76 @@ def test_choices_over_long_and_short_contexts(fp8):
     for _, want, lists, lens, ew, *_ in jobs:
         assert ops.pkd_read_device_error(ew) == 0
         assert torch.equal(lists, want[0]) and torch.equal(lens, want[1])
+
+
+def test_every_call_at_once():
+    """Three threads, each with streams, caches, outputs and workspaces of its own, run the whole step (append,
+    bounds, choice, listed decode, shared prefix on both kernels, dense decode) over and over beside the others."""
+    from test_gpu_prefix import problem
+
+    class Work:
+        def __init__(self, seed, B, Hq, q_len, plen, fp8):
+            self.fp8, self.B, self.q_len = fp8, B, q_len
+            lens = [q_len + (i * 37 + seed) % 300 for i in range(B)]
+            self.p = problem([B], [plen], lens, q_len, Hq, 4, 128, 16, seed, fp8)
+            q, kc, vc, ptab, plens, starts, bt, cl = self.p
+            self.q1 = q[:, 0].contiguous()
+            g = torch.Generator(device="cuda").manual_seed(seed)
+            self.k, self.v = (workloads.randn_f16((B, 4, 128), g, "cuda") for _ in range(2))
+            self.table = workloads.randn_f16((max(lens), 128), g, "cuda").float()
+            self.before = (cl - 1).contiguous()
+            self.k2, self.v2 = torch.zeros_like(kc), torch.zeros_like(vc)
+            self.bounds = torch.zeros((kc.shape[0], 4, 2, 128), dtype=kc.dtype, device="cuda")
+            self.most = dict(max_context_len=max(lens))
+            self.plen, self.stream = plen, torch.cuda.Stream()
+            self.ew = torch.zeros(1, dtype=torch.int32, device="cuda")
+            nbytes = max(ops.paged_decode_prefix_workspace_size(B, q_len, Hq, 4, 128, 16, 1, plen, max(lens)),
+                         ops.paged_decode_blocks_workspace_size(B, Hq, 4, 128, 16, 6),
+                         ops.paged_decode_multi_workspace_size(B, 1, Hq, 4, 128, 16, max(lens)))
+            self.kw = dict(workspace=ops.alloc_workspace(nbytes, "cuda"), error_word=self.ew)
+            self.outs = [torch.empty_like(self.q1), torch.empty_like(self.q1), torch.empty_like(self.q1),
+                         torch.empty_like(q), torch.empty((B, 4, 6), dtype=torch.int32, device="cuda"),
+                         torch.empty((B, 4), dtype=torch.int32, device="cuda")]
+
+        def step(self):
+            q, kc, vc, ptab, plens, starts, bt, cl = self.p
+            s = (1 / 64, 1 / 64) if self.fp8 else ()
+            rot, o1, o2, o3, lists, counts = self.outs
+            f = (lambda name: getattr(ops, name + "_fp8")) if self.fp8 else (lambda name: getattr(ops, name))
+            f("paged_kv_append_rope")(self.q1, self.k, self.v, self.table, bt, self.before, self.k2, self.v2, *s,
+                                      q_out=rot, error_word=self.ew)
+            ops.paged_kv_block_bounds(kc, bt, cl, self.bounds, error_word=self.ew)
+            ops.paged_kv_block_select(self.q1, self.bounds, bt, cl, 6, 16, block_lists=lists, list_lens=counts,
+                                      error_word=self.ew, **self.most)
+            f("paged_decode_attention_blocks")(self.q1, kc, vc, bt, cl, lists, counts, 0.09, *s, out=o1, **self.kw)
+            if self.fp8:
+                ops.paged_decode_attention_fp8(self.q1, kc, vc, bt, cl, 0.09, *s, out=o2, **self.most, **self.kw)
+            else:
+                ops.paged_decode_attention_ex(self.q1, kc, vc, bt, cl, 0.09, out=o2, **self.most, **self.kw)
+            f("paged_decode_attention_prefix")(q, kc, vc, ptab, plens, starts, bt, cl, 0.09, *s, out=o3,
+                                               max_prefix_len=self.plen, **self.most, **self.kw)
+
+        def state(self):
+            return [x.clone() for x in self.outs + [self.k2, self.v2, self.bounds]]
+
+    works = [Work(81, 90, 28, 1, 3000, False), Work(82, 30, 32, 4, 2000, True), Work(83, 4, 16, 1, 500, False)]
+    want = []
+    for w in works:
+        w.step()
+        torch.cuda.synchronize()
+        want.append(w.state())
+
+    def body(w):
+        torch.cuda.set_device(0)
+        with torch.cuda.stream(w.stream):
+            for _ in range(150):
+                w.step()
+
+    for _ in range(3):
+        errors = in_threads([lambda w=w: body(w) for w in works])
+        torch.cuda.synchronize()
+        assert not errors, errors[0]
+        for w, ref in zip(works, want):
+            assert ops.pkd_read_device_error(w.ew) == 0
+            for got, x in zip(w.state(), ref):
+                assert torch.equal(got.view(torch.uint8), x.view(torch.uint8))
