@@ -202,16 +202,22 @@ __device__ __forceinline__ void record_error(int* err, uint32_t bits) {
   if (err) atomicOr(reinterpret_cast<unsigned*>(err), bits);
 }
 
+// Whether L tokens are more than a block-table row holds.  (A row may hold more
+// than 32 bits count; its tokens fit where L is past them.)
+template <int BS>
+__device__ __forceinline__ bool past_row(const DecodeParams& P, int L) {
+  return L > 0 && (L - 1) / BS >= P.max_blocks_per_seq;
+}
+
 // Sequence b's length as the decode kernels read it.  A length past the
 // block-table row (max_blocks_per_seq * BS tokens) is cut to the row and
 // reported as kErrBadBlock, so no table entry past the row is ever read.
 template <int BS>
 __device__ __forceinline__ int row_clamped_len(const DecodeParams& P, int b) {
   const int L = P.context_lens[b];
-  const long long row = (long long)P.max_blocks_per_seq * BS;  // (may pass 32 bits)
-  if (L > row) {
+  if (past_row<BS>(P, L)) {
     record_error(P.error_word, kErrBadBlock);
-    return (int)row;
+    return P.max_blocks_per_seq * BS;
   }
   return L;
 }

@@ -426,7 +426,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// The block's score in fp64, from its bounds at `lo` (then hi) and the group's
+// The block's score in fp64 (one below kSelTop: a block that reached it is not
+// scored again), from its bounds at `lo` (then hi) and the group's
 // queries; whole warp, the same value in every lane.
 template <int D, int KVB>
 __device__ __forceinline__ double exact_score(const char* lo, const __half* q, int G) {
@@ -445,17 +446,16 @@ __device__ __forceinline__ double exact_score(const char* lo, const __half* q, i
         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + (size_t)h * D + d0 + 2 * w));
         const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&wl[w]));
         const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&wh[w]));
-        // the larger of the two products of each dim, exact in fp32: one of these is zero
-        s[(2 * w) % 4] += (double)((x.x < 0.f ? x.x : 0.f) * l.x + (x.x < 0.f ? 0.f : x.x) * u.x);
-        s[(2 * w + 1) % 4] += (double)((x.y < 0.f ? x.y : 0.f) * l.y + (x.y < 0.f ? 0.f : x.y) * u.y);
+        // the larger of the two products of each dim, exact in fp32
+        s[(2 * w) % 4] += (double)(x.x * (x.x < 0.f ? l.x : u.x));
+        s[(2 * w + 1) % 4] += (double)(x.y * (x.y < 0.f ? l.y : u.y));
       }
     }
   }
   double t = (s[0] + s[1]) + (s[2] + s[3]);
   t += __shfl_xor_sync(0xffffffffu, t, 1);
   t += __shfl_xor_sync(0xffffffffu, t, 2);
-  t = t < (double)kSelTop ? fmax(t, -(double)kSelTop) : (double)kSelTop;
-  if (h >= G) t = -(double)kSelTop;
+  t = h < G ? fmax(t, -(double)kSelTop) : -(double)kSelTop;
 #pragma unroll
   for (int m = 4; m < 32; m <<= 1) t = fmax(t, __shfl_xor_sync(0xffffffffu, t, m));
   return t;
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
       float s = fmax_nan(s0, s1);
       s = fmax_nan(s, __shfl_xor_sync(0xffffffffu, s, 1));
       s = fmax_nan(s, __shfl_xor_sync(0xffffffffu, s, 2));
-      s = s < kSelTop ? fmaxf(s, -kSelTop) : kSelTop;
+      s = fmaxf(fminf(s, kSelTop), -kSelTop);  // not a number: kSelTop
       const int i = (tile + t * step) * 16 + 8 * f + r;
       if (c == 0 && i < nblk) {
         if (!ok[t][f]) {
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
           for (unsigned todo = __ballot_sync(0xffffffffu, sk <= whi && sk >= wlo); todo; todo &= todo - 1, ++at) {
             if (at % NW != warp) continue;
             const int k = k0 + __ffs(todo) - 1;
-            const double x = exact(s_wi[k]);
+            const double x = s_ws[k] < kSelTop ? exact(s_wi[k]) : (double)kSelTop;
             if (lane == 0) s_wd[k] = x;
           }
         }
@@ -904,7 +904,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) paged_kv_block_select_kernel(con
         if (i < i1 && !in) s_score[i] = s > whi ? INFINITY : -INFINITY;
         for (unsigned todo = __ballot_sync(0xffffffffu, in); todo; todo &= todo - 1) {
           const int k = ib + __ffs(todo) - 1;
-          const double x = exact(k);
+          const float sk = __shfl_sync(0xffffffffu, s, k - ib);
+          const double x = center + (double)sk < (double)kSelTop ? exact(k) : (double)kSelTop;
           if (lane == 0) s_score[k] = (float)(x - next);
         }
       }

@@ -148,10 +148,9 @@ __global__ void __launch_bounds__(SharedTcTraits<BS, KVB, HD>::THREADS, 1)
     return (tok0 + r / G) * Hq + g * G + r % G;
   };
   int L = ch.len;
-  const long long row_tokens = (long long)P.max_blocks_per_seq * BS;  // (may pass 32 bits)
-  if (L > row_tokens) {
+  if (past_row<BS>(P, L)) {
     if (threadIdx.x == 0) record_error(P.error_word, kErrBadBlock);
-    L = (int)row_tokens;
+    L = P.max_blocks_per_seq * BS;
   }
   const int PS = P.partition_size;
   const int t0 = j * PS;
