@@ -1230,12 +1230,12 @@ PartPlan plan_own(const Shape& s, int q_len, int kv_fp8) {
 // after the SMs came free, contexts being 0.55 of their bound and a CTA's start
 // and end as long as reading 28 KB (147); a partition of all rows costs its fp32
 // outputs twice at 6 MB/us.  `units` is the expected number.
-//   64 x 32/8 heads, 4096 shared + up to 1024 own tokens: 37.6 us with four
-//   partitions, 44.2 with eight; 256 x 28/4, 32768 + up to 512: 113 with four,
-//   117 with five; without own contexts, five: 91; 48 x 4 tokens x 28/4, E4M3,
-//   2 x 8192 + up to 512: 49 with four, 53.5 with five.  (Below half the
-//   estimate is too rough: 128 x 28/4, 2 x 16384 + up to 4096: 126 with two of
-//   seven, 117 with seven, 110 with four.)
+//   64 x 32/8 heads, 4096 shared + up to 1024 own tokens: 37 us with four
+//   partitions, 43 with eight; 256 x 28/4, 32768 + up to 512: 111 with four,
+//   114 with five; without own contexts 107 with four, 90 with five; 48 x 4
+//   tokens x 28/4, E4M3, 2 x 8192 + up to 512: 46 with four, 52 with five.
+//   (Below half the estimate is too rough: 128 x 28/4, 2 x 16384 + up to 4096:
+//   122 with two of seven, 115 with seven, 110 with four.)
 long long shared_split(const Shape& s, int q_len, int max_prefix_len, int kv_fp8, int rows, double units, int sms,
                        long long most) {
   const PartPlan op = plan_own(s, q_len, kv_fp8);
@@ -1488,7 +1488,7 @@ pkd_status prefix_impl(const void* q, const void* k_cache, const void* v_cache, 
   // that one's CTAs have started, and takes the SMs it leaves and then the ones
   // it frees.  (It reads nothing that grid writes, and that grid starts after
   // all work before the call.)  256 x 28 query heads over 32768 shared tokens:
-  // 121 us; with the own contexts first, 129; one after the other, 139.
+  // 111 us; one after the other, 143.
   if (pre.np > 0 && (st = run(pre, static_cast<unsigned char*>(workspace) + own_bytes, true)) != PKD_OK) return st;
   if (own.np > 0 && (st = run(own, workspace, false)) != PKD_OK) return st;
   return launch_merge(head_dim, m, stream);

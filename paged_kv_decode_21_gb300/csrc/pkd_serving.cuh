@@ -26,7 +26,7 @@ constexpr uint32_t kErrBadPosition = 8u;  // a rotation position outside the tab
 //
 // Bound by HBM: every byte is moved once.  CTAs of 128 threads, sixteen heads
 // at D = 128, keep more tokens in different phases on an SM than 256: prompts
-// of 26k tokens, 40 q and 8 kv heads, 133 against 155 us, 6.2 TB/s.
+// of 28842 tokens, 40 q and 8 kv heads, 133 against 155 us, 6.2 TB/s.
 struct RopeAppendParams {
   const __half *q, *k, *v;         // token t's heads at q + t * q_stride (elements), head_dim apart
   long long q_stride, k_stride, v_stride, q_out_stride;

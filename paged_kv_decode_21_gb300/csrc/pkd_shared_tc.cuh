@@ -29,7 +29,13 @@
 // P -> P V -> free S buffer -> Q K^T of one issuing warp, in which every test
 // of a barrier takes over a hundred cycles while the MMAs stream operands from
 // shared memory.  (One 128-token S buffer per row tile, a third less shared-
-// memory traffic but S, softmax and P V in one chain, took 1.4 times the time.)
+// memory traffic but S, softmax and P V in one chain, was slower: 179 us for that
+// call where two of 64 first took 151.)
+//
+// Rounding.  P is rounded to fp16, once, for P V: kind::f16 takes fp16 operands,
+// and V is fp16 (or widened to it).  That is 2^-11 of each weight, as in the other
+// tensor-core decode kernels; the sums of the weights, O, the statistics and the
+// partials are fp32, the sums of P before its rounding.
 // A CTA's start and end take 8 us: the group's lengths 1.1, the first tiles and
 // Q 4, the last 64 tokens' chain and the outputs 3.
 //
