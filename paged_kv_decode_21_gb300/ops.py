@@ -799,7 +799,7 @@ def paged_kv_block_bounds(k_cache, block_tables, context_lens, bounds, start_len
     B = context_lens.shape[0]
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     bt, MB = _table(block_tables, "block_tables", B, dev)
-    most = MB * BS if max_new_tokens is None else int(max_new_tokens)
+    most = min(MB * BS, 0x7FFFFFFF) if max_new_tokens is None else int(max_new_tokens)
     sl = None if start_lens is None else _on(start_lens, "start_lens", _I32, (B,), dev)
     st = _lib.paged_kv_block_bounds(kc, bt, cl, sl, bo, B, Hkv, D, BS, NB,
                                     MB, most, 1 if fp8 else 0, _word(error_word, dev), _raw_stream(stream, dev))

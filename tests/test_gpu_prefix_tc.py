@@ -61,6 +61,7 @@ def verify(p, out, scale, BS, fp8, longest):
     check(out, ref, mag, longest, values(p[2]).abs().nan_to_num(0.0, 0.0).max().item() * scales(fp8)[1])
 
 
+@pytest.mark.filterwarnings("ignore:DEBUG")  # torch's own, of the graph's description
 @pytest.mark.parametrize("shape,plen", [(s, n) for s in SHAPES for n in (1, 33, 4001)]
                          + [(s, n) for s in NARROW for n in (1900, 4001)])
 def test_the_calls_here_run_the_shared_context_kernel(shape, plen, tmp_path):

@@ -175,3 +175,21 @@ def test_lengths_are_read_in_the_order_of_the_given_stream(step, name, which):
     torch.cuda.synchronize()
     for x, w in zip(out, want):
         assert torch.equal(x, w)
+
+
+@pytest.mark.parametrize("which", ["torch", "raw"])
+@pytest.mark.parametrize("name", CALLS)
+def test_capture_of_a_call_that_makes_its_buffers(step, name, which):
+    """A call captured on the stream it is given, its results and workspace from the graph's own memory."""
+    want = alone(step, name)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = getattr(step, name)(stream=given(which, side), **step.known(name))
+    for _ in range(2):
+        for x in out:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, w in zip(out, want):
+            assert torch.equal(x, w)

@@ -95,3 +95,9 @@ def test_workspaces_are_kept_for_the_given_stream(step, name, which, monkeypatch
     side.synchronize()
     for x, w in zip(out, want):
         assert torch.equal(x, w)
+
+
+@pytest.mark.parametrize("which", ["torch", "raw"])
+@pytest.mark.parametrize("name", CALLS)
+def test_capture(step, name, which):
+    streams.test_capture_of_a_call_that_makes_its_buffers(step, name, which)

@@ -63,6 +63,8 @@ def test_bounds_choice_and_listed_decode(data):
     ops.paged_kv_block_bounds(kc, bt, cl, b1, error_word=ew)
     ops.paged_kv_block_bounds(kc, table, cl, b2, max_new_tokens=300, error_word=ew)
     assert torch.equal(b1, b2)
+    ops.paged_kv_block_bounds(kc, table, cl, b2.zero_(), error_word=ew)  # the row's own length as the bound
+    assert torch.equal(b1, b2)
     lists, counts = ops.paged_kv_block_select(q, b2, table, cl, 6, 16, error_word=ew)
     want = ops.paged_kv_block_select(q, b1, bt, cl, 6, 16, error_word=ew)
     assert torch.equal(lists, want[0]) and torch.equal(counts, want[1])
