@@ -775,6 +775,219 @@ size_t paged_decode_blocks_workspace_size(int num_seqs, int num_q_heads, int num
                                           int block_size, int max_listed);
 
 /*
+ * paged_kv_append_rope_axes -- paged_kv_append_rope where the rotation has
+ * several axes (time, height and width of images and video): pair i of a head
+ * turns by the token's position on axis a = pair_axes[i],
+ *   p = positions[a][t],  c_i = rope_table[p][i],  s_i = rope_table[p][rotary_dim / 2 + i]
+ * and everything else is as there (the logical position alone says where k and
+ * v are written).
+ *
+ *   pair_axes      device int32 [rotary_dim / 2], 16-byte aligned, each in
+ *                  [0, num_axes): which axis a pair goes by, in any order
+ *   positions      device int32 [num_axes][num_tokens]
+ *   num_axes       1..PKD_MAX_AXES (PKD_ERR_UNSUPPORTED above)
+ *   other arguments as for paged_kv_append_rope.  With rotary_dim 0,
+ *   rope_table, pair_axes and positions may be NULL
+ * A token with a position outside the table on any axis that a pair goes by is
+ * skipped (PKD_DEVERR_BAD_POSITION), and so is every token when pair_axes names
+ * an axis that there is not.
+ */
+#define PKD_MAX_AXES 8
+pkd_status paged_kv_append_rope_axes(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                     long long k_stride, long long v_stride, const float* rope_table,
+                                     const int32_t* pair_axes, const int32_t* token_starts, const int32_t* positions,
+                                     const int32_t* block_tables, const int32_t* context_lens, void* q_out,
+                                     long long q_out_stride, void* k_cache, void* v_cache, int num_tokens,
+                                     int num_seqs, int num_axes, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int rotary_dim, int interleaved, int max_positions, int block_size,
+                                     int num_blocks, int max_blocks_per_seq, int* error_word, cudaStream_t stream);
+
+/* paged_kv_append_rope_axes_fp8 -- the same into E4M3 caches (scales as for
+   paged_kv_append_rope_fp8). */
+pkd_status paged_kv_append_rope_axes_fp8(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                         long long k_stride, long long v_stride, const float* rope_table,
+                                         const int32_t* pair_axes, const int32_t* token_starts,
+                                         const int32_t* positions, const int32_t* block_tables,
+                                         const int32_t* context_lens, void* q_out, long long q_out_stride,
+                                         void* k_cache, void* v_cache, int num_tokens, int num_seqs, int num_axes,
+                                         int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                                         int interleaved, int max_positions, int block_size, int num_blocks,
+                                         int max_blocks_per_seq, float k_scale, float v_scale, int* error_word,
+                                         cudaStream_t stream);
+
+/*
+ * Four-bit caches.  Every 16 neighbouring dims of a token's key (or value) in
+ * one kv head share a scale: dim d of a group has
+ *   value = (u_d - 8) * e4m3(group's scale byte) * k_scale      (v_scale for V)
+ * with u_d a code of 4 bits and k_scale, v_scale one factor a cache, as for
+ * E4M3 caches.  9 bits for two values, 0.28 of fp16.  A cache is
+ *   uint8 [num_blocks][num_kv_heads][tile], tile = block_size * head_dim * 9 / 16 bytes:
+ *   codes   [head_dim / 32][block_size][16]: the 32 dims of a slab and token, dims
+ *           2i and 2i + 1 in the low and the high half of byte i
+ *   scales  [block_size][head_dim / 16], E4M3, not negative and not a NaN
+ * so that a (block, kv head) is one run of bytes, one asynchronous copy, and the
+ * eight rows of a slab that a matrix load takes lie side by side.  head_dim 64
+ * or 128, block_size 16 or 32; caches 16-byte aligned.
+ *
+ * paged_kv_append_rope_int4 -- paged_kv_append_rope (and _axes) into 4-bit
+ * caches.  With x the rotated fp32 key, or the value, and a = max |x| over the
+ * group,
+ *   scale byte = e4m3(a / (7 k_scale)), to nearest even, at most 448
+ *   step = e4m3(scale byte) * k_scale,  u = 8 + clamp(rint(x / step), -7, 7)   (8 where step is 0)
+ * in IEEE fp32 with every operation rounded by itself, products of the rotation
+ * too, so that the codes are reproducible.  Codes 0 are never written.  k and v
+ * must be finite.
+ *
+ *   pair_axes      as for paged_kv_append_rope_axes, or NULL: one axis, and
+ *                  positions int32 [num_tokens] or NULL as for
+ *                  paged_kv_append_rope (num_axes is then 1)
+ *   head_dim       64 or 128; rotary_dim a multiple of 32 in [0, head_dim]
+ *                  (PKD_ERR_UNSUPPORTED for other multiples of 16)
+ *   block_size     16 or 32
+ *   k_scale, v_scale  finite, > 0
+ */
+pkd_status paged_kv_append_rope_int4(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                     long long k_stride, long long v_stride, const float* rope_table,
+                                     const int32_t* pair_axes, const int32_t* token_starts, const int32_t* positions,
+                                     const int32_t* block_tables, const int32_t* context_lens, void* q_out,
+                                     long long q_out_stride, void* k_cache, void* v_cache, int num_tokens,
+                                     int num_seqs, int num_axes, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int rotary_dim, int interleaved, int max_positions, int block_size,
+                                     int num_blocks, int max_blocks_per_seq, float k_scale, float v_scale,
+                                     int* error_word, cudaStream_t stream);
+
+/*
+ * paged_kv_read_int4 -- the values of runs of tokens in 4-bit caches, as fp16
+ * rows (for a prompt's dense attention, or to move to another cache): token j
+ * of sequence b, logical position start_lens[b] + j, is row t = token_starts[b] + j
+ *   k_out[t][g][:] = value of K, rounded once to fp16;  v_out likewise
+ *
+ *   start_lens     device int32 [num_seqs]
+ *   token_starts   as for paged_kv_append_rope (NULL: num_tokens / num_seqs each)
+ *   k_out, v_out   device fp16, tokens k_out_stride and v_out_stride elements apart
+ *                  (multiples of 8, at least num_kv_heads * head_dim), 16-byte aligned
+ * A token without a valid block is skipped (PKD_DEVERR_BAD_BLOCK), and so are rows
+ * at or past token_starts[num_seqs].  Whether a sequence is that long is the
+ * caller's to know: what was never written is read as it is.
+ */
+pkd_status paged_kv_read_int4(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                              const int32_t* start_lens, const int32_t* token_starts, void* k_out, void* v_out,
+                              long long k_out_stride, long long v_out_stride, int num_tokens, int num_seqs,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                              float k_scale, float v_scale, int* error_word, cudaStream_t stream);
+
+/*
+ * paged_decode_attention_int4 -- decode over 4-bit caches: arguments as for
+ * paged_decode_attention_fp8 (q_len 1: single-query decode; above: causal among
+ * the new tokens, as in paged_decode_attention_multi).
+ *   workspace      paged_decode_int4_workspace_size(...) bytes, 256-byte aligned
+ *                  (NULL where that is 0)
+ * Codes times scales are exact in fp16, so the products see the cache's own
+ * values; the softmax weights are rounded to fp16 for the second product as on
+ * the other tensor-core paths.
+ */
+pkd_status paged_decode_attention_int4(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_tables, const int32_t* context_lens, void* out,
+                                       int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                       int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
+                                       float scale, float k_scale, float v_scale, int partition_size, void* workspace,
+                                       size_t workspace_bytes, int* error_word, cudaStream_t stream);
+
+/* Workspace bytes of paged_decode_attention_int4 (0 = none, or an invalid shape). */
+size_t paged_decode_int4_workspace_size(int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                        int block_size, int max_context_len, int partition_size);
+
+/* What a cache holds, for the calls that take any. */
+typedef enum {
+  PKD_KV_FP16 = 0, /* fp16 [num_blocks][num_kv_heads][block_size][head_dim] */
+  PKD_KV_E4M3 = 1, /* E4M3 bytes in the same order */
+  PKD_KV_INT4 = 2  /* 4-bit tiles, see paged_kv_append_rope_int4 */
+} pkd_kv_type;
+
+/*
+ * paged_kv_attention_weights -- how much the queries attend to every cached
+ * token, gathered over the calls: for every sequence b, kv head g and token
+ * t < L = context_lens[b] in block p = block_tables[b][t / block_size]
+ *   w_t = sum over query tokens j < q_len and heads h of group g of softmax(s_jh)_t
+ *   s_jht = scale * k_scale * dot(q[b][j][h], K_t),  t <= L - q_len + j   (causal, as in
+ *           paged_decode_attention_multi)
+ *   weights[p][g][t % block_size] = (t < start_lens[b] ? decay * weights[p][g][t % block_size] : 0) + w_t
+ * so tokens from start_lens[b] on are new, and what their place held before does
+ * not count.  A query that sees no token gives no weight.  Only K is read.
+ *
+ *   weights        device fp32 [num_blocks][num_kv_heads][block_size], updated
+ *                  in place; places of other tokens are left as they are.  A
+ *                  block must belong to one sequence of the call alone
+ *   start_lens     device int32 [num_seqs] or NULL: no token is new
+ *   decay          finite, in [0, 1]: 1 gathers, 0 keeps this call's weights
+ *                  alone (what was there is not read)
+ *   kv_type        pkd_kv_type of k_cache; k_scale finite, > 0 (1 for fp16)
+ *   q              device fp16 [num_seqs][q_len][num_q_heads][head_dim]
+ *   workspace      paged_kv_attention_weights_workspace_size(...) bytes,
+ *                  256-byte aligned (row statistics, and the scores of few rows)
+ *   max_context_len  at most 2^30; other arguments as for
+ *                  paged_decode_attention_multi
+ * Sums are in fp32, in an order that does not depend on the run.
+ */
+pkd_status paged_kv_attention_weights(const void* q, const void* k_cache, const int32_t* block_tables,
+                                      const int32_t* context_lens, const int32_t* start_lens, float* weights,
+                                      int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                      int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
+                                      float scale, float k_scale, float decay, int kv_type, void* workspace,
+                                      size_t workspace_bytes, int* error_word, cudaStream_t stream);
+
+/* Workspace bytes of paged_kv_attention_weights (0 for an empty batch or an invalid shape). */
+size_t paged_kv_attention_weights_workspace_size(int num_seqs, int q_len, int num_q_heads, int num_kv_heads,
+                                                 int head_dim, int block_size, int max_context_len);
+
+/*
+ * paged_kv_token_select -- the tokens worth keeping: of sequence b's L =
+ * context_lens[b] tokens, for every kv head g, the first sink_tokens, the last
+ * recent_tokens, and of the others those with the largest weights, ties to the
+ * lowest position, max_kept in all; every token where L <= max_kept.
+ *   weights        device fp32 [num_blocks][num_kv_heads][block_size] (as
+ *                  gathered by paged_kv_attention_weights; a weight that is not a
+ *                  number counts as the largest)
+ *   kept           device int32 [num_seqs][num_kv_heads][max_kept]: the chosen
+ *                  positions in ascending order, then -1
+ *   kept_lens      device int32 [num_seqs]: how many, min(L, max_kept)
+ *   max_context_len  host upper bound of context_lens
+ *   max_kept >= 1; sink_tokens + recent_tokens <= max_kept; block_size any
+ *                  positive size
+ * Tokens of a block outside the pool are reported (PKD_DEVERR_BAD_BLOCK) and
+ * come last.
+ */
+pkd_status paged_kv_token_select(const float* weights, const int32_t* block_tables, const int32_t* context_lens,
+                                 int32_t* kept, int32_t* kept_lens, int num_seqs, int num_kv_heads, int block_size,
+                                 int num_blocks, int max_blocks_per_seq, int max_context_len, int max_kept,
+                                 int sink_tokens, int recent_tokens, int* error_word, cudaStream_t stream);
+
+/*
+ * paged_kv_compact -- the kept tokens' rows, copied into blocks of their own:
+ * for every sequence b, kv head g and i < kept_lens[b], with t = kept[b][g][i],
+ *   row i of the context that new_tables[b] lists = row t of the one that block_tables[b] lists
+ * in K, V and (unless NULL) weights.  The caller then takes new_tables and
+ * kept_lens in place of the tables and lengths, and frees the old blocks: they
+ * are only read, so blocks that other sequences share stay whole.  Keys keep the
+ * rotation they were written with.
+ *
+ *   k_cache, v_cache  of kv_type, both tables name blocks of them; rows of the
+ *                  new blocks past kept_lens[b] are left as they are
+ *   weights        device fp32 [num_blocks][num_kv_heads][block_size] or NULL
+ *   kept, kept_lens  as written by paged_kv_token_select; a position outside
+ *                  [0, context_lens[b]) is skipped (PKD_DEVERR_BAD_BLOCK), and
+ *                  kept_lens[b] counts up to max_kept and the new row's room
+ *   new_tables     device int32 [num_seqs][max_new_blocks]: blocks that no table
+ *                  of the call reads, each once
+ *   head_dim 64 or 128, block_size 16 or 32
+ */
+pkd_status paged_kv_compact(void* k_cache, void* v_cache, float* weights, const int32_t* block_tables,
+                            const int32_t* context_lens, const int32_t* kept, const int32_t* kept_lens,
+                            const int32_t* new_tables, int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, int max_blocks_per_seq, int max_kept, int max_new_blocks, int kv_type,
+                            int* error_word, cudaStream_t stream);
+
+/*
  * pkd_selftest_bounded_wait -- exercises the failure path of the library's
  * bounded waits without faulting or hanging the GPU: launches one CTA that
  * waits on a shared-memory barrier nothing will complete; after budget_ns

@@ -11,6 +11,7 @@
 #include "../../include/paged_decode.h"
 #include "pkd_aux.cuh"
 #include "pkd_decode_mma.cuh"
+#include "pkd_int4_launch.h"
 #include "pkd_launch.cuh"
 #include "pkd_src_launch.h"
 #include "pkd_tc_launch.h"
@@ -1557,9 +1558,114 @@ pkd_status blocks_impl(const void* q, const void* k_cache, const void* v_cache, 
   return launch_merge(head_dim, m, stream);
 }
 
+// 4-bit caches: partition_size as paged_decode_attention_ex takes it (0: the
+// automatic one).
+PartPlan plan_int4(const Shape& s, int q_len, int partition_size) {
+  PartPlan p;
+  const int G = s.num_q_heads / s.num_kv_heads;
+  const int qc = pkd::int4_query_chunk(q_len, G);
+  p.chunks = (q_len + qc - 1) / qc;
+  p.P = (int)round_up((size_t)std::max(1, s.max_context_len), 32);
+  p.np = 1;
+  const long long units = (long long)s.num_seqs * s.num_kv_heads * p.chunks;
+  if (partition_size > 0) {
+    p.P = partition_size;
+  } else if (partition_size == 0 && units > 0) {
+    int sms = sm_count();
+    if (sms <= 0) sms = 148;
+    const long long slots = (long long)sms * pkd::kInt4CtasPerSm;
+    long long q = kMinSmallGridPartition;
+    while (q < s.max_context_len && units * ((s.max_context_len + q - 1) / q) > slots) q *= 2;
+    if (q >= s.max_context_len && units < 2 * slots) {
+      // no partition fits one wave: enough of them for four
+      const long long want = (4 * slots + units - 1) / units;
+      q = kMinAutoPartition;
+      while (q * 2 * want <= s.max_context_len) q *= 2;
+    }
+    if (q < s.max_context_len) p.P = (int)q;
+  }
+  if (s.max_context_len > p.P) p.np = (int)(((long long)s.max_context_len + p.P - 1) / p.P);
+  p.grid = units * p.np;
+  return p;
+}
+
+pkd_status check_int4(const Shape& s, int q_len, int partition_size) {
+  const pkd_status st = check_shape(s);
+  if (st != PKD_OK) return st;
+  if (q_len < 1 || s.max_context_len > kMaxPartTokens) return PKD_ERR_SHAPE;
+  if (partition_size < -1 || (partition_size > 0 && (partition_size % 32 != 0 || partition_size > kMaxPartTokens)))
+    return PKD_ERR_SHAPE;
+  if ((long long)s.num_seqs * q_len * s.num_q_heads > 0x7fffffffLL) return PKD_ERR_SHAPE;
+  return PKD_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t paged_decode_int4_workspace_size(int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                        int block_size, int max_context_len, int partition_size) {
+  if (block_size <= 0 || max_context_len < 0) return 0;
+  const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, 1,
+                (int)(((long long)max_context_len + block_size - 1) / block_size) + 1, max_context_len};
+  if (check_int4(s, q_len, partition_size) != PKD_OK) return 0;
+  const PartPlan plan = plan_int4(s, q_len, partition_size);
+  return plan.np > 1 ? layout(nullptr, num_seqs * q_len, num_q_heads, head_dim, plan.np).bytes : 0;
+}
+
+pkd_status paged_decode_attention_int4(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_tables, const int32_t* context_lens, void* out,
+                                       int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                       int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
+                                       float scale, float k_scale, float v_scale, int partition_size, void* workspace,
+                                       size_t workspace_bytes, int* error_word, cudaStream_t stream) {
+  const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
+                max_context_len};
+  pkd_status st = check_int4(s, q_len, partition_size);
+  if (st != PKD_OK) return st;
+  if (!std::isfinite(scale)) return PKD_ERR_SHAPE;
+  if (!(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f)) return PKD_ERR_SHAPE;
+  if (num_seqs == 0) return PKD_OK;
+  st = check_inputs(q, k_cache, v_cache, block_tables, context_lens);
+  if (st != PKD_OK) return st;
+  if (!out) return PKD_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(error_word, 4)) return PKD_ERR_ALIGN;
+  const PartPlan plan = plan_int4(s, q_len, partition_size);
+  if (plan.grid > 0x7fffffffLL) return PKD_ERR_SHAPE;
+  pkd::DecodeParams p = base_params(s, q, k_cache, v_cache, q_len, scale, 1, k_scale * 256.f, v_scale * 256.f,
+                                    error_word);  // 256: the kernel's scales are 2^-8 of the cache's
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.partition_size = plan.P;
+  p.max_partitions = plan.np;
+  p.q_chunks = plan.chunks;
+  p.out = static_cast<__half*>(out);
+  Workspace w{};
+  if (plan.np > 1) {
+    w = layout(workspace, num_seqs * q_len, num_q_heads, head_dim, plan.np);
+    if (!workspace) return PKD_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PKD_ERR_ALIGN;
+    if (workspace_bytes < w.bytes) return PKD_ERR_WORKSPACE;
+    p.tmp_out = w.tmp_out;
+    p.max_logits = w.max_logits;
+    p.exp_sums = w.exp_sums;
+  }
+  if (pkd::failed(pkd::launch_decode_int4(head_dim, block_size, num_q_heads / num_kv_heads, p, plan.grid, stream)))
+    return PKD_ERR_LAUNCH;
+  if (plan.np <= 1) return PKD_OK;
+  pkd::MergeParams m{};
+  m.own = merge_source(w, plan);
+  m.context_lens = context_lens;
+  m.out = static_cast<__half*>(out);
+  m.rows = num_seqs * q_len * num_q_heads;
+  m.q_len = q_len;
+  m.num_q_heads = num_q_heads;
+  m.num_kv_heads = num_kv_heads;
+  m.block_size = block_size;
+  m.skip_single = 1;
+  return launch_merge(head_dim, m, stream);
+}
 
 size_t paged_decode_prefix_workspace_size(int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
                                           int block_size, int num_groups, int max_prefix_len, int max_context_len) {

@@ -1,5 +1,6 @@
-// pkd_serving.cu -- C entry points of the rotated append, the block bounds and
-// the block choice: argument checks and launches.
+// pkd_serving.cu -- C entry points of the rotated append (fp16, E4M3 and 4-bit
+// caches, one position axis or several), the read-back of 4-bit rows, the block
+// bounds and the block choice: argument checks and launches.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -22,8 +23,10 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
                        const int32_t* positions, const int32_t* block_tables, const int32_t* context_lens, void* q_out,
                        long long q_out_stride, void* k_cache, void* v_cache, int num_tokens, int num_seqs,
                        int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim, int interleaved,
-                       int max_positions, int block_size, int num_blocks, int max_blocks_per_seq, bool fp8,
-                       float k_scale, float v_scale, int* error_word, cudaStream_t stream) {
+                       int max_positions, int block_size, int num_blocks, int max_blocks_per_seq, pkd_kv_type kv,
+                       float k_scale, float v_scale, int* error_word, cudaStream_t stream, bool axes = false,
+                       const int32_t* pair_axes = nullptr, int num_axes = 1) {
+  const bool fp8 = kv != PKD_KV_FP16;  // a cache with scales
   if (num_tokens < 0 || num_seqs < 0 || num_q_heads < 0 || num_kv_heads <= 0 || head_dim <= 0 || rotary_dim < 0 ||
       block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0)
     return PKD_ERR_SHAPE;
@@ -32,6 +35,11 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   if (rotary_dim > 0 && max_positions <= 0) return PKD_ERR_SHAPE;
   if (fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f))
     return PKD_ERR_SHAPE;
+  if (num_axes < 1) return PKD_ERR_SHAPE;
+  if (num_axes > PKD_MAX_AXES || (!axes && num_axes != 1)) return PKD_ERR_UNSUPPORTED;
+  if (kv == PKD_KV_INT4 &&
+      ((head_dim != 64 && head_dim != 128) || rotary_dim % 32 != 0 || (block_size != 16 && block_size != 32)))
+    return PKD_ERR_UNSUPPORTED;
   if (num_tokens == 0 || num_seqs == 0) return PKD_OK;
   if (!token_starts && num_tokens % num_seqs != 0) return PKD_ERR_SHAPE;
   const long long q_row = (long long)num_q_heads * head_dim, kv_row = (long long)num_kv_heads * head_dim;
@@ -39,11 +47,11 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   if (k_stride < kv_row || v_stride < kv_row) return PKD_ERR_SHAPE;
   if (!k_new || !v_new || !block_tables || !context_lens || !k_cache || !v_cache) return PKD_ERR_NULL;
   if (num_q_heads > 0 && (!q || !q_out)) return PKD_ERR_NULL;
-  if (rotary_dim > 0 && !rope_table) return PKD_ERR_NULL;
+  if (rotary_dim > 0 && (!rope_table || (axes && (!pair_axes || !positions)))) return PKD_ERR_NULL;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(rope_table, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
-      !aligned(token_starts, 4) || !aligned(positions, 4) || !aligned(error_word, 4) || k_stride % 8 != 0 ||
-      v_stride % 8 != 0)
+      !aligned(token_starts, 4) || !aligned(positions, 4) || !aligned(pair_axes, 16) || !aligned(error_word, 4) ||
+      k_stride % 8 != 0 || v_stride % 8 != 0)
     return PKD_ERR_ALIGN;
   if (num_q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8 != 0 || q_out_stride % 8 != 0))
     return PKD_ERR_ALIGN;
@@ -60,6 +68,8 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   p.table = rope_table;
   p.token_starts = token_starts;
   p.positions = positions;
+  p.pair_axes = pair_axes;
+  p.num_axes = num_axes;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.q_out = static_cast<__half*>(q_out);
@@ -78,10 +88,14 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.error_word = error_word;
-  auto* fn = fp8 ? (interleaved ? pkd::paged_kv_append_rope_kernel<true, true>
-                                : pkd::paged_kv_append_rope_kernel<true, false>)
-                 : (interleaved ? pkd::paged_kv_append_rope_kernel<false, true>
-                                : pkd::paged_kv_append_rope_kernel<false, false>);
+  axes = axes && rotary_dim > 0;
+#define PKD_APPEND(KVB_)                                                                              \
+  (interleaved ? (axes ? pkd::paged_kv_append_rope_kernel<KVB_, true, true>                           \
+                       : pkd::paged_kv_append_rope_kernel<KVB_, true, false>)                         \
+               : (axes ? pkd::paged_kv_append_rope_kernel<KVB_, false, true>                          \
+                       : pkd::paged_kv_append_rope_kernel<KVB_, false, false>))
+  auto* fn = kv == PKD_KV_INT4 ? PKD_APPEND(0) : (kv == PKD_KV_E4M3 ? PKD_APPEND(1) : PKD_APPEND(2));
+#undef PKD_APPEND
   fn<<<(unsigned)num_tokens, pkd::kRopeThreads, 0, stream>>>(p);
   return launched();
 }
@@ -112,7 +126,7 @@ pkd_status paged_kv_append_rope(const void* q, const void* k_new, const void* v_
   return append_rope(q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, token_starts, positions, block_tables,
                      context_lens, q_out, q_out_stride, k_cache, v_cache, num_tokens, num_seqs, num_q_heads,
                      num_kv_heads, head_dim, rotary_dim, interleaved, max_positions, block_size, num_blocks,
-                     max_blocks_per_seq, false, 1.f, 1.f, error_word, stream);
+                     max_blocks_per_seq, PKD_KV_FP16, 1.f, 1.f, error_word, stream);
 }
 
 pkd_status paged_kv_append_rope_fp8(const void* q, const void* k_new, const void* v_new, long long q_stride,
@@ -126,7 +140,98 @@ pkd_status paged_kv_append_rope_fp8(const void* q, const void* k_new, const void
   return append_rope(q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, token_starts, positions, block_tables,
                      context_lens, q_out, q_out_stride, k_cache, v_cache, num_tokens, num_seqs, num_q_heads,
                      num_kv_heads, head_dim, rotary_dim, interleaved, max_positions, block_size, num_blocks,
-                     max_blocks_per_seq, true, k_scale, v_scale, error_word, stream);
+                     max_blocks_per_seq, PKD_KV_E4M3, k_scale, v_scale, error_word, stream);
+}
+
+pkd_status paged_kv_append_rope_axes(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                     long long k_stride, long long v_stride, const float* rope_table,
+                                     const int32_t* pair_axes, const int32_t* token_starts, const int32_t* positions,
+                                     const int32_t* block_tables, const int32_t* context_lens, void* q_out,
+                                     long long q_out_stride, void* k_cache, void* v_cache, int num_tokens,
+                                     int num_seqs, int num_axes, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int rotary_dim, int interleaved, int max_positions, int block_size,
+                                     int num_blocks, int max_blocks_per_seq, int* error_word, cudaStream_t stream) {
+  return append_rope(q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, token_starts, positions, block_tables,
+                     context_lens, q_out, q_out_stride, k_cache, v_cache, num_tokens, num_seqs, num_q_heads,
+                     num_kv_heads, head_dim, rotary_dim, interleaved, max_positions, block_size, num_blocks,
+                     max_blocks_per_seq, PKD_KV_FP16, 1.f, 1.f, error_word, stream, true, pair_axes, num_axes);
+}
+
+pkd_status paged_kv_append_rope_axes_fp8(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                         long long k_stride, long long v_stride, const float* rope_table,
+                                         const int32_t* pair_axes, const int32_t* token_starts,
+                                         const int32_t* positions, const int32_t* block_tables,
+                                         const int32_t* context_lens, void* q_out, long long q_out_stride,
+                                         void* k_cache, void* v_cache, int num_tokens, int num_seqs, int num_axes,
+                                         int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                                         int interleaved, int max_positions, int block_size, int num_blocks,
+                                         int max_blocks_per_seq, float k_scale, float v_scale, int* error_word,
+                                         cudaStream_t stream) {
+  return append_rope(q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, token_starts, positions, block_tables,
+                     context_lens, q_out, q_out_stride, k_cache, v_cache, num_tokens, num_seqs, num_q_heads,
+                     num_kv_heads, head_dim, rotary_dim, interleaved, max_positions, block_size, num_blocks,
+                     max_blocks_per_seq, PKD_KV_E4M3, k_scale, v_scale, error_word, stream, true, pair_axes, num_axes);
+}
+
+pkd_status paged_kv_append_rope_int4(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                     long long k_stride, long long v_stride, const float* rope_table,
+                                     const int32_t* pair_axes, const int32_t* token_starts, const int32_t* positions,
+                                     const int32_t* block_tables, const int32_t* context_lens, void* q_out,
+                                     long long q_out_stride, void* k_cache, void* v_cache, int num_tokens,
+                                     int num_seqs, int num_axes, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int rotary_dim, int interleaved, int max_positions, int block_size,
+                                     int num_blocks, int max_blocks_per_seq, float k_scale, float v_scale,
+                                     int* error_word, cudaStream_t stream) {
+  return append_rope(q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, token_starts, positions, block_tables,
+                     context_lens, q_out, q_out_stride, k_cache, v_cache, num_tokens, num_seqs, num_q_heads,
+                     num_kv_heads, head_dim, rotary_dim, interleaved, max_positions, block_size, num_blocks,
+                     max_blocks_per_seq, PKD_KV_INT4, k_scale, v_scale, error_word, stream, pair_axes != nullptr,
+                     pair_axes, num_axes);
+}
+
+pkd_status paged_kv_read_int4(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                              const int32_t* start_lens, const int32_t* token_starts, void* k_out, void* v_out,
+                              long long k_out_stride, long long v_out_stride, int num_tokens, int num_seqs,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                              float k_scale, float v_scale, int* error_word, cudaStream_t stream) {
+  if (num_tokens < 0) return PKD_ERR_SHAPE;
+  const pkd_status st = check_blocks(num_seqs, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq);
+  if (st != PKD_OK) return st;
+  if (!(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f)) return PKD_ERR_SHAPE;
+  if (num_tokens == 0 || num_seqs == 0) return PKD_OK;
+  if (!token_starts && num_tokens % num_seqs != 0) return PKD_ERR_SHAPE;
+  const long long row = (long long)num_kv_heads * head_dim;
+  if (k_out_stride < row || v_out_stride < row) return PKD_ERR_SHAPE;
+  if (!k_cache || !v_cache || !block_tables || !start_lens || !k_out || !v_out) return PKD_ERR_NULL;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+      !aligned(block_tables, 4) || !aligned(start_lens, 4) || !aligned(token_starts, 4) || !aligned(error_word, 4) ||
+      k_out_stride % 8 != 0 || v_out_stride % 8 != 0)
+    return PKD_ERR_ALIGN;
+  pkd::Int4ReadParams p{};
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.start_lens = start_lens;
+  p.token_starts = token_starts;
+  p.k_out = static_cast<__half*>(k_out);
+  p.v_out = static_cast<__half*>(v_out);
+  p.k_stride = k_out_stride;
+  p.v_stride = v_out_stride;
+  p.num_tokens = num_tokens;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = num_kv_heads;
+  p.num_blocks = num_blocks;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.error_word = error_word;
+  const unsigned grid = (unsigned)(((long long)num_tokens + pkd::kInt4ReadWarps - 1) / pkd::kInt4ReadWarps);
+  auto* fn = head_dim == 128 ? (block_size == 16 ? pkd::paged_kv_read_int4_kernel<128, 16>
+                                                 : pkd::paged_kv_read_int4_kernel<128, 32>)
+                             : (block_size == 16 ? pkd::paged_kv_read_int4_kernel<64, 16>
+                                                 : pkd::paged_kv_read_int4_kernel<64, 32>);
+  fn<<<grid, 32 * pkd::kInt4ReadWarps, 0, stream>>>(p);
+  return launched();
 }
 
 pkd_status paged_kv_block_bounds(const void* k_cache, const int32_t* block_tables, const int32_t* context_lens,

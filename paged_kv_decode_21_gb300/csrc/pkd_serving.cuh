@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 #include "pkd_decode_mma.cuh"
+#include "pkd_int4.cuh"
 
 namespace pkd {
 
@@ -27,20 +28,54 @@ constexpr uint32_t kErrBadPosition = 8u;  // a rotation position outside the tab
 // Bound by HBM: every byte is moved once.  CTAs of 128 threads, sixteen heads
 // at D = 128, keep more tokens in different phases on an SM than 256: prompts
 // of 28842 tokens, 40 q and 8 kv heads, 133 against 155 us, 6.2 TB/s.
+//
+// AXES: pair i goes by the position on axis pair_axes[i], so a thread's eight
+// cosines come from up to eight rows of the table.
+//
+// KVB 0 (4-bit caches): a group of 16 dims is a thread's two chunks, or, where
+// they are R/2 apart, one chunk of each of two neighbouring lanes, which
+// exchange their maxima.  Every operation is rounded by itself, so that the
+// codes do not depend on which products a compiler fuses.
 struct RopeAppendParams {
   const __half *q, *k, *v;         // token t's heads at q + t * q_stride (elements), head_dim apart
   long long q_stride, k_stride, v_stride, q_out_stride;
   const float* table;              // [max_positions][R]: R/2 cosines, then R/2 sines
   const int32_t* token_starts;     // [num_seqs + 1], or null: num_tokens / num_seqs tokens each
-  const int32_t* positions;        // [num_tokens], or null: the logical position
+  const int32_t* positions;        // [num_tokens], or null: the logical position; AXES: [num_axes][num_tokens]
+  const int32_t* pair_axes;        // AXES: [R / 2]
   const int32_t *block_tables, *context_lens;
   __half* q_out;
   void *k_cache, *v_cache;
   int num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, rotary_dim, max_positions, block_size, num_blocks,
-      max_blocks_per_seq;
+      max_blocks_per_seq, num_axes;
   float k_scale, v_scale;
   int* error_word;
 };
+
+// Eight fp32 values as codes 8 + clamp(rint(x / step), -7, 7), value k in bits 4k ..
+__device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float step) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float q = step > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[k], step)), -7.f), 7.f) : 0.f;
+    w |= (uint32_t)((int)q + 8) << (4 * k);
+  }
+  return w;
+}
+__device__ __forceinline__ float absmax8(const float (&x)[8]) {
+  float a = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(x[k]));
+  return a;
+}
+// The scale byte of a group whose largest magnitude is a, and its step.
+__device__ __forceinline__ uint32_t int4_scale_byte(float a, float scale, float& step) {
+  uint16_t two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(__fdiv_rn(a, __fmul_rn(7.f, scale))));
+  const uint32_t byte = two & 0xFFu;
+  step = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(byte << 7))) * kInt4Unscale, scale);
+  return byte;
+}
 
 __device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d, float scale) {
   uint16_t lo, hi;
@@ -63,8 +98,9 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 constexpr int kRopeThreads = 128;
-template <bool F8, bool PAIRS>
+template <int KVB, bool PAIRS, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(const RopeAppendParams P) {
+  constexpr bool F8 = KVB == 1, I4 = KVB == 0;
   const int D = P.head_dim, R = P.rotary_dim, units = D / 16;
   const int slots = kRopeThreads / units;  // heads in flight
   const int c = threadIdx.x % units, slot = threadIdx.x / units;
@@ -102,18 +138,43 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
   const int L = P.context_lens[b];
   const long long at = (long long)L + j;  // logical position
   const long long lb = at / P.block_size;
-  const long long pos = P.positions ? P.positions[t] : at;
+  const long long pos = P.positions && !AXES ? P.positions[t] : at;
   int block = -1;
   if (L >= 0 && lb < P.max_blocks_per_seq) block = P.block_tables[(size_t)b * P.max_blocks_per_seq + lb];
   uint32_t err = 0;
   if (block < 0 || block >= P.num_blocks) err |= kErrBadBlock;
-  if (R > 0 && (pos < 0 || pos >= P.max_positions)) err |= kErrBadPosition;
+  float cs[8], sn[8];
+  if constexpr (AXES) {
+    // the thread's eight pairs: their axes, the positions there, the table's entries
+    bool off = false;
+    if (rot) {
+      const int4 a0 = reinterpret_cast<const int4*>(P.pair_axes)[2 * c];
+      const int4 a1 = reinterpret_cast<const int4*>(P.pair_axes)[2 * c + 1];
+      const int axis[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      int row[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool known = axis[i] >= 0 && axis[i] < P.num_axes;
+        row[i] = known ? P.positions[(size_t)axis[i] * P.num_tokens + t] : -1;
+        off |= row[i] < 0 || row[i] >= P.max_positions;
+        if (row[i] < 0 || row[i] >= P.max_positions) row[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float* at_row = P.table + (long long)row[i] * R + 8 * c + i;
+        cs[i] = at_row[0];
+        sn[i] = at_row[R / 2];
+      }
+    }
+    if (__syncthreads_or(off)) err |= kErrBadPosition;
+  } else {
+    if (R > 0 && (pos < 0 || pos >= P.max_positions)) err |= kErrBadPosition;
+  }
   if (err) {
     if (threadIdx.x == 0) record_error(P.error_word, err);
     return;
   }
-  float cs[8], sn[8];
-  if (rot) {
+  if (!AXES && rot) {
     const float4* row = reinterpret_cast<const float4*>(P.table + pos * R + 8 * c);
     const float4* row2 = reinterpret_cast<const float4*>(P.table + pos * R + R / 2 + 8 * c);
     const float4 a = row[0], a2 = row[1], s = row2[0], s2 = row2[1];
@@ -133,27 +194,31 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
     const bool is_q = h < P.num_q_heads, is_v = h >= P.num_q_heads + P.num_kv_heads;
     const bool turn = rot && !is_v;
     float x[8], y[8];
-    if (turn || (F8 && !is_q)) {
+    if (turn || (KVB != 2 && !is_q)) {
       unpack8(u0, x);
       unpack8(u1, y);
     }
     if (turn) {
+      // y_a = a cos - d sin, y_b = d cos + a sin
+      auto turned = [](float& a, float& d, float co, float si) {
+        const float a0 = a, d0 = d;
+        if constexpr (I4) {
+          a = __fsub_rn(__fmul_rn(a0, co), __fmul_rn(d0, si));
+          d = __fadd_rn(__fmul_rn(d0, co), __fmul_rn(a0, si));
+        } else {
+          a = fmaf(a0, co, -d0 * si);
+          d = fmaf(d0, co, a0 * si);
+        }
+      };
       if constexpr (PAIRS) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], d = x[2 * i + 1], a2 = y[2 * i], d2 = y[2 * i + 1];
-          x[2 * i] = fmaf(a, cs[i], -d * sn[i]);
-          x[2 * i + 1] = fmaf(d, cs[i], a * sn[i]);
-          y[2 * i] = fmaf(a2, cs[4 + i], -d2 * sn[4 + i]);
-          y[2 * i + 1] = fmaf(d2, cs[4 + i], a2 * sn[4 + i]);
+          turned(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+          turned(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[i], d = y[i];
-          x[i] = fmaf(a, cs[i], -d * sn[i]);
-          y[i] = fmaf(d, cs[i], a * sn[i]);
-        }
+        for (int i = 0; i < 8; ++i) turned(x[i], y[i], cs[i], sn[i]);
       }
     }
     if (is_q) {
@@ -163,7 +228,31 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
     } else {
       const int g = h - P.num_q_heads - (is_v ? P.num_kv_heads : 0);
       const size_t row = (row0 + (size_t)g * P.block_size) * D;
-      if constexpr (F8) {
+      if constexpr (I4) {
+        const float sc = is_v ? P.v_scale : P.k_scale;
+        const int BS = P.block_size, in = (int)(at - lb * BS);
+        uint8_t* tile = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) +
+                        ((size_t)block * P.num_kv_heads + g) * ((size_t)BS * D * 9 / 16);
+        uint8_t* scales = tile + (size_t)BS * D / 2 + in * units;
+        auto codes = [&](int e) { return reinterpret_cast<uint32_t*>(tile + ((e / 32) * BS + in) * 16 + e % 32 / 2); };
+        float ax = absmax8(x), ay = absmax8(y), sx, sy;
+        if (rot && !PAIRS) {
+          // the other halves of both groups are the neighbouring lane's
+          const unsigned both = 3u << (threadIdx.x & 30);
+          ax = fmaxf(ax, __shfl_xor_sync(both, ax, 1));
+          ay = fmaxf(ay, __shfl_xor_sync(both, ay, 1));
+          const uint32_t bx = int4_scale_byte(ax, sc, sx), by = int4_scale_byte(ay, sc, sy);
+          if (c % 2 == 0) {
+            scales[e0 / 16] = (uint8_t)bx;
+            scales[e1 / 16] = (uint8_t)by;
+          }
+        } else {
+          scales[e0 / 16] = (uint8_t)int4_scale_byte(fmaxf(ax, ay), sc, sx);
+          sy = sx;
+        }
+        *codes(e0) = pack8_int4(x, sx);
+        *codes(e1) = pack8_int4(y, sy);
+      } else if constexpr (F8) {
         const float sc = is_v ? P.v_scale : P.k_scale;
         uint8_t* o = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + row;
         *reinterpret_cast<uint2*>(o + e0) =

@@ -28,6 +28,8 @@ DEVERR_TIMEOUT = 2
 DEVERR_LAYOUT = 4
 DEVERR_BAD_POSITION = 8
 MAX_SELECT_BLOCKS = 49152
+KV_FP16, KV_E4M3, KV_INT4 = 0, 1, 2
+MAX_AXES = 8
 
 _lock = threading.Lock()
 _lib = None
@@ -132,6 +134,27 @@ def lib():
         L.paged_decode_attention_blocks_fp8.restype = I
         L.paged_decode_blocks_workspace_size.argtypes = [I] * 6
         L.paged_decode_blocks_workspace_size.restype = S
+        axes = [P, P, P, LL, LL, LL] + [P] * 7 + [LL, P, P] + [I] * 12
+        L.paged_kv_append_rope_axes.argtypes = axes + [P, P]
+        L.paged_kv_append_rope_axes.restype = I
+        L.paged_kv_append_rope_axes_fp8.argtypes = axes + [F, F, P, P]
+        L.paged_kv_append_rope_axes_fp8.restype = I
+        L.paged_kv_append_rope_int4.argtypes = axes + [F, F, P, P]
+        L.paged_kv_append_rope_int4.restype = I
+        L.paged_kv_read_int4.argtypes = [P] * 7 + [LL, LL] + [I] * 7 + [F, F, P, P]
+        L.paged_kv_read_int4.restype = I
+        L.paged_decode_attention_int4.argtypes = [P] * 6 + [I] * 9 + [F, F, F, I, P, S, P, P]
+        L.paged_decode_attention_int4.restype = I
+        L.paged_decode_int4_workspace_size.argtypes = [I] * 8
+        L.paged_decode_int4_workspace_size.restype = S
+        L.paged_kv_attention_weights.argtypes = [P] * 6 + [I] * 9 + [F, F, F, I, P, S, P, P]
+        L.paged_kv_attention_weights.restype = I
+        L.paged_kv_attention_weights_workspace_size.argtypes = [I] * 7
+        L.paged_kv_attention_weights_workspace_size.restype = S
+        L.paged_kv_token_select.argtypes = [P] * 5 + [I] * 9 + [P, P]
+        L.paged_kv_token_select.restype = I
+        L.paged_kv_compact.argtypes = [P] * 8 + [I] * 9 + [P, P]
+        L.paged_kv_compact.restype = I
         L.pkd_status_string.argtypes = [I]
         L.pkd_status_string.restype = ctypes.c_char_p
         L.pkd_version.argtypes = []
@@ -646,6 +669,34 @@ def _cache(t, name: str, fp8: bool, dev: int, shape) -> int:
                      f"shape {list(shape)} (4 dimensions) on cuda:{dev}, not {t.dtype} {list(t.shape)} on {t.device}")
 
 
+def _int4_shape(t, name: str):
+    """(num_blocks, num_kv_heads, block_size, head_dim) of a 4-bit cache, uint8
+    [num_blocks][num_kv_heads][block_size][9 * head_dim / 16]."""
+    shape = t.shape
+    if t.dtype is not torch.uint8 or len(shape) != 4 or shape[3] % 9:
+        raise ValueError(f"{name} must be a uint8 tensor [num_blocks][num_kv_heads][block_size][9 * head_dim / 16], "
+                         f"not {t.dtype} {list(shape)}")
+    return shape[0], shape[1], shape[2], shape[3] // 9 * 16
+
+
+def _int4(t, name: str, dev: int, shape) -> int:
+    """Address of a 4-bit cache."""
+    if t.dtype is torch.uint8 and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {torch.uint8} tensor of shape {list(shape)} on cuda:{dev}, not "
+                     f"{t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _any_cache(t, name: str, dev: int):
+    """(address, pkd_kv_type, num_blocks, num_kv_heads, block_size, head_dim) of a cache of any kind, told by its
+    type and the length of its rows: fp16 and E4M3 rows are of 64 or 128 elements, 4-bit ones of 36 or 72 bytes."""
+    shape = t.shape
+    if t.dtype is torch.uint8 and len(shape) == 4 and shape[3] in (36, 72):
+        return (_int4(t, name, dev, shape), KV_INT4, *_int4_shape(t, name))
+    fp8 = t.element_size() == 1
+    return (_cache(t, name, fp8, dev, shape), KV_E4M3 if fp8 else KV_FP16, *shape)
+
+
 def _table(t, name: str, rows: int, dev: int):
     """(address, row length) of an int32 block table."""
     shape = t.shape
@@ -655,13 +706,17 @@ def _table(t, name: str, rows: int, dev: int):
                      f"{list(t.shape)} on {t.device}")
 
 
-def _append_rope(name, fp8, q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache, scales,
-                 token_starts, positions, interleaved, q_out, error_word, stream):
+def _append_rope(name, kind, q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache, scales,
+                 token_starts, positions, interleaved, q_out, error_word, stream, pair_axes=None):
     dev = _device(k_new, "k_new")
     shape = k_cache.shape
-    kc = _cache(k_cache, "k_cache", fp8, dev, shape)
-    vc = _cache(v_cache, "v_cache", fp8, dev, shape)
-    NB, Hkv, BS, D = shape
+    if kind == KV_INT4:
+        NB, Hkv, BS, D = _int4_shape(k_cache, "k_cache")
+        kc, vc = _int4(k_cache, "k_cache", dev, shape), _int4(v_cache, "v_cache", dev, shape)
+    else:
+        kc = _cache(k_cache, "k_cache", kind == KV_E4M3, dev, shape)
+        vc = _cache(v_cache, "v_cache", kind == KV_E4M3, dev, shape)
+        NB, Hkv, BS, D = shape
     T = k_new.shape[0]
     kv = (T, Hkv, D)
     kp, ks = _heads(k_new, "k_new", dev, kv)
@@ -685,11 +740,24 @@ def _append_rope(name, fp8, q, k_new, v_new, rope_table, block_tables, context_l
     B = context_lens.shape[0]
     cl = _on(context_lens, "context_lens", _I32, (B,), dev)
     bt, MB = _table(block_tables, "block_tables", B, dev)
-    fn = _lib.paged_kv_append_rope_fp8 if fp8 else _lib.paged_kv_append_rope
+    fn = getattr(_lib, name)
     ts = None if token_starts is None else _on(token_starts, "token_starts", _I32, (B + 1,), dev)
-    pos = None if positions is None else _on(positions, "positions", _I32, (T,), dev)
-    st = fn(qp, kp, vp, qs, ks, vs, rp if R else None, ts, pos, bt, cl, op, os_, kc, vc, T, B, Hq, Hkv, D, R,
-            1 if interleaved else 0, MP, BS, NB, MB, *scales, _word(error_word, dev), _raw_stream(stream, dev))
+    tail = (1 if interleaved else 0, MP, BS, NB, MB, *scales, _word(error_word, dev), _raw_stream(stream, dev))
+    table = rp if R else None
+    if pair_axes is not None or kind == KV_INT4:
+        A, ax = 1, None
+        if pair_axes is not None:
+            ax = _on(pair_axes, "pair_axes", _I32, (R // 2,), dev)
+            if positions is None or len(positions.shape) != 2:
+                raise ValueError("positions must be [num_axes][tokens] where pair_axes are given")
+            A = positions.shape[0]
+            pos = _on(positions, "positions", _I32, (A, T), dev)
+        else:
+            pos = None if positions is None else _on(positions, "positions", _I32, (T,), dev)
+        st = fn(qp, kp, vp, qs, ks, vs, table, ax, ts, pos, bt, cl, op, os_, kc, vc, T, B, A, Hq, Hkv, D, R, *tail)
+    else:
+        pos = None if positions is None else _on(positions, "positions", _I32, (T,), dev)
+        st = fn(qp, kp, vp, qs, ks, vs, table, ts, pos, bt, cl, op, os_, kc, vc, T, B, Hq, Hkv, D, R, *tail)
     if st:
         _check(st, name)
     return q_out
@@ -702,7 +770,7 @@ def paged_kv_append_rope(q, k_new, v_new, rope_table, block_tables, context_lens
     k and v into the paged caches; token j of sequence b is row token_starts[b] + j and goes to
     logical position context_lens[b] + j.  rope_table is fp32 [max_positions][rotary_dim], cosines
     then sines.  Returns the rotated queries (``q_out``; may be ``q``; None when ``q`` is None)."""
-    return _append_rope("paged_kv_append_rope", False, q, k_new, v_new, rope_table, block_tables, context_lens,
+    return _append_rope("paged_kv_append_rope", KV_FP16, q, k_new, v_new, rope_table, block_tables, context_lens,
                         k_cache, v_cache, (), token_starts, positions, interleaved, q_out, error_word, stream)
 
 
@@ -710,7 +778,7 @@ def paged_kv_append_rope_fp8(q, k_new, v_new, rope_table, block_tables, context_
                              v_scale, token_starts=None, positions=None, interleaved=False, q_out=None,
                              error_word=None, stream=None):
     """paged_kv_append_rope into E4M3 caches (value = code * k_scale / v_scale)."""
-    return _append_rope("paged_kv_append_rope_fp8", True, q, k_new, v_new, rope_table, block_tables, context_lens,
+    return _append_rope("paged_kv_append_rope_fp8", KV_E4M3, q, k_new, v_new, rope_table, block_tables, context_lens,
                         k_cache, v_cache, (float(k_scale), float(v_scale)), token_starts, positions, interleaved,
                         q_out, error_word, stream)
 
@@ -899,6 +967,203 @@ def paged_decode_attention_blocks_fp8(q, k_cache, v_cache, block_tables, context
     return _attention_blocks("paged_decode_attention_blocks_fp8", True, q, k_cache, v_cache, block_tables,
                              context_lens, block_lists, list_lens, scale, (float(k_scale), float(v_scale)), out,
                              workspace, error_word, stream)
+
+
+# ------------------------------------------------------------ several axes, 4-bit caches, eviction
+def paged_kv_append_rope_axes(q, k_new, v_new, rope_table, pair_axes, positions, block_tables, context_lens, k_cache,
+                              v_cache, token_starts=None, interleaved=False, q_out=None, error_word=None,
+                              stream=None):
+    """paged_kv_append_rope where pair i of a head turns by the token's position on axis pair_axes[i]:
+    ``positions`` int32 [num_axes][T], ``pair_axes`` int32 [rotary_dim / 2]."""
+    if pair_axes is None:
+        raise ValueError("pair_axes is needed: paged_kv_append_rope has one axis")
+    return _append_rope("paged_kv_append_rope_axes", KV_FP16, q, k_new, v_new, rope_table, block_tables, context_lens,
+                        k_cache, v_cache, (), token_starts, positions, interleaved, q_out, error_word, stream,
+                        pair_axes)
+
+
+def paged_kv_append_rope_axes_fp8(q, k_new, v_new, rope_table, pair_axes, positions, block_tables, context_lens,
+                                  k_cache, v_cache, k_scale, v_scale, token_starts=None, interleaved=False, q_out=None,
+                                  error_word=None, stream=None):
+    """paged_kv_append_rope_axes into E4M3 caches."""
+    if pair_axes is None:
+        raise ValueError("pair_axes is needed: paged_kv_append_rope_fp8 has one axis")
+    return _append_rope("paged_kv_append_rope_axes_fp8", KV_E4M3, q, k_new, v_new, rope_table, block_tables,
+                        context_lens, k_cache, v_cache, (float(k_scale), float(v_scale)), token_starts, positions,
+                        interleaved, q_out, error_word, stream, pair_axes)
+
+
+def paged_kv_append_rope_int4(q, k_new, v_new, rope_table, block_tables, context_lens, k_cache, v_cache, k_scale,
+                              v_scale, token_starts=None, positions=None, pair_axes=None, interleaved=False,
+                              q_out=None, error_word=None, stream=None):
+    """paged_kv_append_rope into 4-bit caches, uint8 [num_blocks][num_kv_heads][block_size][9 * head_dim / 16]
+    (their bytes in the tiles that the C header describes).  With ``pair_axes``, ``positions`` is
+    [num_axes][T] as for paged_kv_append_rope_axes."""
+    return _append_rope("paged_kv_append_rope_int4", KV_INT4, q, k_new, v_new, rope_table, block_tables, context_lens,
+                        k_cache, v_cache, (float(k_scale), float(v_scale)), token_starts, positions, interleaved,
+                        q_out, error_word, stream, pair_axes)
+
+
+def paged_kv_read_int4(k_cache, v_cache, block_tables, start_lens, k_scale, v_scale, k_out, v_out, token_starts=None,
+                       error_word=None, stream=None):
+    """The values of runs of tokens in 4-bit caches, as fp16 rows: token j of sequence b, logical position
+    start_lens[b] + j, into row token_starts[b] + j of ``k_out`` and ``v_out`` ([T][Hkv][D], any token
+    stride).  Returns (k_out, v_out)."""
+    dev = _device(k_cache, "k_cache")
+    NB, Hkv, BS, D = _int4_shape(k_cache, "k_cache")
+    kc = _int4(k_cache, "k_cache", dev, k_cache.shape)
+    vc = _int4(v_cache, "v_cache", dev, k_cache.shape)
+    T = k_out.shape[0]
+    ko, ks = _heads(k_out, "k_out", dev, (T, Hkv, D))
+    vo, vs = _heads(v_out, "v_out", dev, (T, Hkv, D))
+    B = start_lens.shape[0]
+    sl = _on(start_lens, "start_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    ts = None if token_starts is None else _on(token_starts, "token_starts", _I32, (B + 1,), dev)
+    st = _lib.paged_kv_read_int4(kc, vc, bt, sl, ts, ko, vo, ks, vs, T, B, Hkv, D, BS, NB, MB, float(k_scale),
+                                 float(v_scale), _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_kv_read_int4")
+    return k_out, v_out
+
+
+def _queries(q):
+    """(num_seqs, q_len, num_q_heads, head_dim) of [B][Hq][D] or [B][q_len][Hq][D] queries."""
+    shape = q.shape
+    if len(shape) == 3:
+        return shape[0], 1, shape[1], shape[2]
+    if len(shape) == 4:
+        return tuple(shape)
+    raise ValueError("q must be [num_seqs][num_q_heads][head_dim] or [num_seqs][q_len][num_q_heads][head_dim]")
+
+
+def paged_decode_int4_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                     max_context_len, partition_size=0) -> int:
+    return int(lib().paged_decode_int4_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                      max_context_len, partition_size))
+
+
+def paged_decode_attention_int4(q, k_cache, v_cache, block_tables, context_lens, scale, k_scale, v_scale, out=None,
+                                max_context_len=None, partition_size=0, workspace=None, error_word=None,
+                                stream=None) -> torch.Tensor:
+    """Decode over 4-bit caches; q is [B][Hq][D] (single query) or [B][q_len][Hq][D] (causal among the new
+    tokens).  Returns ``out``."""
+    dev = _device(q, "q")
+    B, QL, Hq, D = _queries(q)
+    qshape = q.shape
+    qp = _on(q, "q", _F16, qshape, dev)
+    NB, Hkv, BS, D2 = _int4_shape(k_cache, "k_cache")
+    if D2 != D:
+        raise ValueError("q / k_cache head_dim mismatch")
+    kc = _int4(k_cache, "k_cache", dev, k_cache.shape)
+    vc = _int4(v_cache, "v_cache", dev, k_cache.shape)
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    if out is None:
+        out = _new_like(q, stream)
+    op = _on(out, "out", _F16, qshape, dev)
+    most = _longest(context_lens, max_context_len, stream, dev)
+    if workspace is None:
+        with _behind(stream, dev):
+            workspace = alloc_workspace(paged_decode_int4_workspace_size(B, QL, Hq, Hkv, D, BS, most, partition_size),
+                                        q.device)
+    ws, wsb = _space(workspace, dev)
+    st = _lib.paged_decode_attention_int4(qp, kc, vc, bt, cl, op, B, QL, Hq, Hkv, D, BS, NB, MB, most, scale,
+                                          float(k_scale), float(v_scale), int(partition_size), ws, wsb,
+                                          _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_decode_attention_int4")
+    return out
+
+
+def paged_kv_attention_weights_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                              max_context_len) -> int:
+    return int(lib().paged_kv_attention_weights_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, head_dim,
+                                                               block_size, max_context_len))
+
+
+def paged_kv_attention_weights(q, k_cache, block_tables, context_lens, weights, scale, k_scale=1.0, start_lens=None,
+                               decay=1.0, max_context_len=None, workspace=None, error_word=None,
+                               stream=None) -> torch.Tensor:
+    """Add every cached token's softmax weight, summed over the queries of its kv head, to ``weights`` (fp32
+    [num_blocks][num_kv_heads][block_size], in place): decay * what is there (0 from start_lens[b] on)
+    + the weight.  k_cache is fp16, E4M3 or 4-bit; q is [B][Hq][D] or [B][q_len][Hq][D] (causal)."""
+    dev = _device(q, "q")
+    B, QL, Hq, D = _queries(q)
+    qp = _on(q, "q", _F16, q.shape, dev)
+    kc, kind, NB, Hkv, BS, D2 = _any_cache(k_cache, "k_cache", dev)
+    if D2 != D:
+        raise ValueError("q / k_cache head_dim mismatch")
+    wp = _on(weights, "weights", _F32, (NB, Hkv, BS), dev)
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    sl = None if start_lens is None else _on(start_lens, "start_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    most = _longest(context_lens, max_context_len, stream, dev)
+    if workspace is None:
+        with _behind(stream, dev):
+            workspace = alloc_workspace(paged_kv_attention_weights_workspace_size(B, QL, Hq, Hkv, D, BS, most),
+                                        q.device)
+    ws, wsb = _space(workspace, dev)
+    st = _lib.paged_kv_attention_weights(qp, kc, bt, cl, sl, wp, B, QL, Hq, Hkv, D, BS, NB, MB, most, scale,
+                                         float(k_scale), float(decay), kind, ws, wsb, _word(error_word, dev),
+                                         _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_kv_attention_weights")
+    return weights
+
+
+def paged_kv_token_select(weights, block_tables, context_lens, max_kept, sink_tokens=0, recent_tokens=0,
+                          max_context_len=None, kept=None, kept_lens=None, error_word=None, stream=None):
+    """The ``max_kept`` tokens of each (sequence, kv head) worth keeping: the first ``sink_tokens``, the last
+    ``recent_tokens`` and those with the largest ``weights`` (fp32 [num_blocks][num_kv_heads][block_size]).
+    Returns (kept int32 [B][Hkv][max_kept], ascending then -1; kept_lens [B])."""
+    dev = _device(weights, "weights")
+    if len(weights.shape) != 3:
+        raise ValueError("weights must be [num_blocks][num_kv_heads][block_size]")
+    NB, Hkv, BS = weights.shape
+    wp = _on(weights, "weights", _F32, weights.shape, dev)
+    B, K = context_lens.shape[0], int(max_kept)
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    if kept is None:
+        with _behind(stream, dev):
+            kept = torch.empty((B, Hkv, max(K, 0)), dtype=_I32, device=weights.device)
+        _returned(stream, dev, kept)
+    if kept_lens is None:
+        with _behind(stream, dev):
+            kept_lens = torch.empty((B,), dtype=_I32, device=weights.device)
+        _returned(stream, dev, kept_lens)
+    st = _lib.paged_kv_token_select(wp, bt, cl, _on(kept, "kept", _I32, (B, Hkv, K), dev),
+                                    _on(kept_lens, "kept_lens", _I32, (B,), dev), B, Hkv, BS, NB, MB,
+                                    _longest(context_lens, max_context_len, stream, dev), K, int(sink_tokens),
+                                    int(recent_tokens), _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_kv_token_select")
+    return kept, kept_lens
+
+
+def paged_kv_compact(k_cache, v_cache, block_tables, context_lens, kept, kept_lens, new_tables, weights=None,
+                     error_word=None, stream=None) -> None:
+    """Copy the kept tokens' rows (and ``weights``) into the blocks of ``new_tables`` [B][max_new_blocks]: row i of
+    the new context is token kept[b][g][i] of the old one.  Caches are fp16, E4M3 or 4-bit; the caller goes on with
+    new_tables and kept_lens."""
+    dev = _device(k_cache, "k_cache")
+    kc, kind, NB, Hkv, BS, D = _any_cache(k_cache, "k_cache", dev)
+    vc, kind_v = _any_cache(v_cache, "v_cache", dev)[:2]
+    if kind_v != kind or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache / v_cache shape mismatch")
+    B = context_lens.shape[0]
+    cl = _on(context_lens, "context_lens", _I32, (B,), dev)
+    bt, MB = _table(block_tables, "block_tables", B, dev)
+    nt, MN = _table(new_tables, "new_tables", B, dev)
+    K = kept.shape[-1]
+    kp = _on(kept, "kept", _I32, (B, Hkv, K), dev)
+    kl = _on(kept_lens, "kept_lens", _I32, (B,), dev)
+    wp = None if weights is None else _on(weights, "weights", _F32, (NB, Hkv, BS), dev)
+    st = _lib.paged_kv_compact(kc, vc, wp, bt, cl, kp, kl, nt, B, Hkv, D, BS, NB, MB, K, MN, kind,
+                               _word(error_word, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_kv_compact")
 
 
 def pkd_read_device_error(error_word, clear=True, stream=None) -> int:
