@@ -1202,6 +1202,7 @@ constexpr long long kFewSharedWork = 36 * 1024;  // 16-row tiles x tokens up to 
 constexpr long long kHalfRowsWork = 36 * 1024;   // units x tokens up to which chunks are of 128 rows,
 constexpr int kHalfRowsUnits = 18;               // with so many partitions left for a unit of 256
 constexpr int kMinListedPartition = 64;  // the shortest partition of a block list
+constexpr int kMaxSmallGridPartitionInt4 = 2048;  // 4-bit caches: the longest partition of the one-wave rule
 constexpr int kMaxPartTokens = 1 << 30;  // the longest prefix, list or context: partition ends stay in 32 bits
 
 // The own contexts behind a prefix: the automatic path and split of
@@ -1559,7 +1560,14 @@ pkd_status blocks_impl(const void* q, const void* k_cache, const void* v_cache, 
 }
 
 // 4-bit caches: partition_size as paged_decode_attention_ex takes it (0: the
-// automatic one).
+// automatic one).  That is the shortest power of two, from 128 tokens on, whose
+// grid fits one resident wave, where it is at most 2048 tokens; else, for fewer
+// units than two waves, about as many partitions as make two of them (at least
+// two: a ragged batch's long contexts then end sooner).
+//   16 x 32/8 heads, 2000-4096 tokens: 1024-token partitions (one wave) 33 us,
+//   512 38, 2048 37; 32 x 40/8, 16K-32K: 4096 240, 8192 (one wave) 269, 1024
+//   262; 128 x 28/4, 8192: 4096 158, unsplit 169; 128 x 32/8, 512-4096: 2048
+//   112, unsplit 118; 48 x 4 tokens x 28/4, 2000-8192: 2048 109, unsplit 142.
 PartPlan plan_int4(const Shape& s, int q_len, int partition_size) {
   PartPlan p;
   const int G = s.num_q_heads / s.num_kv_heads;
@@ -1573,14 +1581,13 @@ PartPlan plan_int4(const Shape& s, int q_len, int partition_size) {
   } else if (partition_size == 0 && units > 0) {
     int sms = sm_count();
     if (sms <= 0) sms = 148;
-    const long long slots = (long long)sms * pkd::kInt4CtasPerSm;
+    const long long slots = (long long)sms * pkd::int4_ctas_per_sm(pkd::int4_rows(q_len, G));
     long long q = kMinSmallGridPartition;
     while (q < s.max_context_len && units * ((s.max_context_len + q - 1) / q) > slots) q *= 2;
-    if (q >= s.max_context_len && units < 2 * slots) {
-      // no partition fits one wave: enough of them for four
-      const long long want = (4 * slots + units - 1) / units;
-      q = kMinAutoPartition;
-      while (q * 2 * want <= s.max_context_len) q *= 2;
+    if (q > kMaxSmallGridPartitionInt4) {
+      const double waves = 2.0 * slots / units;
+      const long long np = waves <= 1.0 ? 1 : std::max(2LL, (long long)(waves + 0.5));
+      for (q = np > 1 ? kMinAutoPartition : s.max_context_len; np > 1 && 2 * q * np <= s.max_context_len * 5LL / 4;) q *= 2;
     }
     if (q < s.max_context_len) p.P = (int)q;
   }

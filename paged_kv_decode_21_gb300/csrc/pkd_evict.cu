@@ -326,6 +326,7 @@ pkd_status paged_kv_attention_weights(const void* q, const void* k_cache, const 
   p.scale_log2 = scale * k_scale * 1.4426950408889634f * (kv_type == PKD_KV_INT4 ? kInt4Unscale : 1.f);
   p.decay = decay;
   p.error_word = error_word;
+  p.bases = kInt4Bases;
   switch (kv_type) {
     case PKD_KV_FP16:
       return head_dim == 128 ? launch_weights<kKvFp16, 128>(plan, p, stream)

@@ -42,6 +42,7 @@ struct WeightsParams {
   int q_tiles;    // second grid, keys again: row tiles of Q in shared memory at a time
   float scale_log2, decay;
   int* error_word;
+  Int4Bases bases;
 };
 
 constexpr int kWeightsWarps = 4;
@@ -92,7 +93,7 @@ struct KeyRow {
   }
 
   // B fragments of all k-steps: b[2 s], b[2 s + 1].
-  __device__ __forceinline__ void fragments(uint32_t (&b)[D / 8]) const {
+  __device__ __forceinline__ void fragments(uint32_t (&b)[D / 8], const Int4Bases& bases) const {
     if constexpr (KV == kKvFp16) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -112,11 +113,12 @@ struct KeyRow {
     } else {
       const uint32_t lo = (s & 0x7Fu) * 0x00800080u;  // the first group's scale twice, as fp16
       const uint32_t hi = D == 128 ? ((s >> 8) & 0x7Fu) * 0x00800080u : lo;
+      const Int4Scale first = int4_scale(lo), second = int4_scale(hi);
       const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         uint32_t d[4];
-        int4_words(w[i], i < 2 ? lo : hi, d);
+        int4_words(w[i], i < 2 ? first : second, bases, d);
 #pragma unroll
         for (int k = 0; k < 4; ++k) b[4 * i + k] = d[k];
       }
@@ -232,8 +234,8 @@ __global__ void __launch_bounds__(32 * kWeightsWarps) paged_weights_rows_kernel(
     }
   for (int t = t0 + 16 * warp; t < t1; t += 16 * NW) {
     uint32_t b0[D / 8], b1[D / 8];
-    keys.next[0].fragments(b0);
-    keys.next[1].fragments(b1);
+    keys.next[0].fragments(b0, P.bases);
+    keys.next[1].fragments(b1, P.bases);
     const bool ok = keys.next_ok;
     keys.request(P, b, g, t + 16 * NW, t1);
 #pragma unroll
@@ -338,8 +340,8 @@ __global__ void __launch_bounds__(32 * kWeightsWarps) paged_weights_keys_kernel(
     __syncthreads();
     for (int t = t0 + 16 * warp; t < t1; t += 16 * NW) {
       uint32_t b0[D / 8], b1[D / 8];
-      keys.next[0].fragments(b0);
-      keys.next[1].fragments(b1);
+      keys.next[0].fragments(b0, P.bases);
+      keys.next[1].fragments(b1, P.bases);
       const bool ok = keys.next_ok;
       keys.request(P, b, g, t + 16 * NW, t1);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};  // tokens 2c, 2c + 1, 8 + 2c, 9 + 2c over the lane's rows

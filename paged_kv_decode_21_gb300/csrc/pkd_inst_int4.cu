@@ -1,4 +1,7 @@
 // Instantiations of the decode kernel over 4-bit caches.
+#include <algorithm>
+#include <cmath>
+
 #include "pkd_int4.cuh"
 #include "pkd_int4_launch.h"
 
@@ -8,7 +11,6 @@ namespace {
 template <int D, int BS, int NT>
 cudaError_t launch(const Int4Params& p, long long grid, cudaStream_t stream) {
   using T = Int4Traits<D, BS, NT>;
-  static_assert(T::MIN_BLOCKS == kInt4CtasPerSm, "the split counts on these");
   auto* fn = paged_decode_int4_kernel<D, BS, NT>;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
   if (failed(e)) return e;
@@ -18,13 +20,19 @@ cudaError_t launch(const Int4Params& p, long long grid, cudaStream_t stream) {
 
 template <int D, int BS>
 cudaError_t launch_rows(const Int4Params& p, long long grid, cudaStream_t stream) {
-  return p.group * p.q_chunk <= 8 ? launch<D, BS, 1>(p, grid, stream) : launch<D, BS, 2>(p, grid, stream);
+  switch (int4_rows(p.d.q_len, p.group)) {
+    case 8: return launch<D, BS, 1>(p, grid, stream);
+    case 16: return launch<D, BS, 2>(p, grid, stream);
+    default: return launch<D, BS, 4>(p, grid, stream);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_decode_int4(int D, int BS, int G, const DecodeParams& p, long long grid, cudaStream_t stream) {
-  const Int4Params ip{p, G, int4_query_chunk(p.q_len, G)};
+  Int4Params ip{p, G, int4_query_chunk(p.q_len, G), p.scale_log2 < 0.f ? 0x80008000u : 0u, kInt4Bases};
+  // (a scale of 0, equal weights: one too small to tell, so that -inf times it stays -inf)
+  ip.d.scale_log2 = std::max(std::fabs(p.scale_log2), 1e-30f);
   if (D == 128 && BS == 16) return launch_rows<128, 16>(ip, grid, stream);
   if (D == 128 && BS == 32) return launch_rows<128, 32>(ip, grid, stream);
   if (D == 64 && BS == 16) return launch_rows<64, 16>(ip, grid, stream);

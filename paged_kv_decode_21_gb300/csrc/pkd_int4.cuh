@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 #include "pkd_decode.cuh"
 #include "pkd_decode_mma.cuh"
+#include "pkd_int4_launch.h"
 #include "pkd_ptx.cuh"
 
 namespace pkd {
@@ -28,8 +29,7 @@ __host__ __device__ constexpr int int4_tile_bytes(int D, int BS) { return BS * D
 //
 // Scale bytes: E4M3 bits shifted to fp16's exponent and mantissa are s * 2^-8
 // exactly, subnormals too (the sign bit is 0); the 2^8 goes into the softmax
-// scale for K and into the result for V.  No byte gives an infinity or a NaN, so
-// rows that were never written cannot poison a product with a weight of 0.
+// scale for K and into the result for V.
 constexpr float kInt4Unscale = 256.f;
 
 __device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) {
@@ -51,21 +51,57 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 constexpr uint32_t kHalf1032 = 0xE408E408u;  // -1032 twice
 constexpr uint32_t kHalf72 = 0xD480D480u;    // -72 twice
 
-// Codes j and j + 4 of a word (j = 0..3) as the halves of d[j], times the
-// scales in the halves of s.
-__device__ __forceinline__ void int4_words(uint32_t x, uint32_t s, uint32_t (&d)[4]) {
-  const uint32_t y = x >> 8;
-  const uint32_t a1 = hmul2_u(s, kHalf1032), a2 = hmul2_u(s, kHalf72);
-  d[0] = hfma2_u((x & 0x000F000Fu) | 0x64006400u, s, a1);
-  d[1] = hfma2_u((x & 0x00F000F0u) | 0x54005400u, s, a2);
-  d[2] = hfma2_u((y & 0x000F000Fu) | 0x64006400u, s, a1);
-  d[3] = hfma2_u((y & 0x00F000F0u) | 0x54005400u, s, a2);
+// (x & MASK) | base, one instruction where base is a register the compiler
+// cannot see through: with both constants known it takes two.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t masked_or(uint32_t x, uint32_t base) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(MASK), "r"(base));
+  return d;
+}
+// 1024 and 64 in both halves, from the kernel's arguments.
+struct Int4Bases {
+  uint32_t b1024, b64;
+};
+constexpr Int4Bases kInt4Bases{0x64006400u, 0x54005400u};
+
+// The scales of two words, or of a word's two halves, with the addends they need.
+struct Int4Scale {
+  uint32_t s, a1, a2;
+};
+__device__ __forceinline__ Int4Scale int4_scale(uint32_t s) { return {s, hmul2_u(s, kHalf1032), hmul2_u(s, kHalf72)}; }
+
+// Half h of x in both halves (a multiply-add takes it without an instruction of its own).
+__device__ __forceinline__ uint32_t both_halves(uint32_t x, int h) {
+  uint32_t d;
+  if (h)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(x));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ Int4Scale both_halves(const Int4Scale& x, int h) {
+  return {both_halves(x.s, h), both_halves(x.a1, h), both_halves(x.a2, h)};
 }
 
-// Scale bytes 0 and 2 (LO), or 1 and 3, of x as an fp16 pair of s * 2^-8.
-template <bool LO>
-__device__ __forceinline__ uint32_t int4_scale_pair(uint32_t x) {
-  return LO ? (x & 0x007F007Fu) << 7 : (x & 0x7F007F00u) >> 1;
+// Codes j and j + 4 of a word (j = 0..3) as the halves of d[j], times the
+// scales in the halves of s.
+__device__ __forceinline__ void int4_words(uint32_t x, const Int4Scale& s, const Int4Bases& base, uint32_t (&d)[4]) {
+  const uint32_t y = x >> 8;
+  d[0] = hfma2_u(masked_or<0x000F000Fu>(x, base.b1024), s.s, s.a1);
+  d[1] = hfma2_u(masked_or<0x00F000F0u>(x, base.b64), s.s, s.a2);
+  d[2] = hfma2_u(masked_or<0x000F000Fu>(y, base.b1024), s.s, s.a1);
+  d[3] = hfma2_u(masked_or<0x00F000F0u>(y, base.b64), s.s, s.a2);
+}
+
+// Two scale bytes as an fp16 pair of s * 2^-8: byte i of a and byte j - 4 of b
+// for sel = int4_scale_sel(i, j).  The selectors' sign mode fills the bytes
+// between with the (clear) sign bit, so that a permutation and a shift do.
+__device__ __forceinline__ uint32_t int4_scale_sel(uint32_t i, uint32_t j) {
+  return (i | (j << 8)) * 0x11u + 0x8080u;
+}
+__device__ __forceinline__ uint32_t int4_scale_pair(uint32_t a, uint32_t b, uint32_t sel) {
+  return prmt(a, b, sel) * 128u;
 }
 
 // ---------------------------------------------------------------- decode
@@ -79,30 +115,66 @@ __device__ __forceinline__ uint32_t int4_scale_pair(uint32_t x) {
 //      in the halves.  Q's A fragments follow that order of dims.
 //   V  the transposed ldmatrix gives lane (r, c) dims 4r .. 4r + 3 of tokens 2c
 //      and 2c + 1, one token a half: rows r and r + 8 of two m-tiles of V^T.
-// Q rows are the group's heads times up to `q_chunk` query tokens; NT = 1 where
-// they fit 8 rows, else 2.
+// Q rows are the group's heads times up to `q_chunk` query tokens, NT tiles of 8
+// of them: 1, 2 or 4.  With 4 the Q fragments stay in shared memory.
+// d = (zero ? 0 : d) + A . B for one m16n8k16 tile; `zero` known when compiled.
+__device__ __forceinline__ void mma_16816_from(float (&d)[4], bool zero, uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (zero) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  } else {
+    const uint32_t a[4] = {a0, a1, a2, a3};
+    mma_16816(d, a, b0, b1);
+  }
+}
+
+// An arrival that announces `bytes`, and a copy that completes on the barrier (shared addresses).
+__device__ __forceinline__ void int4_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void int4_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 struct Int4Params {
   DecodeParams d;
   int group, q_chunk;
+  uint32_t q_sign;  // flips Q where the softmax scale is negative: d.scale_log2 is positive
+  Int4Bases bases;
 };
 
 template <int D, int BS, int NT>
 struct Int4Traits {
   static constexpr int NW = 4;
   static constexpr int THREADS = NW * 32;
-  static constexpr int MIN_BLOCKS = 3;
+  static constexpr int MIN_BLOCKS = NT == 1 ? kInt4CtasPerSm : (NT == 2 ? 3 : 2);
   static constexpr int TILE = int4_tile_bytes(D, BS);
-  static constexpr int SLOT = 2 * TILE;  // K, then V
+  // a ring slot, one barrier: 32 tokens, K's tiles, then V's
+  static constexpr int UNIT = 32, TILES = UNIT / BS;
+  static constexpr int SLOT = 2 * TILES * TILE;
+  static constexpr int SUBS = NT == 4 ? 1 : 2;  // 16-token subtiles per softmax step
   static constexpr int SLABS = D / 32;
   static constexpr int SCALE_OFF = BS * D / 2;
   static constexpr int SB = D / 16;  // scale bytes a token
-  static constexpr int SW_RAW = 72 * 1024 / (NW * SLOT);
+  static constexpr int RING_KIB = MIN_BLOCKS >= 4 ? 54 : 72;
+  static constexpr int SW_RAW = RING_KIB * 1024 / (NW * SLOT);
   static constexpr int SW = SW_RAW > 8 ? 8 : SW_RAW;
   static constexpr int RING_BYTES = NW * SW * SLOT;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int MRG_ACC_OFF = 3 * NW * 16;
+  static constexpr int MRG_ACC_OFF = 3 * NW * ROWS;
   static constexpr int MERGE_BYTES = (MRG_ACC_OFF + NW * ROWS * D) * 4;
-  static constexpr int MAIN_BYTES = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
+  static constexpr int Q_BYTES = NT == 4 ? 2 * (D / 16) * 32 * 16 : 0;  // two 16-row tiles of A fragments
+  static constexpr int MAIN_BYTES = RING_BYTES + Q_BYTES > MERGE_BYTES ? RING_BYTES + Q_BYTES : MERGE_BYTES;
   static constexpr int SMEM_BYTES = MAIN_BYTES + NW * SW * 8;
   static_assert(SW >= 2 && TILE % 16 == 0 && MAIN_BYTES % 16 == 0, "ring");
 };
@@ -112,7 +184,10 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     paged_decode_int4_kernel(const __grid_constant__ Int4Params IP) {
   using T = Int4Traits<D, BS, NT>;
   constexpr int NW = T::NW, SW = T::SW, SLABS = T::SLABS, ROWS = T::ROWS;
+  constexpr int AT = NT == 4 ? 2 : 1;  // 16-row tiles of S
+  constexpr int HF = NT == 1 ? 1 : 2;  // 8-row halves of a tile in use
   const DecodeParams& P = IP.d;
+  const Int4Bases bases = IP.bases;
   extern __shared__ __align__(128) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::MAIN_BYTES);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -139,38 +214,100 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
   if (j >= np_b) return;
   const int t0 = j * PS;
   const int t1 = min(min(t0 + PS, L), L - QL + jq0 + nq);  // nothing past the chunk's last query is read
+  const int units = t1 > t0 ? (t1 - t0 + T::UNIT - 1) / T::UNIT : 0;
   const int nblk = t1 > t0 ? (t1 - t0 + BS - 1) / BS : 0;
   const int32_t* bt = P.block_tables + (size_t)b * P.max_blocks_per_seq + t0 / BS;
-  const size_t block_stride = (size_t)P.num_kv_heads * T::TILE;
+  const uint64_t block_stride = (uint64_t)P.num_kv_heads * T::TILE;
   const char* kbase = reinterpret_cast<const char*>(P.k_cache) + (size_t)g * T::TILE;
   const char* vbase = reinterpret_cast<const char*>(P.v_cache) + (size_t)g * T::TILE;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = lane / 4, c = lane % 4;
+
+  uint64_t* full = bars + warp * SW;
+  unsigned char* ring = smem + (size_t)warp * SW * T::SLOT;
+  if (lane == 0) {
+    for (int s = 0; s < SW; ++s) mbar_init(&full[s], 1);
+    fence_mbarrier_init();
+  }
+  __syncwarp();
+  const int mine = units > warp ? (units - warp + NW - 1) / NW : 0;  // the warp's units: warp, warp + NW, ...
+  // block ids of 32 / TILES of the warp's units at a time, the next ones requested ahead
+  constexpr int TILES = T::TILES, IDS = 32 / TILES;
+  auto ids_at = [&](int first) {
+    const int n = first + lane / TILES, k = (warp + NW * n) * TILES + lane % TILES;
+    return n < mine && k < nblk ? bt[k] : -1;
+  };
+  int ids = ids_at(0), ids_next = ids_at(IDS);
+  uint32_t bad_slots = 0;  // TILES bits a slot: tiles that are not there
+  const uint32_t ring_at = smem_u32(ring), full_at = smem_u32(full);
+  auto issue = [&](int n) {  // copies of the warp's n-th unit, n ascending
+    if (n > 0 && n % IDS == 0) {
+      ids = ids_next;
+      ids_next = ids_at(n + IDS);
+    }
+    const uint32_t slot = (uint32_t)n % SW;
+    // lanes 0 .. 2 TILES - 1 each copy a tile: K's, then V's
+    const int pb = __shfl_sync(0xffffffffu, ids, (n % IDS) * TILES + lane % TILES);
+    const bool good = (uint32_t)pb < (uint32_t)P.num_blocks;
+    const uint32_t there = __ballot_sync(0xffffffffu, good) & ((1u << TILES) - 1);
+    const uint32_t bar = full_at + slot * 8;
+    if (there != (1u << TILES) - 1) {
+      bad_slots |= (~there & ((1u << TILES) - 1)) << (slot * TILES);
+      // (past the last block of the partition there is none)
+      if (lane < TILES && !good && (warp + NW * n) * TILES + lane < nblk) record_error(P.error_word, kErrBadBlock);
+    }
+    if (lane == 0) int4_expect(bar, __popc(there) * 2 * T::TILE);
+    if (lane < 2 * TILES && good)
+      int4_copy(ring_at + slot * T::SLOT + lane * T::TILE,
+                (lane < TILES ? kbase : vbase) + (uint64_t)(uint32_t)pb * block_stride, T::TILE, bar);
+  };
+  int issued = 0;
+  for (; issued < SW && issued < mine; ++issued) issue(issued);
+
   int lim[NT];  // tokens at or past it are masked for the lane's rows r + 8 hf
+  int lim_min = t1;
 #pragma unroll
   for (int hf = 0; hf < NT; ++hf) {
     const int rr = r + 8 * hf;
     lim[hf] = rr < rows ? min(t1, L - QL + jq0 + rr / G + 1) : t1;
+    lim_min = min(lim_min, lim[hf]);
   }
-  const int lim_min = NT == 2 ? min(lim[0], lim[NT - 1]) : lim[0];
 
   // Q as A fragments: k-step 2s + e of slab s has slots (2c, 2c + 1) = dims 8c
   // + 2e and 8c + 2e + 4 of the slab, slots (8 + 2c, 9 + 2c) = the dims behind
-  uint32_t qa[2 * SLABS][2 * NT];
+  auto q_word = [&](int rr, int s) {
+    if (rr >= rows) return make_uint4(0u, 0u, 0u, 0u);
+    uint4 u = *reinterpret_cast<const uint4*>(P.q + out_row(rr) * D + 32 * s + 8 * c);
+    u.x ^= IP.q_sign;
+    u.y ^= IP.q_sign;
+    u.z ^= IP.q_sign;
+    u.w ^= IP.q_sign;
+    return u;
+  };
+  uint32_t qa[AT == 1 ? 2 * SLABS : 1][2 * HF];
+  uint4* qs = reinterpret_cast<uint4*>(smem + T::RING_BYTES);  // [tile][k-step][lane]
+  if constexpr (AT == 1) {
 #pragma unroll
-  for (int hf = 0; hf < NT; ++hf) {
-    const int rr = r + 8 * hf;
-    const __half* qr = P.q + (rr < rows ? out_row(rr) * D : 0);
+    for (int hf = 0; hf < NT; ++hf)
 #pragma unroll
-    for (int s = 0; s < SLABS; ++s) {
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < rows) u = *reinterpret_cast<const uint4*>(qr + 32 * s + 8 * c);
-      qa[2 * s][hf] = prmt(u.x, u.z, 0x5410);
-      qa[2 * s][NT + hf] = prmt(u.x, u.z, 0x7632);
-      qa[2 * s + 1][hf] = prmt(u.y, u.w, 0x5410);
-      qa[2 * s + 1][NT + hf] = prmt(u.y, u.w, 0x7632);
+      for (int s = 0; s < SLABS; ++s) {
+        const uint4 u = q_word(r + 8 * hf, s);
+        qa[2 * s][hf] = prmt(u.x, u.z, 0x5410);
+        qa[2 * s][HF + hf] = prmt(u.x, u.z, 0x7632);
+        qa[2 * s + 1][hf] = prmt(u.y, u.w, 0x5410);
+        qa[2 * s + 1][HF + hf] = prmt(u.y, u.w, 0x7632);
+      }
+  } else {
+    for (int i = warp; i < AT * SLABS; i += NW) {
+      const int at = i / SLABS, s = i % SLABS;
+      const uint4 u = q_word(16 * at + r, s), w = q_word(16 * at + r + 8, s);
+      qs[(at * 2 * SLABS + 2 * s) * 32 + lane] = make_uint4(prmt(u.x, u.z, 0x5410), prmt(w.x, w.z, 0x5410),
+                                                            prmt(u.x, u.z, 0x7632), prmt(w.x, w.z, 0x7632));
+      qs[(at * 2 * SLABS + 2 * s + 1) * 32 + lane] = make_uint4(prmt(u.y, u.w, 0x5410), prmt(w.y, w.w, 0x5410),
+                                                                prmt(u.y, u.w, 0x7632), prmt(w.y, w.w, 0x7632));
     }
+    __syncthreads();
   }
   // O^T: tile 2s + e holds dims 32s + 4r + 2e (rows r) and the dims behind (rows r + 8)
   float o[2 * SLABS][NT][4];
@@ -185,191 +322,193 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     l[hf] = 0.f;
   }
 
-  uint64_t* full = bars + warp * SW;
-  unsigned char* ring = smem + (size_t)warp * SW * T::SLOT;
-  if (lane == 0) {
-    for (int s = 0; s < SW; ++s) mbar_init(&full[s], 1);
-    fence_mbarrier_init();
-  }
-  __syncwarp();
-  const int mine = nblk > warp ? (nblk - warp + NW - 1) / NW : 0;  // the warp's blocks: warp, warp + NW, ...
-  // block ids, 32 of the warp's at a time, the next 32 requested ahead
-  auto ids_at = [&](int first) { return first + lane < mine ? bt[warp + NW * (first + lane)] : -1; };
-  int ids = ids_at(0), ids_next = ids_at(32);
-  uint32_t bad_slots = 0;
-  auto issue = [&](int n) {  // copies of the warp's n-th block, n ascending
-    if (n > 0 && n % 32 == 0) {
-      ids = ids_next;
-      ids_next = ids_at(n + 32);
-    }
-    const int slot = n % SW;
-    const int pb = __shfl_sync(0xffffffffu, ids, n % 32);
-    const bool bad = pb < 0 || pb >= P.num_blocks;
-    bad_slots = bad ? (bad_slots | (1u << slot)) : (bad_slots & ~(1u << slot));
-    if (lane == 0) {
-      if (bad) {
-        record_error(P.error_word, kErrBadBlock);
-        mbar_arrive(&full[slot]);
-      } else {
-        unsigned char* dst = ring + (size_t)slot * T::SLOT;
-        mbar_arrive_expect_tx(&full[slot], T::SLOT);
-        bulk_copy_g2s(dst, kbase + (size_t)pb * block_stride, T::TILE, &full[slot]);
-        bulk_copy_g2s(dst + T::TILE, vbase + (size_t)pb * block_stride, T::TILE, &full[slot]);
-      }
-    }
-  };
-  int issued = 0;
-  for (; issued < SW && issued < mine; ++issued) issue(issued);
-
   // matrix loads: lane l addresses row l % 8 of matrix l / 8, matrices in the
   // order (slab, tokens 0-7), (slab, tokens 8-15), then the next slab's
   const uint32_t lm = (((lane >> 4) * BS) + (lane & 7) + 8 * ((lane >> 3) & 1)) * 16;
-  const int kh = c >> 1;  // K: the lane's dims are in this half of the slab's two groups
-  const int vh = r >> 2;  // V: the same
-  const uint32_t ksel = (uint32_t)(kh | ((kh + 2) << 4)) * 0x101u + 0x4400u;  // bytes (a.h, a.h+2, b.h, b.h+2)
-  const uint32_t vsel = (uint32_t)(vh | ((vh + 2) << 4)) * 0x101u + 0x4400u;
+  // scale bytes 4i .. 4i + 3 of a token are those of slabs 2i and 2i + 1, two
+  // halves each: a lane's K dims are in half c / 2, its V dims in half r / 4
+  const uint32_t ksel = int4_scale_sel(c >> 1, 2 + (c >> 1));  // of one token: slab 2i, slab 2i + 1
+  const uint32_t vsel = int4_scale_sel(r >> 2, 4 + (r >> 2));  // of two tokens; slab 2i + 1: 0x2222 on
+  constexpr int SUBS = T::SUBS, SBW = T::SB / 4;
+  auto lds_words = [](uint32_t at, uint32_t (&w)[SBW]) {
+    if constexpr (SBW == 2)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    else
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+  };
 
   for (int u = 0; u < mine; ++u) {
-    const int slot = u % SW;
-    const bool bad = (bad_slots >> slot) & 1u;
-    if (!mbar_wait_bounded(&full[slot], (u / SW) & 1, P.timeout_ns)) {
+    const uint32_t slot = (uint32_t)u % SW;
+    if (!mbar_wait_bounded(&full[slot], ((uint32_t)u / SW) & 1, P.timeout_ns)) {
       if (lane == 0) record_error(P.error_word, kErrTimeout);
       for (int v = u + 1; v < issued; ++v) mbar_wait_bounded(&full[v % SW], (v / SW) & 1, P.timeout_ns);
       break;
     }
-    if (!bad) {
-      const uint32_t ks = smem_u32(ring + (size_t)slot * T::SLOT);
-      const uint32_t vs = ks + T::TILE;
-      const int base0 = t0 + (warp + NW * u) * BS;
+    const uint32_t at = ring_at + slot * T::SLOT;
+    const int base = t0 + (warp + NW * u) * T::UNIT;  // the unit's first token
+    const uint32_t missing = bad_slots >> (slot * TILES) & ((1u << TILES) - 1);
+    const bool whole = missing == 0 && base + T::UNIT <= t1;
+    if (!whole) {
+      // Rows that were not copied, or may never have been written: their V
+      // scales are zeroed, so that a weight of 0 times them is 0; their scores
+      // become -inf below, whatever K holds.
+      if (base + lane >= t1 || (missing >> (lane / BS)) & 1) {
+        unsigned char* row = ring + slot * T::SLOT + (TILES + lane / BS) * T::TILE + T::SCALE_OFF + lane % BS * T::SB;
+        *reinterpret_cast<uint32_t*>(row) = 0u;
+        if (SBW == 2) *reinterpret_cast<uint32_t*>(row + 4) = 0u;
+      }
+      fence_proxy_async_smem();  // ordered before the next copy into this slot
+      __syncwarp();
+    }
 #pragma unroll
-      for (int rg = 0; rg < BS / 16; ++rg) {
-        const int base = base0 + 16 * rg;
-        if (BS > 16 && base >= t1) break;
-        // ---- S = Q K^T over tokens 0..7 (sa) and 8..15 (sb)
-        float sa[2][4], sb[2][4];
+    for (int step = 0; step < 2 / SUBS; ++step) {
+      if (SUBS == 1 && base + 16 * step >= t1) break;
+      // ---- S = Q K^T: sa over tokens 0..7, sb over 8..15 of a subtile
+      float sa[SUBS][AT][4], sb[SUBS][AT][4];  // (the first product of each starts from zero)
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sa[ch][e] = sb[ch][e] = 0.f;
-        auto qk = [&](int k, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
-          if constexpr (NT == 1) {
-            mma_16816_top(sa[k % 2], qa[k][0], qa[k][1], b00, b01);
-            mma_16816_top(sb[k % 2], qa[k][0], qa[k][1], b10, b11);
-          } else {
-            mma_16816(sa[k % 2], qa[k], b00, b01);
-            mma_16816(sb[k % 2], qa[k], b10, b11);
-          }
-        };
-        const uint32_t ksc = ks + T::SCALE_OFF + (16 * rg + r) * T::SB;
+      for (int sub = 0; sub < SUBS; ++sub) {
+        const int row0 = 16 * (step * SUBS + sub) % BS;
+        const uint32_t ks = at + 16 * (step * SUBS + sub) / BS * T::TILE;
+        uint32_t w0[SBW], w1[SBW];  // scales of tokens r and 8 + r
+        lds_words(ks + T::SCALE_OFF + (row0 + r) * T::SB, w0);
+        lds_words(ks + T::SCALE_OFF + (row0 + 8 + r) * T::SB, w1);
 #pragma unroll
         for (int i = 0; i < SLABS / 2; ++i) {
           uint32_t kb[4];
-          ldsm_x4(ks + lm + (uint32_t)(2 * i * BS + 16 * rg) * 16, kb);
-          // scales of tokens r and 8 + r, slabs 2i and 2i + 1: bytes (slab 2i, slab 2i + 1) of each
-          uint32_t w0, w1;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w0) : "r"(ksc + 4 * i));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w1) : "r"(ksc + 8 * T::SB + 4 * i));
-          const uint32_t w = prmt(w0, w1, ksel);
-          const uint32_t se = int4_scale_pair<true>(w), so = int4_scale_pair<false>(w);  // slab 2i, slab 2i + 1
+          ldsm_x4(ks + lm + (uint32_t)(2 * i * BS + row0) * 16, kb);
+          const Int4Scale s0 = int4_scale(int4_scale_pair(w0[i], w0[i], ksel));
+          const Int4Scale s1 = int4_scale(int4_scale_pair(w1[i], w1[i], ksel));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t sc = h ? so : se;
             uint32_t d0[4], d1[4];
-            int4_words(kb[2 * h], prmt(sc, sc, 0x1010), d0);
-            int4_words(kb[2 * h + 1], prmt(sc, sc, 0x3232), d1);
-            qk(4 * i + 2 * h, d0[0], d0[1], d1[0], d1[1]);
-            qk(4 * i + 2 * h + 1, d0[2], d0[3], d1[2], d1[3]);
-          }
-        }
-        // ---- online softmax of rows r + 8hf over tokens 2c, 2c+1, 8+2c, 9+2c
-        float sc[NT][4];
+            int4_words(kb[2 * h], both_halves(s0, h), bases, d0);
+            int4_words(kb[2 * h + 1], both_halves(s1, h), bases, d1);
 #pragma unroll
-        for (int hf = 0; hf < NT; ++hf) {
-          sc[hf][0] = (sa[0][2 * hf] + sa[1][2 * hf]) * P.scale_log2;
-          sc[hf][1] = (sa[0][2 * hf + 1] + sa[1][2 * hf + 1]) * P.scale_log2;
-          sc[hf][2] = (sb[0][2 * hf] + sb[1][2 * hf]) * P.scale_log2;
-          sc[hf][3] = (sb[0][2 * hf + 1] + sb[1][2 * hf + 1]) * P.scale_log2;
-        }
-        if (base + 16 > lim_min) {
+            for (int e = 0; e < 2; ++e) {
+              const int k = 4 * i + 2 * h + e;
+              if constexpr (AT == 1) {
+                const uint32_t a1 = HF == 2 ? qa[k][1] : 0u, a3 = HF == 2 ? qa[k][3 % (2 * HF)] : 0u;
+                mma_16816_from(sa[sub][0], k == 0, qa[k][0], a1, qa[k][HF], a3, d0[2 * e], d0[2 * e + 1]);
+                mma_16816_from(sb[sub][0], k == 0, qa[k][0], a1, qa[k][HF], a3, d1[2 * e], d1[2 * e + 1]);
+              } else {
 #pragma unroll
-          for (int hf = 0; hf < NT; ++hf) {
-            const int lt = lim[hf] - base;
-            if (2 * c >= lt) sc[hf][0] = -INFINITY;
-            if (2 * c + 1 >= lt) sc[hf][1] = -INFINITY;
-            if (8 + 2 * c >= lt) sc[hf][2] = -INFINITY;
-            if (9 + 2 * c >= lt) sc[hf][3] = -INFINITY;
-          }
-        }
-        float lmax[NT];
-        bool need = false;
-#pragma unroll
-        for (int hf = 0; hf < NT; ++hf) {
-          lmax[hf] = fmaxf(fmaxf(sc[hf][0], sc[hf][1]), fmaxf(sc[hf][2], sc[hf][3]));
-          mt[hf] = fmaxf(mt[hf], lmax[hf]);
-          need |= lmax[hf] > m[hf] + kLazyTau;
-        }
-        if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-          for (int hf = 0; hf < NT; ++hf) {
-            float mx = fmaxf(lmax[hf], __shfl_xor_sync(0xffffffffu, lmax[hf], 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(m[hf], mx);
-            const float alpha = (mn == -INFINITY) ? 1.f : ex2_approx(m[hf] - mn);
-            l[hf] *= alpha;
-            m[hf] = mn;
-            const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * c);
-            const float a_hi = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
-#pragma unroll
-            for (int k = 0; k < 2 * SLABS; ++k) {
-              o[k][hf][0] *= a_lo;
-              o[k][hf][1] *= a_hi;
-              o[k][hf][2] *= a_lo;
-              o[k][hf][3] *= a_hi;
+                for (int t = 0; t < AT; ++t) {
+                  const uint4 w = qs[(t * 2 * SLABS + k) * 32 + lane];
+                  mma_16816_from(sa[sub][t], k == 0, w.x, w.y, w.z, w.w, d0[2 * e], d0[2 * e + 1]);
+                  mma_16816_from(sb[sub][t], k == 0, w.x, w.y, w.z, w.w, d1[2 * e], d1[2 * e + 1]);
+                }
+              }
             }
           }
         }
-        uint32_t pb[NT][2];
+      }
+      // ---- online softmax of rows r + 8hf over tokens 16 sub + (2c, 2c+1, 8+2c, 9+2c)
+      float sc[NT][SUBS][4];
+#pragma unroll
+      for (int hf = 0; hf < NT; ++hf)
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sc[hf][sub][e] = sa[sub][hf / 2][2 * (hf % 2) + e];
+            sc[hf][sub][2 + e] = sb[sub][hf / 2][2 * (hf % 2) + e];
+          }
+      if (!whole || base + T::UNIT > lim_min) {
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub) {
+          const int x = 16 * (step * SUBS + sub);  // the subtile's first token in the unit
+          const bool none = (missing >> (x / BS)) & 1;
+#pragma unroll
+          for (int hf = 0; hf < NT; ++hf) {
+            const int lt = none ? 0 : lim[hf] - base - x;
+            if (2 * c >= lt) sc[hf][sub][0] = -INFINITY;
+            if (2 * c + 1 >= lt) sc[hf][sub][1] = -INFINITY;
+            if (8 + 2 * c >= lt) sc[hf][sub][2] = -INFINITY;
+            if (9 + 2 * c >= lt) sc[hf][sub][3] = -INFINITY;
+          }
+        }
+      }
+      float lmax[NT];  // (scale_log2 > 0: the largest product is the largest score)
+      bool need = false;
+#pragma unroll
+      for (int hf = 0; hf < NT; ++hf) {
+        lmax[hf] = fmaxf(fmaxf(sc[hf][0][0], sc[hf][0][1]), fmaxf(sc[hf][0][2], sc[hf][0][3]));
+        if constexpr (SUBS == 2)
+          lmax[hf] = fmaxf(lmax[hf], fmaxf(fmaxf(sc[hf][SUBS - 1][0], sc[hf][SUBS - 1][1]),
+                                           fmaxf(sc[hf][SUBS - 1][2], sc[hf][SUBS - 1][3])));
+        lmax[hf] *= P.scale_log2;
+        mt[hf] = fmaxf(mt[hf], lmax[hf]);
+        need |= lmax[hf] > m[hf] + kLazyTau;
+      }
+      if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int hf = 0; hf < NT; ++hf) {
-          const float mu = m[hf] == -INFINITY ? 0.f : m[hf];  // a row that has seen no token yet
-          const float p0 = ex2_approx(sc[hf][0] - mu), p1 = ex2_approx(sc[hf][1] - mu);
-          const float p2 = ex2_approx(sc[hf][2] - mu), p3 = ex2_approx(sc[hf][3] - mu);
-          l[hf] += (p0 + p1) + (p2 + p3);
-          pb[hf][0] = pack_half2(p0, p1);
-          pb[hf][1] = pack_half2(p2, p3);
+          float mx = fmaxf(lmax[hf], __shfl_xor_sync(0xffffffffu, lmax[hf], 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[hf], mx);
+          const float alpha = (mn == -INFINITY) ? 1.f : ex2_approx(m[hf] - mn);
+          l[hf] *= alpha;
+          m[hf] = mn;
+          const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * c);
+          const float a_hi = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
+#pragma unroll
+          for (int k = 0; k < 2 * SLABS; ++k) {
+            o[k][hf][0] *= a_lo;
+            o[k][hf][1] *= a_hi;
+            o[k][hf][2] *= a_lo;
+            o[k][hf][3] *= a_hi;
+          }
         }
-        // ---- O^T += V^T P^T
-        const uint32_t vsc = vs + T::SCALE_OFF + (16 * rg + 2 * c) * T::SB;
+      }
+      uint32_t pb[NT][SUBS][2];
+#pragma unroll
+      for (int hf = 0; hf < NT; ++hf) {
+        const float mu = m[hf] == -INFINITY ? 0.f : -m[hf];  // a row that has seen no token yet
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub) {
+          const float p0 = ex2_approx(fmaf(sc[hf][sub][0], P.scale_log2, mu));
+          const float p1 = ex2_approx(fmaf(sc[hf][sub][1], P.scale_log2, mu));
+          const float p2 = ex2_approx(fmaf(sc[hf][sub][2], P.scale_log2, mu));
+          const float p3 = ex2_approx(fmaf(sc[hf][sub][3], P.scale_log2, mu));
+          l[hf] += (p0 + p1) + (p2 + p3);
+          pb[hf][sub][0] = pack_half2(p0, p1);
+          pb[hf][sub][1] = pack_half2(p2, p3);
+        }
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int sub = 0; sub < SUBS; ++sub) {
+        const int row0 = 16 * (step * SUBS + sub) % BS;
+        const uint32_t vs = at + (TILES + 16 * (step * SUBS + sub) / BS) * T::TILE;
+        uint32_t w[4][SBW];  // scales of tokens 2c, 2c + 1, 8 + 2c, 9 + 2c
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          lds_words(vs + T::SCALE_OFF + (row0 + 2 * c + (k >> 1) * 8 + (k & 1)) * T::SB, w[k]);
 #pragma unroll
         for (int i = 0; i < SLABS / 2; ++i) {
           uint32_t vb[4];
-          ldsm_x4_trans(vs + lm + (uint32_t)(2 * i * BS + 16 * rg) * 16, vb);
-          // scales of token pairs (2c, 2c + 1) and (8 + 2c, 9 + 2c)
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            asm volatile("ld.shared.b32 %0, [%1];"
-                         : "=r"(w[k])
-                         : "r"(vsc + ((k >> 1) * 8 + (k & 1)) * T::SB + 4 * i));
-          const uint32_t wl = prmt(w[0], w[1], vsel), wh = prmt(w[2], w[3], vsel);
+          ldsm_x4_trans(vs + lm + (uint32_t)(2 * i * BS + row0) * 16, vb);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = vsel + 0x2222u * h;
             uint32_t dl[4], dh[4];
-            int4_words(vb[2 * h], h ? int4_scale_pair<false>(wl) : int4_scale_pair<true>(wl), dl);
-            int4_words(vb[2 * h + 1], h ? int4_scale_pair<false>(wh) : int4_scale_pair<true>(wh), dh);
+            int4_words(vb[2 * h], int4_scale(int4_scale_pair(w[0][i], w[1][i], sel)), bases, dl);
+            int4_words(vb[2 * h + 1], int4_scale(int4_scale_pair(w[2][i], w[3][i], sel)), bases, dh);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint32_t va[4] = {dl[2 * e], dl[2 * e + 1], dh[2 * e], dh[2 * e + 1]};
 #pragma unroll
-              for (int hf = 0; hf < NT; ++hf) mma_16816(o[2 * (2 * i + h) + e][hf], va, pb[hf][0], pb[hf][1]);
+              for (int hf = 0; hf < NT; ++hf)
+                mma_16816(o[2 * (2 * i + h) + e][hf], va, pb[hf][sub][0], pb[hf][sub][1]);
             }
           }
         }
       }
     }
     __syncwarp();
+    bad_slots &= ~(((1u << TILES) - 1) << (slot * TILES));
     if (issued < mine) {
-      if (lane == 0) fence_proxy_async_smem();  // our reads of the slot precede the next copy into it
+      fence_proxy_async_smem();  // our reads of the slot precede the next copies into it
       issue(issued);
       ++issued;
     }
@@ -379,8 +518,8 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
   __syncthreads();
   float* mrg = reinterpret_cast<float*>(smem);
   float* mrg_m = mrg;
-  float* mrg_mt = mrg + NW * 16;
-  float* mrg_l = mrg + 2 * NW * 16;
+  float* mrg_mt = mrg + NW * ROWS;
+  float* mrg_l = mrg + 2 * NW * ROWS;
   float* mrg_acc = mrg + T::MRG_ACC_OFF;
 #pragma unroll
   for (int hf = 0; hf < NT; ++hf) {
@@ -389,9 +528,9 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     float mx = fmaxf(mt[hf], __shfl_xor_sync(0xffffffffu, mt[hf], 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     if (c == 0) {
-      mrg_m[warp * 16 + 8 * hf + r] = m[hf];
-      mrg_mt[warp * 16 + 8 * hf + r] = mx;
-      mrg_l[warp * 16 + 8 * hf + r] = lv;
+      mrg_m[warp * ROWS + 8 * hf + r] = m[hf];
+      mrg_mt[warp * ROWS + 8 * hf + r] = mx;
+      mrg_l[warp * ROWS + 8 * hf + r] = lv;
     }
     float* acc = mrg_acc + (warp * ROWS + 8 * hf + 2 * c) * D;
 #pragma unroll
@@ -406,13 +545,13 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     const int rr = i / D, d = i % D;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, mrg_mt[w * 16 + rr]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, mrg_mt[w * ROWS + rr]);
     float Z = 0.f, O = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float mw = mrg_m[w * 16 + rr];
+      const float mw = mrg_m[w * ROWS + rr];
       const float cw = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
-      Z = fmaf(cw, mrg_l[w * 16 + rr], Z);
+      Z = fmaf(cw, mrg_l[w * ROWS + rr], Z);
       O = fmaf(cw, mrg_acc[(w * ROWS + rr) * D + d], O);
     }
     O *= P.v_scale;

@@ -5,11 +5,20 @@
 
 namespace pkd {
 
-// Query tokens per CTA for q_len of them and groups of G heads: what fits eight
-// rows where all do, else sixteen.
-inline int int4_query_chunk(int q_len, int G) { return q_len * G <= 8 ? q_len : (q_len < 16 / G ? q_len : 16 / G); }
+// Query rows (tokens times the group's heads) of a CTA, for q_len tokens and
+// groups of G heads: 8, 16 or 32, the fewest that hold all, else 32.
+inline int int4_rows(int q_len, int G) {
+  const long long all = (long long)q_len * G;
+  return all <= 8 ? 8 : (all <= 16 ? 16 : 32);
+}
+// Query tokens of a CTA.
+inline int int4_query_chunk(int q_len, int G) {
+  const int most = int4_rows(q_len, G) / G;
+  return q_len < most ? q_len : most;
+}
 // Resident CTAs per SM.
-constexpr int kInt4CtasPerSm = 3;
+constexpr int kInt4CtasPerSm = 4;
+inline int int4_ctas_per_sm(int rows) { return rows == 8 ? kInt4CtasPerSm : (rows == 16 ? 3 : 2); }
 // p.q_chunks chunks of int4_query_chunk(p.q_len, G) tokens; partials unless a sequence has one partition.
 cudaError_t launch_decode_int4(int D, int BS, int G, const DecodeParams& p, long long grid, cudaStream_t stream);
 
