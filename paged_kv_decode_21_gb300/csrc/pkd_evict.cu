@@ -13,7 +13,7 @@ namespace pkd {
 
 __global__ void __launch_bounds__(kWeightsFinishThreads) paged_weights_scores_kernel(const WeightsParams P,
                                                                                      int chunks) {
-  __shared__ float row_mx[kFinishMaxRows], row_inv[kFinishMaxRows];
+  __shared__ float row_off[kFinishMaxRows];
   const int chunk = blockIdx.x % chunks, bg = blockIdx.x / chunks;
   const int g = bg % P.num_kv_heads, b = bg / P.num_kv_heads;
   const int L = min(clamped_len(P.context_lens, b, P.block_size, P.max_blocks_per_seq, nullptr),
@@ -26,20 +26,21 @@ __global__ void __launch_bounds__(kWeightsFinishThreads) paged_weights_scores_ke
   const bool mine = pb >= 0 && pb < P.num_blocks;
   float* o = P.weights + ((size_t)(mine ? pb : 0) * P.num_kv_heads + g) * P.block_size + t % P.block_size;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  merge_rows(P, bg, L, 0, P.rows, row_mx, row_inv);
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mine && P.decay != 0.f) old = *reinterpret_cast<const float4*>(o);
+  merge_rows(P, bg, L, 0, P.rows, row_off);
   __syncthreads();
   if (!mine) return;
-  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (P.decay != 0.f) old = *reinterpret_cast<const float4*>(o);
   const float before[4] = {old.x, old.y, old.z, old.w};
   float w[4] = {0.f, 0.f, 0.f, 0.f};
   const float* s = P.scores + (size_t)bg * P.rows * P.score_stride + t;
+#pragma unroll 4
   for (int i = 0; i < P.rows; ++i) {
     const float4 x = *reinterpret_cast<const float4*>(s + (size_t)i * P.score_stride);
-    w[0] = fmaf(ex2_approx(x.x - row_mx[i]), row_inv[i], w[0]);
-    w[1] = fmaf(ex2_approx(x.y - row_mx[i]), row_inv[i], w[1]);
-    w[2] = fmaf(ex2_approx(x.z - row_mx[i]), row_inv[i], w[2]);
-    w[3] = fmaf(ex2_approx(x.w - row_mx[i]), row_inv[i], w[3]);
+    w[0] += ex2_approx(x.x - row_off[i]);
+    w[1] += ex2_approx(x.y - row_off[i]);
+    w[2] += ex2_approx(x.z - row_off[i]);
+    w[3] += ex2_approx(x.w - row_off[i]);
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -53,11 +54,14 @@ __global__ void __launch_bounds__(kWeightsFinishThreads) paged_weights_scores_ke
   }
 }
 
-__global__ void __launch_bounds__(kTokenSelectThreads) paged_kv_token_select_kernel(const TokenSelectParams P) {
-  constexpr int NT = kTokenSelectThreads, NWARP = NT / 32;
-  extern __shared__ uint32_t select_keys[];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t found[2];               // the bin, and what remains to be found in it
+constexpr int kSelectBins = 2048;
+template <int NT>
+__global__ void __launch_bounds__(NT) paged_kv_token_select_kernel(const TokenSelectParams P) {
+  constexpr int NWARP = NT / 32, PER = kSelectBins / NWARP / 32;  // bins a lane sums
+  extern __shared__ __align__(16) uint32_t select_keys[];
+  __shared__ uint32_t hist[kSelectBins];
+  __shared__ uint32_t warp_bins[NWARP];
+  __shared__ uint32_t found[2];  // the bin, and what remains to be found in it
   __shared__ int above[NWARP], equal[NWARP];  // per warp's stretch
   const int g = blockIdx.x % P.num_kv_heads, b = blockIdx.x / P.num_kv_heads;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -71,74 +75,153 @@ __global__ void __launch_bounds__(kTokenSelectThreads) paged_kv_token_select_ker
     return;
   }
   const int lo = P.sink, hi = L - P.recent;  // candidates; more of them than are needed, as L > K
-  auto weigh = [&](int t) -> uint32_t {
-    const int pb = P.block_tables[(size_t)b * P.max_blocks_per_seq + t / P.block_size];
+  const int32_t* table = P.block_tables + (size_t)b * P.max_blocks_per_seq;
+  auto place = [&](int t) -> const float* {  // of token t's weight, or null
+    const int pb = table[t / P.block_size];
     if (pb < 0 || pb >= P.num_blocks) {
       record_error(P.error_word, kErrBadBlock);
-      return 0u;
+      return nullptr;
     }
-    return ordered_key(P.weights[((size_t)pb * P.num_kv_heads + g) * P.block_size + t % P.block_size]);
+    return P.weights + ((size_t)pb * P.num_kv_heads + g) * P.block_size + t % P.block_size;
   };
-  for (int t = lo + tid; t < hi && t < P.cached; t += NT) select_keys[t] = weigh(t);
-  auto key = [&](int t) { return t < P.cached ? select_keys[t] : weigh(t); };
+  // A token's key; 0 for the first and last ones, which are taken anyway: they
+  // count in the lowest bin, where none that is looked for lies but tokens
+  // without a block, and those are told apart again below.
+  auto weigh = [&](int t) -> uint32_t {
+    if (t < lo || t >= hi) return 0u;
+    const float* p = place(t);
+    return p ? ordered_key(*p) : 0u;
+  };
+  const int held = min(L, P.cached);
+  if (P.block_shift >= 0) {
+    constexpr int U = 8;
+    const float* base = P.weights + (size_t)g * P.block_size;
+    const size_t stride = (size_t)P.num_kv_heads << P.block_shift;
+    for (int q0 = tid; 4 * q0 < held; q0 += U * NT) {
+      int pb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = 4 * (q0 + u * NT);
+        pb[u] = t < held ? table[t >> P.block_shift] : -1;
+      }
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = 4 * (q0 + u * NT);
+        if ((uint32_t)pb[u] < (uint32_t)P.num_blocks)
+          x[u] = *reinterpret_cast<const float4*>(base + (size_t)(uint32_t)pb[u] * stride +
+                                                  (t & (P.block_size - 1)));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = 4 * (q0 + u * NT);
+        if (t >= held) continue;
+        uint4 k = make_uint4(0u, 0u, 0u, 0u);
+        if ((uint32_t)pb[u] < (uint32_t)P.num_blocks)
+          k = make_uint4(ordered_key(x[u].x), ordered_key(x[u].y), ordered_key(x[u].z), ordered_key(x[u].w));
+        else
+          record_error(P.error_word, kErrBadBlock);
+        if (t < lo || t + 4 > hi) {
+          if (t < lo || t >= hi) k.x = 0u;
+          if (t + 1 < lo || t + 1 >= hi) k.y = 0u;
+          if (t + 2 < lo || t + 2 >= hi) k.z = 0u;
+          if (t + 3 < lo || t + 3 >= hi) k.w = 0u;
+        }
+        *reinterpret_cast<uint4*>(select_keys + t) = k;
+      }
+    }
+  } else {
+    for (int t = tid; t < (held + 3) / 4 * 4; t += NT) select_keys[t] = weigh(t);
+  }
+  // keys of tokens 4 q .. 4 q + 3
+  auto quad = [&](int q, uint32_t (&k)[4]) {
+    if (4 * q + 4 <= P.cached) {
+      const uint4 x = *reinterpret_cast<const uint4*>(select_keys + 4 * q);
+      k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = weigh(4 * q + i);
+    }
+  };
   const int need = K - P.sink - P.recent;
   uint32_t T = 0xFFFFFFFFu;
   uint32_t take = 0;  // of those equal to T, the first so many
   if (need > 0) {
     uint32_t prefix = 0;
     take = need;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += NT) hist[i] = 0;
+    // bits 31..21, 20..10, 9..0: the first pass tells signs, exponents and two
+    // more bits apart, so that few of a warp's additions meet in one bin
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < kSelectBins; i += NT) hist[i] = 0;
       __syncthreads();
-      for (int t = lo + tid; t < hi; t += NT) {
-        const uint32_t k = key(t);
-        if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      for (int q = tid; 4 * q < hi; q += NT) {
+        uint32_t k[4];
+        quad(q, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (pass == 0 || (k[i] >> (shift + bits)) == prefix)
+            atomicAdd(&hist[(k[i] >> shift) & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      if (warp == 0) {
-        // lane l has bins 255 - 8l .. 248 - 8l: from the largest down
-        uint32_t n[8], mine = 0;
+      // From the largest bin down: warp w has bins kSelectBins - 1 - 32 PER w
+      // downwards, its lane l the PER of them from 32 PER w + PER l on.
+      uint32_t n[PER], mine = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mine += n[k] = hist[255 - 8 * lane - k];
-        uint32_t upto = mine;
+      for (int k = 0; k < PER; ++k) mine += n[k] = hist[kSelectBins - 1 - (warp * 32 + lane) * PER - k];
+      uint32_t upto = mine;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t x = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += x;
-        }
-        uint32_t before = upto - mine;
-        if (before < take && upto >= take) {
-          for (int k = 0; k < 8; ++k) {
-            if (before + n[k] >= take) {
-              found[0] = 255 - 8 * lane - k;
-              found[1] = take - before;
-              break;
-            }
-            before += n[k];
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += x;
+      }
+      if (lane == 31) warp_bins[warp] = upto;
+      __syncthreads();
+      uint32_t before = upto - mine;
+      for (int w = 0; w < warp; ++w) before += warp_bins[w];
+      if (before < take && before + mine >= take) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          if (before < take && before + n[k] >= take) {
+            found[0] = kSelectBins - 1 - (warp * 32 + lane) * PER - k;
+            found[1] = take - before;
           }
+          before += n[k];
         }
       }
       __syncthreads();
-      prefix = (prefix << 8) | found[0];
+      prefix = (prefix << bits) | found[0];
       take = found[1];
     }
     T = prefix;
   }
-  // The chosen: first and last ones, keys above T, the first `take` equal to T
-  const int seg = ((L + NWARP - 1) / NWARP + 31) / 32 * 32;
-  const int s0 = min(L, warp * seg), s1 = min(L, s0 + seg);
-  auto kind = [&](int t) {  // 2: chosen, 1: equal to T, 0: neither
-    if (t < lo || t >= hi) return 2;
-    if (need == 0) return 0;
-    const uint32_t k = key(t);
-    return k > T ? 2 : (k == T ? 1 : 0);
+  // The chosen: first and last ones, keys above T, the first `take` equal to T.
+  // Per quad: 2 bits a token, 2: chosen, 1: equal to T
+  const int seg = ((L + NWARP - 1) / NWARP + 127) / 128 * 32;  // quads a warp
+  const int s0 = min((L + 3) / 4, warp * seg), s1 = min((L + 3) / 4, s0 + seg);
+  auto kinds = [&](int q) {
+    uint32_t k[4], x = 0;
+    const int t = 4 * q;
+    if (need > 0 && t < hi && t + 4 > lo) {
+      quad(q, k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x |= (k[i] > T ? 2u << (2 * i) : 0u) | (k[i] == T ? 1u << (2 * i) : 0u);
+    }
+    if (t < lo || t + 4 > hi) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t + i < lo || t + i >= hi) x = (x & ~(3u << (2 * i))) | (t + i < L ? 2u << (2 * i) : 0u);
+      }
+    }
+    return x;
   };
+  auto counts = [](uint32_t x) { return (uint32_t)__popc(x & 0xAAu) | ((uint32_t)__popc(x & 0x55u) << 16); };
   __syncthreads();
   int na = 0, ne = 0;
-  for (int t = s0 + lane; t < s1; t += 32) {
-    const int k = kind(t);
-    na += k == 2;
-    ne += k == 1;
+  for (int q = s0 + lane; q < s1; q += 32) {
+    const uint32_t x = kinds(q);
+    na += __popc(x & 0xAAu);
+    ne += __popc(x & 0x55u);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
@@ -155,18 +238,29 @@ __global__ void __launch_bounds__(kTokenSelectThreads) paged_kv_token_select_ker
     a0 += above[w];
     e0 += equal[w];
   }
-  const unsigned below = (1u << lane) - 1u;
-  for (int t0 = s0; t0 < s1; t0 += 32) {
-    const int t = t0 + lane;
-    const int k = t < s1 ? kind(t) : 0;
-    const unsigned ma = __ballot_sync(0xffffffffu, k == 2), me = __ballot_sync(0xffffffffu, k == 1);
-    const int a = a0 + __popc(ma & below), e = e0 + __popc(me & below);
-    if (k == 2 || (k == 1 && e < (int)take)) {
-      const int at = a + min(e, (int)take);
-      if (at < K) out[at] = t;
+  for (int q0 = s0; q0 < s1; q0 += 32) {
+    const uint32_t x = q0 + lane < s1 ? kinds(q0 + lane) : 0u;
+    const uint32_t mine = counts(x);
+    uint32_t upto = mine;  // both counts at once: at most 128 each
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
     }
-    a0 += __popc(ma);
-    e0 += __popc(me);
+    int a = a0 + (int)((upto - mine) & 0xFFFFu), e = e0 + (int)((upto - mine) >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t kind = (x >> (2 * i)) & 3u;
+      if (kind == 2u || (kind == 1u && e < (int)take)) {
+        const int at = a + min(e, (int)take);
+        if (at < K) out[at] = 4 * (q0 + lane) + i;
+      }
+      a += kind == 2u;
+      e += kind == 1u;
+    }
+    const uint32_t sum = __shfl_sync(0xffffffffu, upto, 31);
+    a0 += (int)(sum & 0xFFFFu);
+    e0 += (int)(sum >> 16);
   }
 }
 
@@ -183,8 +277,9 @@ int sms() {
 }
 
 constexpr int kMaxTokens = 1 << 30;
-constexpr int kRowTiles = 4;    // row tiles of a CTA of the first grid, where there is more than one
-constexpr int kQueryTiles = 16; // and of Q in shared memory in the second
+constexpr unsigned long long kWaitBudgetNs = 100ull * 1000ull * 1000ull;  // 100 ms per bounded wait
+constexpr int kRowTiles = 8;     // row tiles of a CTA of the first grid, where there is more than one
+constexpr int kQueryTiles = 16;  // and of Q in shared memory in the second
 
 struct WeightsPlan {
   long long rows;   // per (b, g)
@@ -210,15 +305,15 @@ pkd_status check_weights(int num_seqs, int q_len, int num_q_heads, int num_kv_he
 WeightsPlan plan_weights(int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int max_context_len) {
   WeightsPlan p{};
   p.rows = (long long)q_len * (num_q_heads / num_kv_heads);
-  p.row_tiles = p.rows <= 16 ? 1 : kRowTiles;
-  p.row_chunks = (int)((p.rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
+  p.row_tiles = p.rows <= 8 ? 0 : (p.rows <= 16 ? 1 : kRowTiles);
+  p.row_chunks = p.row_tiles < 2 ? 1 : (int)((p.rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
   const long long bg = (long long)num_seqs * num_kv_heads;
-  const long long want = 8LL * sms();  // CTAs
+  const long long want = (p.rows <= kFinishMaxRows ? 16LL : 4LL) * sms();  // CTAs
   long long part = 128;
   while (part < 4096 && bg * p.row_chunks * ((max_context_len + part - 1) / part) > want) part *= 2;
   p.part = (int)part;
   p.np = (int)std::max(1LL, (max_context_len + part - 1) / part);
-  p.scores = p.rows <= 16;
+  p.scores = p.rows <= kFinishMaxRows;
   p.score_stride = (long long)round_up((size_t)p.np * p.part, 64);
   p.stats = round_up((size_t)bg * p.np * p.rows * sizeof(float), 256);
   p.total = 2 * p.stats + (p.scores ? round_up((size_t)bg * p.rows * p.score_stride * sizeof(float), 256) : 0);
@@ -230,10 +325,16 @@ pkd_status launch_weights(const WeightsPlan& plan, WeightsParams p, cudaStream_t
   const long long bg = (long long)p.num_seqs * p.num_kv_heads;
   const long long grid = bg * plan.np * plan.row_chunks;
   if (grid > 0x7fffffffLL) return PKD_ERR_SHAPE;
-  if (plan.row_tiles == 1)
-    paged_weights_rows_kernel<KV, D, 1><<<(unsigned)grid, 32 * kWeightsWarps, 0, stream>>>(p);
-  else
-    paged_weights_rows_kernel<KV, D, kRowTiles><<<(unsigned)grid, 32 * kWeightsWarps, 0, stream>>>(p);
+  auto smem = [](int tiles) { return tiles * ((D / 16) * 32 * 16 + 16 * 4); };
+  // (the attributes belong to the kernels: what the largest call needs, the same for all)
+  if (plan.row_tiles < 2) {
+    auto* fn = plan.row_tiles == 0 ? paged_weights_few_kernel<KV, D, 1> : paged_weights_few_kernel<KV, D, 2>;
+    constexpr int bytes = WeightsRing<KV, D>::SMEM;
+    if (failed(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return PKD_ERR_LAUNCH;
+    fn<<<(unsigned)grid, 32 * kWeightsWarps, bytes, stream>>>(p, kWaitBudgetNs);
+  } else {
+    paged_weights_rows_kernel<KV, D, kRowTiles><<<(unsigned)grid, 32 * kWeightsWarps, smem(kRowTiles), stream>>>(p);
+  }
   if (cudaGetLastError() != cudaSuccess) return PKD_ERR_LAUNCH;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -250,8 +351,6 @@ pkd_status launch_weights(const WeightsPlan& plan, WeightsParams p, cudaStream_t
     return failed(cudaLaunchKernelEx(&cfg, paged_weights_scores_kernel, p, chunks)) ? PKD_ERR_LAUNCH : PKD_OK;
   }
   auto* fn = paged_weights_keys_kernel<KV, D>;
-  auto smem = [](int tiles) { return tiles * ((D / 16) * 32 * 16 + 2 * 16 * 4); };
-  // (the attribute belongs to the kernel: what the largest call needs, the same for all)
   if (failed(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(kQueryTiles))))
     return PKD_ERR_LAUNCH;
   p.q_tiles = (int)std::min<long long>(kQueryTiles, (plan.rows + 15) / 16);
@@ -323,7 +422,10 @@ pkd_status paged_kv_attention_weights(const void* q, const void* k_cache, const 
   p.part = plan.part;
   p.np = plan.np;
   p.row_chunks = plan.row_chunks;
-  p.scale_log2 = scale * k_scale * 1.4426950408889634f * (kv_type == PKD_KV_INT4 ? kInt4Unscale : 1.f);
+  const float s = scale * k_scale * 1.4426950408889634f * (kv_type == PKD_KV_INT4 ? kInt4Unscale : 1.f);
+  p.q_sign = s < 0.f ? 0x80008000u : 0u;
+  // (a scale of 0, equal weights: one too small to tell, so that -inf times it stays -inf)
+  p.scale_log2 = std::max(std::fabs(s), 1e-30f);
   p.decay = decay;
   p.error_word = error_word;
   p.bases = kInt4Bases;
@@ -373,11 +475,16 @@ pkd_status paged_kv_token_select(const float* weights, const int32_t* block_tabl
   p.error_word = error_word;
   // keys of longer contexts are read again in every pass
   constexpr int kMostCached = 48 * 1024;
-  p.cached = max_context_len <= max_kept ? 0 : std::min(max_context_len, kMostCached);
-  if (failed(cudaFuncSetAttribute(paged_kv_token_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  4 * kMostCached)))
+  p.cached = max_context_len <= max_kept ? 0 : (int)round_up((size_t)std::min(max_context_len, kMostCached), 4);
+  p.block_shift = -1;
+  if (block_size % 4 == 0 && (block_size & (block_size - 1)) == 0 && aligned(weights, 16))
+    for (p.block_shift = 2; 1 << p.block_shift < block_size;) ++p.block_shift;
+  // a thread has one round of eight loads of four keys, up to 1024 of them
+  const bool wide = p.cached > 8192;
+  auto* fn = wide ? paged_kv_token_select_kernel<1024> : paged_kv_token_select_kernel<256>;
+  if (failed(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostCached)))
     return PKD_ERR_LAUNCH;
-  paged_kv_token_select_kernel<<<(unsigned)grid, kTokenSelectThreads, 4 * p.cached, stream>>>(p);
+  fn<<<(unsigned)grid, wide ? 1024 : 256, 4 * p.cached, stream>>>(p);
   return launched();
 }
 
@@ -416,7 +523,9 @@ pkd_status paged_kv_compact(void* k_cache, void* v_cache, float* weights, const 
   p.max_new_blocks = max_new_blocks;
   p.error_word = error_word;
   const long long most = std::min<long long>(max_kept, (long long)max_new_blocks * block_size);
-  p.chunks = (int)((most + kCompactRows - 1) / kCompactRows);
+  const KvType kv = kv_type == PKD_KV_FP16 ? kKvFp16 : (kv_type == PKD_KV_E4M3 ? kKvE4m3 : kKvInt4);
+  const int rows = compact_rows(kv, head_dim);
+  p.chunks = (int)((most + rows - 1) / rows);
   const long long grid = (long long)num_seqs * num_kv_heads * p.chunks;
   if (grid > 0x7fffffffLL) return PKD_ERR_SHAPE;
 #define PKD_COMPACT(KV_) (head_dim == 128 ? paged_kv_compact_kernel<KV_, 128> : paged_kv_compact_kernel<KV_, 64>)

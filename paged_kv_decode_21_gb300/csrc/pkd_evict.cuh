@@ -16,17 +16,21 @@ enum KvType : int { kKvFp16 = 0, kKvE4m3 = 1, kKvInt4 = 2 };
 // Attention weights.  w_t = sum over rows (query token, head) of
 // exp(s_rt - M_r) / Z_r needs every row's maximum and sum before the first
 // weight, so two grids: the first reads K, and leaves each row's maximum and
-// sum over every partition of the tokens; the second merges those and adds up
-// the weights.  Where rows are few, the first also leaves the scores, 4 bytes a
-// row and token, and the second reads those; where they are many it reads K
-// again and multiplies again, since a score written and read takes 8 bytes and a
-// key 2D and less.
+// sum over every partition of the tokens; the second merges those to
+// log2(Z_r) + M_r, which is all a weight needs, 2^(s - that), and adds up the
+// weights.  Where rows are few, the first also leaves the scores, 4 bytes a row
+// and token, and the second reads those; where they are many it reads K again
+// and multiplies again, since a score written and read takes 8 bytes and a key
+// 2D and less.
 //
-// S = Q K^T by mma.m16n8k16: 16 rows times 8 tokens, keys going from global
-// memory straight into B fragments: lane (r, c) holds the dims of token r that
-// come as its 16-byte loads, and Q's A fragments, kept in shared memory, follow
-// that order of dims (key_dim).  The next 16 tokens' loads are requested before
-// this tile's products.
+// S = Q K^T by mma.m16n8k16: 16 rows times 8 tokens.  Lane (r, c) holds the dims
+// of token r that come as its 16-byte loads, as B fragments, and Q's A fragments
+// (registers for up to 16 rows, shared memory for more) follow that order of
+// dims (below).  Few rows: bound by K's read, so K comes by bulk copies of whole
+// (block, kv head) tiles into a ring of every warp's own, 32 tokens a slot.  Many
+// rows: bound by the products, so keys go from global memory straight into the
+// fragments, 16 tokens a warp and step over fp16 caches, 32 over the others, the
+// next step's requested before this one's products.
 struct WeightsParams {
   const __half* q;
   const void* k_cache;
@@ -37,10 +41,11 @@ struct WeightsParams {
   long long score_stride;
   int num_seqs, q_len, num_q_heads, num_kv_heads, block_size, num_blocks, max_blocks_per_seq;
   int rows;       // R = q_len * group
-  int part, np;   // tokens per partition (a multiple of 64), partitions
+  int part, np;   // tokens per partition (a multiple of 128), partitions
   int row_chunks; // first grid: chunks of 16 RT rows
   int q_tiles;    // second grid, keys again: row tiles of Q in shared memory at a time
-  float scale_log2, decay;
+  float scale_log2, decay;  // scale_log2 > 0
+  uint32_t q_sign;          // flips Q where the scale is negative
   int* error_word;
   Int4Bases bases;
 };
@@ -48,15 +53,14 @@ struct WeightsParams {
 constexpr int kWeightsWarps = 4;
 constexpr int kWeightsFinishThreads = 256;
 
-// The dim that k-step s has in slot pair h (0: slots 2c, 2c + 1; 1: slots 8 +
-// 2c, 9 + 2c), half e, of lane c.
-template <int KV, int D>
-__device__ __forceinline__ int key_dim(int s, int c, int h, int e) {
-  if (KV == kKvFp16) return 32 * (s / 2) + 8 * c + 4 * (s % 2) + 2 * h + e;
-  if (KV == kKvE4m3) return 64 * (s / 4) + 16 * c + 4 * (s % 4) + 2 * h + e;
-  // words of eight codes, halves four dims apart; a lane has D / 4 neighbouring dims
-  return (D / 4) * c + 8 * (s / 2) + 2 * (s % 2) + h + 4 * e;
-}
+// 8-token columns of a warp's step.
+constexpr __host__ __device__ int key_tiles(int KV) { return KV == kKvFp16 ? 2 : 4; }
+
+// The order of dims: k-step s has in slot pair h (0: slots 2c, 2c + 1; 1: slots
+// 8 + 2c, 9 + 2c), half e, of lane c the dim
+//   fp16   32 (s / 2) + 8c + 4 (s % 2) + 2h + e
+//   E4M3   64 (s / 4) + 16c + 4 (s % 4) + 2h + e
+//   4 bits (D / 4) c + 8 (s / 2) + 2 (s % 2) + h + 4e     (words of eight codes, halves four dims apart)
 
 // Raw keys of 8 tokens, one of them (and a quarter of its dims) a lane's.
 template <int KV, int D>
@@ -126,64 +130,110 @@ struct KeyRow {
   }
 };
 
+// Row `row` of Q for (b, g): query token row / G, head row % G of the group.
+template <int D>
+__device__ __forceinline__ const __half* query_row(const WeightsParams& P, int b, int g, int row) {
+  const int G = P.rows / P.q_len;
+  return P.q + (((size_t)b * P.q_len + row / G) * P.num_q_heads + (size_t)g * G + row % G) * D;
+}
+// Eight dims of Q, 8 ch on, as the halves that two neighbouring k-steps take:
+// w[2 p + h] is slot pair h of step s + p for lane c (the order above, the other way round).
+struct QueryWords {
+  int s, c;
+  uint32_t w[4];
+};
+template <int KV, int D>
+__device__ __forceinline__ QueryWords query_words(const uint4 u, int ch, uint32_t sign) {
+  QueryWords q;
+  if constexpr (KV == kKvInt4) {
+    q.c = ch / (D / 32);
+    q.s = 2 * (ch % (D / 32));
+    q.w[0] = prmt(u.x, u.z, 0x5410);
+    q.w[1] = prmt(u.x, u.z, 0x7632);
+    q.w[2] = prmt(u.y, u.w, 0x5410);
+    q.w[3] = prmt(u.y, u.w, 0x7632);
+  } else {
+    q.c = KV == kKvFp16 ? ch % 4 : ch / 2 % 4;
+    q.s = KV == kKvFp16 ? 2 * (ch / 4) : 4 * (ch / 8) + 2 * (ch % 2);
+    q.w[0] = u.x;
+    q.w[1] = u.y;
+    q.w[2] = u.z;
+    q.w[3] = u.w;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) q.w[k] ^= sign;
+  return q;
+}
+// The i-th of the D / 32 such eights that lane c takes.
+template <int KV, int D>
+__device__ __forceinline__ int query_eight(int i, int c) {
+  return KV == kKvFp16 ? 4 * i + c : (KV == kKvE4m3 ? 8 * (i / 2) + 2 * c + i % 2 : (D / 32) * c + i);
+}
+
 // Q's rows 16 rt .. of tiles [first, first + n) as A fragments in shared memory: [tile][k-step][lane] uint4.
 template <int KV, int D>
 __device__ __forceinline__ void load_query_tiles(const WeightsParams& P, uint4* qs, int b, int g, int first, int n) {
-  const int G = P.rows / P.q_len;
-  uint32_t* w = reinterpret_cast<uint32_t*>(qs);
-  for (int i = threadIdx.x; i < n * (D / 16) * 128; i += blockDim.x) {
-    const int reg = i % 4, lane = (i / 4) % 32, s = (i / 128) % (D / 16), rt = i / 128 / (D / 16);
-    const int row = (first + rt) * 16 + lane / 4 + 8 * (reg & 1);
-    uint32_t x = 0;
-    if (row < P.rows) {
-      const unsigned short* q = reinterpret_cast<const unsigned short*>(P.q) +
-                                (((size_t)b * P.q_len + row / G) * P.num_q_heads + (size_t)g * G + row % G) * D;
-      x = q[key_dim<KV, D>(s, lane % 4, reg >> 1, 0)] | ((uint32_t)q[key_dim<KV, D>(s, lane % 4, reg >> 1, 1)] << 16);
+  uint32_t* words = reinterpret_cast<uint32_t*>(qs);
+  constexpr int U = 4;
+  for (int i0 = threadIdx.x; i0 < n * 16 * (D / 8); i0 += U * blockDim.x) {
+    uint4 u[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * blockDim.x, row = first * 16 + i / (D / 8);
+      u[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < n * 16 * (D / 8) && row < P.rows)
+        u[k] = *reinterpret_cast<const uint4*>(query_row<D>(P, b, g, row) + 8 * (i % (D / 8)));
     }
-    w[i] = x;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * blockDim.x, row = i / (D / 8);
+      if (i >= n * 16 * (D / 8)) break;
+      const QueryWords q = query_words<KV, D>(u[k], i % (D / 8), P.q_sign);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        words[(((row / 16 * (D / 16) + q.s + x / 2) * 32 + row % 8 * 4 + q.c) * 4) + 2 * (x % 2) + row / 8 % 2] = q.w[x];
+    }
   }
 }
 
-// Scores (log2 units, masked) of one row tile over 16 tokens: sc[nt][e] of row
-// r + 8 (e / 2), token 8 nt + 2c + e % 2.  lim: tokens that the rows r, r + 8 see from the tile's first on.
-template <int D>
-__device__ __forceinline__ void tile_scores(const uint4* qs, const uint32_t (&b0)[D / 8], const uint32_t (&b1)[D / 8],
-                                            float scale_log2, const int (&lim)[2], float (&sc)[2][4]) {
-  const int lane = threadIdx.x & 31, c = lane % 4;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    const uint4 u = qs[s * 32 + lane];
-    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-    mma_16816(sc[0], a, b0[2 * s], b0[2 * s + 1]);
-    mma_16816(sc[1], a, b1[2 * s], b1[2 * s + 1]);
-  }
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      sc[nt][e] = 8 * nt + 2 * c + e % 2 < lim[e / 2] ? sc[nt][e] * scale_log2 : -INFINITY;
-}
-
-// The keys of a warp's tiles of 16 tokens, a tile requested ahead.
+// A warp's steps over tokens [t0, t1): step n has tokens t0 + STEP (warp + NW n) ..; keys a step ahead, block ids
+// further.
 template <int KV, int D>
 struct KeyStream {
-  KeyRow<KV, D> next[2];
-  bool next_ok;
-  __device__ __forceinline__ void request(const WeightsParams& P, int b, int g, int t, int t1) {
-    const int lane = threadIdx.x & 31, r = lane / 4, c = lane % 4;
-    next_ok = false;
-    if (t < t1) {
-      const int pb = P.block_tables[(size_t)b * P.max_blocks_per_seq + t / P.block_size];
-      next_ok = pb >= 0 && pb < P.num_blocks;
-      if (!next_ok && lane == 0) record_error(P.error_word, kErrBadBlock);
-      const size_t tile = (size_t)(next_ok ? pb : 0) * P.num_kv_heads + g;
+  static constexpr int TILES = key_tiles(KV), STEP = 8 * TILES, HALVES = STEP / 16;
+  static constexpr int IDS = 32 / HALVES;  // steps whose block ids the lanes hold
+  KeyRow<KV, D> next[TILES];
+  int ids;                   // lane: half lane % HALVES of step lane / HALVES of this run of IDS
+  int block[HALVES];         // of the next step's halves; negative where there is none
+  int t0, t1, warp;
+
+  __device__ __forceinline__ int token(int n) const { return t0 + STEP * (warp + kWeightsWarps * n); }
+  __device__ __forceinline__ void fetch_ids(const WeightsParams& P, int b, int n) {
+    const int lane = threadIdx.x & 31, t = token(n + lane / HALVES) + 16 * (lane % HALVES);
+    ids = t < t1 ? P.block_tables[(size_t)b * P.max_blocks_per_seq + t / P.block_size] : -1;
+    if (t < t1 && (ids < 0 || ids >= P.num_blocks)) {
+      record_error(P.error_word, kErrBadBlock);
+      ids = -1;
+    }
+  }
+  __device__ __forceinline__ void start(const WeightsParams& P, int b, int g, int first, int end) {
+    t0 = first;
+    t1 = end;
+    warp = threadIdx.x / 32;
+    request(P, b, g, 0);
+  }
+  __device__ __forceinline__ void request(const WeightsParams& P, int b, int g, int n) {
+    if (n % IDS == 0) fetch_ids(P, b, n);
+    const int lane = threadIdx.x & 31, r = lane / 4, c = lane % 4, t = token(n);
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+    for (int h = 0; h < HALVES; ++h) {
+      block[h] = __shfl_sync(0xffffffffu, ids, n % IDS * HALVES + h);
+      const size_t tile = (size_t)max(block[h], 0) * P.num_kv_heads + g;
+#pragma unroll
+      for (int nt = 2 * h; nt < 2 * h + 2; ++nt) {
         // rows past the length may hold anything; nothing of them is used
-        if (next_ok && t + 8 * nt + r < t1)
-          next[nt].load(P.k_cache, tile, P.block_size, t % P.block_size + 8 * nt + r, c);
+        if (block[h] >= 0 && t + 8 * nt + r < t1)
+          next[nt].load(P.k_cache, tile, P.block_size, (t + 16 * h) % P.block_size + 8 * (nt % 2) + r, c);
         else
           next[nt].clear();
       }
@@ -200,12 +250,213 @@ __device__ __forceinline__ int clamped_len(const int32_t* lens, int b, int block
   return L;
 }
 
-// First grid: CTA (row chunk, partition, b, g).
+// Scores outside [0, lim) of a step's tokens, and of halves without a block, become -inf; sc[nt][e]: row r + 8 (e /
+// 2), token 8 nt + 2c + e % 2.
+template <int TILES>
+__device__ __forceinline__ void mask_scores(float (&sc)[TILES][4], const int (&lim)[2], const int* block) {
+  const int c = threadIdx.x & 3;
+#pragma unroll
+  for (int nt = 0; nt < TILES; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (block[nt / 2] < 0 || 8 * nt + 2 * c + e % 2 >= lim[e / 2]) sc[nt][e] = -INFINITY;
+}
+
+// A row's maximum and sum over its four lanes, then over the warps, into partition j's place.
+template <int NR, int HF>
+__device__ __forceinline__ void store_rows(const WeightsParams& P, float (&m)[NR][HF], float (&l)[NR][HF], float* red,
+                                           int bg, int j, int first) {
+  constexpr int NW = kWeightsWarps, N = 16 * NR;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+#pragma unroll
+  for (int k = 0; k < NR; ++k)
+#pragma unroll
+    for (int hf = 0; hf < HF; ++hf) {
+      float mx = fmaxf(m[k][hf], __shfl_xor_sync(0xffffffffu, m[k][hf], 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      float z = mx == -INFINITY ? 0.f : l[k][hf] * ex2_approx(m[k][hf] - mx);
+      z += __shfl_xor_sync(0xffffffffu, z, 1);
+      z += __shfl_xor_sync(0xffffffffu, z, 2);
+      if (c == 0) {
+        red[warp * N + 16 * k + 8 * hf + r] = mx;
+        red[(NW + warp) * N + 16 * k + 8 * hf + r] = z;
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (HF == 1 ? 8 : N); i += 32 * NW) {
+    const int row = first + i;
+    if (row >= P.rows) break;
+    float mx = -INFINITY, z = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red[w * N + i]);
+    if (mx != -INFINITY)
+#pragma unroll
+      for (int w = 0; w < NW; ++w) z = fmaf(red[(NW + w) * N + i], ex2_approx(red[w * N + i] - mx), z);
+    const size_t at = ((size_t)bg * P.np + j) * P.rows + row;
+    P.row_max[at] = mx;
+    P.row_sum[at] = z;
+  }
+}
+
+// First grid, few rows (HF * 8 of them at most): CTA (partition, b, g).
+template <int KV, int D>
+struct WeightsRing {
+  static constexpr int UNIT = 32;  // tokens of a slot
+  static constexpr int SLOT = KV == kKvInt4 ? UNIT * D * 9 / 16 : UNIT * D * (KV == kKvFp16 ? 2 : 1);
+  static constexpr int SW = KV == kKvFp16 ? (D == 128 ? 3 : 4) : 4;  // slots a warp
+  static constexpr int SMEM = kWeightsWarps * SW * (SLOT + 8);
+};
+template <int KV, int D, int HF>
+__global__ void __launch_bounds__(32 * kWeightsWarps, KV == kKvFp16 && D == 128 ? 2 : 3)
+    paged_weights_few_kernel(const WeightsParams P, unsigned long long timeout_ns) {
+  using T = WeightsRing<KV, D>;
+  constexpr int NW = kWeightsWarps, TILES = T::UNIT / 8, KS = D / 16, SW = T::SW;
+  extern __shared__ __align__(128) unsigned char weights_smem[];
+  __shared__ float red[2 * NW * 16];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int j = blockIdx.x % P.np, bg = blockIdx.x / P.np;
+  const int g = bg % P.num_kv_heads, b = bg / P.num_kv_heads;
+  const int L = clamped_len(P.context_lens, b, P.block_size, P.max_blocks_per_seq, P.error_word);
+  const int t0 = j * P.part, t1 = min(L, t0 + P.part);
+  if (t0 >= L) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+  const int BS = P.block_size, per = T::UNIT / BS;  // tiles a slot: 1 or 2
+  const uint32_t tile_bytes = T::SLOT / per;
+  unsigned char* ring = weights_smem + warp * SW * T::SLOT;
+  uint64_t* full = reinterpret_cast<uint64_t*>(weights_smem + NW * SW * T::SLOT) + warp * SW;
+  if (lane == 0) {
+    for (int s = 0; s < SW; ++s) mbar_init(&full[s], 1);
+    fence_mbarrier_init();
+  }
+  __syncwarp();
+  const int units = (t1 - t0 + T::UNIT - 1) / T::UNIT, nblk = (t1 - t0 + BS - 1) / BS;
+  const int mine = units > warp ? (units - warp + NW - 1) / NW : 0;
+  const int32_t* bt = P.block_tables + (size_t)b * P.max_blocks_per_seq + t0 / BS;
+  // block ids: two places a unit, 16 units at a time, the next ones requested ahead
+  auto ids_at = [&](int first) {
+    const int n = first + lane / 2, k = (warp + NW * n) * per + lane % 2;
+    return n < mine && lane % 2 < per && k < nblk ? bt[k] : -1;
+  };
+  int ids = ids_at(0), ids_next = ids_at(16);
+  uint32_t bad_slots = 0;  // two bits a slot: tiles that are not there
+  const uint32_t ring_at = smem_u32(ring), full_at = smem_u32(full);
+  const char* kbase = static_cast<const char*>(P.k_cache) + (size_t)g * tile_bytes;
+  const uint64_t block_stride = (uint64_t)P.num_kv_heads * tile_bytes;
+  auto issue = [&](int n) {
+    if (n > 0 && n % 16 == 0) {
+      ids = ids_next;
+      ids_next = ids_at(n + 16);
+    }
+    const uint32_t slot = (uint32_t)n % SW, bar = full_at + slot * 8;
+    const int pb = __shfl_sync(0xffffffffu, ids, n % 16 * 2 + lane % 2);
+    const bool good = (uint32_t)pb < (uint32_t)P.num_blocks;
+    const uint32_t there = __ballot_sync(0xffffffffu, good) & (per == 2 ? 3u : 1u);
+    bad_slots |= (~there & 3u) << (2 * slot);
+    if (lane < per && !good && (warp + NW * n) * per + lane < nblk) record_error(P.error_word, kErrBadBlock);
+    if (lane == 0) int4_expect(bar, __popc(there) * tile_bytes);
+    if (lane < per && good)
+      int4_copy(ring_at + slot * T::SLOT + lane * tile_bytes, kbase + (uint64_t)(uint32_t)pb * block_stride, tile_bytes, bar);
+  };
+  int issued = 0;
+  for (; issued < SW && issued < mine; ++issued) issue(issued);
+  uint32_t qa[KS][2 * HF];
+#pragma unroll
+  for (int hf = 0; hf < HF; ++hf) {
+    const int row = r + 8 * hf;
+    const __half* q = query_row<D>(P, b, g, min(row, P.rows - 1));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (row < P.rows) u = *reinterpret_cast<const uint4*>(q + 8 * query_eight<KV, D>(i, c));
+      const QueryWords w = query_words<KV, D>(u, query_eight<KV, D>(i, c), P.q_sign);
+      // (steps by position: the i-th eight of a lane is steps 2i and 2i + 1)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) qa[2 * i + x / 2][HF * (x % 2) + hf] = w.w[x];
+    }
+  }
+  const int G = P.rows / P.q_len;
+  const int all_see = min(t1, L - P.q_len + 1);
+  int see[2] = {0, 0};
+#pragma unroll
+  for (int hf = 0; hf < HF; ++hf)
+    if (r + 8 * hf < P.rows) see[hf] = min(L - P.q_len + (r + 8 * hf) / G + 1, t1);
+  float m[1][HF], l[1][HF];
+#pragma unroll
+  for (int hf = 0; hf < HF; ++hf) {
+    m[0][hf] = -INFINITY;
+    l[0][hf] = 0.f;
+  }
+  float* scores[HF];
+#pragma unroll
+  for (int hf = 0; hf < HF; ++hf)
+    scores[hf] = P.scores + ((size_t)bg * P.rows + min(r + 8 * hf, P.rows - 1)) * P.score_stride + 2 * c;
+  for (int n = 0; n < mine; ++n) {
+    const uint32_t slot = (uint32_t)n % SW;
+    if (!mbar_wait_bounded(&full[slot], ((uint32_t)n / SW) & 1, timeout_ns)) {
+      if (lane == 0) record_error(P.error_word, kErrTimeout);
+      for (int v = n + 1; v < issued; ++v) mbar_wait_bounded(&full[v % SW], (v / SW) & 1, timeout_ns);
+      break;
+    }
+    const unsigned char* at = ring + slot * T::SLOT;
+    const int t = t0 + (warp + NW * n) * T::UNIT;
+    const uint32_t missing = bad_slots >> (2 * slot) & (per == 2 ? 3u : 1u);
+    bad_slots &= ~(3u << (2 * slot));
+    float sc[TILES][4];
+#pragma unroll
+    for (int nt = 0; nt < TILES; ++nt) {
+      KeyRow<KV, D> key;
+      const int row = 8 * nt + r;  // of the slot's tiles, one behind the other
+      key.load(at, row / BS, BS, row % BS, c);
+      uint32_t kb[D / 8];
+      key.fragments(kb, P.bases);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        mma_16816_from(sc[nt], s == 0, qa[s][0], HF == 2 ? qa[s][1] : 0u, qa[s][HF], HF == 2 ? qa[s][2 * HF - 1] : 0u,
+                       kb[2 * s], kb[2 * s + 1]);
+    }
+    __syncwarp();
+    if (issued < mine) {
+      fence_proxy_async_smem();  // our reads of the slot precede the next copies into it
+      issue(issued);
+      ++issued;
+    }
+    if (missing != 0 || t + T::UNIT > all_see) {
+      const int lim[2] = {see[0] - t, see[1] - t};
+      const int block[2] = {missing & 1 ? -1 : 0, (per == 2 ? missing & 2 : missing & 1) ? -1 : 0};
+      mask_scores<TILES>(sc, lim, block);
+    }
+#pragma unroll
+    for (int hf = 0; hf < HF; ++hf) {
+      float x[2 * TILES], mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2 * TILES; ++i) {
+        x[i] = sc[i / 2][2 * hf + i % 2] * P.scale_log2;
+        mx = fmaxf(mx, x[i]);
+      }
+      if (r + 8 * hf < P.rows) {
+#pragma unroll
+        for (int nt = 0; nt < TILES; ++nt)
+          *reinterpret_cast<float2*>(scores[hf] + t + 8 * nt) = make_float2(x[2 * nt], x[2 * nt + 1]);
+      }
+      const float mn = fmaxf(m[0][hf], mx);
+      const float mu = mn == -INFINITY ? 0.f : mn;  // nothing seen so far
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * TILES; ++i) sum += ex2_approx(x[i] - mu);
+      l[0][hf] = fmaf(l[0][hf], ex2_approx(m[0][hf] - mu), sum);
+      m[0][hf] = mn;
+    }
+  }
+  store_rows<1, HF>(P, m, l, red, bg, j, 0);
+}
+
+// First grid, many rows: CTA (chunk of 16 RT rows, partition, b, g).
 template <int KV, int D, int RT>
-__global__ void __launch_bounds__(32 * kWeightsWarps) paged_weights_rows_kernel(const WeightsParams P) {
-  constexpr int NW = kWeightsWarps;
-  __shared__ uint4 qs[RT * (D / 16) * 32];
-  __shared__ float red[2][NW][16 * RT];
+__global__ void __launch_bounds__(32 * kWeightsWarps, 3) paged_weights_rows_kernel(const WeightsParams P) {
+  constexpr int NW = kWeightsWarps, TILES = key_tiles(KV), KS = D / 16, CHUNK = 16 * RT;
+  extern __shared__ __align__(128) unsigned char weights_smem[];
+  uint4* qs = reinterpret_cast<uint4*>(weights_smem);
+  __shared__ float red[2 * NW * CHUNK];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rc = blockIdx.x % P.row_chunks;
   const int rest = blockIdx.x / P.row_chunks;
@@ -214,170 +465,180 @@ __global__ void __launch_bounds__(32 * kWeightsWarps) paged_weights_rows_kernel(
   const int L = clamped_len(P.context_lens, b, P.block_size, P.max_blocks_per_seq, P.error_word);
   const int t0 = j * P.part, t1 = min(L, t0 + P.part);
   if (t0 >= L) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+  const int lane = threadIdx.x % 32, r = lane / 4;
   KeyStream<KV, D> keys;
-  keys.request(P, b, g, t0 + 16 * warp, t1);
-  const int tiles = min(RT, (P.rows - rc * 16 * RT + 15) / 16);
+  keys.start(P, b, g, t0, t1);
+  const int tiles = min(RT, (P.rows - rc * CHUNK + 15) / 16);
   load_query_tiles<KV, D>(P, qs, b, g, rc * RT, tiles);
   __syncthreads();
   const int G = P.rows / P.q_len;
-  int see[RT][2];  // tokens that the lane's rows see
+  const int all_see = min(t1, L - P.q_len + 1);  // tokens that every row sees
+  auto sees = [&](int k, int hf) {
+    const int row = (rc * RT + k) * 16 + r + 8 * hf;
+    return row < P.rows ? min(L - P.q_len + row / G + 1, t1) : 0;
+  };
   float m[RT][2], l[RT][2];
 #pragma unroll
   for (int k = 0; k < RT; ++k)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int row = (rc * RT + k) * 16 + r + 8 * hf;
-      see[k][hf] = row < P.rows ? L - P.q_len + row / G + 1 : 0;
       m[k][hf] = -INFINITY;
       l[k][hf] = 0.f;
     }
-  for (int t = t0 + 16 * warp; t < t1; t += 16 * NW) {
-    uint32_t b0[D / 8], b1[D / 8];
-    keys.next[0].fragments(b0, P.bases);
-    keys.next[1].fragments(b1, P.bases);
-    const bool ok = keys.next_ok;
-    keys.request(P, b, g, t + 16 * NW, t1);
+  for (int n = 0; keys.token(n) < t1; ++n) {
+    const int t = keys.token(n);
+    uint32_t kb[TILES][D / 8];
+    int block[TILES / 2];
+    bool whole = t + 8 * TILES <= all_see;
+#pragma unroll
+    for (int nt = 0; nt < TILES; ++nt) keys.next[nt].fragments(kb[nt], P.bases);
+#pragma unroll
+    for (int h = 0; h < TILES / 2; ++h) {
+      block[h] = keys.block[h];
+      whole &= block[h] >= 0;
+    }
+    keys.request(P, b, g, n + 1);
 #pragma unroll
     for (int k = 0; k < RT; ++k) {
       if (k >= tiles) break;
-      const int lim[2] = {ok ? min(see[k][0], t1) - t : 0, ok ? min(see[k][1], t1) - t : 0};
-      float sc[2][4];
-      tile_scores<D>(qs + k * (D / 16) * 32, b0, b1, P.scale_log2, lim, sc);
+      float sc[TILES][4];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const uint4 w = qs[(k * KS + s) * 32 + lane];
+#pragma unroll
+        for (int nt = 0; nt < TILES; ++nt)
+          mma_16816_from(sc[nt], s == 0, w.x, w.y, w.z, w.w, kb[nt][2 * s], kb[nt][2 * s + 1]);
+      }
+      if (!whole) {
+        const int lim[2] = {sees(k, 0) - t, sees(k, 1) - t};
+        mask_scores<TILES>(sc, lim, block);
+      }
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const float s0 = sc[0][2 * hf], s1 = sc[0][2 * hf + 1], s2 = sc[1][2 * hf], s3 = sc[1][2 * hf + 1];
-        const float mn = fmaxf(m[k][hf], fmaxf(fmaxf(s0, s1), fmaxf(s2, s3)));
+        float mx = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < TILES; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][2 * hf], sc[nt][2 * hf + 1]));
+        const float mn = fmaxf(m[k][hf], mx * P.scale_log2);
         const float mu = mn == -INFINITY ? 0.f : mn;  // nothing seen so far
-        l[k][hf] = l[k][hf] * ex2_approx(m[k][hf] - mu) + (ex2_approx(s0 - mu) + ex2_approx(s1 - mu)) +
-                   (ex2_approx(s2 - mu) + ex2_approx(s3 - mu));
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < TILES; ++nt)
+          sum += ex2_approx(fmaf(sc[nt][2 * hf], P.scale_log2, -mu)) +
+                 ex2_approx(fmaf(sc[nt][2 * hf + 1], P.scale_log2, -mu));
+        l[k][hf] = fmaf(l[k][hf], ex2_approx(m[k][hf] - mu), sum);
         m[k][hf] = mn;
-        const int row = (rc * RT + k) * 16 + r + 8 * hf;
-        if (P.scores && row < P.rows) {
-          float* o = P.scores + ((size_t)bg * P.rows + row) * P.score_stride + t + 2 * c;
-          *reinterpret_cast<float2*>(o) = make_float2(s0, s1);
-          *reinterpret_cast<float2*>(o + 8) = make_float2(s2, s3);
-        }
       }
     }
   }
-  // a row's statistics over its four lanes, then over the warps
-#pragma unroll
-  for (int k = 0; k < RT; ++k)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float mx = fmaxf(m[k][hf], __shfl_xor_sync(0xffffffffu, m[k][hf], 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      float z = mx == -INFINITY ? 0.f : l[k][hf] * ex2_approx(m[k][hf] - mx);
-      z += __shfl_xor_sync(0xffffffffu, z, 1);
-      z += __shfl_xor_sync(0xffffffffu, z, 2);
-      if (c == 0) {
-        red[0][warp][16 * k + 8 * hf + r] = mx;
-        red[1][warp][16 * k + 8 * hf + r] = z;
-      }
-    }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * RT; i += 32 * NW) {
-    const int row = rc * 16 * RT + i;
-    if (row >= P.rows) break;
-    float mx = -INFINITY, z = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red[0][w][i]);
-    if (mx != -INFINITY)
-#pragma unroll
-      for (int w = 0; w < NW; ++w) z = fmaf(red[1][w][i], ex2_approx(red[0][w][i] - mx), z);
-    const size_t at = ((size_t)bg * P.np + j) * P.rows + row;
-    P.row_max[at] = mx;
-    P.row_sum[at] = z;
-  }
+  store_rows<RT, 2>(P, m, l, red, bg, j, rc * CHUNK);
 }
 
-// Rows first .. first + n - 1 of (b, g): maximum and 1 / sum over the partitions written (0 where nothing is seen).
-__device__ __forceinline__ void merge_rows(const WeightsParams& P, int bg, int L, int first, int n, float* mx_out,
-                                           float* inv_out) {
+// Rows first .. first + n - 1 of (b, g): M + log2(Z) over the partitions written (+inf where nothing is seen).
+__device__ __forceinline__ void merge_rows(const WeightsParams& P, int bg, int L, int first, int n, float* out) {
   const int np = min(P.np, (L - 1) / P.part + 1);
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const size_t at = (size_t)bg * P.np * P.rows + first + i;
     float mx = -INFINITY, z = 0.f;
     for (int j = 0; j < np; ++j) mx = fmaxf(mx, P.row_max[at + (size_t)j * P.rows]);
-    if (mx == -INFINITY) mx = 0.f;
-    for (int j = 0; j < np; ++j)
-      z = fmaf(P.row_sum[at + (size_t)j * P.rows], ex2_approx(P.row_max[at + (size_t)j * P.rows] - mx), z);
-    mx_out[i] = mx;
-    inv_out[i] = z > 0.f ? 1.f / z : 0.f;
+    if (mx != -INFINITY)
+      for (int j = 0; j < np; ++j)
+        z = fmaf(P.row_sum[at + (size_t)j * P.rows], ex2_approx(P.row_max[at + (size_t)j * P.rows] - mx), z);
+    out[i] = z > 0.f ? mx + __log2f(z) : INFINITY;
   }
 }
 
 // Second grid, few rows: CTA (1024 tokens, b, g); a thread takes four neighbouring tokens.
-constexpr int kFinishMaxRows = 64;
+constexpr int kFinishMaxRows = 16;
 __global__ void __launch_bounds__(kWeightsFinishThreads) paged_weights_scores_kernel(const WeightsParams P, int chunks);
 
 // Second grid, many rows: CTA (partition, b, g) multiplies again.
 template <int KV, int D>
-__global__ void __launch_bounds__(32 * kWeightsWarps) paged_weights_keys_kernel(const WeightsParams P) {
-  constexpr int NW = kWeightsWarps;
+__global__ void __launch_bounds__(32 * kWeightsWarps, 3) paged_weights_keys_kernel(const WeightsParams P) {
+  constexpr int NW = kWeightsWarps, TILES = key_tiles(KV), KS = D / 16;
   extern __shared__ __align__(16) unsigned char weights_smem[];
   uint4* qs = reinterpret_cast<uint4*>(weights_smem);
-  float* row_mx = reinterpret_cast<float*>(qs + P.q_tiles * (D / 16) * 32);
-  float* row_inv = row_mx + 16 * P.q_tiles;
+  float* row_off = reinterpret_cast<float*>(qs + P.q_tiles * KS * 32);
   const int j = blockIdx.x % P.np, bg = blockIdx.x / P.np;
   const int g = bg % P.num_kv_heads, b = bg / P.num_kv_heads;
   const int L = clamped_len(P.context_lens, b, P.block_size, P.max_blocks_per_seq, nullptr);
   const int t0 = j * P.part, t1 = min(L, t0 + P.part);
   if (t0 >= L) return;
   const int start = P.start_lens ? P.start_lens[b] : L;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+  const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
   const int G = P.rows / P.q_len;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int all_see = min(t1, L - P.q_len + 1);
   for (int first = 0; first < P.rows; first += 16 * P.q_tiles) {
     const int tiles = min(P.q_tiles, (P.rows - first + 15) / 16);
     KeyStream<KV, D> keys;
-    keys.request(P, b, g, t0 + 16 * warp, t1);
+    keys.start(P, b, g, t0, t1);
     __syncthreads();  // the rows before are done with
     load_query_tiles<KV, D>(P, qs, b, g, first / 16, tiles);
-    merge_rows(P, bg, L, first, min(16 * tiles, P.rows - first), row_mx, row_inv);
-    for (int i = P.rows - first + threadIdx.x; i < 16 * tiles; i += 32 * NW) row_mx[i] = row_inv[i] = 0.f;
+    if (first == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    merge_rows(P, bg, L, first, min(16 * tiles, P.rows - first), row_off);
+    for (int i = P.rows - first + threadIdx.x; i < 16 * tiles; i += 32 * NW) row_off[i] = INFINITY;
     __syncthreads();
-    for (int t = t0 + 16 * warp; t < t1; t += 16 * NW) {
-      uint32_t b0[D / 8], b1[D / 8];
-      keys.next[0].fragments(b0, P.bases);
-      keys.next[1].fragments(b1, P.bases);
-      const bool ok = keys.next_ok;
-      keys.request(P, b, g, t + 16 * NW, t1);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};  // tokens 2c, 2c + 1, 8 + 2c, 9 + 2c over the lane's rows
+    for (int n = 0; keys.token(n) < t1; ++n) {
+      const int t = keys.token(n);
+      uint32_t kb[TILES][D / 8];
+      int block[TILES / 2];
+      bool whole = t + 8 * TILES <= all_see;
+#pragma unroll
+      for (int nt = 0; nt < TILES; ++nt) keys.next[nt].fragments(kb[nt], P.bases);
+#pragma unroll
+      for (int h = 0; h < TILES / 2; ++h) {
+        block[h] = keys.block[h];
+        whole &= block[h] >= 0;
+      }
+      keys.request(P, b, g, n + 1);
+      float sum[TILES][2];  // tokens 8 nt + 2c + e over the lane's rows
+#pragma unroll
+      for (int nt = 0; nt < TILES; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
       for (int k = 0; k < tiles; ++k) {
-        int lim[2];
-        float mu[2], iz[2];
+        const float off[2] = {row_off[16 * k + r], row_off[16 * k + 8 + r]};
+        float sc[TILES][4];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int i = 16 * k + r + 8 * hf;
-          lim[hf] = ok && first + i < P.rows ? min(L - P.q_len + (first + i) / G + 1, t1) - t : 0;
-          mu[hf] = row_mx[i];
-          iz[hf] = row_inv[i];
+        for (int s = 0; s < KS; ++s) {
+          const uint4 w = qs[(k * KS + s) * 32 + lane];
+#pragma unroll
+          for (int nt = 0; nt < TILES; ++nt)
+            mma_16816_from(sc[nt], s == 0, w.x, w.y, w.z, w.w, kb[nt][2 * s], kb[nt][2 * s + 1]);
         }
-        float sc[2][4];
-        tile_scores<D>(qs + k * (D / 16) * 32, b0, b1, P.scale_log2, lim, sc);
+        if (!whole) {
+          int lim[2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+          for (int hf = 0; hf < 2; ++hf) {
+            const int row = first + 16 * k + r + 8 * hf;
+            lim[hf] = (row < P.rows ? min(L - P.q_len + row / G + 1, t1) : 0) - t;
+          }
+          mask_scores<TILES>(sc, lim, block);
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sum[2 * nt + e % 2] = fmaf(ex2_approx(sc[nt][e] - mu[e / 2]), iz[e / 2], sum[2 * nt + e % 2]);
+        for (int nt = 0; nt < TILES; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[nt][e % 2] += ex2_approx(fmaf(sc[nt][e], P.scale_log2, -off[e / 2]));
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int nt = 0; nt < TILES; ++nt)
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], k);
-      if (r < 4 && ok) {  // row group r writes the lane's token r
-        const float w = r == 0 ? sum[0] : (r == 1 ? sum[1] : (r == 2 ? sum[2] : sum[3]));
-        const int tok = t + 2 * c + (r & 1) + 8 * (r >> 1);
-        if (tok < t1) {
-          const int pb = P.block_tables[(size_t)b * P.max_blocks_per_seq + tok / P.block_size];
-          float* o = P.weights + ((size_t)pb * P.num_kv_heads + g) * P.block_size + tok % P.block_size;
-          if (first > 0)
-            *o += w;
-          else
-            *o = tok < start && P.decay != 0.f ? fmaf(P.decay, *o, w) : w;
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], k);
+      // lane (r, c) writes token 8 (r / 2) + 2c + r % 2
+      float w = 0.f;
+      int pb = -1;
+#pragma unroll
+      for (int x = 0; x < 2 * TILES; ++x)
+        if (r == x) {
+          w = sum[x / 2][x % 2];
+          pb = block[x / 4];
         }
+      const int tok = t + 8 * (r / 2) + 2 * c + r % 2;
+      if (pb >= 0 && tok < t1) {
+        float* o = P.weights + ((size_t)pb * P.num_kv_heads + g) * P.block_size + tok % P.block_size;
+        if (first > 0)
+          *o += w;
+        else
+          *o = tok < start && P.decay != 0.f ? fmaf(P.decay, *o, w) : w;
       }
     }
   }
@@ -386,18 +647,19 @@ __global__ void __launch_bounds__(32 * kWeightsWarps) paged_weights_keys_kernel(
 // ---------------------------------------------------------------------------
 // Choice of tokens: CTA (b, g).  Weights as ordered 32-bit keys (equal values
 // equal keys, larger ones larger, not a number the largest, no block the
-// smallest); the need-th largest key of the candidates by four passes of 256
-// bins; then every warp writes the chosen tokens of its own stretch, ascending.
+// smallest), kept in shared memory; the need-th largest key of the candidates by
+// four passes of 256 bins; then every warp writes the chosen tokens of its own
+// stretch, ascending.  A thread takes four neighbouring tokens at a time, eight
+// such loads in flight.
 struct TokenSelectParams {
   const float* weights;
   const int32_t *block_tables, *context_lens;
   int32_t *kept, *kept_lens;
   int num_seqs, num_kv_heads, block_size, num_blocks, max_blocks_per_seq, max_kept, sink, recent;
-  int cached;  // keys held in shared memory
+  int cached;  // keys held in shared memory, a multiple of 4
+  int block_shift;  // log2(block_size) where that is a power of two from 4 on and quads of weights are aligned, else -1
   int* error_word;
 };
-
-constexpr int kTokenSelectThreads = 512;
 
 __device__ __forceinline__ uint32_t ordered_key(float x) {
   if (x != x) return 0xFFFFFFFFu;
@@ -406,7 +668,7 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Copy of kept rows: CTA (64 new rows, b, g).  Threads look up where the rows
+// Copy of kept rows: CTA (a few dozen new rows, b, g).  Threads look up where the rows
 // come from and go to, then all copy 16-byte pieces, K's and V's, eight in flight.
 struct CompactParams {
   uint8_t *k_cache, *v_cache;
@@ -416,16 +678,22 @@ struct CompactParams {
   int* error_word;
 };
 
-constexpr int kCompactRows = 64, kCompactThreads = 256;
+constexpr int kCompactThreads = 256;
+// New rows of a CTA: eight 16-byte pieces a thread.
+__host__ __device__ constexpr int compact_rows(int KV, int D) {
+  return KV == kKvFp16 ? 8192 / D : (KV == kKvE4m3 ? 16384 / D : 24576 / D);
+}
 
 template <int KV, int D>
 __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const CompactParams P) {
   // pieces of a row in one cache: 16 bytes each; 4-bit rows: D / 32 of codes, and the scales
   constexpr int PIECES = KV == kKvFp16 ? D / 8 : (KV == kKvE4m3 ? D / 16 : D / 32 + 1);
-  __shared__ int src_block[kCompactRows], src_row[kCompactRows], dst_block[kCompactRows];
+  constexpr int ROWS = compact_rows(KV, D);
+  static_assert(ROWS <= kCompactThreads || KV == kKvInt4, "a thread looks up a row");
+  __shared__ int src_block[ROWS], src_row[ROWS], dst_block[ROWS];
   const int chunk = blockIdx.x % P.chunks, bg = blockIdx.x / P.chunks;
   const int g = bg % P.num_kv_heads, b = bg / P.num_kv_heads;
-  const int i0 = chunk * kCompactRows;
+  const int i0 = chunk * ROWS;
   const int room = min(P.max_kept, (int)min((long long)P.max_new_blocks * P.block_size, 0x7fffffffLL));
   const int n = min(P.kept_lens[b], room) - i0;
   if (n <= 0) {
@@ -433,9 +701,9 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
     return;
   }
   if (chunk == 0 && g == 0 && threadIdx.x == 0 && P.kept_lens[b] > room) record_error(P.error_word, kErrBadBlock);
-  const int BS = P.block_size, rows = min(n, kCompactRows);
-  if (threadIdx.x < rows) {
-    const int i = i0 + threadIdx.x;
+  const int BS = P.block_size, rows = min(n, ROWS);
+  for (int x = threadIdx.x; x < rows; x += kCompactThreads) {
+    const int i = i0 + x;
     const int t = P.kept[(size_t)bg * P.max_kept + i];
     const int to = P.new_tables[(size_t)b * P.max_new_blocks + i / BS];
     int from = -1;
@@ -445,9 +713,9 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
       record_error(P.error_word, kErrBadBlock);
       from = -1;
     }
-    src_block[threadIdx.x] = from;
-    src_row[threadIdx.x] = t % BS;
-    dst_block[threadIdx.x] = to;
+    src_block[x] = from;
+    src_row[x] = t % BS;
+    dst_block[x] = to;
     if (from >= 0 && P.weights)
       P.weights[((size_t)to * P.num_kv_heads + g) * BS + i % BS] =
           P.weights[((size_t)from * P.num_kv_heads + g) * BS + t % BS];

@@ -610,25 +610,40 @@ __global__ void __launch_bounds__(32 * kInt4ReadWarps) paged_kv_read_int4_kernel
   }
   const int row = (int)(at - lb * BS);
   const size_t tile0 = (size_t)block * P.num_kv_heads * TILE;
-  for (int i = lane; i < 2 * P.num_kv_heads * GROUPS; i += 32) {
-    const int d16 = i % GROUPS, hv = i / GROUPS;
-    const bool is_v = hv >= P.num_kv_heads;
-    const int g = is_v ? hv - P.num_kv_heads : hv;
-    const uint8_t* tile = (is_v ? P.v_cache : P.k_cache) + tile0 + (size_t)g * TILE;
-    const uint2 x = *reinterpret_cast<const uint2*>(tile + ((d16 / 2) * BS + row) * 16 + (d16 % 2) * 8);
-    const uint32_t sb = tile[BS * D / 2 + row * GROUPS + d16] & 0x7Fu;
-    const float step = __half2float(__ushort_as_half((unsigned short)(sb << 7))) * kInt4Unscale *
-                       (is_v ? P.v_scale : P.k_scale);
-    uint32_t w[8];
+  constexpr int U = 4;  // groups in flight a lane
+  const int items = 2 * P.num_kv_heads * GROUPS;
+  for (int i0 = lane; i0 < items; i0 += 32 * U) {
+    uint2 x[U];
+    uint32_t sb[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t by = ((k < 4 ? x.x : x.y) >> (8 * (k % 4))) & 0xFFu;
-      w[k] = pack_half2((float)((int)(by & 15u) - 8) * step, (float)((int)(by >> 4) - 8) * step);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 32 * u;
+      if (i >= items) break;
+      const int d16 = i % GROUPS, hv = i / GROUPS;
+      const bool is_v = hv >= P.num_kv_heads;
+      const uint8_t* tile = (is_v ? P.v_cache : P.k_cache) + tile0 + (size_t)(hv - (is_v ? P.num_kv_heads : 0)) * TILE;
+      x[u] = *reinterpret_cast<const uint2*>(tile + ((d16 / 2) * BS + row) * 16 + (d16 % 2) * 8);
+      sb[u] = tile[BS * D / 2 + row * GROUPS + d16];
     }
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? P.v_out + t * P.v_stride : P.k_out + t * P.k_stride) +
-                                          (size_t)g * D + 16 * d16);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 32 * u;
+      if (i >= items) break;
+      const int d16 = i % GROUPS, hv = i / GROUPS;
+      const bool is_v = hv >= P.num_kv_heads;
+      const float step = __half2float(__ushort_as_half((unsigned short)((sb[u] & 0x7Fu) << 7))) * kInt4Unscale *
+                         (is_v ? P.v_scale : P.k_scale);
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t by = ((k < 4 ? x[u].x : x[u].y) >> (8 * (k % 4))) & 0xFFu;
+        w[k] = pack_half2((float)((int)(by & 15u) - 8) * step, (float)((int)(by >> 4) - 8) * step);
+      }
+      uint4* dst = reinterpret_cast<uint4*>((is_v ? P.v_out + t * P.v_stride : P.k_out + t * P.k_stride) +
+                                            (size_t)(hv - (is_v ? P.num_kv_heads : 0)) * D + 16 * d16);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
 }
 

@@ -16,6 +16,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 pkd_status launched() { return cudaGetLastError() == cudaSuccess ? PKD_OK : PKD_ERR_LAUNCH; }
 
+constexpr int kRopeRunTokens = 16;     // tokens an SM from which the append takes runs of them
 constexpr int kMaxRopeHeadDim = 512;  // 16 dims a thread, at least four heads in flight
 
 pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long long q_stride, long long k_stride,
@@ -89,14 +90,22 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   p.v_scale = v_scale;
   p.error_word = error_word;
   axes = axes && rotary_dim > 0;
-#define PKD_APPEND(KVB_)                                                                              \
-  (interleaved ? (axes ? pkd::paged_kv_append_rope_kernel<KVB_, true, true>                           \
-                       : pkd::paged_kv_append_rope_kernel<KVB_, true, false>)                         \
-               : (axes ? pkd::paged_kv_append_rope_kernel<KVB_, false, true>                          \
-                       : pkd::paged_kv_append_rope_kernel<KVB_, false, false>))
-  auto* fn = kv == PKD_KV_INT4 ? PKD_APPEND(0) : (kv == PKD_KV_E4M3 ? PKD_APPEND(1) : PKD_APPEND(2));
+  // runs of tokens where there are enough for four such CTAs an SM
+  int sms = 0, dev = 0;
+  if (pkd::failed(cudaGetDevice(&dev)) ||
+      pkd::failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
+    sms = 148;
+  const bool run = num_tokens >= kRopeRunTokens * sms;
+#define PKD_APPEND(FN_, KVB_)                                                      \
+  (interleaved ? (axes ? pkd::FN_<KVB_, true, true> : pkd::FN_<KVB_, true, false>) \
+               : (axes ? pkd::FN_<KVB_, false, true> : pkd::FN_<KVB_, false, false>))
+#define PKD_APPEND_KV(FN_) \
+  (kv == PKD_KV_INT4 ? PKD_APPEND(FN_, 0) : (kv == PKD_KV_E4M3 ? PKD_APPEND(FN_, 1) : PKD_APPEND(FN_, 2)))
+  auto* fn = run ? PKD_APPEND_KV(paged_kv_append_rope_run_kernel) : PKD_APPEND_KV(paged_kv_append_rope_kernel);
+#undef PKD_APPEND_KV
 #undef PKD_APPEND
-  fn<<<(unsigned)num_tokens, pkd::kRopeThreads, 0, stream>>>(p);
+  const unsigned grid = run ? ((unsigned)num_tokens + pkd::kRopeRun - 1) / pkd::kRopeRun : (unsigned)num_tokens;
+  fn<<<grid, pkd::kRopeThreads, 0, stream>>>(p);
   return launched();
 }
 

@@ -29,8 +29,9 @@ constexpr uint32_t kErrBadPosition = 8u;  // a rotation position outside the tab
 // at D = 128, keep more tokens in different phases on an SM than 256: prompts
 // of 28842 tokens, 40 q and 8 kv heads, 133 against 155 us, 6.2 TB/s.
 //
-// AXES: pair i goes by the position on axis pair_axes[i], so a thread's eight
-// cosines come from up to eight rows of the table.
+// AXES: pair i goes by the position on axis pair_axes[i], so the token's cosines
+// come from several rows of the table: looked up once a token, a thread a pair,
+// and shared.
 //
 // KVB 0 (4-bit caches): a group of 16 dims is a thread's two chunks, or, where
 // they are R/2 apart, one chunk of each of two neighbouring lanes, which
@@ -52,13 +53,30 @@ struct RopeAppendParams {
   int* error_word;
 };
 
-// Eight fp32 values as codes 8 + clamp(rint(x / step), -7, 7), value k in bits 4k ..
-__device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float step) {
+// Eight fp32 values as codes 8 + clamp(rint(x / step), -7, 7), value k in bits 4k
+// ..  Adding 1.5 2^23 + 8 in one fused multiply-add rounds x / step to an integer
+// and leaves the code in the low bits.  The quotient by a reciprocal is within
+// 2^-20 of the exact one where it is below 8 and the IEEE quotient within 2^-21,
+// so they round alike unless the first is nearer than 2e-5 to halfway: then, and
+// where it is not a number, IEEE division decides (one value in 25000).  Only
+// scales that are subnormal or saturated (`edge`) let quotients pass 7.5.
+__device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float step, bool edge) {
+  if (!(step > 0.f)) return 0x88888888u;
+  constexpr float kMagic = 12582912.f + 8.f;
+  const float inv = __frcp_rn(step);
   uint32_t w = 0;
+  float off = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float q = step > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[k], step)), -7.f), 7.f) : 0.f;
-    w |= (uint32_t)((int)q + 8) << (4 * k);
+    const float r = fmaf(x[k], inv, kMagic);
+    off = fmaxf(off, fabsf(fmaf(x[k], inv, kMagic - r)));
+    w |= (__float_as_uint(r) & 15u) << (4 * k);
+  }
+  if (edge || !(off <= 0.49998f)) {
+    w = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      w |= (uint32_t)((int)fminf(fmaxf(rintf(__fdiv_rn(x[k], step)), -7.f), 7.f) + 8) << (4 * k);
   }
   return w;
 }
@@ -77,11 +95,38 @@ __device__ __forceinline__ uint32_t int4_scale_byte(float a, float scale, float&
   return byte;
 }
 
+// Four fp32 values over `scale` as E4M3 codes.
 __device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d, float scale) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fdiv_rn(b, scale)), "f"(__fdiv_rn(a, scale)));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fdiv_rn(d, scale)), "f"(__fdiv_rn(c, scale)));
   return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+__device__ __forceinline__ uint32_t cvt4_e4m3(float a, float b, float c, float d, float by) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * by), "f"(a * by));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * by), "f"(c * by));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+// The same for eight of them, by reciprocals where that cannot differ: `under` and
+// `over` are 1 / scale less and more 2^-21 of it, so the IEEE quotient lies
+// between the two products (each off by 2^-24 at most), and the conversion is
+// monotone; where both give the same codes, so does the quotient.  (under = 0:
+// a scale whose reciprocal is not far inside fp32's range.)
+struct E4m3Scale {
+  float scale, under, over;
+};
+__device__ __forceinline__ E4m3Scale e4m3_scale(float scale) {
+  const float inv = scale > 1e-30f && scale < 1e30f ? __frcp_rn(scale) : 0.f;
+  return {scale, inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f)};
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], const E4m3Scale& s) {
+  if (s.under > 0.f) {
+    const uint2 a = make_uint2(cvt4_e4m3(x[0], x[1], x[2], x[3], s.under), cvt4_e4m3(x[4], x[5], x[6], x[7], s.under));
+    const uint2 b = make_uint2(cvt4_e4m3(x[0], x[1], x[2], x[3], s.over), cvt4_e4m3(x[4], x[5], x[6], x[7], s.over));
+    if (a.x == b.x && a.y == b.y) return a;
+  }
+  return make_uint2(pack4_e4m3(x[0], x[1], x[2], x[3], s.scale), pack4_e4m3(x[4], x[5], x[6], x[7], s.scale));
 }
 
 __device__ __forceinline__ void unpack8(const uint4 u, float (&x)[8]) {
@@ -98,30 +143,147 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 constexpr int kRopeThreads = 128;
-template <int KVB, bool PAIRS, bool AXES>
-__global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(const RopeAppendParams P) {
+constexpr int kRopeCtas = 8;  // an SM
+constexpr int kMaxRopePairs = 256;  // of the largest head_dim
+// A thread's place: which 16 dims (two chunks that rotate together, from e0 and e1 on) of which head slot.
+struct RopeLane {
+  int c, slot, slots, e0, e1;
+  bool rot;
+};
+template <bool PAIRS>
+__device__ __forceinline__ RopeLane rope_lane(const RopeAppendParams& P) {
+  const int units = P.head_dim / 16;
+  RopeLane l;
+  l.slots = kRopeThreads / units;  // heads in flight
+  l.c = threadIdx.x % units;
+  l.slot = threadIdx.x / units;
+  l.rot = l.c < P.rotary_dim / 16;
+  l.e0 = l.rot && !PAIRS ? 8 * l.c : 16 * l.c;
+  l.e1 = l.rot && !PAIRS ? P.rotary_dim / 2 + 8 * l.c : 16 * l.c + 8;
+  return l;
+}
+// Head h of token t: q heads, then k heads, then v heads.
+__device__ __forceinline__ const __half* rope_source(const RopeAppendParams& P, int t, int h) {
+  if (h < P.num_q_heads) return P.q + t * P.q_stride + (long long)h * P.head_dim;
+  h -= P.num_q_heads;
+  if (h < P.num_kv_heads) return P.k + t * P.k_stride + (long long)h * P.head_dim;
+  return P.v + t * P.v_stride + (long long)(h - P.num_kv_heads) * P.head_dim;
+}
+// The thread's 16 dims (u0, u1) of head h: turned, and stored into q_out or into row `in` of the block's tiles.
+template <int KVB, bool PAIRS>
+__device__ __forceinline__ void rope_head(const RopeAppendParams& P, const RopeLane& lane, const float (&cs)[8],
+                                          const float (&sn)[8], const uint4 u0, const uint4 u1, int h, int t,
+                                          size_t tile0, int in, const E4m3Scale& sk8, const E4m3Scale& sv8) {
   constexpr bool F8 = KVB == 1, I4 = KVB == 0;
-  const int D = P.head_dim, R = P.rotary_dim, units = D / 16;
-  const int slots = kRopeThreads / units;  // heads in flight
-  const int c = threadIdx.x % units, slot = threadIdx.x / units;
+  const int D = P.head_dim, units = D / 16, c = lane.c, e0 = lane.e0, e1 = lane.e1;
+  const bool rot = lane.rot;
+      const bool is_q = h < P.num_q_heads, is_v = h >= P.num_q_heads + P.num_kv_heads;
+      const bool turn = rot && !is_v;
+      float x[8], y[8];
+      if (turn || (KVB != 2 && !is_q)) {
+        unpack8(u0, x);
+        unpack8(u1, y);
+      }
+      if (turn) {
+        // y_a = a cos - d sin, y_b = d cos + a sin
+        auto turned = [](float& a, float& d, float co, float si) {
+          const float a0 = a, d0 = d;
+          if constexpr (I4) {
+            a = __fsub_rn(__fmul_rn(a0, co), __fmul_rn(d0, si));
+            d = __fadd_rn(__fmul_rn(d0, co), __fmul_rn(a0, si));
+          } else {
+            a = fmaf(a0, co, -d0 * si);
+            d = fmaf(d0, co, a0 * si);
+          }
+        };
+        if constexpr (PAIRS) {
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            turned(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+            turned(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
+          }
+        } else {
+  #pragma unroll
+          for (int i = 0; i < 8; ++i) turned(x[i], y[i], cs[i], sn[i]);
+        }
+      }
+      if (is_q) {
+        __half* o = P.q_out + t * P.q_out_stride + (long long)h * D;
+        *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
+        *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+      } else {
+        const int g = h - P.num_q_heads - (is_v ? P.num_kv_heads : 0);
+        const size_t row = ((tile0 + g) * P.block_size + in) * D;
+        if constexpr (I4) {
+          const float sc = is_v ? P.v_scale : P.k_scale;
+          const int BS = P.block_size;
+          uint8_t* tile = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) +
+                          (tile0 + g) * ((size_t)BS * D * 9 / 16);
+          uint8_t* scales = tile + (size_t)BS * D / 2 + in * units;
+          auto codes = [&](int e) { return reinterpret_cast<uint32_t*>(tile + ((e / 32) * BS + in) * 16 + e % 32 / 2); };
+          float ax = absmax8(x), ay = absmax8(y), sx, sy;
+          uint32_t bx, by;
+          if (rot && !PAIRS) {
+            // the other halves of both groups are the neighbouring lane's
+            const unsigned both = 3u << (threadIdx.x & 30);
+            ax = fmaxf(ax, __shfl_xor_sync(both, ax, 1));
+            ay = fmaxf(ay, __shfl_xor_sync(both, ay, 1));
+            bx = int4_scale_byte(ax, sc, sx);
+            by = int4_scale_byte(ay, sc, sy);
+            if (c % 2 == 0) {
+              scales[e0 / 16] = (uint8_t)bx;
+              scales[e1 / 16] = (uint8_t)by;
+            }
+          } else {
+            bx = by = int4_scale_byte(fmaxf(ax, ay), sc, sx);
+            sy = sx;
+            scales[e0 / 16] = (uint8_t)bx;
+          }
+          *codes(e0) = pack8_int4(x, sx, bx < 8 || bx == 0x7E);
+          *codes(e1) = pack8_int4(y, sy, by < 8 || by == 0x7E);
+        } else if constexpr (F8) {
+          uint8_t* o = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + row;
+          *reinterpret_cast<uint2*>(o + e0) = pack8_e4m3(x, is_v ? sv8 : sk8);
+          *reinterpret_cast<uint2*>(o + e1) = pack8_e4m3(y, is_v ? sv8 : sk8);
+        } else {
+          __half* o = static_cast<__half*>(is_v ? P.v_cache : P.k_cache) + row;
+          *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
+          *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+        }
+      }
+}
+
+template <int KVB, bool PAIRS, bool AXES>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_kernel(const RopeAppendParams P) {
+  const RopeLane lane = rope_lane<PAIRS>(P);
+  const int R = P.rotary_dim, c = lane.c, slots = lane.slots, e0 = lane.e0, e1 = lane.e1;
+  const bool rot = lane.rot;
   const int heads = P.num_q_heads + 2 * P.num_kv_heads;
   const int t = blockIdx.x;
-  const bool rot = c < R / 16;
-  const int e0 = rot && !PAIRS ? 8 * c : 16 * c;
-  const int e1 = rot && !PAIRS ? R / 2 + 8 * c : 16 * c + 8;
-  auto source = [&](int h) -> const __half* {
-    if (h < P.num_q_heads) return P.q + t * P.q_stride + (long long)h * D;
-    h -= P.num_q_heads;
-    if (h < P.num_kv_heads) return P.k + t * P.k_stride + (long long)h * D;
-    return P.v + t * P.v_stride + (long long)(h - P.num_kv_heads) * D;
-  };
-  int h = slot;
-  const bool mine = slot < slots;
+  auto source = [&](int h) { return rope_source(P, t, h); };
+  int h = lane.slot;
+  const bool mine = lane.slot < slots;
   uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
   if (mine && h < heads) {
     const __half* s = source(h);
     u0 = *reinterpret_cast<const uint4*>(s + e0);
     u1 = *reinterpret_cast<const uint4*>(s + e1);
+  }
+  // AXES: a thread a pair looks up the pair's axis, the position there and the
+  // table's entries, once for all heads
+  __shared__ __align__(16) float turn_cos[AXES ? kMaxRopePairs : 4], turn_sin[AXES ? kMaxRopePairs : 4];
+  bool off = false;
+  if constexpr (AXES) {
+    for (int i = threadIdx.x; i < R / 2; i += kRopeThreads) {
+      const int axis = P.pair_axes[i];
+      const int p = axis >= 0 && axis < P.num_axes ? P.positions[(size_t)axis * P.num_tokens + t] : -1;
+      if (p >= 0 && p < P.max_positions) {
+        turn_cos[i] = P.table[(long long)p * R + i];
+        turn_sin[i] = P.table[(long long)p * R + R / 2 + i];
+      } else {
+        off = true;
+      }
+    }
   }
   // the token's sequence b and its place j in it
   int b, j;
@@ -136,8 +298,9 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
     j = t - b * per;
   }
   const int L = P.context_lens[b];
-  const long long at = (long long)L + j;  // logical position
-  const long long lb = at / P.block_size;
+  // logical position and its block (of a length that is not negative: below 2^32)
+  const long long at = (long long)L + j;
+  const long long lb = (uint32_t)at / (uint32_t)P.block_size;
   const long long pos = P.positions && !AXES ? P.positions[t] : at;
   int block = -1;
   if (L >= 0 && lb < P.max_blocks_per_seq) block = P.block_tables[(size_t)b * P.max_blocks_per_seq + lb];
@@ -145,27 +308,6 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
   if (block < 0 || block >= P.num_blocks) err |= kErrBadBlock;
   float cs[8], sn[8];
   if constexpr (AXES) {
-    // the thread's eight pairs: their axes, the positions there, the table's entries
-    bool off = false;
-    if (rot) {
-      const int4 a0 = reinterpret_cast<const int4*>(P.pair_axes)[2 * c];
-      const int4 a1 = reinterpret_cast<const int4*>(P.pair_axes)[2 * c + 1];
-      const int axis[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-      int row[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool known = axis[i] >= 0 && axis[i] < P.num_axes;
-        row[i] = known ? P.positions[(size_t)axis[i] * P.num_tokens + t] : -1;
-        off |= row[i] < 0 || row[i] >= P.max_positions;
-        if (row[i] < 0 || row[i] >= P.max_positions) row[i] = 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float* at_row = P.table + (long long)row[i] * R + 8 * c + i;
-        cs[i] = at_row[0];
-        sn[i] = at_row[R / 2];
-      }
-    }
     if (__syncthreads_or(off)) err |= kErrBadPosition;
   } else {
     if (R > 0 && (pos < 0 || pos >= P.max_positions)) err |= kErrBadPosition;
@@ -174,6 +316,15 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
     if (threadIdx.x == 0) record_error(P.error_word, err);
     return;
   }
+  if (AXES && rot) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 a = reinterpret_cast<const float4*>(turn_cos)[2 * c + i];
+      const float4 d = reinterpret_cast<const float4*>(turn_sin)[2 * c + i];
+      cs[4 * i] = a.x; cs[4 * i + 1] = a.y; cs[4 * i + 2] = a.z; cs[4 * i + 3] = a.w;
+      sn[4 * i] = d.x; sn[4 * i + 1] = d.y; sn[4 * i + 2] = d.z; sn[4 * i + 3] = d.w;
+    }
+  }
   if (!AXES && rot) {
     const float4* row = reinterpret_cast<const float4*>(P.table + pos * R + 8 * c);
     const float4* row2 = reinterpret_cast<const float4*>(P.table + pos * R + R / 2 + 8 * c);
@@ -181,8 +332,10 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
     cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w; cs[4] = a2.x; cs[5] = a2.y; cs[6] = a2.z; cs[7] = a2.w;
     sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w; sn[4] = s2.x; sn[5] = s2.y; sn[6] = s2.z; sn[7] = s2.w;
   }
-  const size_t row0 = ((size_t)block * P.num_kv_heads) * P.block_size + (size_t)(at - lb * P.block_size);
+  const size_t tile0 = (size_t)block * P.num_kv_heads;
+  const int in = (int)(at - lb * P.block_size);
   if (!mine) return;
+  const E4m3Scale sk8 = e4m3_scale(P.k_scale), sv8 = e4m3_scale(P.v_scale);
   for (; h < heads;) {
     const int hn = h + slots;
     uint4 n0 = u0, n1 = u1;
@@ -191,80 +344,127 @@ __global__ void __launch_bounds__(kRopeThreads) paged_kv_append_rope_kernel(cons
       n0 = *reinterpret_cast<const uint4*>(s + e0);
       n1 = *reinterpret_cast<const uint4*>(s + e1);
     }
-    const bool is_q = h < P.num_q_heads, is_v = h >= P.num_q_heads + P.num_kv_heads;
-    const bool turn = rot && !is_v;
-    float x[8], y[8];
-    if (turn || (KVB != 2 && !is_q)) {
-      unpack8(u0, x);
-      unpack8(u1, y);
+    rope_head<KVB, PAIRS>(P, lane, cs, sn, u0, u1, h, t, tile0, in, sk8, sv8);
+    h = hn;
+    u0 = n0;
+    u1 = n1;
+  }
+}
+
+// The same for many tokens, kRopeRun of them a CTA: their sequences, positions,
+// blocks and cosines are looked up side by side first and kept in shared memory,
+// so that those chains of dependent loads are paid once a run, not once a token;
+// then the CTA walks the heads of all of them, the next head's data requested
+// ahead.
+constexpr int kRopeRun = 4;
+template <int KVB, bool PAIRS, bool AXES>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_run_kernel(const RopeAppendParams P) {
+  static_assert(kRopeRun <= kRopeThreads / 32, "a warp looks up a token");
+  __shared__ __align__(16) float turn[kRopeRun][2 * kMaxRopePairs];  // cosines, then sines
+  __shared__ int block_of[kRopeRun], row_of[kRopeRun], pos_of[kRopeRun];
+  const RopeLane lane = rope_lane<PAIRS>(P);
+  const int R = P.rotary_dim, heads = P.num_q_heads + 2 * P.num_kv_heads;
+  const int first = blockIdx.x * kRopeRun, n = min(kRopeRun, P.num_tokens - first);
+  int k = 0, h = lane.slot;  // token of the run, head
+  const bool mine = lane.slot < lane.slots;
+  auto settle = [&](int& k, int& h) {
+    while (h >= heads && k < n) {
+      h -= heads;
+      ++k;
     }
-    if (turn) {
-      // y_a = a cos - d sin, y_b = d cos + a sin
-      auto turned = [](float& a, float& d, float co, float si) {
-        const float a0 = a, d0 = d;
-        if constexpr (I4) {
-          a = __fsub_rn(__fmul_rn(a0, co), __fmul_rn(d0, si));
-          d = __fadd_rn(__fmul_rn(d0, co), __fmul_rn(a0, si));
-        } else {
-          a = fmaf(a0, co, -d0 * si);
-          d = fmaf(d0, co, a0 * si);
-        }
-      };
-      if constexpr (PAIRS) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          turned(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
-          turned(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turned(x[i], y[i], cs[i], sn[i]);
-      }
-    }
-    if (is_q) {
-      __half* o = P.q_out + t * P.q_out_stride + (long long)h * D;
-      *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
-      *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+  };
+  settle(k, h);
+  uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
+  if (mine && k < n) {
+    const __half* s = rope_source(P, first + k, h);
+    u0 = *reinterpret_cast<const uint4*>(s + lane.e0);
+    u1 = *reinterpret_cast<const uint4*>(s + lane.e1);
+  }
+  const int w = threadIdx.x / 32;
+  if (w < n) {
+    const int t = first + w;
+    int b, j = -1, block = -1, row = 0, pos = -1;
+    if (P.token_starts) {
+      b = find_segment(P.token_starts, P.num_seqs, t);
+      if (b < P.num_seqs) j = t - P.token_starts[b];
     } else {
-      const int g = h - P.num_q_heads - (is_v ? P.num_kv_heads : 0);
-      const size_t row = (row0 + (size_t)g * P.block_size) * D;
-      if constexpr (I4) {
-        const float sc = is_v ? P.v_scale : P.k_scale;
-        const int BS = P.block_size, in = (int)(at - lb * BS);
-        uint8_t* tile = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) +
-                        ((size_t)block * P.num_kv_heads + g) * ((size_t)BS * D * 9 / 16);
-        uint8_t* scales = tile + (size_t)BS * D / 2 + in * units;
-        auto codes = [&](int e) { return reinterpret_cast<uint32_t*>(tile + ((e / 32) * BS + in) * 16 + e % 32 / 2); };
-        float ax = absmax8(x), ay = absmax8(y), sx, sy;
-        if (rot && !PAIRS) {
-          // the other halves of both groups are the neighbouring lane's
-          const unsigned both = 3u << (threadIdx.x & 30);
-          ax = fmaxf(ax, __shfl_xor_sync(both, ax, 1));
-          ay = fmaxf(ay, __shfl_xor_sync(both, ay, 1));
-          const uint32_t bx = int4_scale_byte(ax, sc, sx), by = int4_scale_byte(ay, sc, sy);
-          if (c % 2 == 0) {
-            scales[e0 / 16] = (uint8_t)bx;
-            scales[e1 / 16] = (uint8_t)by;
-          }
-        } else {
-          scales[e0 / 16] = (uint8_t)int4_scale_byte(fmaxf(ax, ay), sc, sx);
-          sy = sx;
-        }
-        *codes(e0) = pack8_int4(x, sx);
-        *codes(e1) = pack8_int4(y, sy);
-      } else if constexpr (F8) {
-        const float sc = is_v ? P.v_scale : P.k_scale;
-        uint8_t* o = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + row;
-        *reinterpret_cast<uint2*>(o + e0) =
-            make_uint2(pack4_e4m3(x[0], x[1], x[2], x[3], sc), pack4_e4m3(x[4], x[5], x[6], x[7], sc));
-        *reinterpret_cast<uint2*>(o + e1) =
-            make_uint2(pack4_e4m3(y[0], y[1], y[2], y[3], sc), pack4_e4m3(y[4], y[5], y[6], y[7], sc));
-      } else {
-        __half* o = static_cast<__half*>(is_v ? P.v_cache : P.k_cache) + row;
-        *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
-        *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+      const int per = P.num_tokens / P.num_seqs;
+      b = t / per;
+      j = t - b * per;
+    }
+    uint32_t err = 0;
+    if (j >= 0) {  // (past the last sequence: left as it is)
+      const int L = P.context_lens[b];
+      const long long at = (long long)L + j;  // of a length that is not negative: below 2^32
+      const long long lb = (uint32_t)at / (uint32_t)P.block_size;
+      if (L >= 0 && lb < P.max_blocks_per_seq) block = P.block_tables[(size_t)b * P.max_blocks_per_seq + lb];
+      row = (int)(at - lb * P.block_size);
+      if (block < 0 || block >= P.num_blocks) err |= kErrBadBlock;
+      if constexpr (!AXES) {
+        const long long p = P.positions ? P.positions[t] : at;
+        if (R > 0 && (p < 0 || p >= P.max_positions))
+          err |= kErrBadPosition;
+        else
+          pos = (int)p;
+      }
+      if (err) block = -1;
+    }
+    if (threadIdx.x % 32 == 0) {
+      if (err) record_error(P.error_word, err);
+      block_of[w] = block;
+      row_of[w] = row;
+      pos_of[w] = pos;
+    }
+  }
+  __syncthreads();
+  bool off = false;
+  for (int i = threadIdx.x; i < n * (R / 2); i += kRopeThreads) {
+    const int x = i / (R / 2), pair = i % (R / 2);
+    if (block_of[x] < 0) continue;
+    int p = pos_of[x];
+    if constexpr (AXES) {
+      const int axis = P.pair_axes[pair];
+      p = axis >= 0 && axis < P.num_axes ? P.positions[(size_t)axis * P.num_tokens + first + x] : -1;
+      if (p < 0 || p >= P.max_positions) {
+        row_of[x] = -1;  // (block_of may still be read by others)
+        off = true;
+        continue;
       }
     }
+    turn[x][pair] = P.table[(long long)p * R + pair];
+    turn[x][kMaxRopePairs + pair] = P.table[(long long)p * R + R / 2 + pair];
+  }
+  if (AXES && __syncthreads_or(off)) {
+    if (threadIdx.x == 0) record_error(P.error_word, kErrBadPosition);
+  }
+  if (!AXES) __syncthreads();
+  if (!mine) return;
+  const E4m3Scale sk8 = e4m3_scale(P.k_scale), sv8 = e4m3_scale(P.v_scale);
+  float cs[8], sn[8];
+  int turned_for = -1;
+  while (k < n) {
+    int kn = k, hn = h + lane.slots;
+    settle(kn, hn);
+    uint4 n0 = u0, n1 = u1;
+    if (kn < n) {
+      const __half* s = rope_source(P, first + kn, hn);
+      n0 = *reinterpret_cast<const uint4*>(s + lane.e0);
+      n1 = *reinterpret_cast<const uint4*>(s + lane.e1);
+    }
+    if (lane.rot && k != turned_for) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 a = reinterpret_cast<const float4*>(turn[k])[2 * lane.c + i];
+        const float4 d = reinterpret_cast<const float4*>(turn[k] + kMaxRopePairs)[2 * lane.c + i];
+        cs[4 * i] = a.x; cs[4 * i + 1] = a.y; cs[4 * i + 2] = a.z; cs[4 * i + 3] = a.w;
+        sn[4 * i] = d.x; sn[4 * i + 1] = d.y; sn[4 * i + 2] = d.z; sn[4 * i + 3] = d.w;
+      }
+      turned_for = k;
+    }
+    if (block_of[k] >= 0 && row_of[k] >= 0)
+      rope_head<KVB, PAIRS>(P, lane, cs, sn, u0, u1, h, first + k, (size_t)block_of[k] * P.num_kv_heads, row_of[k],
+                            sk8, sv8);
+    k = kn;
     h = hn;
     u0 = n0;
     u1 = n1;

@@ -117,3 +117,62 @@ def test_bad_positions_and_refusals():
         call(p=p.repeat(3, 1).contiguous())                       # nine axes
     with pytest.raises(ops.PagedDecodeError):
         call(ax=torch.cat((i32(0), ax))[1:])                      # not on a 16-byte boundary
+
+
+@pytest.mark.parametrize("kind", ["fp16", "e4m3", "int4"])
+@pytest.mark.parametrize("axes,pairs,Hq,H,D", [(0, False, 5, 2, 128), (3, True, 0, 3, 64), (3, False, 9, 1, 128)])
+def test_many_tokens_are_few_tokens_many_times(kind, axes, pairs, Hq, H, D):
+    """The kernel for many tokens (thousands) against the one for few, bit for bit: odd runs, bad blocks and
+    positions, rows behind the last run, in place."""
+    BS, T, behind = 16, 5003, 7
+    runs = [0, 1, 2000, 3, 2990, 9]
+    past = [5, 30, 0, 17, 1, 100]
+    assert sum(runs) == T
+    g = torch.Generator().manual_seed(axes + D)
+    x = torch.randn((T + behind, Hq + 2 * H, D), generator=g).half().to(DEV)
+    q = x[:, :Hq] if Hq else None
+    k, v = x[:, Hq:Hq + H], x[:, Hq + H:]
+    ang = torch.rand((60, D // 2), generator=g, dtype=torch.float64) * 6.28
+    table = torch.cat((ang.cos(), ang.sin()), 1).float().to(DEV)
+    pos = torch.randint(0, 60, (max(axes, 1), T + behind), generator=g, dtype=torch.int64).to(torch.int32)
+    pos[0, 17], pos[-1, 2500] = 60, -1
+    which = (torch.arange(D // 2) % max(axes, 1)).to(torch.int32).to(DEV)
+    bt, _ = deal_tables([a + b for a, b in zip(past, runs)], BS, 190, 400, 3)
+    bt[2, 7], bt[4, 11] = -1, 400
+    row = 9 * D // 16 if kind == "int4" else D
+    dtype = torch.float16 if kind == "fp16" else torch.uint8
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call(k, v, q, pos, starts, past, bt, kc, vc):
+        kw = dict(token_starts=i32(*starts), interleaved=pairs, q_out=q, error_word=err)
+        p = pos.contiguous().to(DEV)
+        scales = () if kind == "fp16" else (0.25, 0.3)
+        if kind == "int4":
+            ops.paged_kv_append_rope_int4(q, k, v, table, bt, past, kc, vc, *scales,
+                                          positions=p if axes else p[0], pair_axes=which if axes else None, **kw)
+        elif axes:
+            fn = ops.paged_kv_append_rope_axes if kind == "fp16" else ops.paged_kv_append_rope_axes_fp8
+            fn(q, k, v, table, which, p, bt, past, kc, vc, *scales, **kw)
+        else:
+            fn = ops.paged_kv_append_rope if kind == "fp16" else ops.paged_kv_append_rope_fp8
+            fn(q, k, v, table, bt, past, kc, vc, *scales, positions=p[0], **kw)
+        return ops.pkd_read_device_error(err)
+
+    a = [torch.full((400, H, BS, row), 3, dtype=dtype, device=DEV) for _ in range(2)]
+    b = [t.clone() for t in a]
+    starts = [0]
+    for n in runs:
+        starts.append(starts[-1] + n)
+    qa = x[:, :Hq].clone() if Hq else None
+    bits = call(k, v, qa, pos, starts, i32(*past), bt, *a)
+    assert bits == ops.DEVERR_BAD_BLOCK | ops.DEVERR_BAD_POSITION
+    qb = x[:, :Hq].clone() if Hq else None
+    seen = 0
+    for i, n in enumerate(runs):                   # the same, at most 1000 tokens a call
+        for j in range(0, n, 1000):
+            m = min(1000, n - j)
+            s = slice(starts[i] + j, starts[i] + j + m)
+            seen |= call(k[s], v[s], qb[s] if Hq else None, pos[:, s], [0, m], i32(past[i] + j), bt[i:i + 1], *b)
+    assert seen == bits
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert Hq == 0 or torch.equal(qa, qb)
