@@ -26,21 +26,30 @@ __global__ void __launch_bounds__(kWeightsFinishThreads) paged_weights_scores_ke
   const bool mine = pb >= 0 && pb < P.num_blocks;
   float* o = P.weights + ((size_t)(mine ? pb : 0) * P.num_kv_heads + g) * P.block_size + t % P.block_size;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the old weights and the first rows' scores along with the statistics
+  constexpr int U = 4;
+  const float* s = P.scores + (size_t)bg * P.rows * P.score_stride + t;
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f), x[U];
   if (mine && P.decay != 0.f) old = *reinterpret_cast<const float4*>(o);
-  merge_rows(P, bg, L, 0, P.rows, row_off);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (mine && u < P.rows) x[u] = *reinterpret_cast<const float4*>(s + (size_t)u * P.score_stride);
+  merge_rows(P, bg, L, 0, P.rows, row_off, kWeightsFinishThreads);
   __syncthreads();
   if (!mine) return;
   const float before[4] = {old.x, old.y, old.z, old.w};
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-  const float* s = P.scores + (size_t)bg * P.rows * P.score_stride + t;
-#pragma unroll 4
-  for (int i = 0; i < P.rows; ++i) {
-    const float4 x = *reinterpret_cast<const float4*>(s + (size_t)i * P.score_stride);
-    w[0] += ex2_approx(x.x - row_off[i]);
-    w[1] += ex2_approx(x.y - row_off[i]);
-    w[2] += ex2_approx(x.z - row_off[i]);
-    w[3] += ex2_approx(x.w - row_off[i]);
+  for (int i0 = 0; i0 < P.rows; i0 += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= P.rows) break;
+      if (i0 > 0) x[u] = *reinterpret_cast<const float4*>(s + (size_t)(i0 + u) * P.score_stride);
+      const float off = row_off[i0 + u];
+      w[0] += ex2_approx(x[u].x - off);
+      w[1] += ex2_approx(x[u].y - off);
+      w[2] += ex2_approx(x[u].z - off);
+      w[3] += ex2_approx(x[u].w - off);
+    }
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -308,8 +317,8 @@ WeightsPlan plan_weights(int num_seqs, int q_len, int num_q_heads, int num_kv_he
   p.row_tiles = p.rows <= 8 ? 0 : (p.rows <= 16 ? 1 : kRowTiles);
   p.row_chunks = p.row_tiles < 2 ? 1 : (int)((p.rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
   const long long bg = (long long)num_seqs * num_kv_heads;
-  const long long want = (p.rows <= kFinishMaxRows ? 16LL : 4LL) * sms();  // CTAs
   long long part = 128;
+  const long long want = (p.rows <= kFinishMaxRows ? 16LL : 4LL) * sms();  // CTAs
   while (part < 4096 && bg * p.row_chunks * ((max_context_len + part - 1) / part) > want) part *= 2;
   p.part = (int)part;
   p.np = (int)std::max(1LL, (max_context_len + part - 1) / part);

@@ -52,6 +52,7 @@ struct WeightsParams {
 
 constexpr int kWeightsWarps = 4;
 constexpr int kWeightsFinishThreads = 256;
+constexpr int kManyRowsCtas = 3;  // an SM
 
 // 8-token columns of a warp's step.
 constexpr __host__ __device__ int key_tiles(int KV) { return KV == kKvFp16 ? 2 : 4; }
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(32 * kWeightsWarps, KV == kKvFp16 && D == 128 
 
 // First grid, many rows: CTA (chunk of 16 RT rows, partition, b, g).
 template <int KV, int D, int RT>
-__global__ void __launch_bounds__(32 * kWeightsWarps, 3) paged_weights_rows_kernel(const WeightsParams P) {
+__global__ void __launch_bounds__(32 * kWeightsWarps, kManyRowsCtas) paged_weights_rows_kernel(const WeightsParams P) {
   constexpr int NW = kWeightsWarps, TILES = key_tiles(KV), KS = D / 16, CHUNK = 16 * RT;
   extern __shared__ __align__(128) unsigned char weights_smem[];
   uint4* qs = reinterpret_cast<uint4*>(weights_smem);
@@ -534,15 +535,28 @@ __global__ void __launch_bounds__(32 * kWeightsWarps, 3) paged_weights_rows_kern
 }
 
 // Rows first .. first + n - 1 of (b, g): M + log2(Z) over the partitions written (+inf where nothing is seen).
-__device__ __forceinline__ void merge_rows(const WeightsParams& P, int bg, int L, int first, int n, float* out) {
+__device__ __forceinline__ void merge_rows(const WeightsParams& P, int bg, int L, int first, int n, float* out,
+                                           int threads) {
   const int np = min(P.np, (L - 1) / P.part + 1);
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+  constexpr int U = 8;  // partitions in flight
+  for (int i = threadIdx.x; i < n; i += threads) {
     const size_t at = (size_t)bg * P.np * P.rows + first + i;
     float mx = -INFINITY, z = 0.f;
-    for (int j = 0; j < np; ++j) mx = fmaxf(mx, P.row_max[at + (size_t)j * P.rows]);
-    if (mx != -INFINITY)
-      for (int j = 0; j < np; ++j)
-        z = fmaf(P.row_sum[at + (size_t)j * P.rows], ex2_approx(P.row_max[at + (size_t)j * P.rows] - mx), z);
+    for (int j0 = 0; j0 < np; j0 += U) {
+      float m[U], l[U], top = mx;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        m[u] = j0 + u < np ? P.row_max[at + (size_t)(j0 + u) * P.rows] : -INFINITY;
+        l[u] = j0 + u < np ? P.row_sum[at + (size_t)(j0 + u) * P.rows] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
+      if (top == -INFINITY) continue;
+      z *= ex2_approx(mx - top);
+#pragma unroll
+      for (int u = 0; u < U; ++u) z = fmaf(l[u], ex2_approx(m[u] - top), z);
+      mx = top;
+    }
     out[i] = z > 0.f ? mx + __log2f(z) : INFINITY;
   }
 }
@@ -553,7 +567,7 @@ __global__ void __launch_bounds__(kWeightsFinishThreads) paged_weights_scores_ke
 
 // Second grid, many rows: CTA (partition, b, g) multiplies again.
 template <int KV, int D>
-__global__ void __launch_bounds__(32 * kWeightsWarps, 3) paged_weights_keys_kernel(const WeightsParams P) {
+__global__ void __launch_bounds__(32 * kWeightsWarps, kManyRowsCtas) paged_weights_keys_kernel(const WeightsParams P) {
   constexpr int NW = kWeightsWarps, TILES = key_tiles(KV), KS = D / 16;
   extern __shared__ __align__(16) unsigned char weights_smem[];
   uint4* qs = reinterpret_cast<uint4*>(weights_smem);
@@ -574,7 +588,7 @@ __global__ void __launch_bounds__(32 * kWeightsWarps, 3) paged_weights_keys_kern
     __syncthreads();  // the rows before are done with
     load_query_tiles<KV, D>(P, qs, b, g, first / 16, tiles);
     if (first == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    merge_rows(P, bg, L, first, min(16 * tiles, P.rows - first), row_off);
+    merge_rows(P, bg, L, first, min(16 * tiles, P.rows - first), row_off, 32 * NW);
     for (int i = P.rows - first + threadIdx.x; i < 16 * tiles; i += 32 * NW) row_off[i] = INFINITY;
     __syncthreads();
     for (int n = 0; keys.token(n) < t1; ++n) {
