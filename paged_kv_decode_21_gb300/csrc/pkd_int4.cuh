@@ -109,14 +109,22 @@ __device__ __forceinline__ uint32_t int4_scale_pair(uint32_t a, uint32_t b, uint
 // meaning of rows are those of paged_decode_mma_kernel; here a warp's ring
 // holds whole (block, kv head) tiles, brought by two plain bulk copies.
 //
+// Both products have the cache as their A operand (16 rows: tokens, or dims) and
+// the queries as their B operand (8 columns): S^T = K Q^T, O^T = V^T P^T, so that
+// eight query rows and less waste no half of a tile.  (With Q as A, of 16 rows,
+// single queries took twice the products for S, and moves that put zeros into
+// the operands' registers: 386 instructions per 16 tokens instead of @@.)
 // Fragments (c = lane % 4, r = lane / 4), for a slab of 32 dims:
 //   K  an ldmatrix of 8 tokens x 16 bytes gives lane (r, c) the codes of dims 8c
-//      .. 8c + 7 of token r: two k-steps' B operands, dims (8c + j, 8c + j + 4)
-//      in the halves.  Q's A fragments follow that order of dims.
+//      .. 8c + 7 of token r: two k-steps' A operands, dims (8c + j, 8c + j + 4)
+//      in the halves.  Q's B fragments follow that order of dims.
+//   S^T  lane (r, c) receives tokens r and r + 8 of query rows 2c and 2c + 1;
+//      packed in pairs of rows and transposed in 8 x 8 matrices (movmatrix),
+//      the weights are P^T's B fragments.
 //   V  the transposed ldmatrix gives lane (r, c) dims 4r .. 4r + 3 of tokens 2c
 //      and 2c + 1, one token a half: rows r and r + 8 of two m-tiles of V^T.
-// Q rows are the group's heads times up to `q_chunk` query tokens, NT tiles of 8
-// of them: 1, 2 or 4.  With 4 the Q fragments stay in shared memory.
+// Query rows are the group's heads times up to `q_chunk` query tokens, NT tiles
+// of 8 of them: 1, 2 or 4.  With 4 the Q fragments stay in shared memory.
 // d = (zero ? 0 : d) + A . B for one m16n8k16 tile; `zero` known when compiled.
 __device__ __forceinline__ void mma_16816_from(float (&d)[4], bool zero, uint32_t a0, uint32_t a1, uint32_t a2,
                                                uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -146,6 +154,13 @@ __device__ __forceinline__ void int4_copy(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// An 8 x 8 matrix of 16-bit elements, lane (r, c) holding row r's columns 2c and 2c + 1, transposed.
+__device__ __forceinline__ uint32_t transposed_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 struct Int4Params {
   DecodeParams d;
   int group, q_chunk;
@@ -171,9 +186,9 @@ struct Int4Traits {
   static constexpr int SW = SW_RAW > 8 ? 8 : SW_RAW;
   static constexpr int RING_BYTES = NW * SW * SLOT;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int MRG_ACC_OFF = 3 * NW * ROWS;
+  static constexpr int MRG_ACC_OFF = 2 * NW * ROWS;
   static constexpr int MERGE_BYTES = (MRG_ACC_OFF + NW * ROWS * D) * 4;
-  static constexpr int Q_BYTES = NT == 4 ? 2 * (D / 16) * 32 * 16 : 0;  // two 16-row tiles of A fragments
+  static constexpr int Q_BYTES = NT == 4 ? 2 * (D / 16) * 32 * 16 : 0;  // B fragments of four 8-row tiles
   static constexpr int MAIN_BYTES = RING_BYTES + Q_BYTES > MERGE_BYTES ? RING_BYTES + Q_BYTES : MERGE_BYTES;
   static constexpr int SMEM_BYTES = MAIN_BYTES + NW * SW * 8;
   static_assert(SW >= 2 && TILE % 16 == 0 && MAIN_BYTES % 16 == 0, "ring");
@@ -184,8 +199,6 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     paged_decode_int4_kernel(const __grid_constant__ Int4Params IP) {
   using T = Int4Traits<D, BS, NT>;
   constexpr int NW = T::NW, SW = T::SW, SLABS = T::SLABS, ROWS = T::ROWS;
-  constexpr int AT = NT == 4 ? 2 : 1;  // 16-row tiles of S
-  constexpr int HF = NT == 1 ? 1 : 2;  // 8-row halves of a tile in use
   const DecodeParams& P = IP.d;
   const Int4Bases bases = IP.bases;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -240,13 +253,15 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
   };
   int ids = ids_at(0), ids_next = ids_at(IDS);
   uint32_t bad_slots = 0;  // TILES bits a slot: tiles that are not there
+  uint32_t in_slot = 0;    // the next copies'
   const uint32_t ring_at = smem_u32(ring), full_at = smem_u32(full);
   auto issue = [&](int n) {  // copies of the warp's n-th unit, n ascending
     if (n > 0 && n % IDS == 0) {
       ids = ids_next;
       ids_next = ids_at(n + IDS);
     }
-    const uint32_t slot = (uint32_t)n % SW;
+    const uint32_t slot = in_slot;
+    in_slot = in_slot + 1 == SW ? 0 : in_slot + 1;
     // lanes 0 .. 2 TILES - 1 each copy a tile: K's, then V's
     const int pb = __shfl_sync(0xffffffffu, ids, (n % IDS) * TILES + lane % TILES);
     const bool good = (uint32_t)pb < (uint32_t)P.num_blocks;
@@ -265,16 +280,11 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
   int issued = 0;
   for (; issued < SW && issued < mine; ++issued) issue(issued);
 
-  int lim[NT];  // tokens at or past it are masked for the lane's rows r + 8 hf
-  int lim_min = t1;
-#pragma unroll
-  for (int hf = 0; hf < NT; ++hf) {
-    const int rr = r + 8 * hf;
-    lim[hf] = rr < rows ? min(t1, L - QL + jq0 + rr / G + 1) : t1;
-    lim_min = min(lim_min, lim[hf]);
-  }
+  // tokens at or past it are masked for query row rr (the first row sees the fewest)
+  auto limit = [&](int rr) { return rr < rows ? min(t1, L - QL + jq0 + rr / G + 1) : t1; };
+  const int lim_min = limit(0);
 
-  // Q as A fragments: k-step 2s + e of slab s has slots (2c, 2c + 1) = dims 8c
+  // Q as B fragments: k-step 2s + e of slab s has slots (2c, 2c + 1) = dims 8c
   // + 2e and 8c + 2e + 4 of the slab, slots (8 + 2c, 9 + 2c) = the dims behind
   auto q_word = [&](int rr, int s) {
     if (rr >= rows) return make_uint4(0u, 0u, 0u, 0u);
@@ -285,27 +295,27 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     u.w ^= IP.q_sign;
     return u;
   };
-  uint32_t qa[AT == 1 ? 2 * SLABS : 1][2 * HF];
-  uint4* qs = reinterpret_cast<uint4*>(smem + T::RING_BYTES);  // [tile][k-step][lane]
-  if constexpr (AT == 1) {
+  uint32_t qb[NT < 4 ? 2 * SLABS : 1][NT][2];
+  uint4* qs = reinterpret_cast<uint4*>(smem + T::RING_BYTES);  // [k-step][tile pair][lane]
+  if constexpr (NT < 4) {
 #pragma unroll
     for (int hf = 0; hf < NT; ++hf)
 #pragma unroll
       for (int s = 0; s < SLABS; ++s) {
         const uint4 u = q_word(r + 8 * hf, s);
-        qa[2 * s][hf] = prmt(u.x, u.z, 0x5410);
-        qa[2 * s][HF + hf] = prmt(u.x, u.z, 0x7632);
-        qa[2 * s + 1][hf] = prmt(u.y, u.w, 0x5410);
-        qa[2 * s + 1][HF + hf] = prmt(u.y, u.w, 0x7632);
+        qb[2 * s][hf][0] = prmt(u.x, u.z, 0x5410);
+        qb[2 * s][hf][1] = prmt(u.x, u.z, 0x7632);
+        qb[2 * s + 1][hf][0] = prmt(u.y, u.w, 0x5410);
+        qb[2 * s + 1][hf][1] = prmt(u.y, u.w, 0x7632);
       }
   } else {
-    for (int i = warp; i < AT * SLABS; i += NW) {
-      const int at = i / SLABS, s = i % SLABS;
-      const uint4 u = q_word(16 * at + r, s), w = q_word(16 * at + r + 8, s);
-      qs[(at * 2 * SLABS + 2 * s) * 32 + lane] = make_uint4(prmt(u.x, u.z, 0x5410), prmt(w.x, w.z, 0x5410),
-                                                            prmt(u.x, u.z, 0x7632), prmt(w.x, w.z, 0x7632));
-      qs[(at * 2 * SLABS + 2 * s + 1) * 32 + lane] = make_uint4(prmt(u.y, u.w, 0x5410), prmt(w.y, w.w, 0x5410),
-                                                                prmt(u.y, u.w, 0x7632), prmt(w.y, w.w, 0x7632));
+    for (int i = warp; i < 2 * SLABS; i += NW) {
+      const int pair = i / SLABS, s = i % SLABS;
+      const uint4 u = q_word(16 * pair + r, s), w = q_word(16 * pair + r + 8, s);
+      qs[(2 * s * 2 + pair) * 32 + lane] = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632),
+                                                      prmt(w.x, w.z, 0x5410), prmt(w.x, w.z, 0x7632));
+      qs[((2 * s + 1) * 2 + pair) * 32 + lane] = make_uint4(prmt(u.y, u.w, 0x5410), prmt(u.y, u.w, 0x7632),
+                                                            prmt(w.y, w.w, 0x5410), prmt(w.y, w.w, 0x7632));
     }
     __syncthreads();
   }
@@ -315,12 +325,16 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
   for (int k = 0; k < 2 * SLABS; ++k)
 #pragma unroll
     for (int hf = 0; hf < NT; ++hf) o[k][hf][0] = o[k][hf][1] = o[k][hf][2] = o[k][hf][3] = 0.f;
-  float m[NT], mt[NT], l[NT];
+  // per row 8 hf + 2c + x: the shift (within 2^tau of the maximum, and as good as
+  // that in a partial), and the lane's own sum
+  float m[NT][2], l[NT][2];
 #pragma unroll
-  for (int hf = 0; hf < NT; ++hf) {
-    m[hf] = mt[hf] = -INFINITY;
-    l[hf] = 0.f;
-  }
+  for (int hf = 0; hf < NT; ++hf)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      m[hf][x] = -INFINITY;
+      l[hf][x] = 0.f;
+    }
 
   // matrix loads: lane l addresses row l % 8 of matrix l / 8, matrices in the
   // order (slab, tokens 0-7), (slab, tokens 8-15), then the next slab's
@@ -337,9 +351,9 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
       asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
   };
 
+  uint32_t slot = 0, parity = 0;
   for (int u = 0; u < mine; ++u) {
-    const uint32_t slot = (uint32_t)u % SW;
-    if (!mbar_wait_bounded(&full[slot], ((uint32_t)u / SW) & 1, P.timeout_ns)) {
+    if (!mbar_wait_bounded(&full[slot], parity, P.timeout_ns)) {
       if (lane == 0) record_error(P.error_word, kErrTimeout);
       for (int v = u + 1; v < issued; ++v) mbar_wait_bounded(&full[v % SW], (v / SW) & 1, P.timeout_ns);
       break;
@@ -363,8 +377,8 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
 #pragma unroll
     for (int step = 0; step < 2 / SUBS; ++step) {
       if (SUBS == 1 && base + 16 * step >= t1) break;
-      // ---- S = Q K^T: sa over tokens 0..7, sb over 8..15 of a subtile
-      float sa[SUBS][AT][4], sb[SUBS][AT][4];  // (the first product of each starts from zero)
+      // ---- S^T = K Q^T: st[.][hf][2 y + x] is token r + 8 y, row 8 hf + 2c + x
+      float st[SUBS][NT][4];  // (the first product of each starts from zero)
 #pragma unroll
       for (int sub = 0; sub < SUBS; ++sub) {
         const int row0 = 16 * (step * SUBS + sub) % BS;
@@ -386,93 +400,87 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int k = 4 * i + 2 * h + e;
-              if constexpr (AT == 1) {
-                const uint32_t a1 = HF == 2 ? qa[k][1] : 0u, a3 = HF == 2 ? qa[k][3 % (2 * HF)] : 0u;
-                mma_16816_from(sa[sub][0], k == 0, qa[k][0], a1, qa[k][HF], a3, d0[2 * e], d0[2 * e + 1]);
-                mma_16816_from(sb[sub][0], k == 0, qa[k][0], a1, qa[k][HF], a3, d1[2 * e], d1[2 * e + 1]);
+              if constexpr (NT < 4) {
+#pragma unroll
+                for (int hf = 0; hf < NT; ++hf)
+                  mma_16816_from(st[sub][hf], k == 0, d0[2 * e], d1[2 * e], d0[2 * e + 1], d1[2 * e + 1], qb[k][hf][0],
+                                 qb[k][hf][1]);
               } else {
 #pragma unroll
-                for (int t = 0; t < AT; ++t) {
-                  const uint4 w = qs[(t * 2 * SLABS + k) * 32 + lane];
-                  mma_16816_from(sa[sub][t], k == 0, w.x, w.y, w.z, w.w, d0[2 * e], d0[2 * e + 1]);
-                  mma_16816_from(sb[sub][t], k == 0, w.x, w.y, w.z, w.w, d1[2 * e], d1[2 * e + 1]);
+                for (int pair = 0; pair < 2; ++pair) {
+                  const uint4 w = qs[(k * 2 + pair) * 32 + lane];
+                  mma_16816_from(st[sub][2 * pair], k == 0, d0[2 * e], d1[2 * e], d0[2 * e + 1], d1[2 * e + 1], w.x,
+                                 w.y);
+                  mma_16816_from(st[sub][2 * pair + 1], k == 0, d0[2 * e], d1[2 * e], d0[2 * e + 1], d1[2 * e + 1], w.z,
+                                 w.w);
                 }
               }
             }
           }
         }
       }
-      // ---- online softmax of rows r + 8hf over tokens 16 sub + (2c, 2c+1, 8+2c, 9+2c)
-      float sc[NT][SUBS][4];
-#pragma unroll
-      for (int hf = 0; hf < NT; ++hf)
-#pragma unroll
-        for (int sub = 0; sub < SUBS; ++sub)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sc[hf][sub][e] = sa[sub][hf / 2][2 * (hf % 2) + e];
-            sc[hf][sub][2 + e] = sb[sub][hf / 2][2 * (hf % 2) + e];
-          }
+      // ---- online softmax
       if (!whole || base + T::UNIT > lim_min) {
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-          const int x = 16 * (step * SUBS + sub);  // the subtile's first token in the unit
-          const bool none = (missing >> (x / BS)) & 1;
+          const int first = 16 * (step * SUBS + sub);  // the subtile's first token in the unit
+          const bool none = (missing >> (first / BS)) & 1;
 #pragma unroll
-          for (int hf = 0; hf < NT; ++hf) {
-            const int lt = none ? 0 : lim[hf] - base - x;
-            if (2 * c >= lt) sc[hf][sub][0] = -INFINITY;
-            if (2 * c + 1 >= lt) sc[hf][sub][1] = -INFINITY;
-            if (8 + 2 * c >= lt) sc[hf][sub][2] = -INFINITY;
-            if (9 + 2 * c >= lt) sc[hf][sub][3] = -INFINITY;
-          }
+          for (int hf = 0; hf < NT; ++hf)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int lt = none ? 0 : limit(8 * hf + 2 * c + x) - base - first;
+              if (r >= lt) st[sub][hf][x] = -INFINITY;
+              if (r + 8 >= lt) st[sub][hf][2 + x] = -INFINITY;
+            }
         }
       }
-      float lmax[NT];  // (scale_log2 > 0: the largest product is the largest score)
+      float lmax[NT][2];  // (scale_log2 > 0: the largest product is the largest score)
       bool need = false;
 #pragma unroll
-      for (int hf = 0; hf < NT; ++hf) {
-        lmax[hf] = fmaxf(fmaxf(sc[hf][0][0], sc[hf][0][1]), fmaxf(sc[hf][0][2], sc[hf][0][3]));
-        if constexpr (SUBS == 2)
-          lmax[hf] = fmaxf(lmax[hf], fmaxf(fmaxf(sc[hf][SUBS - 1][0], sc[hf][SUBS - 1][1]),
-                                           fmaxf(sc[hf][SUBS - 1][2], sc[hf][SUBS - 1][3])));
-        lmax[hf] *= P.scale_log2;
-        mt[hf] = fmaxf(mt[hf], lmax[hf]);
-        need |= lmax[hf] > m[hf] + kLazyTau;
-      }
+      for (int hf = 0; hf < NT; ++hf)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          lmax[hf][x] = fmaxf(st[0][hf][x], st[0][hf][2 + x]);
+          if constexpr (SUBS == 2)
+            lmax[hf][x] = fmaxf(lmax[hf][x], fmaxf(st[SUBS - 1][hf][x], st[SUBS - 1][hf][2 + x]));
+          lmax[hf][x] *= P.scale_log2;
+          need |= lmax[hf][x] > m[hf][x] + kLazyTau;
+        }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-        for (int hf = 0; hf < NT; ++hf) {
-          float mx = fmaxf(lmax[hf], __shfl_xor_sync(0xffffffffu, lmax[hf], 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[hf], mx);
-          const float alpha = (mn == -INFINITY) ? 1.f : ex2_approx(m[hf] - mn);
-          l[hf] *= alpha;
-          m[hf] = mn;
-          const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * c);
-          const float a_hi = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
+        for (int hf = 0; hf < NT; ++hf)
 #pragma unroll
-          for (int k = 0; k < 2 * SLABS; ++k) {
-            o[k][hf][0] *= a_lo;
-            o[k][hf][1] *= a_hi;
-            o[k][hf][2] *= a_lo;
-            o[k][hf][3] *= a_hi;
+          for (int x = 0; x < 2; ++x) {
+            float mx = lmax[hf][x];
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            const float mn = fmaxf(m[hf][x], mx);
+            const float alpha = (mn == -INFINITY) ? 1.f : ex2_approx(m[hf][x] - mn);
+            l[hf][x] *= alpha;
+            m[hf][x] = mn;
+#pragma unroll
+            for (int k = 0; k < 2 * SLABS; ++k) {  // O^T's columns are the same rows
+              o[k][hf][x] *= alpha;
+              o[k][hf][2 + x] *= alpha;
+            }
           }
-        }
       }
       uint32_t pb[NT][SUBS][2];
 #pragma unroll
       for (int hf = 0; hf < NT; ++hf) {
-        const float mu = m[hf] == -INFINITY ? 0.f : -m[hf];  // a row that has seen no token yet
+        // (a row that has seen no token yet: shift 0)
+        const float mu0 = m[hf][0] == -INFINITY ? 0.f : -m[hf][0], mu1 = m[hf][1] == -INFINITY ? 0.f : -m[hf][1];
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-          const float p0 = ex2_approx(fmaf(sc[hf][sub][0], P.scale_log2, mu));
-          const float p1 = ex2_approx(fmaf(sc[hf][sub][1], P.scale_log2, mu));
-          const float p2 = ex2_approx(fmaf(sc[hf][sub][2], P.scale_log2, mu));
-          const float p3 = ex2_approx(fmaf(sc[hf][sub][3], P.scale_log2, mu));
-          l[hf] += (p0 + p1) + (p2 + p3);
-          pb[hf][sub][0] = pack_half2(p0, p1);
-          pb[hf][sub][1] = pack_half2(p2, p3);
+          const float p0 = ex2_approx(fmaf(st[sub][hf][0], P.scale_log2, mu0));
+          const float p1 = ex2_approx(fmaf(st[sub][hf][1], P.scale_log2, mu1));
+          const float p2 = ex2_approx(fmaf(st[sub][hf][2], P.scale_log2, mu0));
+          const float p3 = ex2_approx(fmaf(st[sub][hf][3], P.scale_log2, mu1));
+          l[hf][0] += p0 + p2;
+          l[hf][1] += p1 + p3;
+          pb[hf][sub][0] = transposed_8x8(pack_half2(p0, p1));
+          pb[hf][sub][1] = transposed_8x8(pack_half2(p2, p3));
         }
       }
       // ---- O^T += V^T P^T
@@ -507,6 +515,10 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     }
     __syncwarp();
     bad_slots &= ~(((1u << TILES) - 1) << (slot * TILES));
+    if (++slot == SW) {
+      slot = 0;
+      parity ^= 1;
+    }
     if (issued < mine) {
       fence_proxy_async_smem();  // our reads of the slot precede the next copies into it
       issue(issued);
@@ -518,19 +530,19 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
   __syncthreads();
   float* mrg = reinterpret_cast<float*>(smem);
   float* mrg_m = mrg;
-  float* mrg_mt = mrg + NW * ROWS;
-  float* mrg_l = mrg + 2 * NW * ROWS;
+  float* mrg_l = mrg + NW * ROWS;
   float* mrg_acc = mrg + T::MRG_ACC_OFF;
 #pragma unroll
   for (int hf = 0; hf < NT; ++hf) {
-    float lv = l[hf] + __shfl_xor_sync(0xffffffffu, l[hf], 1);
-    lv += __shfl_xor_sync(0xffffffffu, lv, 2);
-    float mx = fmaxf(mt[hf], __shfl_xor_sync(0xffffffffu, mt[hf], 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (c == 0) {
-      mrg_m[warp * ROWS + 8 * hf + r] = m[hf];
-      mrg_mt[warp * ROWS + 8 * hf + r] = mx;
-      mrg_l[warp * ROWS + 8 * hf + r] = lv;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float lv = l[hf][x];
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) lv += __shfl_xor_sync(0xffffffffu, lv, k);
+      if (r == 0) {
+        mrg_m[warp * ROWS + 8 * hf + 2 * c + x] = m[hf][x];
+        mrg_l[warp * ROWS + 8 * hf + 2 * c + x] = lv;
+      }
     }
     float* acc = mrg_acc + (warp * ROWS + 8 * hf + 2 * c) * D;
 #pragma unroll
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     const int rr = i / D, d = i % D;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, mrg_mt[w * ROWS + rr]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, mrg_m[w * ROWS + rr]);
     float Z = 0.f, O = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
