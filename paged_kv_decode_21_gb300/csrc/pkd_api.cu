@@ -1193,6 +1193,7 @@ struct PartPlan {
   int np = 0;
   int rows = 0;       // kSharedTc: query rows per chunk
   bool wide = false;  // E4M3 block lists: the four-per-SM build
+  bool order = false;  // 4-bit caches: the grid walks its pieces longest first
   long long grid = 0;
 };
 
@@ -1593,7 +1594,21 @@ PartPlan plan_int4(const Shape& s, int q_len, int partition_size) {
   }
   if (s.max_context_len > p.P) p.np = (int)(((long long)s.max_context_len + p.P - 1) / p.P);
   p.grid = units * p.np;
+  // Longest first where a few waves of long pieces leave a tail: the order's
+  // kernel takes 3 us.
+  if (partition_size == 0 && s.num_seqs >= 2 && s.num_seqs <= pkd::kOrderMaxSeqs &&
+      std::min(p.P, s.max_context_len) >= kOrderMinContext) {
+    int sms = sm_count();
+    if (sms <= 0) sms = 148;
+    const long long slots = (long long)sms * pkd::int4_ctas_per_sm(pkd::int4_rows(q_len, G));
+    p.order = p.grid >= slots && p.grid < kOrderMaxWaves * slots;
+  }
   return p;
+}
+
+size_t int4_workspace(const Shape& s, int q_len, const PartPlan& plan) {
+  return (plan.np > 1 ? layout(nullptr, s.num_seqs * q_len, s.num_q_heads, s.head_dim, plan.np).bytes : 0) +
+         (plan.order ? order_bytes(s.num_seqs, plan.np) : 0);
 }
 
 pkd_status check_int4(const Shape& s, int q_len, int partition_size) {
@@ -1616,8 +1631,7 @@ size_t paged_decode_int4_workspace_size(int num_seqs, int q_len, int num_q_heads
   const Shape s{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, 1,
                 (int)(((long long)max_context_len + block_size - 1) / block_size) + 1, max_context_len};
   if (check_int4(s, q_len, partition_size) != PKD_OK) return 0;
-  const PartPlan plan = plan_int4(s, q_len, partition_size);
-  return plan.np > 1 ? layout(nullptr, num_seqs * q_len, num_q_heads, head_dim, plan.np).bytes : 0;
+  return int4_workspace(s, q_len, plan_int4(s, q_len, partition_size));
 }
 
 pkd_status paged_decode_attention_int4(const void* q, const void* k_cache, const void* v_cache,
@@ -1657,6 +1671,14 @@ pkd_status paged_decode_attention_int4(const void* q, const void* k_cache, const
     p.tmp_out = w.tmp_out;
     p.max_logits = w.max_logits;
     p.exp_sums = w.exp_sums;
+  }
+  // (a workspace without room for the order runs the plain one)
+  if (plan.order && workspace && aligned(workspace, 256) && workspace_bytes >= int4_workspace(s, q_len, plan)) {
+    int32_t* order = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + w.bytes);
+    pkd::piece_order_kernel<<<(num_seqs + 127) / 128, 128, 0, stream>>>(context_lens, num_seqs, plan.P, plan.np, order,
+                                                                        0, nullptr);
+    if (cudaGetLastError() != cudaSuccess) return PKD_ERR_LAUNCH;
+    p.piece_order = order;
   }
   if (pkd::failed(pkd::launch_decode_int4(head_dim, block_size, num_q_heads / num_kv_heads, p, plan.grid, stream)))
     return PKD_ERR_LAUNCH;

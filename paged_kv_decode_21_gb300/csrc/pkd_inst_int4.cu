@@ -14,8 +14,22 @@ cudaError_t launch(const Int4Params& p, long long grid, cudaStream_t stream) {
   auto* fn = paged_decode_int4_kernel<D, BS, NT>;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
   if (failed(e)) return e;
-  fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(p);
-  return cudaGetLastError();
+  if (!p.d.piece_order) {
+    fn<<<(unsigned)grid, T::THREADS, T::SMEM_BYTES, stream>>>(p);
+    return cudaGetLastError();
+  }
+  // a programmatic dependent of the order kernel
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(T::THREADS);
+  cfg.dynamicSmemBytes = T::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 template <int D, int BS>

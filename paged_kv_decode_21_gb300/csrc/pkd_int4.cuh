@@ -208,8 +208,18 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
   const int np_grid = P.max_partitions, G = IP.group, QC = IP.q_chunk;
   const int qc = blockIdx.x % P.q_chunks;
   const int rest = blockIdx.x / P.q_chunks;
-  const int j = rest % np_grid, bg = rest / np_grid;
-  const int g = bg % P.num_kv_heads, b = bg / P.num_kv_heads;
+  int j, b, g;
+  if (P.piece_order) {  // longest first, written by the grid this one is the programmatic dependent of
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int piece = P.piece_order[rest / P.num_kv_heads];
+    g = rest % P.num_kv_heads;
+    b = piece / np_grid;
+    j = piece % np_grid;
+  } else {
+    j = rest % np_grid;
+    g = rest / np_grid % P.num_kv_heads;
+    b = rest / np_grid / P.num_kv_heads;
+  }
   const int jq0 = qc * QC, QL = P.q_len, tok0 = b * QL;
   const int L = row_clamped_len<BS>(P, b);
   const int nq = min(QC, QL - jq0), rows = G * nq;
