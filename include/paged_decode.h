@@ -951,9 +951,9 @@ size_t paged_kv_attention_weights_workspace_size(int num_seqs, int q_len, int nu
  *   kept           device int32 [num_seqs][num_kv_heads][max_kept]: the chosen
  *                  positions in ascending order, then -1
  *   kept_lens      device int32 [num_seqs]: how many, min(L, max_kept)
- *   max_context_len  host upper bound of context_lens
- *   max_kept >= 1; sink_tokens + recent_tokens <= max_kept; block_size any
- *                  positive size
+ *   max_context_len  host upper bound of context_lens, at most 2^30
+ *   max_kept       in [1, 2^30]; sink_tokens + recent_tokens <= max_kept;
+ *                  block_size any positive size
  * Tokens of a block outside the pool are reported (PKD_DEVERR_BAD_BLOCK) and
  * come last.
  */
@@ -979,7 +979,7 @@ pkd_status paged_kv_token_select(const float* weights, const int32_t* block_tabl
  *                  kept_lens[b] counts up to max_kept and the new row's room
  *   new_tables     device int32 [num_seqs][max_new_blocks]: blocks that no table
  *                  of the call reads, each once
- *   head_dim 64 or 128, block_size 16 or 32
+ *   head_dim 64 or 128, block_size 16 or 32; max_kept in [1, 2^30]
  */
 pkd_status paged_kv_compact(void* k_cache, void* v_cache, float* weights, const int32_t* block_tables,
                             const int32_t* context_lens, const int32_t* kept, const int32_t* kept_lens,

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kWeightsFinishThreads) paged_weights_scores_ke
   }
 }
 
+constexpr int kMaxTokens = 1 << 30;  // the longest context, and the most tokens kept
 constexpr int kSelectBins = 2048;
 template <int NT>
 __global__ void __launch_bounds__(NT) paged_kv_token_select_kernel(const TokenSelectParams P) {
@@ -74,8 +75,9 @@ __global__ void __launch_bounds__(NT) paged_kv_token_select_kernel(const TokenSe
   __shared__ int above[NWARP], equal[NWARP];  // per warp's stretch
   const int g = blockIdx.x % P.num_kv_heads, b = blockIdx.x / P.num_kv_heads;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int L = max(0, clamped_len(P.context_lens, b, P.block_size, P.max_blocks_per_seq,
-                                   g == 0 && tid == 0 ? P.error_word : nullptr));
+  // (counts of four tokens at a time stay in 32 bits)
+  const int L = min(kMaxTokens, max(0, clamped_len(P.context_lens, b, P.block_size, P.max_blocks_per_seq,
+                                                   g == 0 && tid == 0 ? P.error_word : nullptr)));
   const int K = P.max_kept;
   int32_t* out = P.kept + (size_t)blockIdx.x * K;
   if (g == 0 && tid == 0) P.kept_lens[b] = min(L, K);
@@ -285,7 +287,6 @@ int sms() {
   return n;
 }
 
-constexpr int kMaxTokens = 1 << 30;
 constexpr unsigned long long kWaitBudgetNs = 100ull * 1000ull * 1000ull;  // 100 ms per bounded wait
 constexpr int kRowTiles = 8;     // row tiles of a CTA of the first grid, where there is more than one
 constexpr int kQueryTiles = 16;  // and of Q in shared memory in the second
@@ -456,7 +457,7 @@ pkd_status paged_kv_token_select(const float* weights, const int32_t* block_tabl
                                  int num_blocks, int max_blocks_per_seq, int max_context_len, int max_kept,
                                  int sink_tokens, int recent_tokens, int* error_word, cudaStream_t stream) {
   if (num_seqs < 0 || num_kv_heads <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 ||
-      max_context_len < 0 || max_kept < 1 || sink_tokens < 0 || recent_tokens < 0 ||
+      max_context_len < 0 || max_context_len > kMaxTokens || max_kept < 1 || max_kept > kMaxTokens || sink_tokens < 0 || recent_tokens < 0 ||
       (long long)sink_tokens + recent_tokens > max_kept ||
       (long long)max_context_len > (long long)max_blocks_per_seq * block_size)
     return PKD_ERR_SHAPE;
@@ -503,7 +504,7 @@ pkd_status paged_kv_compact(void* k_cache, void* v_cache, float* weights, const 
                             int num_blocks, int max_blocks_per_seq, int max_kept, int max_new_blocks, int kv_type,
                             int* error_word, cudaStream_t stream) {
   if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
-      max_blocks_per_seq <= 0 || max_kept < 1 || max_new_blocks < 1)
+      max_blocks_per_seq <= 0 || max_kept < 1 || max_kept > kMaxTokens || max_new_blocks < 1)
     return PKD_ERR_SHAPE;
   if ((head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32)) return PKD_ERR_UNSUPPORTED;
   if (kv_type < PKD_KV_FP16 || kv_type > PKD_KV_INT4) return PKD_ERR_SHAPE;

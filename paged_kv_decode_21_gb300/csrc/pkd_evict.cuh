@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(32 * kWeightsWarps, kManyRowsCtas) paged_weigh
 // Choice of tokens: CTA (b, g).  Weights as ordered 32-bit keys (equal values
 // equal keys, larger ones larger, not a number the largest, no block the
 // smallest), kept in shared memory; the need-th largest key of the candidates by
-// four passes of 256 bins; then every warp writes the chosen tokens of its own
+// three passes of 2048 bins; then every warp writes the chosen tokens of its own
 // stretch, ascending.  A thread takes four neighbouring tokens at a time, eight
 // such loads in flight.
 struct TokenSelectParams {

@@ -113,7 +113,7 @@ __device__ __forceinline__ uint32_t int4_scale_pair(uint32_t a, uint32_t b, uint
 // the queries as their B operand (8 columns): S^T = K Q^T, O^T = V^T P^T, so that
 // eight query rows and less waste no half of a tile.  (With Q as A, of 16 rows,
 // single queries took twice the products for S, and moves that put zeros into
-// the operands' registers: 386 instructions per 16 tokens instead of @@.)
+// the operands' registers: 386 instructions per 16 tokens instead of 356.)
 // Fragments (c = lane % 4, r = lane / 4), for a slab of 32 dims:
 //   K  an ldmatrix of 8 tokens x 16 bytes gives lane (r, c) the codes of dims 8c
 //      .. 8c + 7 of token r: two k-steps' A operands, dims (8c + j, 8c + j + 4)

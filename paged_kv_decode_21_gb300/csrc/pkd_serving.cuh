@@ -57,9 +57,9 @@ struct RopeAppendParams {
 // ..  Adding 1.5 2^23 + 8 in one fused multiply-add rounds x / step to an integer
 // and leaves the code in the low bits.  The quotient by a reciprocal is within
 // 2^-20 of the exact one where it is below 8 and the IEEE quotient within 2^-21,
-// so they round alike unless the first is nearer than 2e-5 to halfway: then, and
-// where it is not a number, IEEE division decides (one value in 25000).  Only
-// scales that are subnormal or saturated (`edge`) let quotients pass 7.5.
+// so they round alike unless the first is nearer than 2e-5 to halfway: then IEEE
+// division decides (one value in 25000), as it does for scales that are subnormal
+// or saturated (`edge`), which alone let quotients pass 7.5.
 __device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float step, bool edge) {
   if (!(step > 0.f)) return 0x88888888u;
   constexpr float kMagic = 12582912.f + 8.f;

@@ -146,3 +146,10 @@ def test_compact(L):
         if i != 2:                                             # weights may be left out
             assert call(p={i: None}) == 1, i
     assert call(p={2: None, 3: None}) == 1 and call(err=ODD) == 4
+
+
+def test_counts_past_32_bits_are_refused(L):
+    big = (1 << 30) + 1
+    sel = lambda K=8, mc=100, MB=1 << 27: L.paged_kv_token_select(*[FAKE] * 5, 2, 2, 16, 64, MB, mc, K, 0, 0, None, None)  # noqa: E731
+    assert sel(K=big) == 2 and sel(mc=big) == 2
+    assert L.paged_kv_compact(*[FAKE] * 8, 2, 2, 128, 16, 64, 8, big, 2, 0, None, None) == 2

@@ -373,3 +373,19 @@ def test_refusals():
             ops.paged_kv_compact(*args)
 
 
+
+
+def test_select_with_thousands_of_equal_keys_at_the_border():
+    """Thousands of weights that agree in their leading bits, and thousands that are equal, at the border."""
+    BS, n = 16, 30000
+    NB = n // BS
+    bt = torch.randperm(NB, generator=torch.Generator().manual_seed(2)).to(torch.int32)[None].to(DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    w = torch.empty((NB, 3, BS), device=DEV)
+    w[:, 0] = 1.0 + torch.rand((NB, BS), generator=g, device=DEV) * 2.0 ** -4
+    w[:, 1] = 0.5
+    w[:, 2] = torch.where(torch.rand((NB, BS), generator=g, device=DEV) < 0.5, 0.25, 0.75)
+    for K, sink, recent in ((7000, 0, 0), (20000, 5, 11), (100, 50, 50)):
+        kept, _ = ops.paged_kv_token_select(w, bt, i32(n), K, sink, recent)
+        want, _ = ref.token_select(w, bt, [n], K, sink, recent, BS)
+        assert torch.equal(kept.cpu(), want), K
