@@ -662,9 +662,17 @@ __global__ void __launch_bounds__(32 * kWeightsWarps, kManyRowsCtas) paged_weigh
 // Choice of tokens: CTA (b, g).  Weights as ordered 32-bit keys (equal values
 // equal keys, larger ones larger, not a number the largest, no block the
 // smallest), kept in shared memory; the need-th largest key of the candidates by
-// three passes of 2048 bins; then every warp writes the chosen tokens of its own
-// stretch, ascending.  A thread takes four neighbouring tokens at a time, eight
-// such loads in flight.
+// at most three passes of 2048 bins, the first as the keys come; then every warp
+// votes on its own stretch, counts and writes the chosen tokens, ascending.  A
+// thread loads four neighbouring tokens at a time, eight such loads in flight.
+//
+// Bound by latencies and instructions, not by its bytes: of a CTA's 19 us for 28,000
+// tokens 7.5 are the tables and weights coming in with the first counts, 3.3-4.9
+// the passes over the bits, 2.3 the votes, 1.7 the writing.  48 x 8 rows of
+// 8000-32768 tokens 44 us (58 with the first pass apart and ranks by token), 32 x
+// 8 rows of 1150 7.8.  One CTA of 1024 threads an SM, as the keys fill its shared
+// memory; 512 threads took 58, two CTAs of 512 with 22,000 keys each 126, as the
+// longer rows are read again.
 struct TokenSelectParams {
   const float* weights;
   const int32_t *block_tables, *context_lens;
@@ -682,8 +690,14 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Copy of kept rows: CTA (a few dozen new rows, b, g).  Threads look up where the rows
-// come from and go to, then all copy 16-byte pieces, K's and V's, eight in flight.
+// Copy of kept rows: a warp takes a few dozen new rows of one (b, g).  Its lanes look
+// up where the rows come from and go to, a row a lane, then copy 16-byte pieces,
+// K's and V's, four in flight a lane; warps do not wait for one another, so one's
+// look-ups (three dependent loads) run beside the others' copies.
+// Bound by HBM, by 128- and 256-byte pieces in no order: 48 x 8 x 2048 rows of E4M3
+// 71 us, 5.8 TB/s, 32 x 8 x 1024 of fp16 47 us, 5.8 TB/s (256 threads that look up
+// together first, eight pieces in flight: 78 and 48; 10 or 12 CTAs an SM: 72 and 76;
+// six pieces in flight: 73).
 struct CompactParams {
   uint8_t *k_cache, *v_cache;
   float* weights;
@@ -692,32 +706,34 @@ struct CompactParams {
   int* error_word;
 };
 
-constexpr int kCompactThreads = 256;
-// New rows of a CTA: eight 16-byte pieces a thread.
+constexpr int kCompactThreads = 128;
+constexpr int kCompactCtas = 9;  // an SM
+// New rows of a warp: a dozen to two dozen 16-byte pieces a lane.
 __host__ __device__ constexpr int compact_rows(int KV, int D) {
-  return KV == kKvFp16 ? 8192 / D : (KV == kKvE4m3 ? 16384 / D : 24576 / D);
+  return KV == kKvFp16 && D == 128 ? 16 : 32;
 }
 
 template <int KV, int D>
-__global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const CompactParams P) {
+__global__ void __launch_bounds__(kCompactThreads, kCompactCtas) paged_kv_compact_kernel(const CompactParams P) {
   // pieces of a row in one cache: 16 bytes each; 4-bit rows: D / 32 of codes, and the scales
   constexpr int PIECES = KV == kKvFp16 ? D / 8 : (KV == kKvE4m3 ? D / 16 : D / 32 + 1);
-  constexpr int ROWS = compact_rows(KV, D);
-  static_assert(ROWS <= kCompactThreads || KV == kKvInt4, "a thread looks up a row");
-  __shared__ int src_block[ROWS], src_row[ROWS], dst_block[ROWS];
+  constexpr int ROWS = compact_rows(KV, D), WARPS = kCompactThreads / 32;
+  static_assert(ROWS <= 32, "a lane looks up a row");
+  const int lane = threadIdx.x % 32;
   const int chunk = blockIdx.x % P.chunks, bg = blockIdx.x / P.chunks;
   const int g = bg % P.num_kv_heads, b = bg / P.num_kv_heads;
-  const int i0 = chunk * ROWS;
+  const int i0 = (chunk * WARPS + (int)threadIdx.x / 32) * ROWS;
   const int room = min(P.max_kept, (int)min((long long)P.max_new_blocks * P.block_size, 0x7fffffffLL));
-  const int n = min(P.kept_lens[b], room) - i0;
-  if (n <= 0) {
-    if (chunk == 0 && g == 0 && threadIdx.x == 0 && P.kept_lens[b] < 0) record_error(P.error_word, kErrBadBlock);
-    return;
-  }
-  if (chunk == 0 && g == 0 && threadIdx.x == 0 && P.kept_lens[b] > room) record_error(P.error_word, kErrBadBlock);
-  const int BS = P.block_size, rows = min(n, ROWS);
-  for (int x = threadIdx.x; x < rows; x += kCompactThreads) {
-    const int i = i0 + x;
+  const int kept = P.kept_lens[b];
+  if (chunk == 0 && g == 0 && threadIdx.x == 0 && (kept < 0 || kept > room)) record_error(P.error_word, kErrBadBlock);
+  const int rows = min(min(kept, room) - i0, ROWS);
+  if (rows <= 0) return;
+  const int BS = P.block_size;
+  const size_t TILE = KV == kKvInt4 ? (size_t)BS * D * 9 / 16 : (size_t)BS * PIECES * 16;
+  size_t src = 0, dst = 0;  // the tiles' first bytes
+  int src_row = -1;         // -1: nothing to copy
+  if (lane < rows) {
+    const int i = i0 + lane;
     const int t = P.kept[(size_t)bg * P.max_kept + i];
     const int to = P.new_tables[(size_t)b * P.max_new_blocks + i / BS];
     int from = -1;
@@ -725,48 +741,47 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
       from = P.block_tables[(size_t)b * P.max_blocks_per_seq + t / BS];
     if (from < 0 || from >= P.num_blocks || to < 0 || to >= P.num_blocks) {
       record_error(P.error_word, kErrBadBlock);
-      from = -1;
+    } else {
+      const size_t from_tile = (size_t)from * P.num_kv_heads + g, to_tile = (size_t)to * P.num_kv_heads + g;
+      src = from_tile * TILE;
+      dst = to_tile * TILE;
+      src_row = t % BS;
+      if (P.weights) P.weights[to_tile * BS + i % BS] = P.weights[from_tile * BS + src_row];
     }
-    src_block[x] = from;
-    src_row[x] = t % BS;
-    dst_block[x] = to;
-    if (from >= 0 && P.weights)
-      P.weights[((size_t)to * P.num_kv_heads + g) * BS + i % BS] =
-          P.weights[((size_t)from * P.num_kv_heads + g) * BS + t % BS];
   }
-  __syncthreads();
-  constexpr int U = 8;
+  constexpr int U = 4;
+  constexpr int ITEMS = ROWS * 2 * PIECES;
+  static_assert(ITEMS % 32 == 0, "whole warps look at every row");
   const int items = rows * 2 * PIECES;
-  for (int at = threadIdx.x; at < items; at += U * kCompactThreads) {
+  for (int at = 0; at < items; at += 32 * U) {
     uint4 x[U];
     uint8_t* to[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int it = at + u * kCompactThreads;
-      to[u] = nullptr;
-      if (it >= items) continue;
+      const int it = at + u * 32 + lane;
       const int piece = it % PIECES, kv = it / PIECES % 2, i = it / (2 * PIECES);
-      if (src_block[i] < 0) continue;
-      uint8_t* cache = kv ? P.v_cache : P.k_cache;
-      const size_t from_tile = (size_t)src_block[i] * P.num_kv_heads + g;
-      const size_t to_tile = (size_t)dst_block[i] * P.num_kv_heads + g;
-      const int from_row = src_row[i], to_row = (i0 + i) % BS;
+      const int from_row = __shfl_sync(0xffffffffu, src_row, i);
+      const size_t from = __shfl_sync(0xffffffffu, src, i), into = __shfl_sync(0xffffffffu, dst, i);
+      to[u] = nullptr;
+      if (it >= items || from_row < 0) continue;
+      const uint8_t* s = (kv ? P.v_cache : P.k_cache) + from;
+      uint8_t* o = (kv ? P.v_cache : P.k_cache) + into;
+      const int to_row = (i0 + i) % BS;
       if constexpr (KV == kKvInt4) {
-        const size_t TILE = (size_t)BS * D * 9 / 16;
         if (piece < D / 32) {
-          x[u] = *reinterpret_cast<const uint4*>(cache + from_tile * TILE + (piece * BS + from_row) * 16);
-          to[u] = cache + to_tile * TILE + (piece * BS + to_row) * 16;
+          x[u] = *reinterpret_cast<const uint4*>(s + (piece * BS + from_row) * 16);
+          to[u] = o + (piece * BS + to_row) * 16;
         } else {
-          const uint8_t* s = cache + from_tile * TILE + BS * (D / 2) + from_row * (D / 16);
-          uint8_t* o = cache + to_tile * TILE + BS * (D / 2) + to_row * (D / 16);
+          s += BS * (D / 2) + from_row * (D / 16);
+          o += BS * (D / 2) + to_row * (D / 16);
           if constexpr (D == 128)
             *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(s);
           else
             *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(s);
         }
       } else {
-        x[u] = *reinterpret_cast<const uint4*>(cache + ((from_tile * BS + from_row) * PIECES + piece) * 16);
-        to[u] = cache + ((to_tile * BS + to_row) * PIECES + piece) * 16;
+        x[u] = *reinterpret_cast<const uint4*>(s + (from_row * PIECES + piece) * 16);
+        to[u] = o + (to_row * PIECES + piece) * 16;
       }
     }
 #pragma unroll

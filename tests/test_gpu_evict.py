@@ -374,7 +374,6 @@ def test_refusals():
 
 
 
-
 def test_select_with_thousands_of_equal_keys_at_the_border():
     """Thousands of weights that agree in their leading bits, and thousands that are equal, at the border."""
     BS, n = 16, 30000
@@ -389,3 +388,15 @@ def test_select_with_thousands_of_equal_keys_at_the_border():
         kept, _ = ops.paged_kv_token_select(w, bt, i32(n), K, sink, recent)
         want, _ = ref.token_select(w, bt, [n], K, sink, recent, BS)
         assert torch.equal(kept.cpu(), want), K
+
+
+@pytest.mark.parametrize("K", [14999, 15000, 30000])
+def test_select_of_long_contexts_few_and_many_kept(K):
+    BS, n = 16, 60000
+    NB = n // BS + 1
+    bt = torch.randperm(NB, generator=torch.Generator().manual_seed(4)).to(torch.int32)[None].to(DEV)
+    w = torch.rand((NB, 2, BS), generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+    w[:, 1] = (w[:, 1] * 5).floor()
+    kept, _ = ops.paged_kv_token_select(w, bt, i32(n), K, 33, 70)
+    want, _ = ref.token_select(w, bt, [n], K, 33, 70, BS)
+    assert torch.equal(kept.cpu(), want)
