@@ -1562,13 +1562,18 @@ pkd_status blocks_impl(const void* q, const void* k_cache, const void* v_cache, 
 
 // 4-bit caches: partition_size as paged_decode_attention_ex takes it (0: the
 // automatic one).  That is the shortest power of two, from 128 tokens on, whose
-// grid fits one resident wave, where it is at most 2048 tokens; else, for fewer
-// units than two waves, about as many partitions as make two of them (at least
-// two: a ragged batch's long contexts then end sooner).
-//   16 x 32/8 heads, 2000-4096 tokens: 1024-token partitions (one wave) 33 us,
-//   512 38, 2048 37; 32 x 40/8, 16K-32K: 4096 240, 8192 (one wave) 269, 1024
-//   262; 128 x 28/4, 8192: 4096 158, unsplit 169; 128 x 32/8, 512-4096: 2048
-//   112, unsplit 118; 48 x 4 tokens x 28/4, 2000-8192: 2048 109, unsplit 142.
+// grid fits one resident wave, where it is at most 2048 tokens: 16 x 32/8 heads,
+// 2000-4096 tokens, one wave at 1024: 32 us, 2048 33, 4096 40.  Else as many
+// partitions as make 1.2 waves (one wave and a bit leaves most of the GPU idle at
+// its end), of at most 4096 tokens where there is more than one and of 8192 where
+// there is one and less than four waves, as pieces end at different times and
+// their beginnings and the merge cost about 6 us each:
+//   128 x 32/8, 512-4096, 1.7 waves: whole 89, 2048 94; 80 x 32/8, 8192, 1.05:
+//   4096 170, whole 189; 128 x 28/4, 8192, 0.8: 4096 137, 2048 142, whole 140;
+//   32 x 40/8, 16K-32K, 0.4: 4096 188, 8192 203, 2048 199; 128 x 40/8,
+//   2000-16384, 1.7: 8192 268, 4096 281, whole 277; 48 x 4 tokens x 28/4,
+//   2000-8192, 0.6: 4096 91, 2048 97, whole 140; 8 tokens, 1.3: whole 144, 4096 152.
+constexpr long long kMaxPartitionInt4 = 4096;
 PartPlan plan_int4(const Shape& s, int q_len, int partition_size) {
   PartPlan p;
   const int G = s.num_q_heads / s.num_kv_heads;
@@ -1586,9 +1591,12 @@ PartPlan plan_int4(const Shape& s, int q_len, int partition_size) {
     long long q = kMinSmallGridPartition;
     while (q < s.max_context_len && units * ((s.max_context_len + q - 1) / q) > slots) q *= 2;
     if (q > kMaxSmallGridPartitionInt4) {
-      const double waves = 2.0 * slots / units;
-      const long long np = waves <= 1.0 ? 1 : std::max(2LL, (long long)(waves + 0.5));
-      for (q = np > 1 ? kMinAutoPartition : s.max_context_len; np > 1 && 2 * q * np <= s.max_context_len * 5LL / 4;) q *= 2;
+      const long long np = std::max(1LL, (6 * slots + 5 * units - 1) / (5 * units));
+      if (np > 1) {
+        for (q = kMinAutoPartition; q < kMaxPartitionInt4 && 2 * q * (2 * np - 1) <= 2LL * s.max_context_len;) q *= 2;
+      } else {
+        q = units < 4 * slots ? 2 * kMaxPartitionInt4 : s.max_context_len;
+      }
     }
     if (q < s.max_context_len) p.P = (int)q;
   }

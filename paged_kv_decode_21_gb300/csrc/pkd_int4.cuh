@@ -125,6 +125,15 @@ __device__ __forceinline__ uint32_t int4_scale_pair(uint32_t a, uint32_t b, uint
 //      and 2c + 1, one token a half: rows r and r + 8 of two m-tiles of V^T.
 // Query rows are the group's heads times up to `q_chunk` query tokens, NT tiles
 // of 8 of them: 1, 2 or 4.  With 4 the Q fragments stay in shared memory.
+//
+// Bound by instructions: of a 16-token subtile's 356 (one row tile) half are the
+// codes' way into fp16 pairs, 16 the products; 0.58 a cycle and scheduler, HBM at
+// half its rate.  128 x 32/8 heads, 512-4096 tokens, 88 us; 32 x 40/8, 16K-32K, 184;
+// the bytes alone 50 and 135.  Four row tiles (48 x 4 tokens x 28/4): 714
+// instructions, 0.38 a cycle of the 8 warps that their accumulators leave room
+// for.  Three or five CTAs an SM for one row tile: 207 and 216 against 193 us at 16K-32K;
+// chunks of two row tiles for 28 rows: +6%; the next scores beside a subtile's
+// P V: no change; K scales spread by permutations, or shifts as multiplications: +5%.
 // d = (zero ? 0 : d) + A . B for one m16n8k16 tile; `zero` known when compiled.
 __device__ __forceinline__ void mma_16816_from(float (&d)[4], bool zero, uint32_t a0, uint32_t a1, uint32_t a2,
                                                uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -186,8 +195,10 @@ struct Int4Traits {
   static constexpr int SW = SW_RAW > 8 ? 8 : SW_RAW;
   static constexpr int RING_BYTES = NW * SW * SLOT;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int MRG_ACC_OFF = 2 * NW * ROWS;
-  static constexpr int MERGE_BYTES = (MRG_ACC_OFF + NW * ROWS * D) * 4;
+  // the warps' maxima and sums; per row their factors, its sum and its place; their O's, rows of PITCH floats
+  static constexpr int MRG_C_OFF = 2 * NW * ROWS, MRG_Z_OFF = MRG_C_OFF + NW * ROWS, MRG_ACC_OFF = MRG_Z_OFF + 2 * ROWS;
+  static constexpr int PITCH = D + 4;  // (four query rows and two quads of dims at a time meet no bank twice)
+  static constexpr int MERGE_BYTES = (MRG_ACC_OFF + NW * ROWS * PITCH) * 4;
   static constexpr int Q_BYTES = NT == 4 ? 2 * (D / 16) * 32 * 16 : 0;  // B fragments of four 8-row tiles
   static constexpr int MAIN_BYTES = RING_BYTES + Q_BYTES > MERGE_BYTES ? RING_BYTES + Q_BYTES : MERGE_BYTES;
   static constexpr int SMEM_BYTES = MAIN_BYTES + NW * SW * 8;
@@ -554,39 +565,67 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
         mrg_l[warp * ROWS + 8 * hf + 2 * c + x] = lv;
       }
     }
-    float* acc = mrg_acc + (warp * ROWS + 8 * hf + 2 * c) * D;
+    float* acc = mrg_acc + (warp * ROWS + 8 * hf + 2 * c) * T::PITCH + 4 * r;
 #pragma unroll
-    for (int k = 0; k < 2 * SLABS; ++k) {
-      const int d = 32 * (k / 2) + 4 * r + 2 * (k % 2);
-      *reinterpret_cast<float2*>(acc + d) = make_float2(o[k][hf][0], o[k][hf][2]);
-      *reinterpret_cast<float2*>(acc + D + d) = make_float2(o[k][hf][1], o[k][hf][3]);
+    for (int k = 0; k < SLABS; ++k) {  // dims 32k + 4r ..
+      const float(&lo)[4] = o[2 * k][hf];
+      const float(&hi)[4] = o[2 * k + 1][hf];
+      *reinterpret_cast<float4*>(acc + 32 * k) = make_float4(lo[0], lo[2], hi[0], hi[2]);
+      *reinterpret_cast<float4*>(acc + T::PITCH + 32 * k) = make_float4(lo[1], lo[3], hi[1], hi[3]);
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * D; i += T::THREADS) {
-    const int rr = i / D, d = i % D;
+  static_assert(NW == 4 && ROWS <= T::THREADS, "a factor a warp, a thread a row");
+  float4* mrg_c = reinterpret_cast<float4*>(mrg + T::MRG_C_OFF);
+  float* mrg_z = mrg + T::MRG_Z_OFF;
+  int* mrg_row = reinterpret_cast<int*>(mrg_z + ROWS);
+  if (threadIdx.x < rows) {
+    const int rr = threadIdx.x;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, mrg_m[w * ROWS + rr]);
-    float Z = 0.f, O = 0.f;
+    float Z = 0.f, f[NW];
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float mw = mrg_m[w * ROWS + rr];
-      const float cw = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
-      Z = fmaf(cw, mrg_l[w * ROWS + rr], Z);
-      O = fmaf(cw, mrg_acc[(w * ROWS + rr) * D + d], O);
+      f[w] = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
+      Z = fmaf(f[w], mrg_l[w * ROWS + rr], Z);
     }
-    O *= P.v_scale;
-    const size_t row = out_row(rr);
+    const size_t row = out_row(rr);  // (rows of all sequences stay in 31 bits)
+    mrg_c[rr] = make_float4(f[0], f[1], f[2], f[3]);
+    mrg_z[rr] = Z;
+    mrg_row[rr] = (int)row;
+    if (!final_out) {
+      P.max_logits[row * P.max_partitions + j] = M * 0.69314718055994530942f;
+      P.exp_sums[row * P.max_partitions + j] = Z;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * (D / 4); i += T::THREADS) {
+    const int rr = i / (D / 4), d = i % (D / 4) * 4;
+    const float4 fc = mrg_c[rr];
+    const float f[NW] = {fc.x, fc.y, fc.z, fc.w};
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float4 a = *reinterpret_cast<const float4*>(mrg_acc + (w * ROWS + rr) * T::PITCH + d);
+      O.x = fmaf(f[w], a.x, O.x);
+      O.y = fmaf(f[w], a.y, O.y);
+      O.z = fmaf(f[w], a.z, O.z);
+      O.w = fmaf(f[w], a.w, O.w);
+    }
+    O.x *= P.v_scale;
+    O.y *= P.v_scale;
+    O.z *= P.v_scale;
+    O.w *= P.v_scale;
+    const size_t row = mrg_row[rr];
     if (final_out) {
-      P.out[row * D + d] = __float2half_rn(Z > 0.f ? O / Z : 0.f);
+      const float Z = mrg_z[rr];
+      const bool any = Z > 0.f;
+      *reinterpret_cast<uint2*>(P.out + row * D + d) =
+          make_uint2(any ? pack_half2(O.x / Z, O.y / Z) : 0u, any ? pack_half2(O.z / Z, O.w / Z) : 0u);
     } else {
-      const size_t pidx = row * P.max_partitions + j;
-      P.tmp_out[pidx * D + d] = O;
-      if (d == 0) {
-        P.max_logits[pidx] = M * 0.69314718055994530942f;
-        P.exp_sums[pidx] = Z;
-      }
+      *reinterpret_cast<float4*>(P.tmp_out + (row * P.max_partitions + j) * D + d) = O;
     }
   }
 }
