@@ -31,6 +31,17 @@ enum KvType : int { kKvFp16 = 0, kKvE4m3 = 1, kKvInt4 = 2 };
 // rows: bound by the products, so keys go from global memory straight into the
 // fragments, 16 tokens a warp and step over fp16 caches, 32 over the others, the
 // next step's requested before this one's products.
+//
+// One query row of 4 (64 x 32/8 heads, 512-4096 tokens, fp16): 54 us for the
+// first grid, 5.7 TB/s, and 13 for the second, latencies of its merge and scores
+// (HBM at 22%).  112 rows (8 x 16 tokens x 28/4, 4000-16384 tokens, E4M3): 48 and
+// 40 us, the products at 70% of what mma.sync does while a full SM runs, and SMs
+// with two or three CTAs of 1024 tokens next to one another; Q's fragments are 3 of
+// a CTA's 35 us (7 when every thread wrote words where they went).  For that case:
+// two columns of keys a step, 4 to 6 CTAs an SM, or chunks of 2 or 4 row tiles: 109
+// to 401 against 97 us for both; tcgen05 products with the scores in tensor memory,
+// one softmax thread a row: 91 to 110 (fp16 142 against 104), better only from
+// 128 rows and many sequences on.
 struct WeightsParams {
   const __half* q;
   const void* k_cache;
@@ -172,27 +183,35 @@ __device__ __forceinline__ int query_eight(int i, int c) {
 }
 
 // Q's rows 16 rt .. of tiles [first, first + n) as A fragments in shared memory: [tile][k-step][lane] uint4.
+// A warp a tile, a lane its own fragments, two tiles in flight.
 template <int KV, int D>
 __device__ __forceinline__ void load_query_tiles(const WeightsParams& P, uint4* qs, int b, int g, int first, int n) {
-  uint32_t* words = reinterpret_cast<uint32_t*>(qs);
-  constexpr int U = 4;
-  for (int i0 = threadIdx.x; i0 < n * 16 * (D / 8); i0 += U * blockDim.x) {
-    uint4 u[U];
+  constexpr int U = 2, EIGHTS = D / 32, KS = D / 16;
+  const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+  for (int k0 = threadIdx.x / 32; k0 < n; k0 += U * kWeightsWarps) {
+    uint4 u[U][2][EIGHTS];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = i0 + k * blockDim.x, row = first * 16 + i / (D / 8);
-      u[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < n * 16 * (D / 8) && row < P.rows)
-        u[k] = *reinterpret_cast<const uint4*>(query_row<D>(P, b, g, row) + 8 * (i % (D / 8)));
-    }
+    for (int x = 0; x < U; ++x)
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = i0 + k * blockDim.x, row = i / (D / 8);
-      if (i >= n * 16 * (D / 8)) break;
-      const QueryWords q = query_words<KV, D>(u[k], i % (D / 8), P.q_sign);
+      for (int hf = 0; hf < 2; ++hf) {
+        const int k = k0 + x * kWeightsWarps, row = (first + k) * 16 + r + 8 * hf;
+        const __half* q = k < n && row < P.rows ? query_row<D>(P, b, g, row) : nullptr;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        words[(((row / 16 * (D / 16) + q.s + x / 2) * 32 + row % 8 * 4 + q.c) * 4) + 2 * (x % 2) + row / 8 % 2] = q.w[x];
+        for (int i = 0; i < EIGHTS; ++i)
+          u[x][hf][i] = q ? *reinterpret_cast<const uint4*>(q + 8 * query_eight<KV, D>(i, c)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int k = k0 + x * kWeightsWarps;
+      if (k >= n) break;
+#pragma unroll
+      for (int i = 0; i < EIGHTS; ++i) {
+        const int ch = query_eight<KV, D>(i, c);
+        const QueryWords lo = query_words<KV, D>(u[x][0][i], ch, P.q_sign);
+        const QueryWords hi = query_words<KV, D>(u[x][1][i], ch, P.q_sign);
+        qs[(k * KS + lo.s) * 32 + lane] = make_uint4(lo.w[0], hi.w[0], lo.w[1], hi.w[1]);
+        qs[(k * KS + lo.s + 1) * 32 + lane] = make_uint4(lo.w[2], hi.w[2], lo.w[3], hi.w[3]);
+      }
     }
   }
 }

