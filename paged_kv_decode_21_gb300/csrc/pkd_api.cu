@@ -619,7 +619,7 @@ pkd_status check_inputs(const void* q, const void* k_cache, const void* v_cache,
 
 extern "C" {
 
-int pkd_version(void) { return 1 * 10000 + 2 * 100 + 0; }
+int pkd_version(void) { return 1 * 10000 + 3 * 100 + 0; }
 
 const char* pkd_status_string(int status) {
   switch (status) {
