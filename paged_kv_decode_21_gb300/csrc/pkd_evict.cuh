@@ -35,9 +35,9 @@ enum KvType : int { kKvFp16 = 0, kKvE4m3 = 1, kKvInt4 = 2 };
 // One query row of 4 (64 x 32/8 heads, 512-4096 tokens, fp16): 54 us for the
 // first grid, 5.7 TB/s, and 13 for the second, latencies of its merge and scores
 // (HBM at 22%).  112 rows (8 x 16 tokens x 28/4, 4000-16384 tokens, E4M3): 48 and
-// 40 us, the products at 70% of what mma.sync does while a full SM runs, and SMs
-// with two or three CTAs of 1024 tokens next to one another; Q's fragments are 3 of
-// a CTA's 35 us (7 when every thread wrote words where they went).  For that case:
+// 47 us, 89 one behind the other, the products at 43% of mma.sync's peak, 70%
+// while an SM has three CTAs; Q's fragments are 3 of a CTA's 35 us (7 when every
+// thread wrote words where they went).  For that case:
 // two columns of keys a step, 4 to 6 CTAs an SM, or chunks of 2 or 4 row tiles: 109
 // to 401 against 97 us for both; tcgen05 products with the scores in tensor memory,
 // one softmax thread a row: 91 to 110 (fp16 142 against 104), better only from

@@ -128,7 +128,7 @@ __device__ __forceinline__ uint32_t int4_scale_pair(uint32_t a, uint32_t b, uint
 //
 // Bound by instructions: of a 16-token subtile's 356 (one row tile) half are the
 // codes' way into fp16 pairs, 16 the products; 0.58 a cycle and scheduler, HBM at
-// half its rate.  128 x 32/8 heads, 512-4096 tokens, 88 us; 32 x 40/8, 16K-32K, 184;
+// half its rate.  128 x 32/8 heads, 512-4096 tokens, 83 us; 32 x 40/8, 16K-32K, 180;
 // the bytes alone 50 and 135.  Four row tiles (48 x 4 tokens x 28/4): 714
 // instructions, 0.38 a cycle of the 8 warps that their accumulators leave room
 // for.  Three or five CTAs an SM for one row tile: 207 and 216 against 193 us at 16K-32K;

@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
 // ahead.
 //
 // Prompts of 28842 tokens, 40 q and 8 kv heads: 4-bit caches 153 us (a token a CTA
-// 165), 4.7 TB/s; fp16 133 as before.  20081 tokens, 32 and 8, E4M3, three axes: 93
+// 165), 4.7 TB/s; fp16 133 as before.  20082 tokens, 32 and 8, E4M3, three axes: 93
 // us, 4.9 TB/s.  Instructions (0.6 a cycle and scheduler) beside HBM at 58%: the
 // quotients that codes are rounded from, by reciprocals where both neighbours of
 // the reciprocal give the same codes, else by IEEE divisions (by divisions and a
