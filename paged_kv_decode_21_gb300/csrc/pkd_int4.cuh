@@ -37,6 +37,11 @@ __device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) 
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+__device__ __forceinline__ uint32_t hadd2_u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -638,12 +643,14 @@ struct Int4ReadParams {
   long long k_stride, v_stride;
   int num_tokens, num_seqs, num_kv_heads, num_blocks, max_blocks_per_seq;
   float k_scale, v_scale;
+  Int4Bases bases;
   int* error_word;
 };
 
-// A warp per token; a lane takes the 16 dims of a group, 8 bytes of codes and
-// one of scale, and writes 32 bytes, four such groups in flight.  28842 tokens of 8
-// heads: 35 us, 4.3 TB/s, mostly writing (one group in flight: 36).
+// A warp per token; a lane takes 8 dims at a time, a word of codes, and writes 16 bytes
+// behind its neighbour's, eight words in flight (16 dims and 32 bytes a lane, so that
+// every store met half of each sector: 35 us).  28842 tokens of 8
+// heads: 26.6 us, 5.7 TB/s, mostly writing.
 constexpr int kInt4ReadWarps = 8;
 template <int D, int BS>
 __global__ void __launch_bounds__(32 * kInt4ReadWarps) paged_kv_read_int4_kernel(const Int4ReadParams P) {
@@ -672,39 +679,43 @@ __global__ void __launch_bounds__(32 * kInt4ReadWarps) paged_kv_read_int4_kernel
   }
   const int row = (int)(at - lb * BS);
   const size_t tile0 = (size_t)block * P.num_kv_heads * TILE;
-  constexpr int U = 4;  // groups in flight a lane
-  const int items = 2 * P.num_kv_heads * GROUPS;
+  constexpr int U = 8;  // words in flight a lane
+  constexpr int WORDS = D / 8;
+  const int items = 2 * P.num_kv_heads * WORDS;
   for (int i0 = lane; i0 < items; i0 += 32 * U) {
-    uint2 x[U];
-    uint32_t sb[U];
+    uint32_t x[U], sb[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + 32 * u;
       if (i >= items) break;
-      const int d16 = i % GROUPS, hv = i / GROUPS;
+      const int word = i % WORDS, hv = i / WORDS;
       const bool is_v = hv >= P.num_kv_heads;
       const uint8_t* tile = (is_v ? P.v_cache : P.k_cache) + tile0 + (size_t)(hv - (is_v ? P.num_kv_heads : 0)) * TILE;
-      x[u] = *reinterpret_cast<const uint2*>(tile + ((d16 / 2) * BS + row) * 16 + (d16 % 2) * 8);
-      sb[u] = tile[BS * D / 2 + row * GROUPS + d16];
+      x[u] = *reinterpret_cast<const uint32_t*>(tile + ((word / 4) * BS + row) * 16 + (word % 4) * 4);
+      sb[u] = tile[BS * D / 2 + row * GROUPS + word / 2];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + 32 * u;
       if (i >= items) break;
-      const int d16 = i % GROUPS, hv = i / GROUPS;
+      const int word = i % WORDS, hv = i / WORDS;
       const bool is_v = hv >= P.num_kv_heads;
       const float step = __half2float(__ushort_as_half((unsigned short)((sb[u] & 0x7Fu) << 7))) * kInt4Unscale *
                          (is_v ? P.v_scale : P.k_scale);
-      uint32_t w[8];
+      // u - 8 of dims j and j + 4, exact in fp16; their values in fp32, rounded once
+      const uint32_t y = x[u] >> 8;
+      const uint32_t c[4] = {hadd2_u(masked_or<0x000F000Fu>(x[u], P.bases.b1024), kHalf1032),
+                             hadd2_u(masked_or<0x00F000F0u>(x[u], P.bases.b64), kHalf72),
+                             hadd2_u(masked_or<0x000F000Fu>(y, P.bases.b1024), kHalf1032),
+                             hadd2_u(masked_or<0x00F000F0u>(y, P.bases.b64), kHalf72)};
+      float2 f[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t by = ((k < 4 ? x[u].x : x[u].y) >> (8 * (k % 4))) & 0xFFu;
-        w[k] = pack_half2((float)((int)(by & 15u) - 8) * step, (float)((int)(by >> 4) - 8) * step);
-      }
-      uint4* dst = reinterpret_cast<uint4*>((is_v ? P.v_out + t * P.v_stride : P.k_out + t * P.k_stride) +
-                                            (size_t)(hv - (is_v ? P.num_kv_heads : 0)) * D + 16 * d16);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      for (int k = 0; k < 4; ++k) f[k] = __half22float2(*reinterpret_cast<const __half2*>(&c[k]));
+      __half* dst = (is_v ? P.v_out + t * P.v_stride : P.k_out + t * P.k_stride) +
+                    (size_t)(hv - (is_v ? P.num_kv_heads : 0)) * D + 8 * word;
+      *reinterpret_cast<uint4*>(dst) =
+          make_uint4(pack_half2(f[0].x * step, f[1].x * step), pack_half2(f[2].x * step, f[3].x * step),
+                     pack_half2(f[0].y * step, f[1].y * step), pack_half2(f[2].y * step, f[3].y * step));
     }
   }
 }

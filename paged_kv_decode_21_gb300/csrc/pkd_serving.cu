@@ -234,6 +234,7 @@ pkd_status paged_kv_read_int4(const void* k_cache, const void* v_cache, const in
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  p.bases = pkd::kInt4Bases;
   p.error_word = error_word;
   const unsigned grid = (unsigned)(((long long)num_tokens + pkd::kInt4ReadWarps - 1) / pkd::kInt4ReadWarps);
   auto* fn = head_dim == 128 ? (block_size == 16 ? pkd::paged_kv_read_int4_kernel<128, 16>

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
 // quotients that codes are rounded from, by reciprocals where both neighbours of
 // the reciprocal give the same codes, else by IEEE divisions (by divisions and a
 // token a CTA: 125 for the three axes, and 271 for the 4-bit ones read back too,
-// now 194).
+// now 186).
 constexpr int kRopeRun = 4;
 template <int KVB, bool PAIRS, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_run_kernel(const RopeAppendParams P) {
