@@ -354,26 +354,40 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
 // The same for many tokens, kRopeRun of them a CTA: their sequences, positions,
 // blocks and cosines are looked up side by side first and kept in shared memory,
 // so that those chains of dependent loads are paid once a run, not once a token;
-// then the CTA walks the heads of all of them, the next head's data requested
-// ahead.
+// then the CTA walks the heads of all of them.  Where codes are written, a thread's
+// heads come by asynchronous copies into places of its own, three ahead of the
+// one it turns; fp16 rows, which need no more instructions than the copies leave
+// room for, come one ahead in registers.
 //
-// Prompts of 28842 tokens, 40 q and 8 kv heads: 4-bit caches 153 us (a token a CTA
-// 165), 4.7 TB/s; fp16 133 as before.  20082 tokens, 32 and 8, E4M3, three axes: 93
-// us, 4.9 TB/s.  Instructions (0.6 a cycle and scheduler) beside HBM at 58%: the
-// quotients that codes are rounded from, by reciprocals where both neighbours of
-// the reciprocal give the same codes, else by IEEE divisions (by divisions and a
-// token a CTA: 125 for the three axes, and 271 for the 4-bit ones read back too,
-// now 186).
+// Prompts of 28842 tokens, 40 q and 8 kv heads, three axes: 4-bit caches 137 us, 5.4
+// TB/s (one ahead in registers 156); 20082 tokens, 32 and 8, E4M3, three axes: 82
+// us, 5.5 TB/s (97).  fp16, 28842 tokens, one axis: 134 us, 6.2 TB/s (with the
+// copies 172).  Two ahead 83 and 138, five 91 and 153; runs of eight tokens 91 and
+// 153, seven CTAs an SM 84 and 135, ten 142 and 287.  The quotients that codes are
+// rounded from go by reciprocals where both neighbours of the reciprocal give the
+// same codes, else by IEEE divisions (all by divisions, a token a CTA: 125 for E4M3).
 constexpr int kRopeRun = 4;
+constexpr int kRopeAhead = 4;  // places a thread has for heads on their way
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 template <int KVB, bool PAIRS, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_run_kernel(const RopeAppendParams P) {
   static_assert(kRopeRun <= kRopeThreads / 32, "a warp looks up a token");
+  constexpr bool RING = KVB != 2;
   __shared__ __align__(16) float turn[kRopeRun][2 * kMaxRopePairs];  // cosines, then sines
   __shared__ int block_of[kRopeRun], row_of[kRopeRun], pos_of[kRopeRun];
   const RopeLane lane = rope_lane<PAIRS>(P);
   const int R = P.rotary_dim, heads = P.num_q_heads + 2 * P.num_kv_heads;
   const int first = blockIdx.x * kRopeRun, n = min(kRopeRun, P.num_tokens - first);
-  int k = 0, h = lane.slot;  // token of the run, head
+  int k = 0, h = lane.slot;    // token of the run, head
+  int ka = 0, ha = lane.slot;  // and those to request next
   const bool mine = lane.slot < lane.slots;
   auto settle = [&](int& k, int& h) {
     while (h >= heads && k < n) {
@@ -382,12 +396,30 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
     }
   };
   settle(k, h);
-  uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
-  if (mine && k < n) {
-    const __half* s = rope_source(P, first + k, h);
-    u0 = *reinterpret_cast<const uint4*>(s + lane.e0);
-    u1 = *reinterpret_cast<const uint4*>(s + lane.e1);
-  }
+  settle(ka, ha);
+  __shared__ uint4 ring[RING ? kRopeAhead : 1][2][kRopeThreads];  // a thread's own places
+  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;                  // without a ring: the next head
+  uint32_t slot = 0;  // the next request's
+  auto request = [&]() {
+    if (mine && ka < n) {
+      const __half* s = rope_source(P, first + ka, ha);
+      if constexpr (RING) {
+        cp_async_16(&ring[slot][0][threadIdx.x], s + lane.e0);
+        cp_async_16(&ring[slot][1][threadIdx.x], s + lane.e1);
+      } else {
+        n0 = *reinterpret_cast<const uint4*>(s + lane.e0);
+        n1 = *reinterpret_cast<const uint4*>(s + lane.e1);
+      }
+      ha += lane.slots;
+      settle(ka, ha);
+    }
+    if constexpr (RING) {
+      cp_async_commit();
+      slot = slot + 1 == kRopeAhead ? 0 : slot + 1;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i + 1 < (RING ? kRopeAhead : 2); ++i) request();
   const int w = threadIdx.x / 32;
   if (w < n) {
     const int t = first + w;
@@ -446,19 +478,20 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
     if (threadIdx.x == 0) record_error(P.error_word, kErrBadPosition);
   }
   if (!AXES) __syncthreads();
-  if (!mine) return;
+  if (!mine) return;  // (nothing of its own in flight)
   const E4m3Scale sk8 = e4m3_scale(P.k_scale), sv8 = e4m3_scale(P.v_scale);
   float cs[8], sn[8];
   int turned_for = -1;
+  uint32_t at = 0;
   while (k < n) {
-    int kn = k, hn = h + lane.slots;
-    settle(kn, hn);
-    uint4 n0 = u0, n1 = u1;
-    if (kn < n) {
-      const __half* s = rope_source(P, first + kn, hn);
-      n0 = *reinterpret_cast<const uint4*>(s + lane.e0);
-      n1 = *reinterpret_cast<const uint4*>(s + lane.e1);
+    uint4 u0 = n0, u1 = n1;
+    if constexpr (RING) {
+      cp_async_wait<kRopeAhead - 2>();
+      u0 = ring[at][0][threadIdx.x];
+      u1 = ring[at][1][threadIdx.x];
+      at = at + 1 == kRopeAhead ? 0 : at + 1;
     }
+    request();
     if (lane.rot && k != turned_for) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -472,10 +505,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
     if (block_of[k] >= 0 && row_of[k] >= 0)
       rope_head<KVB, PAIRS>(P, lane, cs, sn, u0, u1, h, first + k, (size_t)block_of[k] * P.num_kv_heads, row_of[k],
                             sk8, sv8);
-    k = kn;
-    h = hn;
-    u0 = n0;
-    u1 = n1;
+    h += lane.slots;
+    settle(k, h);
   }
 }
 
