@@ -92,11 +92,14 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   axes = axes && rotary_dim > 0;
   // runs of tokens where there are enough for four such CTAs an SM: fewer tokens are
   // latency, 7.1 us for 128 of them a CTA each
-  int sms = 0, dev = 0;
-  if (pkd::failed(cudaGetDevice(&dev)) ||
-      pkd::failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
-    sms = 148;
-  const bool run = num_tokens >= kRopeRunTokens * sms;
+  bool run = num_tokens >= kRopeRunTokens * 64;  // (fewer than sm_103a's SMs: a step's call asks nothing)
+  if (run) {
+    int sms = 0, dev = 0;
+    if (pkd::failed(cudaGetDevice(&dev)) ||
+        pkd::failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
+      sms = 148;
+    run = num_tokens >= kRopeRunTokens * sms;
+  }
 #define PKD_APPEND(FN_, KVB_)                                                      \
   (interleaved ? (axes ? pkd::FN_<KVB_, true, true> : pkd::FN_<KVB_, true, false>) \
                : (axes ? pkd::FN_<KVB_, false, true> : pkd::FN_<KVB_, false, false>))
