@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_decode_reduce_ke
   const int L = context_lens[b];
   const int PS = tail_order ? tail_half_partition(L) : partition_size;
   // partitions the first kernel wrote (none past its grid)
-  const int np = min((L + PS - 1) / PS, max_partitions);
+  const int np = partitions_of(L, PS, max_partitions);
   // min_partitions_to_merge > 0: those sequences were written by the
   // partition kernel itself; 0 merges every sequence (empty ones get zeros)
   if (min_partitions_to_merge > 0 && np <= min_partitions_to_merge) return;
@@ -165,8 +165,7 @@ __global__ void __launch_bounds__(32 * kReduceRowsPerCta) paged_merge_kernel(con
         const int y = find_segment(P.group_starts, P.num_groups, b);
         if (y < P.num_groups && P.group_starts[y] <= b) len = P.shared_lens[y];
       }
-      len = max(len, 0);
-      n[1] = min((len + P.shared.part - 1) / P.shared.part, P.shared.np);
+      n[1] = partitions_of(len, P.shared.part, P.shared.np);
     }
     if (P.own.o && own_tokens > 0) n[0] = (int)min((own_tokens + P.own.part - 1) / P.own.part, (long long)P.own.np);
   }
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(128) piece_order_kernel(const int32_t* __restr
   int lmax = 0;
   for (int i = threadIdx.x; i < 4 * n4; i += blockDim.x) {
     const int L = i < num_seqs ? max(context_lens[i], 0) : 0;
-    const int n = min((L + PS - 1) / PS, NP);
+    const int n = partitions_of(L, PS, NP);
     s_np[i] = n;
     s_last[i] = n > 0 ? L - (n - 1) * PS : 0;
     lmax = max(lmax, L);
@@ -455,7 +454,7 @@ __global__ void __launch_bounds__(128) piece_order_kernel(const int32_t* __restr
   const int n_b = s_np[b], last_b = s_last[b];
   int full = 0, full_before = 0, lasts = 0, last_rank = 0, empty_before = 0;
   int half_long = 0;  // tail split: sequences with at least half the longest one's tokens
-  const int lhalf = (s_lmax + 1) / 2;
+  const int lhalf = half_up(s_lmax);
   auto count = [&](int n, int li, int i) {
     const int f = n > 0 ? n - 1 : 0;
     const bool before = i < b;

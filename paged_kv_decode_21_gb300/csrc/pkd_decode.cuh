@@ -39,6 +39,7 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 #include "pkd_ptx.cuh"
+#include "pkd_split.h"
 
 namespace pkd {
 
@@ -151,9 +152,6 @@ __device__ __forceinline__ bool find_group_chunk(const int32_t* group_starts, co
 constexpr int kPieceWhole = 0;       // the whole sequence, written to out
 constexpr int kPieceFirstHalf = 1;   // tokens [0, tail_half_partition(L)), a partial
 constexpr int kPieceSecondHalf = 2;  // the rest, a partial
-// The partition of such a split sequence of L tokens: half of it, rounded up
-// to whole 64-token tiles (so a sequence of at most 64 tokens stays whole).
-__host__ __device__ __forceinline__ int tail_half_partition(int L) { return ((L + 1) / 2 + 63) / 64 * 64; }
 
 template <int D, int BS, int G, int VARIANT>
 struct DecodeTraits {
@@ -532,7 +530,7 @@ __global__ void __launch_bounds__(DecodeTraits<D, BS, G, VARIANT>::THREADS,
   const int PS = P.partition_size;
   // partitions of the sequence inside the grid (a length past max_context_len
   // is read up to the grid's last partition)
-  const int np_b = min((L + PS - 1) / PS, np_grid);
+  const int np_b = partitions_of(L, PS, np_grid);
   const bool final_out = (P.mode == 0) && np_b <= 1;
   const int h0 = g * G;
 

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(MmaTraits<D, BS, G, QC, KVB, CPS>::THREADS,
   }
   const int nq = min(QC, QL - jq0);      // the CTA's query tokens (>= 1)
   const int PS = P.partition_size;
-  const int np_b = min((L + PS - 1) / PS, np_grid);  // partitions inside the grid
+  const int np_b = partitions_of(L, PS, np_grid);  // partitions inside the grid
   const bool final_out = (P.mode == 0) && np_b <= 1;
   const int h0 = g * G;
   const int Hq = P.num_q_heads;

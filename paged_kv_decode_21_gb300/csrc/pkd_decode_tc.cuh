@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(TcTraits<BS, KVB, HD>::THREADS, TcTraits<BS, K
   const int nq = min(T::ROWS / G, QL - jq0);  // its query tokens (>= 1)
   const int rows = G * nq;                    // tile rows in use
   const int PS = half ? tail_half_partition(L) : P.partition_size;
-  const int np_b = min((L + PS - 1) / PS, np_grid);
+  const int np_b = partitions_of(L, PS, np_grid);
   const bool final_out = (P.mode == 0) && np_b <= 1;
   const int Hq = P.num_q_heads;
   auto out_row = [&](int rr) { return ((size_t)b * QL + jq0 + rr / G) * Hq + g * G + rr % G; };

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(WsTraits<D, BS, G>::THREADS, WsTraits<D, BS, G
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int L = row_clamped_len<BS>(P, b);
   const int PS = P.partition_size;
-  const int np_b = min((L + PS - 1) / PS, np_grid);  // partitions inside the grid
+  const int np_b = partitions_of(L, PS, np_grid);  // partitions inside the grid
   const bool final_out = (P.mode == 0) && np_b <= 1;
   const int h0 = g * G;
   if (L <= 0) {
