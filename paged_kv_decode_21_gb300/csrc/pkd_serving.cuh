@@ -58,8 +58,10 @@ struct RopeAppendParams {
 // and leaves the code in the low bits.  The quotient by a reciprocal is within
 // 2^-20 of the exact one where it is below 8 and the IEEE quotient within 2^-21,
 // so they round alike unless the first is nearer than 2e-5 to halfway: then IEEE
-// division decides (one value in 25000), as it does for scales that are subnormal
-// or saturated (`edge`), which alone let quotients pass 7.5.
+// division decides (one value in 25000), as it does where `edge` says so: for scales
+// that are subnormal or saturated, which alone let quotients pass 7.5, and for cache
+// scales at the ends of fp32's range, where a step's reciprocal is infinite or
+// subnormal.
 __device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float step, bool edge) {
   if (!(step > 0.f)) return 0x88888888u;
   constexpr float kMagic = 12582912.f + 8.f;
@@ -220,6 +222,8 @@ __device__ __forceinline__ void rope_head(const RopeAppendParams& P, const RopeL
           uint8_t* tile = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) +
                           (tile0 + g) * ((size_t)BS * D * 9 / 16);
           uint8_t* scales = tile + (size_t)BS * D / 2 + in * units;
+          // (a scale byte's value lies in 2^-9 .. 448, so steps and reciprocals of the others are normal)
+          const bool far = !(sc > 0x1p-110f && sc < 0x1p110f);
           auto codes = [&](int e) { return reinterpret_cast<uint32_t*>(tile + ((e / 32) * BS + in) * 16 + e % 32 / 2); };
           float ax = absmax8(x), ay = absmax8(y), sx, sy;
           uint32_t bx, by;
@@ -239,8 +243,8 @@ __device__ __forceinline__ void rope_head(const RopeAppendParams& P, const RopeL
             sy = sx;
             scales[e0 / 16] = (uint8_t)bx;
           }
-          *codes(e0) = pack8_int4(x, sx, bx < 8 || bx == 0x7E);
-          *codes(e1) = pack8_int4(y, sy, by < 8 || by == 0x7E);
+          *codes(e0) = pack8_int4(x, sx, far || bx < 8 || bx == 0x7E);
+          *codes(e1) = pack8_int4(y, sy, far || by < 8 || by == 0x7E);
         } else if constexpr (F8) {
           uint8_t* o = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + row;
           *reinterpret_cast<uint2*>(o + e0) = pack8_e4m3(x, is_v ? sv8 : sk8);
