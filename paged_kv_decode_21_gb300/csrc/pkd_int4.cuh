@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(Int4Traits<D, BS, NT>::THREADS, Int4Traits<D, 
     const size_t row = mrg_row[rr];
     if (final_out) {
       const float Z = mrg_z[rr];
-      const bool any = Z > 0.f;
+      const bool any = Z != 0.f;  // Z = 0: the query saw no token; a query that is not a number has a result that is none
       *reinterpret_cast<uint2*>(P.out + row * D + d) =
           make_uint2(any ? pack_half2(O.x / Z, O.y / Z) : 0u, any ? pack_half2(O.z / Z, O.w / Z) : 0u);
     } else {
