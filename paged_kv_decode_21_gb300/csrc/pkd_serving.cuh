@@ -370,6 +370,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
 // 153, seven CTAs an SM 84 and 135, ten 142 and 287.  The quotients that codes are
 // rounded from go by reciprocals where both neighbours of the reciprocal give the
 // same codes, else by IEEE divisions (all by divisions, a token a CTA: 125 for E4M3).
+// Whether a position that token t's pairs first, first + step .. go by lies outside the table.
+__device__ __forceinline__ bool off_table(const RopeAppendParams& P, int t, int first, int step) {
+  bool off = false;
+  for (int i = first; i < P.rotary_dim / 2; i += step) {
+    const int axis = P.pair_axes[i];
+    const int p = axis >= 0 && axis < P.num_axes ? P.positions[(size_t)axis * P.num_tokens + t] : -1;
+    off |= p < 0 || p >= P.max_positions;
+  }
+  return off;
+}
 constexpr int kRopeRun = 4;
 constexpr int kRopeAhead = 4;  // places a thread has for heads on their way
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
@@ -452,6 +462,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
           pos = (int)p;
       }
       if (err) block = -1;
+      if constexpr (AXES) {
+        // a token without a block is looked at here, as it is skipped below
+        if (err && __any_sync(0xffffffffu, off_table(P, t, threadIdx.x % 32, 32))) err |= kErrBadPosition;
+      }
     }
     if (threadIdx.x % 32 == 0) {
       if (err) record_error(P.error_word, err);
