@@ -882,6 +882,8 @@ pkd_status paged_kv_read_int4(const void* k_cache, const void* v_cache, const in
  * the new tokens, as in paged_decode_attention_multi).
  *   workspace      paged_decode_int4_workspace_size(...) bytes, 256-byte aligned
  *                  (NULL where that is 0)
+ *   scale, k_scale, v_scale  finite, the last two > 0; 370 * scale * k_scale and
+ *                  256 * v_scale within fp32's range too (PKD_ERR_SHAPE)
  * Codes times scales are exact in fp16, so the products see the cache's own
  * values; the softmax weights are rounded to fp16 for the second product as on
  * the other tensor-core paths.
@@ -922,6 +924,7 @@ typedef enum {
  *   decay          finite, in [0, 1]: 1 gathers, 0 keeps this call's weights
  *                  alone (what was there is not read)
  *   kv_type        pkd_kv_type of k_cache; k_scale finite, > 0 (1 for fp16)
+ *   scale          finite; 370 * scale * k_scale within fp32's range
  *   q              device fp16 [num_seqs][q_len][num_q_heads][head_dim]
  *   workspace      paged_kv_attention_weights_workspace_size(...) bytes,
  *                  256-byte aligned (row statistics, and the scores of few rows)

@@ -1654,6 +1654,9 @@ pkd_status paged_decode_attention_int4(const void* q, const void* k_cache, const
   if (st != PKD_OK) return st;
   if (!std::isfinite(scale)) return PKD_ERR_SHAPE;
   if (!(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f)) return PKD_ERR_SHAPE;
+  // (256: the kernel's scales are 2^-8 of the cache's; past fp32's range nothing would be left of the scores or the result)
+  if (!std::isfinite(scale * (k_scale * 256.f) * 1.4426950408889634f) || !std::isfinite(v_scale * 256.f))
+    return PKD_ERR_SHAPE;
   if (num_seqs == 0) return PKD_OK;
   st = check_inputs(q, k_cache, v_cache, block_tables, context_lens);
   if (st != PKD_OK) return st;
@@ -1662,7 +1665,7 @@ pkd_status paged_decode_attention_int4(const void* q, const void* k_cache, const
   const PartPlan plan = plan_int4(s, q_len, partition_size);
   if (plan.grid > 0x7fffffffLL) return PKD_ERR_SHAPE;
   pkd::DecodeParams p = base_params(s, q, k_cache, v_cache, q_len, scale, 1, k_scale * 256.f, v_scale * 256.f,
-                                    error_word);  // 256: the kernel's scales are 2^-8 of the cache's
+                                    error_word);
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.max_blocks_per_seq = max_blocks_per_seq;

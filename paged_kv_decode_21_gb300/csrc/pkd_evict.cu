@@ -457,6 +457,8 @@ pkd_status paged_kv_attention_weights(const void* q, const void* k_cache, const 
   if (!std::isfinite(scale) || !std::isfinite(k_scale) || k_scale <= 0.f || !(decay >= 0.f && decay <= 1.f))
     return PKD_ERR_SHAPE;
   if (kv_type < PKD_KV_FP16 || kv_type > PKD_KV_INT4) return PKD_ERR_SHAPE;
+  const float s = scale * k_scale * 1.4426950408889634f * (kv_type == PKD_KV_INT4 ? kInt4Unscale : 1.f);
+  if (!std::isfinite(s)) return PKD_ERR_SHAPE;
   if (num_seqs == 0 || max_context_len == 0) return PKD_OK;
   if (!q || !k_cache || !block_tables || !context_lens || !weights) return PKD_ERR_NULL;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(weights, 16) || !aligned(block_tables, 4) ||
@@ -489,7 +491,6 @@ pkd_status paged_kv_attention_weights(const void* q, const void* k_cache, const 
   p.part = plan.part;
   p.np = plan.np;
   p.row_chunks = plan.row_chunks;
-  const float s = scale * k_scale * 1.4426950408889634f * (kv_type == PKD_KV_INT4 ? kInt4Unscale : 1.f);
   p.q_sign = s < 0.f ? 0x80008000u : 0u;
   // (a scale of 0, equal weights: one too small to tell, so that -inf times it stays -inf)
   p.scale_log2 = std::max(std::fabs(s), 1e-30f);
