@@ -366,9 +366,21 @@ pkd_status check_weights(int num_seqs, int q_len, int num_q_heads, int num_kv_he
 
 // The split does not depend on the cache's type, so that one workspace size
 // serves a shape: partitions of 128 to 4096 tokens that make four CTAs an SM of
-// the second grid's shape (with twice or three times as many the 112-row case
-// takes 91 us instead of 89, with half as many about 140); sixteen where rows are few,
-// as those read and wait more.
+// the second grid, whose CTAs take every row of their tokens (the first has one for
+// every chunk of rows besides; counted by those, 448 rows of 32 (b, g) with 4000-16384
+// tokens made one second-grid CTA for every SM: 702 us instead of 282, 65536 rows of 2
+// with 8192 tokens 109 ms instead of 10).  Twice or three times as many CTAs: 112 rows
+// 91 us instead of 89, 448 rows 291 instead of 282; half as many about 140 and 433.
+// (128 tokens only where the first grid stays within that too: 256 rows of 8 (b, g) with
+// 8192 tokens 74 us, with 256 tokens 56, as every CTA loads all the queries.)
+// Sixteen CTAs an SM where rows are few, as those read and wait more.
+//
+// Scores are kept for up to 16 rows, whatever a key weighs: 8 bytes a row and
+// token written and read against reading the keys again, 72 bytes of 128 dims in 4
+// bits.  Past 9 rows the scores are the more bytes, but the second reading is bound
+// by its products, not by bytes.  64 x 512-4096 tokens x 8 heads, scores against keys
+// again: 4 bits, 4 rows 48 and 129 us, 16 rows 70 and 130 (64 dims 56 and 107);
+// E4M3 68 and 119, fp16 87 and 160; 16 x 16K-32K tokens, 16 rows, 4 bits 161 and 259.
 WeightsPlan plan_weights(int num_seqs, int q_len, int num_q_heads, int num_kv_heads, int max_context_len) {
   WeightsPlan p{};
   p.rows = (long long)q_len * (num_q_heads / num_kv_heads);
@@ -377,7 +389,8 @@ WeightsPlan plan_weights(int num_seqs, int q_len, int num_q_heads, int num_kv_he
   const long long bg = (long long)num_seqs * num_kv_heads;
   long long part = 128;
   const long long want = (p.rows <= kFinishMaxRows ? 16LL : 4LL) * sms();  // CTAs
-  while (part < 4096 && bg * p.row_chunks * ((max_context_len + part - 1) / part) > want) part *= 2;
+  auto ctas = [&](long long each) { return each * ((max_context_len + part - 1) / part); };
+  while (part < 4096 && (ctas(bg) > want || (part < 256 && ctas(bg * p.row_chunks) > want))) part *= 2;
   p.part = (int)part;
   p.np = (int)std::max(1LL, (max_context_len + part - 1) / part);
   p.scores = p.rows <= kFinishMaxRows;
