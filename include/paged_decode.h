@@ -957,8 +957,9 @@ size_t paged_kv_attention_weights_workspace_size(int num_seqs, int q_len, int nu
  *   max_context_len  host upper bound of context_lens, at most 2^30
  *   max_kept       in [1, 2^30]; sink_tokens + recent_tokens <= max_kept;
  *                  block_size any positive size
- * Tokens of a block outside the pool are reported (PKD_DEVERR_BAD_BLOCK) and
- * come last.
+ * Where weights decide (L > max_kept), tokens of a block outside the pool are
+ * reported (PKD_DEVERR_BAD_BLOCK) and come last; the first and last tokens, and all
+ * of a context that is kept whole, are listed whatever their blocks.
  */
 pkd_status paged_kv_token_select(const float* weights, const int32_t* block_tables, const int32_t* context_lens,
                                  int32_t* kept, int32_t* kept_lens, int num_seqs, int num_kv_heads, int block_size,

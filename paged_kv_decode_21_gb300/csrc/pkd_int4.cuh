@@ -109,36 +109,7 @@ __device__ __forceinline__ uint32_t int4_scale_pair(uint32_t a, uint32_t b, uint
   return prmt(a, b, sel) * 128u;
 }
 
-// ---------------------------------------------------------------- decode
-// The split of the work, the online softmax, the merge of the warps and the
-// meaning of rows are those of paged_decode_mma_kernel; here a warp's ring
-// holds whole (block, kv head) tiles, brought by two plain bulk copies.
-//
-// Both products have the cache as their A operand (16 rows: tokens, or dims) and
-// the queries as their B operand (8 columns): S^T = K Q^T, O^T = V^T P^T, so that
-// eight query rows and less waste no half of a tile.  (With Q as A, of 16 rows,
-// single queries took twice the products for S, and moves that put zeros into
-// the operands' registers: 386 instructions per 16 tokens instead of 356.)
-// Fragments (c = lane % 4, r = lane / 4), for a slab of 32 dims:
-//   K  an ldmatrix of 8 tokens x 16 bytes gives lane (r, c) the codes of dims 8c
-//      .. 8c + 7 of token r: two k-steps' A operands, dims (8c + j, 8c + j + 4)
-//      in the halves.  Q's B fragments follow that order of dims.
-//   S^T  lane (r, c) receives tokens r and r + 8 of query rows 2c and 2c + 1;
-//      packed in pairs of rows and transposed in 8 x 8 matrices (movmatrix),
-//      the weights are P^T's B fragments.
-//   V  the transposed ldmatrix gives lane (r, c) dims 4r .. 4r + 3 of tokens 2c
-//      and 2c + 1, one token a half: rows r and r + 8 of two m-tiles of V^T.
-// Query rows are the group's heads times up to `q_chunk` query tokens, NT tiles
-// of 8 of them: 1, 2 or 4.  With 4 the Q fragments stay in shared memory.
-//
-// Bound by instructions: of a 16-token subtile's 356 (one row tile) half are the
-// codes' way into fp16 pairs, 16 the products; 0.58 a cycle and scheduler, HBM at
-// half its rate.  128 x 32/8 heads, 512-4096 tokens, 83 us; 32 x 40/8, 16K-32K, 180;
-// the bytes alone 50 and 135.  Four row tiles (48 x 4 tokens x 28/4): 714
-// instructions, 0.38 a cycle of the 8 warps that their accumulators leave room
-// for.  Three or five CTAs an SM for one row tile: 207 and 216 against 193 us at 16K-32K;
-// chunks of two row tiles for 28 rows: +6%; the next scores beside a subtile's
-// P V: no change; K scales spread by permutations, or shifts as multiplications: +5%.
+// ---------------------------------------------------------------- instructions
 // d = (zero ? 0 : d) + A . B for one m16n8k16 tile; `zero` known when compiled.
 __device__ __forceinline__ void mma_16816_from(float (&d)[4], bool zero, uint32_t a0, uint32_t a1, uint32_t a2,
                                                uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -175,6 +146,36 @@ __device__ __forceinline__ uint32_t transposed_8x8(uint32_t x) {
   return y;
 }
 
+// ---------------------------------------------------------------- decode
+// The split of the work, the online softmax, the merge of the warps and the
+// meaning of rows are those of paged_decode_mma_kernel; here a warp's ring
+// holds whole (block, kv head) tiles, brought by two plain bulk copies.
+//
+// Both products have the cache as their A operand (16 rows: tokens, or dims) and
+// the queries as their B operand (8 columns): S^T = K Q^T, O^T = V^T P^T, so that
+// eight query rows and less waste no half of a tile.  (With Q as A, of 16 rows,
+// single queries took twice the products for S, and moves that put zeros into
+// the operands' registers: 386 instructions per 16 tokens instead of 356.)
+// Fragments (c = lane % 4, r = lane / 4), for a slab of 32 dims:
+//   K  an ldmatrix of 8 tokens x 16 bytes gives lane (r, c) the codes of dims 8c
+//      .. 8c + 7 of token r: two k-steps' A operands, dims (8c + j, 8c + j + 4)
+//      in the halves.  Q's B fragments follow that order of dims.
+//   S^T  lane (r, c) receives tokens r and r + 8 of query rows 2c and 2c + 1;
+//      packed in pairs of rows and transposed in 8 x 8 matrices (movmatrix),
+//      the weights are P^T's B fragments.
+//   V  the transposed ldmatrix gives lane (r, c) dims 4r .. 4r + 3 of tokens 2c
+//      and 2c + 1, one token a half: rows r and r + 8 of two m-tiles of V^T.
+// Query rows are the group's heads times up to `q_chunk` query tokens, NT tiles
+// of 8 of them: 1, 2 or 4.  With 4 the Q fragments stay in shared memory.
+//
+// Bound by instructions: of a 16-token subtile's 356 (one row tile) half are the
+// codes' way into fp16 pairs, 16 the products; 0.58 a cycle and scheduler, HBM at
+// half its rate.  128 x 32/8 heads, 512-4096 tokens, 83 us; 32 x 40/8, 16K-32K, 180;
+// the bytes alone 50 and 135.  Four row tiles (48 x 4 tokens x 28/4): 714
+// instructions, 0.38 a cycle of the 8 warps that their accumulators leave room
+// for.  Three or five CTAs an SM for one row tile: 207 and 216 against 193 us at 16K-32K;
+// chunks of two row tiles for 28 rows: +6%; the next scores beside a subtile's
+// P V: no change; K scales spread by permutations, or shifts as multiplications: +5%.
 struct Int4Params {
   DecodeParams d;
   int group, q_chunk;

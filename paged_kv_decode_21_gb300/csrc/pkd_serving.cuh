@@ -179,82 +179,82 @@ __device__ __forceinline__ void rope_head(const RopeAppendParams& P, const RopeL
   constexpr bool F8 = KVB == 1, I4 = KVB == 0;
   const int D = P.head_dim, units = D / 16, c = lane.c, e0 = lane.e0, e1 = lane.e1;
   const bool rot = lane.rot;
-      const bool is_q = h < P.num_q_heads, is_v = h >= P.num_q_heads + P.num_kv_heads;
-      const bool turn = rot && !is_v;
-      float x[8], y[8];
-      if (turn || (KVB != 2 && !is_q)) {
-        unpack8(u0, x);
-        unpack8(u1, y);
-      }
-      if (turn) {
-        // y_a = a cos - d sin, y_b = d cos + a sin
-        auto turned = [](float& a, float& d, float co, float si) {
-          const float a0 = a, d0 = d;
-          if constexpr (I4) {
-            a = __fsub_rn(__fmul_rn(a0, co), __fmul_rn(d0, si));
-            d = __fadd_rn(__fmul_rn(d0, co), __fmul_rn(a0, si));
-          } else {
-            a = fmaf(a0, co, -d0 * si);
-            d = fmaf(d0, co, a0 * si);
-          }
-        };
-        if constexpr (PAIRS) {
-  #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            turned(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
-            turned(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
-          }
-        } else {
-  #pragma unroll
-          for (int i = 0; i < 8; ++i) turned(x[i], y[i], cs[i], sn[i]);
-        }
-      }
-      if (is_q) {
-        __half* o = P.q_out + t * P.q_out_stride + (long long)h * D;
-        *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
-        *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+  const bool is_q = h < P.num_q_heads, is_v = h >= P.num_q_heads + P.num_kv_heads;
+  const bool turn = rot && !is_v;
+  float x[8], y[8];
+  if (turn || (KVB != 2 && !is_q)) {
+    unpack8(u0, x);
+    unpack8(u1, y);
+  }
+  if (turn) {
+    // y_a = a cos - d sin, y_b = d cos + a sin
+    auto turned = [](float& a, float& d, float co, float si) {
+      const float a0 = a, d0 = d;
+      if constexpr (I4) {
+        a = __fsub_rn(__fmul_rn(a0, co), __fmul_rn(d0, si));
+        d = __fadd_rn(__fmul_rn(d0, co), __fmul_rn(a0, si));
       } else {
-        const int g = h - P.num_q_heads - (is_v ? P.num_kv_heads : 0);
-        const size_t row = ((tile0 + g) * P.block_size + in) * D;
-        if constexpr (I4) {
-          const float sc = is_v ? P.v_scale : P.k_scale;
-          const int BS = P.block_size;
-          uint8_t* tile = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) +
-                          (tile0 + g) * ((size_t)BS * D * 9 / 16);
-          uint8_t* scales = tile + (size_t)BS * D / 2 + in * units;
-          // (a scale byte's value lies in 2^-9 .. 448, so steps and reciprocals of the others are normal)
-          const bool far = !(sc > 0x1p-110f && sc < 0x1p110f);
-          auto codes = [&](int e) { return reinterpret_cast<uint32_t*>(tile + ((e / 32) * BS + in) * 16 + e % 32 / 2); };
-          float ax = absmax8(x), ay = absmax8(y), sx, sy;
-          uint32_t bx, by;
-          if (rot && !PAIRS) {
-            // the other halves of both groups are the neighbouring lane's
-            const unsigned both = 3u << (threadIdx.x & 30);
-            ax = fmaxf(ax, __shfl_xor_sync(both, ax, 1));
-            ay = fmaxf(ay, __shfl_xor_sync(both, ay, 1));
-            bx = int4_scale_byte(ax, sc, sx);
-            by = int4_scale_byte(ay, sc, sy);
-            if (c % 2 == 0) {
-              scales[e0 / 16] = (uint8_t)bx;
-              scales[e1 / 16] = (uint8_t)by;
-            }
-          } else {
-            bx = by = int4_scale_byte(fmaxf(ax, ay), sc, sx);
-            sy = sx;
-            scales[e0 / 16] = (uint8_t)bx;
-          }
-          *codes(e0) = pack8_int4(x, sx, far || bx < 8 || bx == 0x7E);
-          *codes(e1) = pack8_int4(y, sy, far || by < 8 || by == 0x7E);
-        } else if constexpr (F8) {
-          uint8_t* o = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + row;
-          *reinterpret_cast<uint2*>(o + e0) = pack8_e4m3(x, is_v ? sv8 : sk8);
-          *reinterpret_cast<uint2*>(o + e1) = pack8_e4m3(y, is_v ? sv8 : sk8);
-        } else {
-          __half* o = static_cast<__half*>(is_v ? P.v_cache : P.k_cache) + row;
-          *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
-          *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
-        }
+        a = fmaf(a0, co, -d0 * si);
+        d = fmaf(d0, co, a0 * si);
       }
+    };
+    if constexpr (PAIRS) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        turned(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+        turned(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turned(x[i], y[i], cs[i], sn[i]);
+    }
+  }
+  if (is_q) {
+    __half* o = P.q_out + t * P.q_out_stride + (long long)h * D;
+    *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
+    *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+  } else {
+    const int g = h - P.num_q_heads - (is_v ? P.num_kv_heads : 0);
+    const size_t row = ((tile0 + g) * P.block_size + in) * D;
+    if constexpr (I4) {
+      const float sc = is_v ? P.v_scale : P.k_scale;
+      const int BS = P.block_size;
+      uint8_t* tile = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) +
+                      (tile0 + g) * ((size_t)BS * D * 9 / 16);
+      uint8_t* scales = tile + (size_t)BS * D / 2 + in * units;
+      // (a scale byte's value lies in 2^-9 .. 448, so steps and reciprocals of the others are normal)
+      const bool far = !(sc > 0x1p-110f && sc < 0x1p110f);
+      auto codes = [&](int e) { return reinterpret_cast<uint32_t*>(tile + ((e / 32) * BS + in) * 16 + e % 32 / 2); };
+      float ax = absmax8(x), ay = absmax8(y), sx, sy;
+      uint32_t bx, by;
+      if (rot && !PAIRS) {
+        // the other halves of both groups are the neighbouring lane's
+        const unsigned both = 3u << (threadIdx.x & 30);
+        ax = fmaxf(ax, __shfl_xor_sync(both, ax, 1));
+        ay = fmaxf(ay, __shfl_xor_sync(both, ay, 1));
+        bx = int4_scale_byte(ax, sc, sx);
+        by = int4_scale_byte(ay, sc, sy);
+        if (c % 2 == 0) {
+          scales[e0 / 16] = (uint8_t)bx;
+          scales[e1 / 16] = (uint8_t)by;
+        }
+      } else {
+        bx = by = int4_scale_byte(fmaxf(ax, ay), sc, sx);
+        sy = sx;
+        scales[e0 / 16] = (uint8_t)bx;
+      }
+      *codes(e0) = pack8_int4(x, sx, far || bx < 8 || bx == 0x7E);
+      *codes(e1) = pack8_int4(y, sy, far || by < 8 || by == 0x7E);
+    } else if constexpr (F8) {
+      uint8_t* o = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + row;
+      *reinterpret_cast<uint2*>(o + e0) = pack8_e4m3(x, is_v ? sv8 : sk8);
+      *reinterpret_cast<uint2*>(o + e1) = pack8_e4m3(y, is_v ? sv8 : sk8);
+    } else {
+      __half* o = static_cast<__half*>(is_v ? P.v_cache : P.k_cache) + row;
+      *reinterpret_cast<uint4*>(o + e0) = turn ? pack8(x) : u0;
+      *reinterpret_cast<uint4*>(o + e1) = turn ? pack8(y) : u1;
+    }
+  }
 }
 
 template <int KVB, bool PAIRS, bool AXES>
@@ -355,6 +355,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
   }
 }
 
+// Whether a position that token t's pairs first, first + step .. go by lies outside the table.
+__device__ __forceinline__ bool off_table(const RopeAppendParams& P, int t, int first, int step) {
+  bool off = false;
+  for (int i = first; i < P.rotary_dim / 2; i += step) {
+    const int axis = P.pair_axes[i];
+    const int p = axis >= 0 && axis < P.num_axes ? P.positions[(size_t)axis * P.num_tokens + t] : -1;
+    off |= p < 0 || p >= P.max_positions;
+  }
+  return off;
+}
+
 // The same for many tokens, kRopeRun of them a CTA: their sequences, positions,
 // blocks and cosines are looked up side by side first and kept in shared memory,
 // so that those chains of dependent loads are paid once a run, not once a token;
@@ -370,16 +381,6 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_kv_append_rope_
 // 153, seven CTAs an SM 84 and 135, ten 142 and 287.  The quotients that codes are
 // rounded from go by reciprocals where both neighbours of the reciprocal give the
 // same codes, else by IEEE divisions (all by divisions, a token a CTA: 125 for E4M3).
-// Whether a position that token t's pairs first, first + step .. go by lies outside the table.
-__device__ __forceinline__ bool off_table(const RopeAppendParams& P, int t, int first, int step) {
-  bool off = false;
-  for (int i = first; i < P.rotary_dim / 2; i += step) {
-    const int axis = P.pair_axes[i];
-    const int p = axis >= 0 && axis < P.num_axes ? P.positions[(size_t)axis * P.num_tokens + t] : -1;
-    off |= p < 0 || p >= P.max_positions;
-  }
-  return off;
-}
 constexpr int kRopeRun = 4;
 constexpr int kRopeAhead = 4;  // places a thread has for heads on their way
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
