@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/paged_decode.h"
+#include "pkd_append_rule.h"
 #include "pkd_serving.cuh"
 
 namespace {
@@ -16,7 +17,6 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 pkd_status launched() { return cudaGetLastError() == cudaSuccess ? PKD_OK : PKD_ERR_LAUNCH; }
 
-constexpr int kRopeRunTokens = 16;     // tokens an SM from which the append takes runs of them
 constexpr int kMaxRopeHeadDim = 512;  // 16 dims a thread, at least four heads in flight
 
 pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long long q_stride, long long k_stride,
@@ -90,15 +90,14 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   p.v_scale = v_scale;
   p.error_word = error_word;
   axes = axes && rotary_dim > 0;
-  // runs of tokens where there are enough for four such CTAs an SM: fewer tokens are
-  // latency, 7.1 us for 128 of them a CTA each
-  bool run = num_tokens >= kRopeRunTokens * 64;  // (fewer than sm_103a's SMs: a step's call asks nothing)
+  bool run = num_tokens >= pkd::kRopeRunTokens * 64;  // (fewer than sm_103a's SMs: a step's call asks nothing)
   if (run) {
     int sms = 0, dev = 0;
     if (pkd::failed(cudaGetDevice(&dev)) ||
         pkd::failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0)
       sms = 148;
-    run = num_tokens >= kRopeRunTokens * sms;
+    run = pkd::takes_runs(num_tokens / sms, q_row + 2 * kv_row, 2 * kv_row, kv, interleaved != 0,
+                          2 * rotary_dim > head_dim, axes);
   }
 #define PKD_APPEND(FN_, KVB_)                                                      \
   (interleaved ? (axes ? pkd::FN_<KVB_, true, true> : pkd::FN_<KVB_, true, false>) \

@@ -376,8 +376,8 @@ __device__ __forceinline__ bool off_table(const RopeAppendParams& P, int t, int 
 //
 // Prompts of 28842 tokens, 40 q and 8 kv heads, three axes: 4-bit caches 137 us, 5.4
 // TB/s (one ahead in registers 156); 20082 tokens, 32 and 8, E4M3, three axes: 82
-// us, 5.5 TB/s (97).  fp16, 28842 tokens, one axis: 134 us, 6.2 TB/s (with the
-// copies 172).  Two ahead 83 and 138, five 91 and 153; runs of eight tokens 91 and
+// us, 5.5 TB/s (97).  fp16, 28842 tokens, three axes: 139 us, one axis 134, as with
+// a token a CTA (with the copies 172); which calls come here: takes_runs.  Two ahead 83 and 138, five 91 and 153; runs of eight tokens 91 and
 // 153, seven CTAs an SM 84 and 135, ten 142 and 287.  The quotients that codes are
 // rounded from go by reciprocals where both neighbours of the reciprocal give the
 // same codes, else by IEEE divisions (all by divisions, a token a CTA: 125 for E4M3).
