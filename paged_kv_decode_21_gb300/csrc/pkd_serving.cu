@@ -88,6 +88,8 @@ pkd_status append_rope(const void* q, const void* k_new, const void* v_new, long
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  p.k8 = pkd::e4m3_scale(k_scale);
+  p.v8 = pkd::e4m3_scale(v_scale);
   p.error_word = error_word;
   axes = axes && rotary_dim > 0;
   bool run = num_tokens >= pkd::kRopeRunTokens * 64;  // (fewer than sm_103a's SMs: a step's call asks nothing)
