@@ -714,7 +714,9 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
 // K's and V's, four in flight a lane; warps do not wait for one another, so one's
 // look-ups (three dependent loads) run beside the others' copies.
 // Bound by HBM, by 128- and 256-byte pieces in no order: 48 x 8 x 2048 rows of E4M3
-// 71 us, 5.8 TB/s, 32 x 8 x 1024 of fp16 47 us, 5.8 TB/s (256 threads that look up
+// 71 us, 5.8 TB/s, 32 x 8 x 1024 of fp16 47 us, 5.8 TB/s.  4-bit rows lie in pieces of
+// 16 bytes, half a sector each, one of 8: 48 x 8 x 2048 of them 122 us, 1.9 TB/s of
+// their bytes (256 threads that look up
 // together first, eight pieces in flight: 78 and 48; 10 or 12 CTAs an SM: 72 and 76;
 // six pieces in flight: 73).
 struct CompactParams {

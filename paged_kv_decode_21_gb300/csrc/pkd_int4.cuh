@@ -168,12 +168,16 @@ __device__ __forceinline__ uint32_t transposed_8x8(uint32_t x) {
 // Query rows are the group's heads times up to `q_chunk` query tokens, NT tiles
 // of 8 of them: 1, 2 or 4.  With 4 the Q fragments stay in shared memory.
 //
-// Bound by instructions: of a 16-token subtile's 356 (one row tile) half are the
-// codes' way into fp16 pairs, 16 the products; 0.58 a cycle and scheduler, HBM at
-// half its rate.  128 x 32/8 heads, 512-4096 tokens, 83 us; 32 x 40/8, 16K-32K, 180;
-// the bytes alone 50 and 135.  Four row tiles (48 x 4 tokens x 28/4): 714
-// instructions, 0.38 a cycle of the 8 warps that their accumulators leave room
-// for.  Three or five CTAs an SM for one row tile: 207 and 216 against 193 us at 16K-32K;
+// Bound by its instructions' dependencies and pipes.  Of a 16-token subtile's 356
+// (one row tile) half are the codes' way into fp16 pairs, 16 the products.  They
+// fill 0.59 of a scheduler's cycles, HBM at half its rate: the registers leave 3.9
+// warps a scheduler, and of the 6.5 cycles from one instruction of a warp to its
+// next 1.3 wait for the one before, 1.1 for another warp's turn, 1.0 for a pipe
+// (ALU 50%, fp16 31%, tensor 23% busy), 0.8 for loads, 0.6 for the dispatch.
+// 128 x 32/8 heads, 512-4096 tokens, 83 us; 32 x 40/8, 16K-32K, 180; the bytes
+// alone 50 and 135.  Four row tiles (48 x 4 tokens x 28/4): 714 instructions, 0.38 a
+// cycle of the 1.8 warps a scheduler that their accumulators leave room for, 1.6 of
+// 4.7 cycles waiting for the instruction before, 0.5 for loads.  Three or five CTAs an SM for one row tile: 207 and 216 against 193 us at 16K-32K;
 // chunks of two row tiles for 28 rows: +6%; the next scores beside a subtile's
 // P V: no change; K scales spread by permutations, or shifts as multiplications: +5%.
 struct Int4Params {
