@@ -263,7 +263,8 @@ __device__ __forceinline__ void rope_head(const RopeAppendParams& P, const RopeL
 // (One axis into E4M3 caches: seven CTAs an SM, as 64 registers spill.  1, 256, 1024 and 8192 tokens of 32/8 heads 3.0,
 // 3.7, 5.3 and 36 us; eight 3.1, 3.8, 5.45 and 34.5.)
 template <int KVB, bool PAIRS, bool AXES>
-__global__ void __launch_bounds__(kRopeThreads, KVB == 1 && !AXES ? 7 : kRopeCtas) paged_kv_append_rope_kernel(const RopeAppendParams P) {
+__global__ void __launch_bounds__(kRopeThreads, KVB == 1 && !AXES ? 7 : kRopeCtas)
+    paged_kv_append_rope_kernel(const RopeAppendParams P) {
   const RopeLane lane = rope_lane<PAIRS>(P);
   const int R = P.rotary_dim, c = lane.c, slots = lane.slots, e0 = lane.e0, e1 = lane.e1;
   const bool rot = lane.rot;
@@ -380,11 +381,12 @@ __device__ __forceinline__ bool off_table(const RopeAppendParams& P, int t, int 
 //
 // Prompts of 28842 tokens, 40 q and 8 kv heads, three axes: 4-bit caches 137 us, 5.4
 // TB/s (one ahead in registers 156); 20082 tokens, 32 and 8, E4M3, three axes: 82
-// us, 5.5 TB/s (97).  fp16, 28842 tokens, three axes: 139 us, one axis 134, as with
-// a token a CTA (with the copies 172); which calls come here: takes_runs.  Two ahead 83 and 138, five 91 and 153; runs of eight tokens 91 and
-// 153, seven CTAs an SM 84 and 135, ten 142 and 287.  The quotients that codes are
-// rounded from go by reciprocals where both neighbours of the reciprocal give the
-// same codes, else by IEEE divisions (all by divisions, a token a CTA: 125 for E4M3).
+// us, 5.5 TB/s (97).  fp16, 28842 tokens, three axes: 139 us; one axis 134, as with a
+// token a CTA (with the copies 172).  Which calls come here: takes_runs.  Two ahead
+// 83 and 138, five 91 and 153; runs of eight tokens 91 and 153, seven CTAs an SM 84
+// and 135, ten 142 and 287.  The quotients that codes are rounded from go by
+// reciprocals where both neighbours of the reciprocal give the same codes, else by
+// IEEE divisions (all by divisions, a token a CTA: 125 for E4M3).
 constexpr int kRopeRun = 4;
 constexpr int kRopeAhead = 4;  // places a thread has for heads on their way
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
